@@ -13,8 +13,10 @@ The functions carry the C names:
     dqn_set_weights, dqn_set_epsilon, dqn_collect, dqn_destroy
     (include/dqn.h), and
     per_create, per_sample, per_gather, per_update, per_destroy
-    (include/per.h),
-plus helpers: `alloc_outputs`, `alloc_dqn_outputs` and the `Collector` and
+    (include/per.h).
+The operators of a policy with memory (include/policy.h) are `recurrence` and
+`recurrence_step`; they take part in torch's autograd (policy.py).
+There are also helpers: `alloc_outputs`, `alloc_dqn_outputs` and the `Collector` and
 `DqnCollector` and `PerSampler` convenience classes.
 """
 from __future__ import annotations
@@ -143,6 +145,13 @@ def load_library(path: str = LIB_PATH):
                  "dqn_set_weights", "dqn_set_epsilon", "dqn_collect", "per_create", "per_sample", "per_gather",
                  "per_update"):
         getattr(L, name).restype = C.c_int
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        pass
+    else:
+        from . import policy
+        policy.declare(L)
     _lib = L
     return L
 
@@ -614,3 +623,15 @@ class PerSampler:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------- policies with memory
+_POLICY = ("recurrence", "recurrence_step")
+
+
+def __getattr__(name):
+    # torch is imported only with the first function that needs it
+    if name in _POLICY:
+        from . import policy
+        return getattr(policy, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

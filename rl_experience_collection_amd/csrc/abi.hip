@@ -21,6 +21,7 @@
 #include "per.hpp"
 #include "gae.hpp"
 #include "pack.hpp"
+#include "policy.hpp"
 
 // The fixed scratch of gae_scan_noalloc (see NoAllocDevice below): 4 MiB +
 // 256 bytes per device.
@@ -361,6 +362,17 @@ struct rollout_s {
   size_t stamp_words = 0;
   bool stamping = false;
 };
+
+// The error text of the entry points in other files; a C caller must not
+// see an exception of the text's own allocation.
+int rl::set_error(int code, const char* text) {
+  try {
+    g_last_error = text;
+  } catch (...) {
+    g_last_error.clear();
+  }
+  return code;
+}
 
 extern "C" {
 

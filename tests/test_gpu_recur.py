@@ -1,0 +1,303 @@
+"""The gated linear recurrence (include/policy.h, recur_*) on the GPU against
+its 64-bit form, element by element within the bound that policy_ref derives."""
+import numpy as np
+import pytest
+import torch
+
+import policy_ref as ref
+from parity import gpu_available
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not gpu_available(), reason="needs an MI355X")]
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def rx():
+    import rl_experience_collection_amd as rx
+    return rx
+
+
+def inputs(L, N, D, name, sig, p_done, seed, h0=True):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(L, N, D, generator=g).to(TYPES[name])
+    gate = torch.randn(L, N, D, generator=g) * 2 + 1
+    gate = (gate if sig else torch.sigmoid(gate) * torch.sign(gate)).to(TYPES[name])
+    return dict(x=x, gate=gate, h0=torch.randn(N, D, generator=g) if h0 else None,
+                dones=(torch.rand(L, N, generator=g) < p_done).to(torch.uint8) if p_done else None,
+                dh=torch.randn(L, N, D, generator=g).to(TYPES[name]),
+                dl=torch.randn(N, D, generator=g))
+
+
+def f64(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+def within(got, want, bound, what):
+    got = f64(got)
+    assert got.shape == want.shape
+    off = np.abs(got - want) - bound
+    assert (off <= 0).all(), (what, float(off.max()), np.unravel_index(off.argmax(), off.shape))
+
+
+def check(rx, i, name, sig, gpu=None, train=True):
+    """gpu: the device tensors to pass (other strides), by default copies."""
+    form = "sigmoid" if sig else "linear"
+    gpu = dict({k: None if v is None else v.cuda() for k, v in i.items()}, **(gpu or {}))
+    n = {k: f64(v) for k, v in i.items()}
+    want = ref.recurrence_grad(n["x"], n["gate"], n["h0"], n["dones"], n["dh"], n["dl"], sig, name)
+    leaves = [gpu[k].detach().requires_grad_() for k in ("x", "gate", "h0") if gpu[k] is not None]
+    h, last = rx.recurrence(leaves[0], leaves[1], leaves[2] if len(leaves) > 2 else None,
+                            gpu["dones"], form=form)
+    within(h, want["h"], want["eh"], "h")
+    within(last, want["h_last"], want["elast"], "h_last")
+    if train:
+        g = torch.autograd.grad((h, last), leaves, (gpu["dh"], gpu["dl"]))
+        within(g[0], want["dx"], want["edx"], "dx")
+        within(g[1], want["dgate"], want["edg"], "dgate")
+        if len(leaves) > 2:
+            within(g[2], want["dh0"], want["edh0"], "dh0")
+    return h, last
+
+
+SIZES = [(1, 1, 1), (2, 3, 5), (7, 1, 64), (8, 2, 65), (9, 4, 6), (63, 1, 1), (64, 3, 33),
+         (65, 2, 128), (129, 5, 7), (500, 16, 45), (513, 1, 130), (1500, 2, 70), (2049, 1, 3),
+         (4097, 3, 1)]
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("sig", [False, True])
+@pytest.mark.parametrize("L,N,D", SIZES)
+def test_matches_the_formula(rx, L, N, D, sig, name):
+    check(rx, inputs(L, N, D, name, sig, 0.05, L * 31 + D), name, sig)
+
+
+@pytest.mark.parametrize("p_done", [0.0, 0.5, 1.0])
+@pytest.mark.parametrize("L,N,D", [(70, 3, 10), (1100, 2, 6)])
+def test_dones(rx, L, N, D, p_done):
+    check(rx, inputs(L, N, D, "f32", True, p_done, 5), "f32", True)
+    check(rx, inputs(L, N, D, "bf16", False, p_done, 6, h0=False), "bf16", False)
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+def test_wide_rows_of_many_episodes(rx, name):
+    check(rx, inputs(33, 700, 66, name, True, 0.02, 8), name, True)
+
+
+@pytest.mark.parametrize("L", [50, 1300])
+@pytest.mark.parametrize("name", ["f32", "f16"])
+def test_strides(rx, L, name):
+    """Batch-first, a slice of wider rows, an odd offset, a gate shared by
+    every row: the same results."""
+    i = inputs(L, 3, 12, name, True, 0.05, 9)
+    bf = lambda t: t.transpose(0, 1).contiguous().cuda().transpose(0, 1)
+    check(rx, i, name, True, dict(x=bf(i["x"]), gate=bf(i["gate"])))
+
+    def sliced(t, lo):
+        wide = torch.full((L, 3, 19), 7.0, dtype=t.dtype, device="cuda")
+        wide[:, :, lo:lo + 12] = t.cuda()
+        return wide[:, :, lo:lo + 12]
+
+    check(rx, i, name, True, dict(x=sliced(i["x"], 4), gate=sliced(i["gate"], 3),
+                                  dh=sliced(i["dh"], 1)))
+    shared = dict(i, gate=i["gate"][:, :1].expand(L, 3, 12))
+    check(rx, shared, name, True, dict(gate=i["gate"][:, :1].cuda().expand(L, 3, 12)))
+    # a gradient that is one row repeated (the sum's), and none at all for h
+    rep = dict(i, dh=i["dh"][:1, :1].expand(L, 3, 12))
+    check(rx, rep, name, True, dict(dh=i["dh"][:1, :1].cuda().expand(L, 3, 12)))
+
+
+def test_gradient_of_a_broadcast_gate_is_the_sum(rx):
+    i = inputs(40, 6, 8, "f32", True, 0.1, 10)
+    one = i["gate"][:, :1].cuda().requires_grad_()
+    h, last = rx.recurrence(i["x"].cuda(), one.expand(40, 6, 8), i["h0"].cuda(), i["dones"].cuda())
+    g, = torch.autograd.grad(h, one, i["dh"].cuda())
+    n = {k: f64(v) for k, v in i.items()}
+    w = ref.recurrence_grad(n["x"], np.repeat(n["gate"][:, :1], 6, 1), n["h0"], n["dones"], n["dh"],
+                            None, True, "f32")
+    # six values summed by torch: five more roundings of their magnitudes
+    bound = w["edg"].sum(1) + 5 * ref.U * np.abs(w["dgate"]).sum(1)
+    within(g[:, 0], w["dgate"].sum(1), bound, "dgate")
+
+
+@pytest.mark.parametrize("L", [40, 1300])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_a_finished_episode_stays_behind_its_done(rx, L, bad):
+    """Row 0 goes bad at step 5 and is done at step 9: from step 10 on its
+    states, and up to step 9 its neighbours, are the clean run's bits; the
+    gradients of the clean steps likewise."""
+    i = inputs(L, 2, 3, "f32", True, 0.0, 11)
+    i["dones"] = torch.zeros(L, 2, dtype=torch.uint8)
+    i["dones"][9, 0] = 1
+    c = {k: v.cuda() for k, v in i.items()}
+    h, last = rx.recurrence(c["x"], c["gate"], c["h0"], c["dones"])
+    x = c["x"].clone()
+    x[5, 0, 1] = bad
+    hb, lastb = rx.recurrence(x, c["gate"], c["h0"], c["dones"])
+    torch.cuda.synchronize()
+    assert torch.equal(hb[10:], h[10:]) and torch.equal(lastb, last)
+    assert torch.equal(hb[:5], h[:5]) and torch.equal(hb[:, 1], h[:, 1])
+    assert not torch.isfinite(hb[5:10, 0, 1]).any()
+
+    def grads(x, dh):
+        leaves = [x.clone().requires_grad_(), c["gate"].clone().requires_grad_(),
+                  c["h0"].clone().requires_grad_()]
+        out = rx.recurrence(*leaves, c["dones"])
+        return torch.autograd.grad(out, leaves, (dh, c["dl"]))
+
+    clean = grads(c["x"], c["dh"])
+    dh = c["dh"].clone()
+    dh[20, 0, 1] = bad  # behind the done, seen from steps up to 9
+    g = grads(x, dh)
+    assert torch.equal(g[0][:10], clean[0][:10])
+    assert torch.equal(g[1][:5], clean[1][:5]) and torch.equal(g[2], clean[2])
+    assert torch.equal(g[1][10:, 0, 0], clean[1][10:, 0, 0])
+    assert not torch.isfinite(g[0][10:21, 0, 1]).any()
+
+
+def test_extreme_gates(rx):
+    """Gates far out on both sides, infinite ones among them: a is 0 or 1."""
+    L, N, D = 20, 2, 4
+    i = inputs(L, N, D, "f32", True, 0.0, 12)
+    i["gate"][::4] = 300.0
+    i["gate"][1::4] = -300.0
+    i["gate"][2::8] = float("inf")
+    i["gate"][6::8] = -float("inf")
+    check(rx, i, "f32", True)
+
+
+def test_a_gate_that_is_not_a_number_reaches_its_channel_only(rx):
+    i = inputs(30, 2, 4, "f32", True, 0.0, 13)
+    c = {k: v.cuda() for k, v in i.items() if v is not None}
+    h, _ = rx.recurrence(c["x"], c["gate"], c["h0"])
+    c["gate"][3, 1, 2] = float("nan")
+    hb, _ = rx.recurrence(c["x"], c["gate"], c["h0"])
+    assert torch.isnan(hb[3:, 1, 2]).all()
+    hb[3:, 1, 2] = h[3:, 1, 2]
+    assert torch.equal(h, hb)
+
+
+def test_cut_rollouts_compose(rx):
+    i = inputs(300, 4, 6, "f32", True, 0.05, 14)
+    c = {k: v.cuda() for k, v in i.items()}
+    n = {k: f64(v) for k, v in i.items()}
+    w = ref.recurrence(n["x"], n["gate"], n["h0"], n["dones"], True, "f32")
+    state = c["h0"]
+    for lo, hi in [(0, 1), (1, 10), (10, 10), (10, 200), (200, 300)]:
+        h, state = rx.recurrence(c["x"][lo:hi], c["gate"][lo:hi], state, c["dones"][lo:hi])
+        within(h, w["h"][lo:hi], w["eh"][lo:hi], (lo, hi))
+    within(state, w["h_last"], w["elast"], "h_last")
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N,D", [(1, 1), (3, 7), (128, 128), (1000, 45)])
+@pytest.mark.parametrize("sig", [False, True])
+def test_steps_follow_the_scan(rx, N, D, name, sig):
+    i = inputs(6, N, D, name, sig, 0.3, 15)
+    c = {k: v.cuda() for k, v in i.items()}
+    n = {k: f64(v) for k, v in i.items()}
+    w = ref.recurrence(n["x"], n["gate"], n["h0"], n["dones"], sig, name)
+    form = "sigmoid" if sig else "linear"
+    state, place = c["h0"], c["h0"].clone()
+    for t in range(6):
+        resets = c["dones"][t - 1] if t else None
+        h, state = rx.recurrence_step(c["x"][t], c["gate"][t], state, resets, form)
+        within(h, w["h"][t], w["eh"][t], t)
+        rx.recurrence_step(c["x"][t], c["gate"][t], place, resets, form, out_state=place)
+        assert torch.equal(place, state)
+
+
+def test_empty_sizes(rx):
+    h0 = torch.randn(3, 4, device="cuda")
+    h, last = rx.recurrence(torch.zeros(0, 3, 4, device="cuda"), torch.zeros(0, 3, 4, device="cuda"), h0)
+    assert h.shape == (0, 3, 4) and torch.equal(last, h0)
+    _, last = rx.recurrence(torch.zeros(0, 3, 4, device="cuda"), torch.zeros(0, 3, 4, device="cuda"))
+    assert torch.equal(last, torch.zeros_like(last))
+    for shape in [(5, 0, 4), (5, 3, 0)]:
+        z = torch.zeros(shape, device="cuda", requires_grad=True)
+        h, last = rx.recurrence(z, z)
+        assert h.shape == shape
+        torch.autograd.grad(h.sum() + last.sum(), z)
+    l0 = h0.clone().requires_grad_()
+    h, last = rx.recurrence(torch.zeros(0, 3, 4, device="cuda"), torch.zeros(0, 3, 4, device="cuda"), l0)
+    g, = torch.autograd.grad(last, l0, h0)
+    assert torch.equal(g, h0)
+
+
+def test_rows_between_the_outputs_are_left_alone(rx):
+    """The C entry points with output rows wider apart than D."""
+    import ctypes as C
+    from rl_experience_collection_amd import policy
+    L, N, D, R = 70, 3, 5, 8
+    i = inputs(L, N, D, "f32", True, 0.05, 16)
+    c = {k: v.cuda() for k, v in i.items()}
+    out = torch.full((3, L + 1, N, R), 7.0, device="cuda")
+    a = policy.RecurArgs(steps=L, rows=N, width=D, dtype=0, form=1, x_step=N * D, x_row=D,
+                         gate_step=N * D, gate_row=D, h_step=N * R, h_row=R, x=c["x"].data_ptr(),
+                         gate=c["gate"].data_ptr(), dones=c["dones"].data_ptr(), h=out[0].data_ptr())
+    s = torch.cuda.current_stream().cuda_stream
+    assert rx.load_library().recur_forward(C.byref(a), s) == 0
+    g = policy.RecurGradArgs(steps=L, rows=N, width=D, dtype=0, form=1, x_step=N * D, x_row=D,
+                             gate_step=N * D, gate_row=D, h_step=N * R, h_row=R, dh_step=N * D,
+                             dh_row=D, dx_step=N * R, dx_row=R, dgate_step=N * R, dgate_row=R,
+                             x=c["x"].data_ptr(), gate=c["gate"].data_ptr(), h=out[0].data_ptr(),
+                             dones=c["dones"].data_ptr(), dh=c["dh"].data_ptr(),
+                             dx=out[1].data_ptr(), dgate=out[2].data_ptr())
+    assert rx.load_library().recur_backward(C.byref(g), s) == 0
+    torch.cuda.synchronize()
+    assert (out[:, L] == 7).all() and (out[:, :, :, D:] == 7).all()
+    n = {k: f64(v) for k, v in i.items()}
+    w = ref.recurrence_grad(n["x"], n["gate"], None, n["dones"], n["dh"], None, True, "f32")
+    within(out[0, :L, :, :D], w["h"], w["eh"], "h")
+    within(out[1, :L, :, :D], w["dx"], w["edx"], "dx")
+    within(out[2, :L, :, :D], w["dgate"], w["edg"], "dgate")
+
+
+def test_repeats_are_bit_identical_and_streams_do_not_mix(rx):
+    """Two streams at once on their own data, against each alone."""
+    data = [{k: v.cuda() for k, v in inputs(3000, 2, 40, "bf16", True, 0.02, s).items()} for s in (1, 2)]
+    alone = [rx.recurrence(c["x"], c["gate"], c["h0"], c["dones"]) for c in data]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in data]
+    got = []
+    for _ in range(4):
+        for c, st in zip(data, streams):
+            with torch.cuda.stream(st):
+                got.append(rx.recurrence(c["x"], c["gate"], c["h0"], c["dones"]))
+    torch.cuda.synchronize()
+    for k, (h, last) in enumerate(got):
+        assert torch.equal(h, alone[k % 2][0]) and torch.equal(last, alone[k % 2][1])
+
+
+@pytest.mark.parametrize("L,N,D", [(40, 5, 9), (2500, 1, 50)])
+def test_captured_training_pass(rx, L, N, D):
+    """Two graphs, each a forward and a backward pass, replayed in turn with
+    eager calls between: every replay gives the eager bits."""
+    data = [inputs(L, N, D, "bf16", True, 0.05, s) for s in (21, 22, 23)]
+    buf = {k: v.cuda() for k, v in data[0].items()}
+
+    def once(c):
+        leaves = [c[k].detach().requires_grad_() for k in ("x", "gate", "h0")]
+        out = rx.recurrence(*leaves, c["dones"])
+        return [t.detach() for t in out] + list(torch.autograd.grad(out, leaves, (c["dh"], c["dl"])))
+
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        once(buf)
+    st.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            out = once(buf)
+        graphs.append((g, out))
+    for d in data + data:
+        for k, v in d.items():
+            buf[k].copy_(v)
+        want = once({k: v.cuda() for k, v in d.items()})
+        for g, out in graphs:
+            g.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(out, want):
+                assert torch.equal(a, b)
