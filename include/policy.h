@@ -1,7 +1,9 @@
 /*
  * policy.h -- C ABI of the operators of a policy with memory in librollout.so
  * (gfx950), from the previous action to the next action's logits:
+ *   embed_*   scaled embedding lookup, its gradient summed by sorted index
  *   recur_*   gated linear recurrence over a rollout, its gradient, its step
+ *   logits_*  penalties, bias and mask on logits, and their gradient
  * Same conventions as rollout.h: DEVICE buffers owned by the caller,
  * asynchronous on the given stream (NULL = the default stream), ROLLOUT_OK or
  * a negative ROLLOUT_E* code with the message in rollout_last_error(), checks
@@ -49,7 +51,7 @@ typedef enum { POLICY_F32 = 0, POLICY_BF16 = 1, POLICY_F16 = 2 } policy_dtype;
 typedef enum { RECUR_LINEAR = 0, RECUR_SIGMOID = 1 } recur_form;
 
 typedef struct {
-  int32_t steps, rows, width; /* L, N, D >= 0; N * D < 2^31 */
+  int32_t steps, rows, width; /* L, N, D >= 0; N * D < 2^29 */
   int32_t dtype;              /* policy_dtype */
   int32_t form;               /* recur_form */
   int64_t x_step, x_row;      /* strides in elements */
@@ -115,6 +117,91 @@ int recur_step(int32_t rows, int32_t width, int32_t dtype, int32_t form, const v
                int64_t x_row, const void *gate, int64_t gate_row, const float *state,
                const uint8_t *resets, void *h, int64_t h_row, float *new_state,
                void *hip_stream);
+
+/* --------------------------------------------------------------- embedding
+ * out[i] = scale * weight[index[i]], rounded once; an index outside [0, vocab)
+ * (an episode's first step has no previous action: -1) gives a row of zeros
+ * and takes no part in the gradient.  weight: [vocab][width] with rows
+ * weight_row elements apart; out: [count][width], rows out_row apart; index:
+ * [count] of index_bytes 4 (i32) or 8 (i64).  The gradient is dense:
+ *   dweight[v] = scale * sum of dout[i] over the i with index[i] == v,
+ * summed in fp32 in ascending order of i within fixed pieces that depend on
+ * the indices and sizes alone (results are deterministic), rounded once; rows
+ * without an index are zero.  vocab and count are at most 2^31 - 2, width
+ * at most 2^24.  dweight must not overlap dout or index. */
+int embed_forward(int32_t dtype, const void *weight, int64_t vocab, int32_t width,
+                  int64_t weight_row, const void *index, int32_t index_bytes, int64_t count,
+                  float scale, void *out, int64_t out_row, void *hip_stream);
+/* Workspace in bytes of embed_backward, or a negative ROLLOUT_E* code. */
+int64_t embed_workspace(int32_t dtype, int64_t vocab, int32_t width, int64_t count);
+/* count = 0 clears dweight.  Errors of both: ROLLOUT_EINVAL (NULL or
+ * misaligned buffer, unknown dtype or index size, negative or too large a
+ * size, rows closer than width (a row stride of 0 repeats one row of dout),
+ * workspace too small), ROLLOUT_EHIP. */
+int embed_backward(int32_t dtype, const void *dout, int64_t dout_row, const void *index,
+                   int32_t index_bytes, int64_t count, int64_t vocab, int32_t width, float scale,
+                   void *dweight, int64_t dweight_row, void *workspace, int64_t workspace_bytes,
+                   void *hip_stream);
+
+/* ------------------------------------------------------------------ logits
+ * With c = the times token v occurs among the first history_len[r] (all
+ * history_width when NULL; clamped into 0 .. history_width) entries of row
+ * r's history, entries outside [0, vocab) not counted, and z = logits[r][v]:
+ *   z = c > 0 ? (z > 0 ? z / repetition : z * repetition) : z
+ *   z = z - (c > 0 ? presence : 0) - frequency * c
+ *   z = z + bias[v]
+ *   out[r][v] = allowed(r, v) ? z : -infinity,
+ * evaluated in fp32, rounded once.  A row with nothing allowed is all
+ * -infinity.  What a masked place holds (NaN included) does not matter.
+ * The gradient: dlogits = allowed ? dout * (c > 0 ? (z > 0 ? 1 / repetition :
+ * repetition) : 1) : 0 and dbias[v] = the sum of dout over the rows that
+ * allow v, in fp32, in a fixed order.
+ *
+ * The penalties are per row where the _rows array [rows] f32 is given, else
+ * the scalar for every row.  repetition must be positive.  The mask is
+ *   LOGITS_MASK_BYTES  [mask_count][vocab] u8, rows mask_row bytes apart,
+ *                      not 0 = allowed
+ *   LOGITS_MASK_BITS   [mask_count][ceil(vocab / 32)] u32, rows mask_row words
+ *                      apart, bit v % 32 of word v / 32 set = allowed
+ * and row r uses mask row mask_rows[r] (a value outside [0, mask_count) allows
+ * everything) or, where mask_rows is NULL, r (mask_count = rows) or 0
+ * (mask_count = 1).  out may be logits itself (same rows, same stride), and
+ * dlogits may be dout. */
+typedef enum { LOGITS_MASK_NONE = 0, LOGITS_MASK_BYTES = 1, LOGITS_MASK_BITS = 2 } logits_mask;
+
+typedef struct {
+  int64_t rows;         /* R >= 0 */
+  int32_t vocab;        /* V, 0 .. 2^24 */
+  int32_t dtype;        /* policy_dtype of logits, out, dout, dlogits */
+  const void *logits;   /* [R][V], rows logits_row elements apart */
+  int64_t logits_row;
+  const float *bias;    /* NULL: none; rows bias_row apart (0: one for all) */
+  int64_t bias_row;
+  const int32_t *history; /* NULL: none; [R][history_width], rows history_row apart */
+  int64_t history_row;
+  const int32_t *history_len;  /* NULL: all of the width */
+  int32_t history_width;
+  int32_t mask_kind;    /* logits_mask */
+  float repetition, presence, frequency; /* 1, 0, 0: no penalty */
+  const float *repetition_rows, *presence_rows, *frequency_rows; /* NULL: the scalars */
+  const void *mask;
+  int64_t mask_row, mask_count;
+  const int32_t *mask_rows; /* NULL: row r, or 0 where mask_count is 1 */
+} logits_args;
+
+/* Errors: ROLLOUT_EINVAL (NULL or misaligned buffer, unknown dtype or mask
+ * kind, a negative or too large a size, rows closer than their width, a scalar repetition
+ * that is not positive and finite, mask_count neither 1 nor rows without
+ * mask_rows, workspace too small), ROLLOUT_EHIP. */
+int logits_forward(const logits_args *args, void *out, int64_t out_row, void *hip_stream);
+/* Workspace in bytes of logits_backward with dbias (none is needed without). */
+int64_t logits_workspace(int64_t rows, int32_t vocab);
+/* dlogits or dbias [vocab] may be NULL (not computed); of args, the bias and
+ * the presence and frequency penalties are not read, and the logits only
+ * with a history and a repetition other than the scalar 1. */
+int logits_backward(const logits_args *args, const void *dout, int64_t dout_row, void *dlogits,
+                    int64_t dlogits_row, float *dbias, void *workspace, int64_t workspace_bytes,
+                    void *hip_stream);
 
 #ifdef __cplusplus
 }

@@ -14,8 +14,9 @@ The functions carry the C names:
     (include/dqn.h), and
     per_create, per_sample, per_gather, per_update, per_destroy
     (include/per.h).
-The operators of a policy with memory (include/policy.h) are `recurrence` and
-`recurrence_step`; they take part in torch's autograd (policy.py).
+The operators of a policy with memory (include/policy.h) are `embed`,
+`recurrence`, `recurrence_step` and `shape_logits` (policy.py); all but the
+step take part in torch's autograd.
 There are also helpers: `alloc_outputs`, `alloc_dqn_outputs` and the `Collector` and
 `DqnCollector` and `PerSampler` convenience classes.
 """
@@ -626,7 +627,7 @@ class PerSampler:
 
 
 # ---------------------------------------------------------- policies with memory
-_POLICY = ("recurrence", "recurrence_step")
+_POLICY = ("embed", "recurrence", "recurrence_step", "shape_logits")
 
 
 def __getattr__(name):

@@ -9,7 +9,7 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(os.path.dirname(PKG), "_build", "rollout")
 LIB = os.path.join(PKG, "librollout.so")
 SOURCES = ["abi.hip", "pack.hip", "rollout.hip", "value.hip", "gae.hip", "dqn.hip", "per.hip",
-           "policy_abi.hip", "recur.hip"]
+           "policy_abi.hip", "embed.hip", "recur.hip", "logits.hip"]
 # measurement kernels used by bench.py only, in a library of their own
 PROBE_LIB = os.path.join(PKG, "libbenchprobes.so")
 PROBE_SOURCES = ["bench_probes.hip"]

@@ -48,8 +48,8 @@ int check_recur_sizes(const char* who, int32_t steps, int32_t rows, int32_t widt
   if (steps < 0 || rows < 0 || width < 0)
     return fail(ROLLOUT_EINVAL, "%s: negative size (steps %d, rows %d, width %d)", who, steps, rows,
                 width);
-  if ((int64_t)rows * width >= (int64_t)1 << 31)
-    return fail(ROLLOUT_EINVAL, "%s: rows * width must be below 2^31 (got %d * %d)", who, rows, width);
+  if ((int64_t)rows * width >= (int64_t)1 << 29)
+    return fail(ROLLOUT_EINVAL, "%s: rows * width must be below 2^29 (got %d * %d)", who, rows, width);
   if (!known_dtype(dtype)) return fail(ROLLOUT_EINVAL, "%s: unknown dtype %d", who, dtype);
   return ROLLOUT_OK;
 }
@@ -75,6 +75,77 @@ int check_recur_workspace(const char* who, int32_t steps, int32_t rows, int32_t 
     return fail(ROLLOUT_EINVAL, "%s: workspace of %lld bytes needed, %lld given", who,
                 (long long)need, workspace ? (long long)bytes : 0LL);
   return check_buffer(who, "workspace", workspace, 16);
+}
+
+constexpr int32_t kMaxWidth = 1 << 24;
+constexpr int64_t kMaxCount = ((int64_t)1 << 31) - 2;
+
+int check_embed_sizes(const char* who, int32_t dtype, int64_t vocab, int32_t width, int64_t count) {
+  if (!known_dtype(dtype)) return fail(ROLLOUT_EINVAL, "%s: unknown dtype %d", who, dtype);
+  if (vocab < 0 || vocab > kMaxCount || count < 0 || count > kMaxCount)
+    return fail(ROLLOUT_EINVAL, "%s: vocab and count must be in 0 .. 2^31 - 2 (got %lld, %lld)", who,
+                (long long)vocab, (long long)count);
+  if (width < 0 || width > kMaxWidth)
+    return fail(ROLLOUT_EINVAL, "%s: width must be in 0 .. 2^24 (got %d)", who, width);
+  return ROLLOUT_OK;
+}
+
+int check_index(const char* who, const void* index, int32_t bytes) {
+  if (bytes != 4 && bytes != 8)
+    return fail(ROLLOUT_EINVAL, "%s: index_bytes must be 4 or 8 (got %d)", who, bytes);
+  return check_buffer(who, "index", index, (size_t)bytes);
+}
+
+// Rows of at least `width` elements, one after another.
+int check_rows(const char* who, const char* name, int64_t row, int64_t width) {
+  if (row < width)
+    return fail(ROLLOUT_EINVAL, "%s: rows of %s are %lld apart, closer than their width %lld", who,
+                name, (long long)row, (long long)width);
+  return ROLLOUT_OK;
+}
+
+int check_logits(const char* who, const logits_args* a, bool read_logits) {
+  if (!a) return fail(ROLLOUT_EINVAL, "%s: arguments are NULL", who);
+  if (!known_dtype(a->dtype)) return fail(ROLLOUT_EINVAL, "%s: unknown dtype %d", who, a->dtype);
+  if (a->rows < 0 || a->vocab < 0 || a->vocab > kMaxWidth || a->history_width < 0)
+    return fail(ROLLOUT_EINVAL,
+                "%s: rows and history_width must not be negative, vocab in 0 .. 2^24 (got %lld, %d, %d)",
+                who, (long long)a->rows, a->history_width, a->vocab);
+  if (!(a->repetition > 0.0f && a->repetition <= 3.402823466e38f))
+    return fail(ROLLOUT_EINVAL, "%s: repetition must be positive and finite (got %g)", who,
+                (double)a->repetition);
+  if (a->mask_kind != LOGITS_MASK_NONE && a->mask_kind != LOGITS_MASK_BYTES &&
+      a->mask_kind != LOGITS_MASK_BITS)
+    return fail(ROLLOUT_EINVAL, "%s: unknown mask_kind %d", who, a->mask_kind);
+  if (a->rows == 0 || a->vocab == 0) return ROLLOUT_OK;
+  if (read_logits) {
+    RL_CHECK(check_buffer(who, "logits", a->logits, element_bytes(a->dtype)));
+    RL_CHECK(check_rows(who, "logits", a->logits_row, a->vocab));
+  }
+  RL_CHECK(check_optional(who, "bias", a->bias, 4));
+  if (a->bias && a->bias_row != 0) RL_CHECK(check_rows(who, "bias", a->bias_row, a->vocab));
+  RL_CHECK(check_optional(who, "history", a->history, 4));
+  if (a->history && a->history_row < 0)
+    return fail(ROLLOUT_EINVAL, "%s: negative stride of history", who);
+  RL_CHECK(check_optional(who, "history_len", a->history_len, 4));
+  RL_CHECK(check_optional(who, "repetition_rows", a->repetition_rows, 4));
+  RL_CHECK(check_optional(who, "presence_rows", a->presence_rows, 4));
+  RL_CHECK(check_optional(who, "frequency_rows", a->frequency_rows, 4));
+  if (a->mask_kind != LOGITS_MASK_NONE) {
+    const bool bits = a->mask_kind == LOGITS_MASK_BITS;
+    if (a->mask_count < 0 || a->mask_count > kMaxCount)
+      return fail(ROLLOUT_EINVAL, "%s: mask_count %lld out of range", who, (long long)a->mask_count);
+    RL_CHECK(check_optional(who, "mask_rows", a->mask_rows, 4));
+    if (!a->mask_rows && a->mask_count != 1 && a->mask_count != a->rows)
+      return fail(ROLLOUT_EINVAL, "%s: without mask_rows the mask has 1 or %lld rows (got %lld)", who,
+                  (long long)a->rows, (long long)a->mask_count);
+    if (a->mask_count > 0) {
+      RL_CHECK(check_buffer(who, "mask", a->mask, bits ? 4 : 1));
+      if (a->mask_count > 1)
+        RL_CHECK(check_rows(who, "mask", a->mask_row, bits ? (a->vocab + 31) / 32 : a->vocab));
+    }
+  }
+  return ROLLOUT_OK;
 }
 
 }  // namespace
@@ -158,6 +229,97 @@ int recur_step(int32_t rows, int32_t width, int32_t dtype, int32_t form, const v
   return launched(rl::recur_step_launch(rows, width, dtype, form, x, x_row, gate, gate_row, state,
                                         resets, h, h_row, new_state,
                                         static_cast<hipStream_t>(hip_stream)),
+                  who);
+}
+
+int embed_forward(int32_t dtype, const void* weight, int64_t vocab, int32_t width,
+                  int64_t weight_row, const void* index, int32_t index_bytes, int64_t count,
+                  float scale, void* out, int64_t out_row, void* hip_stream) {
+  const char* who = "embed_forward";
+  RL_CHECK(check_embed_sizes(who, dtype, vocab, width, count));
+  if (count == 0 || width == 0) return ROLLOUT_OK;
+  const size_t eb = element_bytes(dtype);
+  if (vocab > 0) {
+    RL_CHECK(check_buffer(who, "weight", weight, eb));
+    RL_CHECK(check_rows(who, "weight", weight_row, width));
+  }
+  RL_CHECK(check_index(who, index, index_bytes));
+  RL_CHECK(check_buffer(who, "out", out, eb));
+  RL_CHECK(check_rows(who, "out", out_row, width));
+  rl::EmbedForward a{weight, index, out, vocab, count, weight_row, out_row, dtype, width, index_bytes,
+                     scale};
+  return launched(rl::embed_forward_launch(a, static_cast<hipStream_t>(hip_stream)), who);
+}
+
+int64_t embed_workspace(int32_t dtype, int64_t vocab, int32_t width, int64_t count) {
+  RL_CHECK(check_embed_sizes("embed_workspace", dtype, vocab, width, count));
+  return vocab == 0 || width == 0 ? 0 : rl::embed_workspace_bytes(vocab, width, count);
+}
+
+int embed_backward(int32_t dtype, const void* dout, int64_t dout_row, const void* index,
+                   int32_t index_bytes, int64_t count, int64_t vocab, int32_t width, float scale,
+                   void* dweight, int64_t dweight_row, void* workspace, int64_t workspace_bytes,
+                   void* hip_stream) {
+  const char* who = "embed_backward";
+  RL_CHECK(check_embed_sizes(who, dtype, vocab, width, count));
+  if (vocab == 0 || width == 0) return ROLLOUT_OK;
+  const size_t eb = element_bytes(dtype);
+  if (count > 0) {
+    RL_CHECK(check_buffer(who, "dout", dout, eb));
+    if (dout_row != 0) RL_CHECK(check_rows(who, "dout", dout_row, width));
+    RL_CHECK(check_index(who, index, index_bytes));
+  }
+  RL_CHECK(check_buffer(who, "dweight", dweight, eb));
+  RL_CHECK(check_rows(who, "dweight", dweight_row, width));
+  const int64_t need = rl::embed_workspace_bytes(vocab, width, count);
+  if (!workspace || workspace_bytes < need)
+    return fail(ROLLOUT_EINVAL, "%s: workspace of %lld bytes needed, %lld given", who,
+                (long long)need, workspace ? (long long)workspace_bytes : 0LL);
+  RL_CHECK(check_buffer(who, "workspace", workspace, 16));
+  rl::EmbedBackward a{dout, index, dweight, workspace, vocab, count, dout_row, dweight_row,
+                      dtype, width, index_bytes, scale};
+  return launched(rl::embed_backward_launch(a, static_cast<hipStream_t>(hip_stream)), who);
+}
+
+int logits_forward(const logits_args* a, void* out, int64_t out_row, void* hip_stream) {
+  const char* who = "logits_forward";
+  RL_CHECK(check_logits(who, a, true));
+  if (a->rows == 0 || a->vocab == 0) return ROLLOUT_OK;
+  RL_CHECK(check_buffer(who, "out", out, element_bytes(a->dtype)));
+  RL_CHECK(check_rows(who, "out", out_row, a->vocab));
+  return launched(rl::logits_forward_launch(*a, out, out_row, static_cast<hipStream_t>(hip_stream)),
+                  who);
+}
+
+int64_t logits_workspace(int64_t rows, int32_t vocab) {
+  if (rows < 0 || vocab < 0 || vocab > kMaxWidth)
+    return fail(ROLLOUT_EINVAL, "logits_workspace: bad size (%lld, %d)", (long long)rows, vocab);
+  return rl::logits_workspace_bytes(rows, vocab);
+}
+
+int logits_backward(const logits_args* a, const void* dout, int64_t dout_row, void* dlogits,
+                    int64_t dlogits_row, float* dbias, void* workspace, int64_t workspace_bytes,
+                    void* hip_stream) {
+  const char* who = "logits_backward";
+  RL_CHECK(check_logits(who, a, a && rl::logits_gradient_reads_logits(*a)));
+  if (a->vocab == 0) return ROLLOUT_OK;
+  RL_CHECK(check_optional(who, "dbias", dbias, 4));
+  if (a->rows > 0) {
+    const size_t eb = element_bytes(a->dtype);
+    RL_CHECK(check_buffer(who, "dout", dout, eb));
+    if (dout_row != 0) RL_CHECK(check_rows(who, "dout", dout_row, a->vocab));
+    RL_CHECK(check_optional(who, "dlogits", dlogits, eb));
+    if (dlogits) RL_CHECK(check_rows(who, "dlogits", dlogits_row, a->vocab));
+    if (dbias) {
+      const int64_t need = rl::logits_workspace_bytes(a->rows, a->vocab);
+      if (!workspace || workspace_bytes < need)
+        return fail(ROLLOUT_EINVAL, "%s: workspace of %lld bytes needed, %lld given", who,
+                    (long long)need, workspace ? (long long)workspace_bytes : 0LL);
+      RL_CHECK(check_buffer(who, "workspace", workspace, 16));
+    }
+  }
+  return launched(rl::logits_backward_launch(*a, dout, dout_row, dlogits, dlogits_row, dbias,
+                                             workspace, static_cast<hipStream_t>(hip_stream)),
                   who);
 }
 

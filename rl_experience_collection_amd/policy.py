@@ -1,9 +1,11 @@
 """Python binding of include/policy.h: the operators of a policy with memory.
 
+    embed                           scaled embedding lookup
     recurrence, recurrence_step     gated linear recurrence over [L, N, D]
+    shape_logits                    penalties, bias and mask on logits
 
-`recurrence` takes part in torch's autograd; its gradient runs in the
-library's kernels too.  Calls run on torch's current stream, on the current
+`embed`, `recurrence` and `shape_logits` take part in torch's autograd; their
+gradients run in the library's kernels too.  Calls run on torch's current stream, on the current
 device, where their tensors must live; outputs and workspaces come from
 torch's allocator, so captured graphs keep their own.
 """
@@ -15,7 +17,10 @@ import torch
 
 POLICY_F32, POLICY_BF16, POLICY_F16 = 0, 1, 2
 RECUR_LINEAR, RECUR_SIGMOID = 0, 1
-EXPORTED = ("recur_workspace", "recur_forward", "recur_backward", "recur_step")
+LOGITS_MASK_NONE, LOGITS_MASK_BYTES, LOGITS_MASK_BITS = 0, 1, 2
+EXPORTED = ("recur_workspace", "recur_forward", "recur_backward", "recur_step",
+            "embed_forward", "embed_workspace", "embed_backward",
+            "logits_forward", "logits_workspace", "logits_backward")
 
 _DTYPES = {torch.float32: POLICY_F32, torch.bfloat16: POLICY_BF16, torch.float16: POLICY_F16}
 _FORMS = {"linear": RECUR_LINEAR, "sigmoid": RECUR_SIGMOID}
@@ -40,16 +45,36 @@ class RecurGradArgs(C.Structure):
                 [("workspace_bytes", C.c_int64)])
 
 
+class LogitsArgs(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("vocab", C.c_int32), ("dtype", C.c_int32),
+                ("logits", C.c_void_p), ("logits_row", C.c_int64),
+                ("bias", C.c_void_p), ("bias_row", C.c_int64),
+                ("history", C.c_void_p), ("history_row", C.c_int64),
+                ("history_len", C.c_void_p), ("history_width", C.c_int32),
+                ("mask_kind", C.c_int32),
+                ("repetition", C.c_float), ("presence", C.c_float), ("frequency", C.c_float),
+                ("repetition_rows", C.c_void_p), ("presence_rows", C.c_void_p),
+                ("frequency_rows", C.c_void_p),
+                ("mask", C.c_void_p), ("mask_row", C.c_int64), ("mask_count", C.c_int64),
+                ("mask_rows", C.c_void_p)]
+
+
 def declare(lib):
     """Argument types of the entry points of include/policy.h."""
     vp, i32, i64 = C.c_void_p, C.c_int32, C.c_int64
     lib.recur_workspace.argtypes = [i32, i32, i32, i32]
-    lib.recur_workspace.restype = i64
     lib.recur_forward.argtypes = [C.POINTER(RecurArgs), vp]
     lib.recur_backward.argtypes = [C.POINTER(RecurGradArgs), vp]
     lib.recur_step.argtypes = [i32, i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp]
-    for name in ("recur_forward", "recur_backward", "recur_step"):
-        getattr(lib, name).restype = C.c_int
+    lib.embed_forward.argtypes = [i32, vp, i64, i32, i64, vp, i32, i64, C.c_float, vp, i64, vp]
+    lib.embed_workspace.argtypes = [i32, i64, i32, i64]
+    lib.embed_backward.argtypes = [i32, vp, i64, vp, i32, i64, i64, i32, C.c_float, vp, i64, vp,
+                                   i64, vp]
+    lib.logits_forward.argtypes = [C.POINTER(LogitsArgs), vp, i64, vp]
+    lib.logits_workspace.argtypes = [i64, i32]
+    lib.logits_backward.argtypes = [C.POINTER(LogitsArgs), vp, i64, vp, i64, vp, vp, i64, vp]
+    for name in EXPORTED:
+        getattr(lib, name).restype = i64 if name.endswith("_workspace") else C.c_int
 
 
 def _call(fn, *args):
@@ -237,3 +262,195 @@ def recurrence_step(x, gate, state, resets=None, form: str = "sigmoid", out_stat
     _call(_lib().recur_step, N, D, dt, f, _ptr(x), x_row, _ptr(gate), gate_row, _ptr(state),
           _ptr(resets), _ptr(h), D, _ptr(new), stream)
     return h, new
+
+
+# ----------------------------------------------------------------- embedding
+_INDEX_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+class _Embed(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, weight, index, scale):
+        V, D = weight.shape
+        stream = _here("embed", weight, index)
+        out = torch.empty(tuple(index.shape) + (D,), dtype=weight.dtype, device=weight.device)
+        _call(_lib().embed_forward, _DTYPES[weight.dtype], _ptr(weight), V, D,
+              max(D, weight.stride(0)), _ptr(index), _INDEX_BYTES[index.dtype], index.numel(), scale,
+              _ptr(out), D, stream)
+        ctx.save_for_backward(index)
+        ctx.vocab, ctx.scale = V, scale
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        index, = ctx.saved_tensors
+        V, D, count = ctx.vocab, dout.shape[-1], index.numel()
+        lib, stream = _lib(), _here("embed", dout, index)
+        dout = dout.contiguous()
+        dweight = torch.empty((V, D), dtype=dout.dtype, device=dout.device)
+        dt = _DTYPES[dout.dtype]
+        size = lib.embed_workspace(dt, V, D, count)
+        ws = _workspace(dout, size)
+        _call(lib.embed_backward, dt, _ptr(dout), D, _ptr(index), _INDEX_BYTES[index.dtype], count,
+              V, D, ctx.scale, _ptr(dweight), D, _ptr(ws), size, stream)
+        return dweight, None, None
+
+
+def embed(weight, index, scale: float = 1.0):
+    """scale * weight[index] (include/policy.h): weight [V, D] float32, bfloat16
+    or float16 with contiguous rows, index a contiguous int32 or int64 tensor
+    of any shape; returns index.shape + [D] in weight's dtype.  An index outside
+    [0, V), such as the -1 of an episode's first step, gives zeros.  The
+    gradient flows to weight and is dense."""
+    _element("weight", weight)
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [V, D], got {tuple(weight.shape)}")
+    _unit("weight", weight, 2)
+    if weight.shape[0] > 1 and weight.stride(0) < weight.shape[1]:
+        raise ValueError("weight's rows must not overlap")
+    if index.dtype not in _INDEX_BYTES:
+        raise ValueError(f"index must be int32 or int64, got {index.dtype}")
+    if not index.is_contiguous():
+        raise ValueError("index must be contiguous")
+    return _Embed.apply(weight, index, float(scale))
+
+
+# -------------------------------------------------------------------- logits
+def _logits_args(logits, bias, history, history_len, penalties, mask, mask_rows):
+    """The C struct; every tensor has been checked."""
+    V = logits.shape[-1]
+    a = LogitsArgs(vocab=V, dtype=_DTYPES[logits.dtype], history_width=0, mask_kind=0,
+                   repetition=1.0, presence=0.0, frequency=0.0)
+    a.rows = logits.numel() // V if V else 0
+    a.logits = _ptr(logits)
+    a.logits_row = logits.stride(0) if logits.dim() == 2 and logits.shape[0] > 1 else V
+    if bias is not None:
+        a.bias, a.bias_row = _ptr(bias), V if bias.dim() > 1 else 0
+    if history is not None:
+        a.history, a.history_row, a.history_width = _ptr(history), history.shape[-1], history.shape[-1]
+        a.history_len = _ptr(history_len)
+    for name, value in penalties:
+        if isinstance(value, torch.Tensor):
+            setattr(a, name + "_rows", _ptr(value))
+        else:
+            setattr(a, name, value)
+    if mask is not None:
+        a.mask, a.mask_row = _ptr(mask), mask.shape[-1]
+        a.mask_kind = LOGITS_MASK_BITS if mask.dtype == torch.int32 else LOGITS_MASK_BYTES
+        a.mask_count = mask.numel() // mask.shape[-1] if mask.shape[-1] else 0
+        a.mask_rows = _ptr(mask_rows)
+    return a
+
+
+class _ShapeLogits(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, bias, history, history_len, penalties, mask, mask_rows, out):
+        rows = [v for _, v in penalties if isinstance(v, torch.Tensor)]
+        stream = _here("shape_logits", logits, bias, history, history_len, mask, mask_rows, out, *rows)
+        a = _logits_args(logits, bias, history, history_len, penalties, mask, mask_rows)
+        if out is None:
+            out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out_row = out.stride(0) if out.dim() == 2 and out.shape[0] > 1 else a.vocab
+        _call(_lib().logits_forward, C.byref(a), _ptr(out), out_row, stream)
+        # of the penalties only the repetition scales the gradient
+        rep = penalties[0][1]
+        ctx.repetition = None if isinstance(rep, torch.Tensor) else rep
+        if history is None or ctx.repetition == 1.0:
+            logits, history, history_len = None, None, None
+        ctx.save_for_backward(logits, history, history_len, mask, mask_rows,
+                              rep if ctx.repetition is None else None)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        logits, history, history_len, mask, mask_rows, rep = ctx.saved_tensors
+        lib, stream = _lib(), _here("shape_logits", dout, logits, mask)
+        V = dout.shape[-1]
+        dout = dout.contiguous()
+        a = _logits_args(dout if logits is None else logits, None, history, history_len,
+                         (("repetition", ctx.repetition if rep is None else rep),), mask, mask_rows)
+        dlogits = torch.empty_like(dout) if ctx.needs_input_grad[0] else None
+        dbias = torch.empty(V, dtype=torch.float32, device=dout.device) \
+            if ctx.needs_input_grad[1] else None
+        size = lib.logits_workspace(a.rows, V) if dbias is not None else 0
+        ws = _workspace(dout, size)
+        _call(lib.logits_backward, C.byref(a), _ptr(dout), V, _ptr(dlogits), V, _ptr(dbias), _ptr(ws),
+              size, stream)
+        return dlogits, dbias, None, None, None, None, None, None
+
+
+def _per_row(name, value, lead):
+    if isinstance(value, torch.Tensor):
+        _exact(name, value, torch.float32, lead)
+        if value.requires_grad:
+            raise ValueError(f"{name} takes no gradient")
+        return value
+    return float(value)
+
+
+def shape_logits(logits, bias=None, history=None, history_len=None, repetition=1.0, presence=0.0,
+                 frequency=0.0, mask=None, mask_rows=None, out=None):
+    """Penalties for tokens of the history, then the bias, then the mask
+    (include/policy.h); returns a tensor like `logits`, -inf where masked.
+
+    logits: [..., V] float32, bfloat16 or float16, contiguous (or [R, V] with
+    contiguous rows).  bias: [V] or logits' shape, float32.  history: [..., H]
+    int32 token ids (others, such as a padding of -1, are ignored), of which
+    the first history_len [...] int32 count.  repetition, presence and
+    frequency: a number or one float32 per row [...].  mask: uint8 or bool
+    [..., V], or int32 [..., ceil(V / 32)] with token v at bit v % 32 of word
+    v // 32; one row per row of logits, a single row for all, or any number of
+    rows chosen by mask_rows [...] int32 (a value that names no row allows
+    everything).  out: written instead of a new tensor; may be `logits`.
+    Gradients flow to logits and to a bias of shape [V]."""
+    _element("logits", logits)
+    if logits.dim() < 1:
+        raise ValueError("logits must be [..., V]")
+    V, lead = logits.shape[-1], tuple(logits.shape[:-1])
+    if not logits.is_contiguous():
+        _unit("logits", logits, 2)
+        if logits.stride(0) < V:
+            raise ValueError("logits' rows must not overlap")
+    if bias is not None:
+        _exact("bias", bias, torch.float32, (V,) if bias.dim() == 1 else lead + (V,))
+        if bias.requires_grad and bias.dim() > 1:
+            raise ValueError("only a bias of shape [V] takes a gradient")
+    if history is not None:
+        H = history.shape[-1] if history.dim() else 0
+        _exact("history", history, torch.int32, lead + (H,))
+        _exact("history_len", history_len, torch.int32, lead)
+    elif history_len is not None:
+        raise ValueError("history_len needs a history")
+    penalties = (("repetition", _per_row("repetition", repetition, lead)),
+                 ("presence", _per_row("presence", presence, lead)),
+                 ("frequency", _per_row("frequency", frequency, lead)))
+    if mask is not None:
+        if mask.dtype == torch.bool:
+            mask = mask.view(torch.uint8)
+        if mask.dtype not in (torch.uint8, torch.int32):
+            raise ValueError(f"mask must be uint8, bool or int32, got {mask.dtype}")
+        width = (V + 31) // 32 if mask.dtype == torch.int32 else V
+        if mask.dim() < 1 or mask.shape[-1] != width:
+            raise ValueError(f"mask's last dimension must be {width}, got shape {tuple(mask.shape)}")
+        if not mask.is_contiguous():
+            raise ValueError("mask must be contiguous")
+        if mask_rows is not None:
+            _exact("mask_rows", mask_rows, torch.int32, lead)
+        elif mask.numel() != width and tuple(mask.shape[:-1]) != lead:
+            raise ValueError(f"mask must have one row or rows {lead}, got shape {tuple(mask.shape)}")
+    elif mask_rows is not None:
+        raise ValueError("mask_rows needs a mask")
+    if out is not None:
+        _no_grad("shape_logits with out", logits, bias)
+        if out.dtype != logits.dtype or out.shape != logits.shape:
+            raise ValueError("out must have logits' dtype and shape")
+        if not out.is_contiguous():
+            _unit("out", out, 2)
+            if out.stride(0) < V:
+                raise ValueError("out's rows must not overlap")
+        with torch.no_grad():
+            _ShapeLogits.apply(logits, bias, history, history_len, penalties, mask, mask_rows, out)
+        return out
+    return _ShapeLogits.apply(logits, bias, history, history_len, penalties, mask, mask_rows, None)

@@ -90,3 +90,61 @@ def recurrence_grad(x, gate, h0, dones, dh, dh_last, sig, name):
         mag = np.where(m[t], np.abs(a[t]) * dmag, 0.0)
         err = np.where(m[t], np.abs(a[t]) * derr + STEP * U * np.abs(a[t]) * dmag, 0.0)
     return dict(f, dx=dx, dgate=dg, dh0=G, edx=edx, edg=edg, edh0=err + half("f32", G))
+
+
+def embed(weight, index, scale, name):
+    V = weight.shape[0]
+    known = (index >= 0) & (index < V)
+    out = np.where(known[..., None], weight[np.where(known, index, 0)] * scale, 0.0) if V else \
+        np.zeros(index.shape + (weight.shape[1],))
+    return out, U * np.abs(out) + half(name, out)
+
+
+def embed_grad(dout, index, V, scale, name):
+    """Summing n values in any order in 32 bits is off by at most n - 1
+    roundings of the sum of their magnitudes; the scale is one more."""
+    index, dout = index.reshape(-1), dout.reshape(-1, dout.shape[-1])
+    known = (index >= 0) & (index < V)
+    dw, mag = np.zeros((2, V, dout.shape[1]))
+    np.add.at(dw, index[known], dout[known])
+    np.add.at(mag, index[known], np.abs(dout[known]))
+    n = np.bincount(index[known], minlength=V)[:, None] if V else np.zeros((0, 1))
+    err = (n + 1) * U * mag * abs(scale)
+    dw = dw * scale
+    return dw, err + half(name, np.abs(dw) + err)
+
+
+def logits(z, name, bias=None, history=None, history_len=None, repetition=1.0, presence=0.0,
+           frequency=0.0, allowed=None, dout=None):
+    """[R, V] float64 in and out: out and its bound (division, presence,
+    frequency's product and difference, bias: 5 roundings of the magnitudes),
+    and with dout the gradients and theirs."""
+    R, V = z.shape
+    count = np.zeros((R, V))
+    if history is not None:
+        H = history.shape[1]
+        lens = np.full(R, H) if history_len is None else np.clip(history_len, 0, H)
+        for r in range(R):
+            for v in history[r, :lens[r]]:
+                if 0 <= v < V:
+                    count[r, v] += 1
+    rho, alpha, beta = (np.broadcast_to(np.asarray(x, np.float64).reshape(-1, 1), (R, V))
+                        for x in (repetition, presence, frequency))
+    seen = count > 0
+    with np.errstate(invalid="ignore"):
+        factor = np.where(seen, np.where(z > 0, 1 / rho, rho), 1.0)
+        y = z * factor
+        b = 0.0 if bias is None else np.broadcast_to(bias, (R, V))
+        out = y - alpha * seen - beta * count + b
+        mag = np.abs(y) + np.abs(alpha) * seen + np.abs(beta) * count + np.abs(b)
+        err = 5 * U * mag
+        bound = err + half(name, np.abs(out) + err)
+    ok = np.ones((R, V), bool) if allowed is None else np.broadcast_to(allowed, (R, V))
+    res = dict(out=np.where(ok, out, -np.inf), eout=np.where(ok, bound, 0.0))
+    if dout is not None:
+        g = np.where(ok, dout, 0.0)
+        res["dlogits"] = g * np.where(ok, factor, 1.0)
+        res["edl"] = U * np.abs(res["dlogits"]) + half(name, res["dlogits"])
+        res["dbias"] = g.sum(0)
+        res["edb"] = R * U * np.abs(g).sum(0) + half("f32", res["dbias"])
+    return res

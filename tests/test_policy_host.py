@@ -53,7 +53,7 @@ def _recur_args(policy, **kw):
 
 @pytest.mark.parametrize("change,text", [
     (dict(steps=-1), "negative size"), (dict(rows=-2), "negative size"),
-    (dict(rows=1 << 20, width=1 << 11), "2\\^31"), (dict(dtype=3), "dtype"), (dict(form=2), "form"),
+    (dict(rows=1 << 20, width=1 << 11), "2\\^29"), (dict(dtype=3), "dtype"), (dict(form=2), "form"),
     (dict(x=None), "x is NULL"), (dict(gate=None), "gate is NULL"), (dict(h=None), "h is NULL"),
     (dict(x=66), "aligned"), (dict(dtype=1, gate=65), "aligned"), (dict(h0=2), "h0 is not aligned"),
     (dict(x_step=-6), "stride"), (dict(h_row=-1), "stride"),
@@ -137,3 +137,160 @@ def test_reference_recurrence_gradient_against_differences(sig):
             num[i] = (loss(*up) - loss(*dn)) / 2e-6
         # a central difference of step 1e-6: truncation ~1e-12, rounding ~1e-9
         assert np.abs(num - got).max() < 1e-7
+
+
+# ----------------------------------------------------------------- embedding
+def test_embed_c_refusals(rx):
+    lib = rx.load_library()
+
+    def fwd(dtype=0, weight=64, V=5, D=4, wrow=4, index=64, ib=4, count=3, out=64, orow=4):
+        return lib.embed_forward(dtype, weight, V, D, wrow, index, ib, count, 1.0, out, orow, None)
+
+    for kw, text in [(dict(dtype=7), "dtype"), (dict(weight=None), "weight is NULL"),
+                     (dict(V=-1), "vocab"), (dict(V=2 ** 31), "vocab"), (dict(D=-1), "width"),
+                     (dict(D=2 ** 24 + 1), "width"), (dict(wrow=3), "weight are 3 apart"),
+                     (dict(index=None), "index is NULL"), (dict(ib=2), "index_bytes"),
+                     (dict(ib=8, index=68), "index is not aligned"), (dict(count=-1), "count"),
+                     (dict(out=None), "out is NULL"), (dict(out=66), "out is not aligned"),
+                     (dict(orow=2), "out are 2 apart")]:
+        assert fwd(**kw) == EINVAL, kw
+        assert text in rx.rollout_last_error(), (kw, rx.rollout_last_error())
+    assert fwd(count=0) == OK and fwd(D=0) == OK
+
+    size = lib.embed_workspace(0, 5, 4, 3)
+    assert size > 0 and lib.embed_workspace(0, 5, 4, -3) == EINVAL
+    assert lib.embed_workspace(0, 0, 4, 3) == 0
+
+    def bwd(dtype=0, dout=64, drow=4, index=64, ib=4, count=3, V=5, D=4, dw=64, wrow=4, ws=64, size=size):
+        return lib.embed_backward(dtype, dout, drow, index, ib, count, V, D, 1.0, dw, wrow, ws, size, None)
+
+    for kw, text in [(dict(dout=None), "dout is NULL"), (dict(drow=3), "dout are 3 apart"),
+                     (dict(dw=None), "dweight is NULL"), (dict(wrow=0), "dweight are 0 apart"),
+                     (dict(ws=None), "workspace"), (dict(size=size - 1), "workspace"),
+                     (dict(ws=72), "workspace is not aligned"), (dict(ib=1), "index_bytes")]:
+        assert bwd(**kw) == EINVAL, kw
+        assert text in rx.rollout_last_error(), (kw, rx.rollout_last_error())
+    assert bwd(V=0) == OK and bwd(D=0) == OK
+
+
+def test_embed_binding_refusals(rx):
+    w, i = torch.zeros(5, 4), torch.zeros(3, dtype=torch.int32)
+    for kw, text in [(dict(weight=w.double()), "float32"), (dict(weight=w[0]), r"\[V, D\]"),
+                     (dict(weight=w.t()), "last dimension"),
+                     (dict(weight=w[:1].expand(5, 4)), "overlap"), (dict(index=i.float()), "int32"),
+                     (dict(index=torch.zeros(4, 4, dtype=torch.int32)[:, 1]), "contiguous")]:
+        with pytest.raises(ValueError, match=text):
+            rx.embed(**dict(dict(weight=w, index=i), **kw))
+
+
+def test_reference_embed_gradient_against_differences():
+    rng = np.random.default_rng(4)
+    w, idx = rng.standard_normal((4, 3)), np.array([0, 2, -1, 2, 9, 3])
+    dout = rng.standard_normal((6, 3))
+    got, _ = ref.embed_grad(dout, idx, 4, 1.7, "f32")
+    for i in np.ndindex(w.shape):
+        e = np.zeros_like(w)
+        e[i] = 1.0  # linear: a difference of any step is the gradient
+        num = ((ref.embed(w + e, idx, 1.7, "f32")[0] - ref.embed(w, idx, 1.7, "f32")[0]) * dout).sum()
+        assert abs(num - got[i]) < 1e-12
+
+
+# -------------------------------------------------------------------- logits
+def test_logits_struct_size(policy):
+    assert C.sizeof(policy.LogitsArgs) == 8 + 8 + 16 + 16 + 16 + 8 + 8 + 12 + 4 + 24 + 24 + 8
+
+
+def _logits_args(policy, **kw):
+    a = policy.LogitsArgs(rows=3, vocab=40, dtype=0, logits=64, logits_row=40, repetition=1.0)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("change,text", [
+    (dict(dtype=5), "dtype"), (dict(rows=-1), "rows"), (dict(vocab=-1), "vocab"),
+    (dict(vocab=(1 << 24) + 1), "vocab"), (dict(history_width=-1), "history_width"),
+    (dict(repetition=0.0), "repetition"), (dict(repetition=-1.0), "repetition"),
+    (dict(repetition=float("nan")), "repetition"), (dict(repetition=float("inf")), "repetition"),
+    (dict(mask_kind=3), "mask_kind"), (dict(logits=None), "logits is NULL"),
+    (dict(logits_row=39), "logits are 39 apart"), (dict(logits=66), "aligned"),
+    (dict(bias=66), "bias is not aligned"), (dict(bias=64, bias_row=7), "bias are 7 apart"),
+    (dict(history=64, history_row=-1), "history"), (dict(mask_kind=2, mask_count=3), "mask is NULL"),
+    (dict(mask_kind=2, mask=64, mask_count=2, mask_row=2), "without mask_rows"),
+    (dict(mask_kind=2, mask=64, mask_count=3, mask_row=1), "mask are 1 apart"),
+    (dict(mask_kind=1, mask=64, mask_count=3, mask_row=39), "mask are 39 apart"),
+    (dict(mask_kind=2, mask=66, mask_count=1, mask_row=2), "mask is not aligned"),
+    (dict(mask_kind=1, mask=64, mask_count=-1), "mask_count")])
+def test_logits_c_refusals(rx, policy, change, text):
+    lib = rx.load_library()
+    assert lib.logits_forward(C.byref(_logits_args(policy, **change)), 64, 40, None) == EINVAL
+    assert text in rx.rollout_last_error(), rx.rollout_last_error()
+
+
+def test_logits_other_c_refusals(rx, policy):
+    lib = rx.load_library()
+    a = _logits_args(policy)
+    assert lib.logits_forward(None, 64, 40, None) == EINVAL
+    assert lib.logits_forward(C.byref(a), None, 40, None) == EINVAL
+    assert lib.logits_forward(C.byref(a), 64, 39, None) == EINVAL
+    assert lib.logits_workspace(-1, 4) == EINVAL and lib.logits_workspace(0, 4) == 0
+    size = lib.logits_workspace(3, 40)
+    assert size > 0
+    assert lib.logits_backward(None, 64, 40, 64, 40, None, None, 0, None) == EINVAL
+    assert lib.logits_backward(C.byref(a), None, 40, 64, 40, None, None, 0, None) == EINVAL
+    assert lib.logits_backward(C.byref(a), 64, 40, 64, 39, None, None, 0, None) == EINVAL
+    assert lib.logits_backward(C.byref(a), 64, 40, 64, 40, 64, None, 0, None) == EINVAL
+    assert lib.logits_backward(C.byref(a), 64, 40, 64, 40, 64, 64, size - 1, None) == EINVAL
+    assert "workspace" in rx.rollout_last_error()
+    pen = _logits_args(policy, logits=None, history=64, history_width=2, history_row=2, repetition=1.5)
+    assert lib.logits_backward(C.byref(pen), 64, 40, 64, 40, None, None, 0, None) == EINVAL
+    assert "logits is NULL" in rx.rollout_last_error()
+    for z in (dict(rows=0), dict(vocab=0)):
+        assert lib.logits_forward(C.byref(_logits_args(policy, **z)), None, 0, None) == OK
+
+
+def test_shape_logits_binding_refusals(rx):
+    z = torch.zeros(3, 40)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    for kw, text in [(dict(logits=z.double()), "float32"), (dict(logits=z.t()), "last dimension"),
+                     (dict(logits=z[:1].expand(3, 40)), "overlap"),
+                     (dict(logits=torch.tensor(1.0)), "V"), (dict(bias=torch.zeros(39)), "bias"),
+                     (dict(bias=torch.zeros(40).half()), "bias"),
+                     (dict(bias=torch.zeros(3, 40, requires_grad=True)), "gradient"),
+                     (dict(history=i32(4, 5)), "history"), (dict(history=i32(3, 5).long()), "history"),
+                     (dict(history_len=i32(3)), "needs a history"),
+                     (dict(history=i32(3, 5), history_len=i32(4)), "history_len"),
+                     (dict(presence=torch.zeros(4)), "presence"),
+                     (dict(frequency=torch.zeros(3, requires_grad=True)), "gradient"),
+                     (dict(mask=torch.zeros(3, 39, dtype=torch.bool)), "last dimension"),
+                     (dict(mask=i32(3, 40)), "last dimension"), (dict(mask=torch.zeros(3, 40)), "mask must be"),
+                     (dict(mask=i32(4, 2)), "one row or rows"), (dict(mask_rows=i32(3)), "needs a mask"),
+                     (dict(mask=i32(7, 2), mask_rows=i32(2)), "mask_rows"),
+                     (dict(out=torch.zeros(3, 41)), "out"),
+                     (dict(logits=z.clone().requires_grad_(), out=z), "no_grad")]:
+        with pytest.raises(ValueError, match=text):
+            rx.shape_logits(**dict(dict(logits=z), **kw))
+
+
+def test_reference_logits_gradient_against_differences():
+    rng = np.random.default_rng(5)
+    R, V = 3, 6
+    z, bias, dout = rng.standard_normal((R, V)), rng.standard_normal(V), rng.standard_normal((R, V))
+    hist = rng.integers(-1, V + 1, (R, 5))
+    ok = rng.random((R, V)) < 0.7
+    kw = dict(history=hist, history_len=np.array([5, 0, 3]), repetition=[1.3, 1.2, 0.8],
+              presence=[0.1, 0.2, 0.3], frequency=[0.5, 0.1, 0.0], allowed=ok)
+    g = ref.logits(z, "f32", bias=bias, dout=dout, **kw)
+
+    def loss(z, bias):
+        return (np.where(ok, ref.logits(z, "f32", bias=bias, **kw)["out"], 0.0) * dout).sum()
+
+    for i in np.ndindex(z.shape):
+        e = np.zeros_like(z)
+        e[i] = 1e-6
+        num = (loss(z + e, bias) - loss(z - e, bias)) / 2e-6
+        assert abs(num - g["dlogits"][i]) < 1e-7  # piecewise linear; rounding ~1e-9
+    for v in range(V):
+        e = np.zeros(V)
+        e[v] = 1e-6
+        assert abs((loss(z, bias + e) - loss(z, bias - e)) / 2e-6 - g["dbias"][v]) < 1e-7
