@@ -33,19 +33,47 @@ struct F16 {
 };
 
 // V consecutive elements as one memory access (V * kBytes of 2, 4, 8 or 16).
+// The address needs an element's alignment only: gfx950 loads and stores
+// such accesses whole, and rows of any width and stride then take the same
+// path as aligned ones.
 template <class T, int V>
-struct alignas(V * T::kBytes) Pack {
+struct alignas(T::kBytes) Pack {
   typename T::raw v[V];
 };
 
+// 16 bytes in registers, and at an address aligned to a 2-byte element.
+typedef uint32_t quad_value __attribute__((ext_vector_type(4)));
+typedef uint32_t quad __attribute__((ext_vector_type(4), aligned(2)));
+
 template <class T, int V>
 __device__ __forceinline__ Pack<T, V> load_pack(const typename T::raw* p) {
-  return *reinterpret_cast<const Pack<T, V>*>(p);
+  if constexpr (V * T::kBytes == 16) {
+    return __builtin_bit_cast(Pack<T, V>, (quad_value)*reinterpret_cast<const quad*>(p));
+  } else {
+    return *reinterpret_cast<const Pack<T, V>*>(p);
+  }
 }
 template <class T, int V>
 __device__ __forceinline__ void store_pack(typename T::raw* p, const Pack<T, V>& x) {
   *reinterpret_cast<Pack<T, V>*>(p) = x;
 }
+// The same past the caches, for outputs too large to be found there again.
+template <class T, int V>
+__device__ __forceinline__ void store_pack(typename T::raw* p, const Pack<T, V>& x, bool past) {
+  if constexpr (V * T::kBytes == 16) {
+    const quad_value q = __builtin_bit_cast(quad_value, x);
+    if (past)
+      __builtin_nontemporal_store((quad)q, reinterpret_cast<quad*>(p));
+    else
+      *reinterpret_cast<quad*>(p) = q;
+  } else {
+    store_pack<T, V>(p, x);
+  }
+}
+// Outputs above this many bytes are stored past the caches.  A copy of 256 MiB
+// measured 90 us through them and 73 us past them; a smaller output is worth
+// more to its reader in the 256 MiB cache than the store saves.
+constexpr int64_t kPastBytes = (int64_t)96 << 20;
 template <class T, int V>
 __device__ __forceinline__ void widen_pack(const Pack<T, V>& x, float (&f)[V]) {
 #pragma unroll
@@ -57,6 +85,23 @@ __device__ __forceinline__ Pack<T, V> narrow_pack(const float (&f)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) x.v[i] = T::narrow(f[i]);
   return x;
+}
+
+// Elements e .. e + V - 1 of an array of n >= V: the access is moved back to
+// lie inside the array (load_inside), and the elements that exist are put in
+// their places when they are used (settle), so that the load sits behind no
+// branch.  Lanes with e >= n load the last V and use nothing.
+template <class T, int V>
+__device__ __forceinline__ Pack<T, V> load_inside(const typename T::raw* p, int32_t e, int32_t n) {
+  return load_pack<T, V>(p + min(e, n - V));
+}
+template <class T, int V>
+__device__ __forceinline__ void settle(Pack<T, V>& x, int32_t e, int32_t n) {
+  if constexpr (V * T::kBytes == 16) {
+    const int32_t back = e - (n - V);
+    if (back > 0 && back < V)
+      x = __builtin_bit_cast(Pack<T, V>, __builtin_bit_cast(unsigned __int128, x) >> (8 * T::kBytes * back));
+  }
 }
 
 inline bool aligned_to(const void* p, size_t bytes) {

@@ -1,12 +1,25 @@
 // Penalties, bias and mask on logits, and their gradient (include/policy.h).
 //
-// A workgroup owns a tile: whole rows where a row is short, a run of one
-// row's columns where it is long.  It counts the history's tokens that fall
-// into the tile in LDS (integer adds, so their order does not matter), then
-// passes over the tile once.  The gradient needs a logit only where a count
-// is not zero (its sign picks the factor) and loads just those.
-#include <initializer_list>
-
+// Two shapes.  Rows of at most 2048 logits that lie one after another are
+// taken several at a time: a tile is a run of whole rows addressed as one
+// array.  Longer (or strided) rows are cut into runs of columns, one row at a
+// time.  In both a thread owns fixed 16-byte packs of the tile, loads them
+// first, and while they are on their way the workgroup counts the history's
+// tokens that fall into the tile in LDS (integer adds: their order does not
+// matter).  In the first shape rows and packs do not line up, and most packs
+// hold a counted token: the tile's values are staged in LDS, the history
+// entry that counts a token first replaces the token's value there, and the
+// mask becomes one bit per element of the tile, so that the last pass over
+// the packs has no branch per element.
+//
+// The gradient needs a logit only where a token occurred (its sign picks the
+// factor).  Short rows load all of them; long ones load the marked logits
+// alone, or, where the history is so dense that nearly every line of the row
+// holds one, whole packs ahead of time.
+// dbias is summed by the pass that forms dlogits: a thread's packs cover the
+// same columns in every tile, so it adds up its own columns in registers
+// over all tiles it takes, and one more kernel joins the workgroups' sums in
+// a fixed order.
 #include "elem.hpp"
 #include "policy.hpp"
 
@@ -15,231 +28,622 @@ namespace rl {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 4096;     // elements of a tile, at most
-constexpr int kTileRows = 256;  // rows of a tile, at most
-constexpr int kShortRow = 2048; // rows up to this long are tiled whole
+constexpr int kTile = 2048;      // elements of a tile of whole rows, at most
+constexpr int kTileRows = 128;   // its rows, at most
+constexpr int kRunPacks = 2;     // packs per thread of a run of columns
+constexpr int kFlatGroups = 2048;
+constexpr int kBiasGroups = 2048;  // about, of runs in all
 constexpr float kBanned = -__builtin_inff();
 
 struct LogitsArgs {
   logits_args a;
-  const void* dout;   // gradient
-  void* out;          // out or dlogits
+  const void* dout;  // gradient
+  void* out;         // out or dlogits
+  float* partial;    // gradient: [groups][vocab] sums of dbias, or NULL
   int64_t dout_row, out_row;
-  int32_t tile_rows, tile_cols;  // rows of a tile (1 for long rows), columns of a tile
-  int32_t spread;                // lanes that share a row's history (a power of two)
-  uint32_t magic;                // for a quotient by vocab (short rows)
-  bool penalties;
+  int32_t tile_rows;     // rows of a tile
+  uint32_t magic_vocab;  // for a quotient by vocab
+  uint32_t magic_words;  // for one by the words of a row of bits
+  uint32_t magic_width;  // for one by history_width
+  bool penalties;        // the history matters
+  bool dense;            // gradient: logits are loaded whole
+  bool past;             // the output is stored past the caches
 };
-
-struct RowTerms {
-  float rho, alpha, beta;
-  int64_t mask;  // offset of the row's mask, or -1
-};
-
-__device__ __forceinline__ RowTerms row_terms(const logits_args& a, int64_t r) {
-  RowTerms t;
-  t.rho = a.repetition_rows ? a.repetition_rows[r] : a.repetition;
-  t.alpha = a.presence_rows ? a.presence_rows[r] : a.presence;
-  t.beta = a.frequency_rows ? a.frequency_rows[r] : a.frequency;
-  t.mask = -1;
-  if (a.mask_kind != LOGITS_MASK_NONE) {
-    const int64_t m = a.mask_rows ? (int64_t)a.mask_rows[r] : (a.mask_count == 1 ? 0 : r);
-    if (m >= 0 && m < a.mask_count) t.mask = m * a.mask_row;
-  }
-  return t;
-}
-
-__device__ __forceinline__ bool allowed(const logits_args& a, int64_t at, int32_t v) {
-  if (at < 0) return true;
-  if (a.mask_kind == LOGITS_MASK_BYTES) return static_cast<const uint8_t*>(a.mask)[at + v] != 0;
-  return (static_cast<const uint32_t*>(a.mask)[at + (v >> 5)] >> (v & 31)) & 1u;
-}
 
 __device__ __forceinline__ uint32_t quotient(uint32_t n, uint32_t d, uint32_t magic) {
   return d == 1 ? n : __umulhi(n, magic);
 }
 
-// FLAT: tiles of whole rows whose elements lie one after another, addressed
-// as one run.  Otherwise a tile is a run of columns of one row.
-template <class T, int V, bool GRAD, bool FLAT>
-__global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs p) {
+// Offset of a row's mask, or -1 where everything is allowed.
+__device__ __forceinline__ int64_t mask_offset(const logits_args& a, int64_t r) {
+  if (a.mask_kind == LOGITS_MASK_NONE) return -1;
+  const int64_t m = a.mask_rows ? (int64_t)a.mask_rows[r] : (a.mask_count == 1 ? 0 : r);
+  return m >= 0 && m < a.mask_count ? m * a.mask_row : -1;
+}
+// z / rho from 1 / rho (itself rounded to nearest): one Newton correction of
+// the quotient.  Where that says nothing (an infinite z, a rho so far from 1
+// that terms_of left no reciprocal) the division itself.
+__device__ __forceinline__ float divide(float z, float rho, float inv) {
+  const float q = z * inv;
+  const float c = __builtin_fmaf(__builtin_fmaf(-q, rho, z), inv, q);
+  return __builtin_fabsf(q) < __builtin_inff() ? c : z / rho;
+}
+
+struct Terms {
+  float rho, inv, alpha, beta;
+};
+__device__ __forceinline__ Terms terms_of(float rho, float alpha, float beta) {
+  const bool plain = rho > 0x1p-100f && rho < 0x1p100f;
+  return Terms{rho, plain ? 1.0f / rho : __builtin_nanf(""), alpha, beta};
+}
+__device__ __forceinline__ float penalise(float z, const Terms& t, uint32_t count) {
+  z = z > 0.0f ? divide(z, t.rho, t.inv) : z * t.rho;
+  z -= t.alpha;
+  return z - t.beta * (float)count;
+}
+
+// The first `n` of a pack's elements.
+template <class T, int V>
+__device__ __forceinline__ void store_some(typename T::raw* p, const Pack<T, V>& x, int n, bool past) {
+  if (n >= V) {
+    store_pack<T, V>(p, x, past);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < n) p[i] = x.v[i];
+}
+
+// N 32-bit words from LDS, four at a time where N allows.
+template <int N>
+__device__ __forceinline__ void read_words(const uint32_t* p, uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p + i);
+      w[i] = q.x;
+      w[i + 1] = q.y;
+      w[i + 2] = q.z;
+      w[i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = p[i];
+  }
+}
+template <int N>
+__device__ __forceinline__ void write_words(uint32_t* p, const uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      *reinterpret_cast<uint4*>(p + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = w[i];
+  }
+}
+
+// A cell of a tile whose token occurred: its logit penalised, or its gradient
+// scaled.
+template <bool GRAD>
+__device__ __forceinline__ void replace(uint32_t* val, const uint32_t* count, const uint32_t* pos,
+                                        const Terms& t, int32_t c) {
+  float f = __uint_as_float(val[c]);
+  if (GRAD)
+    f = (pos[c >> 5] >> (c & 31)) & 1u ? divide(f, t.rho, t.inv) : f * t.rho;
+  else
+    f = penalise(f, t, (count[c >> 1] >> ((c & 1) << 4)) & 0xffffu);
+  val[c] = __float_as_uint(f);
+}
+
+// ------------------------------------------------------- tiles of whole rows
+template <class T, int V, bool GRAD>
+__global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
   using raw = typename T::raw;
-  __shared__ uint32_t s_count[kTile];
-  __shared__ RowTerms s_row[FLAT ? kTileRows : 1];
+  constexpr int kPacks = kTile / (kThreads * V);
+  constexpr int kAhead = 4;  // history entries loaded before the first is used
+  __shared__ alignas(16) uint32_t s_val[kTile];  // the tile's values (fp32), penalised in place
+  __shared__ alignas(16) uint32_t s_count[kTile / 2];  // two 16-bit counts a word
+  __shared__ uint32_t s_ban[kTile / 32 + 1];     // a bit per element: not allowed
+  __shared__ uint32_t s_pos[GRAD ? kTile / 32 : 1];  // a bit per element: its logit is above 0
+  __shared__ Terms s_terms[kTileRows];
+  __shared__ int32_t s_len[kTileRows];
   const logits_args& a = p.a;
-  const int tid = threadIdx.x;
-  const int32_t vocab = a.vocab;
-  const int64_t tiles = FLAT ? (a.rows + p.tile_rows - 1) / p.tile_rows : a.rows;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int32_t vocab = a.vocab, width = a.history_width;
+  const bool masked = a.mask_kind != LOGITS_MASK_NONE;
+  const int64_t tiles = (a.rows + p.tile_rows - 1) / p.tile_rows;
+  // per element of the thread's packs, whose columns are the same in every
+  // tile: the running sums of dbias (gradient) or a bias that all rows share
+  float col[kPacks][V];
+#pragma unroll
+  for (int k = 0; k < kPacks; ++k)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      col[k][i] = 0.0f;
+      if (!GRAD && a.bias && a.bias_row == 0) {
+        const uint32_t e = (uint32_t)((k * kThreads + tid) * V + i);
+        col[k][i] = a.bias[e - quotient(e, (uint32_t)vocab, p.magic_vocab) * vocab];
+      }
+    }
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int64_t r0 = FLAT ? tile * p.tile_rows : tile;
-    const int32_t rows = FLAT ? (int32_t)min((int64_t)p.tile_rows, a.rows - r0) : 1;
-    const int32_t c0 = FLAT ? 0 : (int32_t)blockIdx.y * p.tile_cols;
-    const int32_t cols = FLAT ? vocab : min(p.tile_cols, vocab - c0);
-    const int32_t n = FLAT ? rows * vocab : cols;
-    __syncthreads();  // the previous tile's counts are read
-    for (int32_t r = tid; r < rows; r += kThreads) s_row[r] = row_terms(a, r0 + r);
+    const int64_t r0 = tile * p.tile_rows;
+    const int32_t rows = (int32_t)min((int64_t)p.tile_rows, a.rows - r0);
+    const int32_t n = rows * vocab;
+    const raw* in = static_cast<const raw*>(GRAD ? p.dout : a.logits) + r0 * vocab;
+    const raw* z0 = static_cast<const raw*>(a.logits) + r0 * vocab;
+    raw* out = static_cast<raw*>(p.out) + r0 * vocab;
+    const int32_t* h = p.penalties ? a.history + r0 * width : nullptr;
+    const int32_t entries = p.penalties ? rows * width : 0;
+    // elements from the tile's start to the array's end, as far as a pack reaches
+    const int32_t reach = (int32_t)min((int64_t)(kTile + V), (a.rows - r0) * vocab);
+    // Every load that waits for nothing, before the first wait.
+    int32_t len = 0;
+    float rho = 1.0f, alpha = 0.0f, beta = 0.0f;
     if (p.penalties) {
-      for (int32_t e = tid; e < n; e += kThreads) s_count[e] = 0;
+      const int64_t r = r0 + min(tid, rows - 1);
+      len = a.history_len ? a.history_len[r] : width;
+      rho = a.repetition_rows ? a.repetition_rows[r] : a.repetition;
+      alpha = a.presence_rows ? a.presence_rows[r] : a.presence;
+      beta = a.frequency_rows ? a.frequency_rows[r] : a.frequency;
+    }
+    Pack<T, V> x[kPacks], z[GRAD ? kPacks : 1];
+    int32_t token[kAhead];
+#pragma unroll
+    for (int k = 0; k < kPacks; ++k)
+      x[k] = load_inside<T, V>(in, (k * kThreads + tid) * V, reach);
+    if (GRAD && p.penalties) {
+#pragma unroll
+      for (int k = 0; k < kPacks; ++k)
+        z[GRAD ? k : 0] = load_inside<T, V>(z0, (k * kThreads + tid) * V, reach);
+    }
+    if (p.penalties) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) token[j] = h[min(j * kThreads + tid, entries - 1)];
+    }
+    if (masked || p.penalties) {
+      __syncthreads();  // the previous tile's words are read
+      if (p.penalties) {
+        if (tid < rows) {
+          s_terms[tid] = terms_of(rho, alpha, beta);
+          s_len[tid] = min(max(len, 0), width);
+        }
+        for (int i = tid * 4; i < kTile / 2; i += kThreads * 4)
+          *reinterpret_cast<uint4*>(&s_count[i]) = make_uint4(0, 0, 0, 0);
+        if (GRAD && tid < kTile / 32) s_pos[tid] = 0u;
+      }
+      if (masked && tid < kTile / 32 + 1) s_ban[tid] = 0u;
       __syncthreads();
-      const int lane = tid & (p.spread - 1), step = kThreads / p.spread;
-      for (int32_t r = tid / p.spread; r < rows; r += step) {
-        const int32_t* h = a.history + (r0 + r) * a.history_row;
-        const int32_t len = a.history_len ? min(max(a.history_len[r0 + r], 0), a.history_width)
-                                          : a.history_width;
-        for (int32_t i = lane; i < len; i += p.spread) {
-          const int32_t v = h[i];
-          if (v >= c0 && v - c0 < cols) atomicAdd(&s_count[r * vocab + v - c0], 1u);
+      if (a.mask_kind == LOGITS_MASK_BITS) {
+        // a row's words are shifted to the row's place among the tile's bits
+        const int32_t W = (vocab + 31) >> 5;
+        for (int32_t i = tid; i < rows * W; i += kThreads) {
+          const int32_t r = (int32_t)quotient((uint32_t)i, (uint32_t)W, p.magic_words);
+          const int32_t j = i - r * W;
+          const int64_t at = mask_offset(a, r0 + r);
+          if (at < 0) continue;
+          uint32_t ban = ~static_cast<const uint32_t*>(a.mask)[at + j];
+          const int32_t left = vocab - 32 * j;
+          if (left < 32) ban &= (1u << left) - 1u;
+          const int32_t bit = r * vocab + 32 * j, sh = bit & 31;
+          atomicOr(&s_ban[bit >> 5], ban << sh);
+          if (sh) atomicOr(&s_ban[(bit >> 5) + 1], ban >> (32 - sh));
+        }
+      } else if (masked) {
+#pragma unroll 4
+        for (int32_t e = tid; e < kTile; e += kThreads) {
+          bool ban = false;
+          if (e < n) {
+            const int32_t r = (int32_t)quotient((uint32_t)e, (uint32_t)vocab, p.magic_vocab);
+            const int64_t at = mask_offset(a, r0 + r);
+            ban = at >= 0 && static_cast<const uint8_t*>(a.mask)[at + e - r * vocab] == 0;
+          }
+          const uint64_t bits = __ballot(ban);
+          if (lane == 0) s_ban[e >> 5] = (uint32_t)bits;
+          if (lane == 32) s_ban[e >> 5] = (uint32_t)(bits >> 32);
         }
       }
     }
-    __syncthreads();
-    const raw* in = static_cast<const raw*>(GRAD ? p.dout : a.logits) +
-                    r0 * (GRAD ? p.dout_row : a.logits_row) + c0;
-    const raw* z0 = static_cast<const raw*>(a.logits) + r0 * a.logits_row + c0;
-    raw* out = static_cast<raw*>(p.out) + r0 * p.out_row + c0;
-    for (int32_t e = tid * V; e < n; e += kThreads * V) {
-      float f[V];
-      widen_pack<T, V>(load_pack<T, V>(in + e), f);
+    if (p.penalties) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int32_t r = FLAT ? (int32_t)quotient((uint32_t)(e + i), (uint32_t)vocab, p.magic) : 0;
-        const int32_t v = FLAT ? e + i - r * vocab : c0 + e + i;
-        const RowTerms& t = s_row[r];
-        const uint32_t count = p.penalties ? s_count[e + i] : 0u;
+      for (int k = 0; k < kPacks; ++k) {
+        const int32_t e = (k * kThreads + tid) * V;
+        if (e >= n) continue;
+        settle<T, V>(x[k], e, reach);
+        uint32_t word[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) word[i] = __float_as_uint(T::widen(x[k].v[i]));
+        write_words<V>(s_val + e, word);
         if (GRAD) {
-          if (count) {
-            const float z = T::widen(z0[e + i]);
-            f[i] = z > 0.0f ? f[i] / t.rho : f[i] * t.rho;
-          }
-          if (!allowed(a, t.mask, v)) f[i] = 0.0f;
-        } else {
-          if (count) {
-            f[i] = f[i] > 0.0f ? f[i] / t.rho : f[i] * t.rho;
-            f[i] -= t.alpha;
-            f[i] -= t.beta * (float)count;
-          }
-          if (a.bias) f[i] += a.bias[(r0 + r) * a.bias_row + v];
-          if (!allowed(a, t.mask, v)) f[i] = kBanned;
+          settle<T, V>(z[GRAD ? k : 0], e, reach);
+          float g[V];
+          widen_pack<T, V>(z[GRAD ? k : 0], g);
+          uint32_t bits = 0;
+#pragma unroll
+          for (int i = 0; i < V; ++i) bits |= (g[i] > 0.0f ? 1u : 0u) << i;
+          atomicOr(&s_pos[e >> 5], bits << (e & 31));
         }
       }
-      store_pack<T, V>(out + e, narrow_pack<T, V>(f));
+      // Count the tokens; the entry that counts a token first owns it and,
+      // once all are counted, replaces the token's value.
+      for (int32_t e0 = 0; e0 < entries; e0 += kAhead * kThreads) {
+        int32_t cell[kAhead], row[kAhead];
+        if (e0 > 0) {
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j)
+            token[j] = h[min(e0 + j * kThreads + tid, entries - 1)];
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const int32_t e = e0 + j * kThreads + tid;
+          cell[j] = -1;
+          if (e < entries) {
+            row[j] = (int32_t)quotient((uint32_t)e, (uint32_t)width, p.magic_width);
+            if (e - row[j] * width < s_len[row[j]] && token[j] >= 0 && token[j] < vocab) {
+              const int32_t c = row[j] * vocab + token[j], sh = (c & 1) << 4;
+              const uint32_t old = atomicAdd(&s_count[c >> 1], 1u << sh);
+              if (((old >> sh) & 0xffffu) == 0u) cell[j] = c;
+            }
+          }
+        }
+        if (entries <= kAhead * kThreads) {
+          __syncthreads();
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j)
+            if (cell[j] >= 0) replace<GRAD>(s_val, s_count, s_pos, s_terms[row[j]], cell[j]);
+        }
+      }
+      if (entries > kAhead * kThreads) {
+        // too many entries to keep their owners: every cell is looked at
+        __syncthreads();
+        for (int32_t c = tid; c < n; c += kThreads)
+          if ((s_count[c >> 1] >> ((c & 1) << 4)) & 0xffffu) {
+            const int32_t r = (int32_t)quotient((uint32_t)c, (uint32_t)vocab, p.magic_vocab);
+            replace<GRAD>(s_val, s_count, s_pos, s_terms[r], c);
+          }
+      }
+    }
+    if (masked || p.penalties) __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPacks; ++k) {
+      const int32_t e = (k * kThreads + tid) * V;
+      if (e >= n) continue;
+      float f[V];
+      if (p.penalties) {
+        uint32_t word[V];
+        read_words<V>(s_val + e, word);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = __uint_as_float(word[i]);
+      } else {
+        settle<T, V>(x[k], e, reach);
+        widen_pack<T, V>(x[k], f);
+      }
+      const uint32_t ban = masked ? s_ban[e >> 5] >> (e & 31) : 0u;
+      if (!GRAD && a.bias && a.bias_row == 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] += col[k][i];
+      } else if (!GRAD && a.bias) {
+        const int32_t r = (int32_t)quotient((uint32_t)e, (uint32_t)vocab, p.magic_vocab);
+        int32_t v = e - r * vocab;
+        const float* b = a.bias + (r0 + r) * a.bias_row;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (e + i < n) f[i] += b[v];
+          if (++v == vocab) {
+            v = 0;
+            b += a.bias_row;
+          }
+        }
+      }
+      if (GRAD && p.partial) {
+        float g[V];
+        widen_pack<T, V>(x[k], g);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          col[k][i] += e + i < n && !((ban >> i) & 1u) ? g[i] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = (ban >> i) & 1u ? (GRAD ? 0.0f : kBanned) : f[i];
+      if (!GRAD || p.out) store_some<T, V>(out + e, narrow_pack<T, V>(f), n - e, p.past);
+    }
+  }
+  if (GRAD && p.partial) {
+    // this workgroup's sum of each column, row by row of its tile
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPacks; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) s_val[(k * kThreads + tid) * V + i] = __float_as_uint(col[k][i]);
+    __syncthreads();
+    for (int32_t v = tid; v < vocab; v += kThreads) {
+      float sum = 0.0f;
+      for (int32_t r = 0; r < p.tile_rows; ++r) sum += __uint_as_float(s_val[r * vocab + v]);
+      p.partial[(int64_t)blockIdx.x * vocab + v] = sum;
     }
   }
 }
 
-// dbias: a workgroup sums one run of rows for 64 columns, its four waves
-// taking every fourth row; the runs' sums are joined in order afterwards.
-constexpr int kBiasRuns = 256;
+// ------------------------------------------------ runs of columns of one row
+// The mask of the V columns from c0 + e, as loaded: a byte of bits, or V bytes
+// (moved back like load_inside).
+template <int V, int MASK>
+__device__ __forceinline__ uint64_t load_mask(const logits_args& a, int64_t at, int32_t c0, int32_t e,
+                                              int32_t n) {
+  const uint8_t* m = static_cast<const uint8_t*>(a.mask);
+  if constexpr (MASK == LOGITS_MASK_BITS) {
+    return m[at * 4 + ((c0 + min(e, n - 1)) >> 3)];
+  } else if constexpr (V == 8) {
+    typedef uint64_t eight __attribute__((aligned(1)));
+    return *reinterpret_cast<const eight*>(m + at + c0 + min(e, n - V));
+  } else if constexpr (V == 4) {
+    typedef uint32_t four __attribute__((aligned(1)));
+    return *reinterpret_cast<const four*>(m + at + c0 + min(e, n - V));
+  } else {
+    return m[at + c0 + min(e, n - V)];
+  }
+}
+// Bit i: column c0 + e + i is allowed.
+template <int V, int MASK>
+__device__ __forceinline__ uint32_t mask_bits(uint64_t raw, int32_t c0, int32_t e, int32_t n) {
+  if constexpr (MASK == LOGITS_MASK_BITS) {
+    return (uint32_t)raw >> ((c0 + e) & 7);
+  } else {
+    const int32_t back = e - (n - V);
+    if (back > 0) raw >>= 8 * back;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) bits |= ((raw >> (8 * i)) & 0xffu ? 1u : 0u) << i;
+    return bits;
+  }
+}
 
-template <class T>
-__global__ __launch_bounds__(kThreads) void bias_run_kernel(LogitsArgs p, float* partial,
-                                                            int64_t run_rows) {
+template <class T, int V, bool GRAD, int MASK>
+__global__ __launch_bounds__(kThreads) void logits_runs_kernel(LogitsArgs p) {
   using raw = typename T::raw;
-  __shared__ float s_sum[4][64];
+  constexpr int kRun = kThreads * V * kRunPacks;
+  __shared__ alignas(16) uint32_t s_count[kRun];
   const logits_args& a = p.a;
+  const int tid = threadIdx.x;
+  const int32_t c0 = (int32_t)blockIdx.x * kRun;
+  const int32_t n = min(kRun, a.vocab - c0);
+  // Columns a load may reach.  The last run may hold fewer than a pack: its
+  // loads then begin before it, in the same row (vocab >= V).
+  const int32_t rest = a.vocab - c0;
+  // the running sums of dbias of the thread's columns
+  float col[kRunPacks][V] = {};
+  for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
+    const raw* in = GRAD ? static_cast<const raw*>(p.dout) + r * p.dout_row + c0
+                         : static_cast<const raw*>(a.logits) + r * a.logits_row + c0;
+    const raw* z0 = static_cast<const raw*>(a.logits) + r * a.logits_row + c0;
+    raw* out = static_cast<raw*>(p.out) + r * p.out_row + c0;
+    const int32_t* h = a.history + r * a.history_row;
+    // Every load before the first wait.  Loads return in order, so what is
+    // needed first is loaded first: the row's terms and history, then the
+    // packs; the mask last, as its address may wait for the row's index.
+    int32_t token[4], len = 0;
+    float rho = 1.0f, alpha = 0.0f, beta = 0.0f;
+    int64_t mrow = r;
+    if (MASK != LOGITS_MASK_NONE && a.mask_rows) mrow = a.mask_rows[r];
+    if (p.penalties) {
+      len = a.history_len ? a.history_len[r] : a.history_width;
+      rho = a.repetition_rows ? a.repetition_rows[r] : a.repetition;
+      alpha = a.presence_rows ? a.presence_rows[r] : a.presence;
+      beta = a.frequency_rows ? a.frequency_rows[r] : a.frequency;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) token[j] = h[min(j * kThreads + tid, a.history_width - 1)];
+    }
+    Pack<T, V> x[kRunPacks], z[GRAD ? kRunPacks : 1];
+#pragma unroll
+    for (int k = 0; k < kRunPacks; ++k)
+      x[k] = load_inside<T, V>(in, (k * kThreads + tid) * V, rest);
+    if (GRAD && p.dense) {
+#pragma unroll
+      for (int k = 0; k < kRunPacks; ++k)
+        z[GRAD ? k : 0] = load_inside<T, V>(z0, (k * kThreads + tid) * V, rest);
+    }
+    constexpr int B = V < 4 ? V : 4;  // bias elements of an access
+    Pack<F32, B> bias[GRAD ? 1 : kRunPacks][V / B];
+    if (!GRAD && a.bias) {
+      const uint32_t* b = reinterpret_cast<const uint32_t*>(a.bias) + r * a.bias_row + c0;
+#pragma unroll
+      for (int k = 0; k < kRunPacks; ++k)
+#pragma unroll
+        for (int j = 0; j < V / B; ++j)
+          bias[GRAD ? 0 : k][j] = load_inside<F32, B>(b, (k * kThreads + tid) * V + j * B, rest);
+    }
+    uint64_t mraw[kRunPacks] = {};
+    bool free_row = true;  // everything is allowed
+    if (MASK != LOGITS_MASK_NONE) {
+      if (!a.mask_rows && a.mask_count == 1) mrow = 0;
+      free_row = mrow < 0 || mrow >= a.mask_count;
+#pragma unroll
+      for (int k = 0; k < kRunPacks; ++k)
+        mraw[k] = load_mask<V, MASK>(a, free_row ? 0 : mrow * a.mask_row, c0, (k * kThreads + tid) * V,
+                                     rest);
+    }
+    len = min(max(len, 0), a.history_width);
+    Terms t{};
+    if (len) {
+      t = terms_of(rho, alpha, beta);
+      __syncthreads();  // the previous row's counts are read
+#pragma unroll
+      for (int k = 0; k < kRunPacks; ++k) {
+        const uint32_t zero[V] = {};
+        write_words<V>(&s_count[(k * kThreads + tid) * V], zero);
+      }
+      __syncthreads();
+      for (int32_t i0 = tid; i0 < len; i0 += 4 * kThreads) {
+        if (i0 != tid) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) token[j] = h[min(i0 + j * kThreads, len - 1)];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i0 + j * kThreads < len && token[j] >= c0 && token[j] - c0 < n)
+            atomicAdd(&s_count[token[j] - c0], 1u);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < kRunPacks; ++k) {
+      const int32_t e = (k * kThreads + tid) * V;
+      if (e >= n) continue;
+      settle<T, V>(x[k], e, rest);
+      const uint32_t ok = MASK == LOGITS_MASK_NONE || free_row ? ~0u
+                                                               : mask_bits<V, MASK>(mraw[k], c0, e, rest);
+      float f[V];
+      widen_pack<T, V>(x[k], f);
+      if (GRAD && p.partial) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) col[k][i] += (ok >> i) & 1u ? f[i] : 0.0f;
+      }
+      if (len) {
+        uint32_t c[V], any = 0u;
+        read_words<V>(&s_count[e], c);
+#pragma unroll
+        for (int i = 0; i < V; ++i) any |= c[i];
+        if (any) {
+          if (GRAD && p.dense) settle<T, V>(z[GRAD ? k : 0], e, rest);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            if (!c[i]) continue;
+            if (GRAD) {
+              if ((ok >> i) & 1u) {
+                const float zi = T::widen(p.dense ? z[GRAD ? k : 0].v[i] : z0[e + i]);
+                f[i] = zi > 0.0f ? divide(f[i], t.rho, t.inv) : f[i] * t.rho;
+              }
+            } else {
+              f[i] = penalise(f[i], t, c[i]);
+            }
+          }
+        }
+      }
+      if (!GRAD && a.bias) {
+#pragma unroll
+        for (int j = 0; j < V / B; ++j) {
+          Pack<F32, B>& b = bias[GRAD ? 0 : k][j];
+          settle<F32, B>(b, e + j * B, rest);
+#pragma unroll
+          for (int i = 0; i < B; ++i) f[j * B + i] += F32::widen(b.v[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = (ok >> i) & 1u ? f[i] : (GRAD ? 0.0f : kBanned);
+      if (!GRAD || p.out) store_some<T, V>(out + e, narrow_pack<T, V>(f), n - e, p.past);
+    }
+  }
+  if (GRAD && p.partial) {
+    float* to = p.partial + (int64_t)blockIdx.y * a.vocab + c0;
+#pragma unroll
+    for (int k = 0; k < kRunPacks; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int32_t e = (k * kThreads + tid) * V + i;
+        if (e < n) to[e] = col[k][i];
+      }
+  }
+}
+
+// dbias[v] = the sum of the groups' sums of column v: 16 waves take every
+// 16th group of 64 columns, then the waves' sums are added in order.
+__global__ __launch_bounds__(1024) void bias_join_kernel(const float* partial, int32_t groups,
+                                                         int32_t vocab, float* dbias) {
+  __shared__ float s_sum[16][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t v = (int64_t)blockIdx.x * 64 + lane;
-  const int64_t lo = blockIdx.y * run_rows, hi = min(a.rows, lo + run_rows);
   float sum = 0.0f;
-  if (v < a.vocab) {
-    const raw* g = static_cast<const raw*>(p.dout) + v;
-    for (int64_t r = lo + w; r < hi; r += 4) {
-      const RowTerms t = row_terms(a, r);
-      if (allowed(a, t.mask, (int32_t)v)) sum += T::widen(g[r * p.dout_row]);
-    }
+  if (v < vocab) {
+#pragma unroll 8
+    for (int32_t k = w; k < groups; k += 16) sum += partial[(int64_t)k * vocab + v];
   }
   s_sum[w][lane] = sum;
   __syncthreads();
-  if (w == 0 && v < a.vocab)
-    partial[blockIdx.y * (int64_t)a.vocab + v] =
-        (s_sum[0][lane] + s_sum[1][lane]) + (s_sum[2][lane] + s_sum[3][lane]);
+  if (w == 0 && v < vocab) {
+    for (int j = 1; j < 16; ++j) sum += s_sum[j][lane];
+    dbias[v] = sum;
+  }
 }
 
-__global__ __launch_bounds__(kThreads) void bias_join_kernel(const float* partial, int32_t runs,
-                                                             int32_t vocab, float* dbias) {
-  const int64_t v = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (v >= vocab) return;
-  float sum = 0.0f;
-  for (int32_t k = 0; k < runs; ++k) sum += partial[(int64_t)k * vocab + v];
-  dbias[v] = sum;
+// Rows of a tile of whole rows.
+int32_t tile_rows_of(int32_t vocab) {
+  const int32_t rows = kTile / vocab;
+  return rows < kTileRows ? rows : kTileRows;
 }
-
-__global__ __launch_bounds__(kThreads) void clear_kernel(float* p, int64_t n) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i < n) p[i] = 0.0f;
+// Workgroups along the rows: dbias is summed over as many partial sums.
+int64_t flat_groups(int64_t rows, int32_t vocab) {
+  const int64_t tiles = (rows + tile_rows_of(vocab) - 1) / tile_rows_of(vocab);
+  return tiles < kFlatGroups ? tiles : kFlatGroups;
 }
-
-int64_t bias_runs(int64_t rows) { return rows < 4 * kBiasRuns ? (rows + 3) / 4 : kBiasRuns; }
-
-bool neutral(const logits_args& a) {
-  return !a.history || a.history_width == 0 ||
-         (!a.repetition_rows && !a.presence_rows && !a.frequency_rows && a.repetition == 1.0f &&
-          a.presence == 0.0f && a.frequency == 0.0f);
+int64_t run_groups(int64_t rows, int32_t vocab, bool bias) {
+  // with dbias few groups of many rows, as each adds a row of partial sums to
+  // the traffic, but enough to fill the chip
+  const int64_t runs = (vocab + 4095) / 4096;
+  const int64_t most = bias ? (kBiasGroups + runs - 1) / runs : 65535;
+  return rows < most ? rows : most;
 }
 
 template <class T, int V, bool GRAD>
-hipError_t launch_tiles(LogitsArgs p, bool flat, hipStream_t stream) {
-  const int64_t most = (int64_t)1 << 22;  // larger grids loop
+hipError_t launch(LogitsArgs p, bool flat, float* dbias, hipStream_t stream) {
+  const logits_args& a = p.a;
+  int64_t groups;
   if (flat) {
-    const int64_t tiles = (p.a.rows + p.tile_rows - 1) / p.tile_rows;
-    hipLaunchKernelGGL((logits_kernel<T, V, GRAD, true>),
-                       dim3((unsigned)(tiles < most ? tiles : most)), dim3(kThreads), 0, stream, p);
-  } else {
-    const unsigned runs = (unsigned)((p.a.vocab + p.tile_cols - 1) / p.tile_cols);
-    const int64_t cap = 1 << 16;
-    hipLaunchKernelGGL((logits_kernel<T, V, GRAD, false>),
-                       dim3((unsigned)(p.a.rows < cap ? p.a.rows : cap), runs), dim3(kThreads), 0,
+    groups = flat_groups(a.rows, a.vocab);
+    hipLaunchKernelGGL((logits_rows_kernel<T, V, GRAD>), dim3((unsigned)groups), dim3(kThreads), 0,
                        stream, p);
+  } else {
+    constexpr int kRun = kThreads * V * kRunPacks;
+    groups = run_groups(a.rows, a.vocab, dbias != nullptr);
+    const dim3 grid((unsigned)((a.vocab + kRun - 1) / kRun), (unsigned)groups);
+    auto kernel = a.mask_kind == LOGITS_MASK_BITS    ? logits_runs_kernel<T, V, GRAD, LOGITS_MASK_BITS>
+                  : a.mask_kind == LOGITS_MASK_BYTES ? logits_runs_kernel<T, V, GRAD, LOGITS_MASK_BYTES>
+                                                     : logits_runs_kernel<T, V, GRAD, LOGITS_MASK_NONE>;
+    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, p);
   }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !dbias) return e;
+  hipLaunchKernelGGL(bias_join_kernel, dim3((unsigned)(((int64_t)a.vocab + 63) / 64)), dim3(1024), 0,
+                     stream, p.partial, (int32_t)groups, a.vocab, dbias);
   return hipGetLastError();
 }
 
 template <class T, bool GRAD>
-hipError_t tiles(LogitsArgs p, hipStream_t stream) {
+hipError_t shape(LogitsArgs p, float* dbias, hipStream_t stream) {
   const logits_args& a = p.a;
-  const int64_t V = a.vocab;
-  const bool dense = p.out_row == V && (GRAD ? p.dout_row == V : true) &&
-                     (a.logits_row == V || (GRAD && !p.penalties));
-  const bool flat = V <= kShortRow && dense;
-  constexpr int kPack = 16 / T::kBytes;
+  const bool dense = (!p.out || p.out_row == a.vocab) && (!GRAD || p.dout_row == a.vocab) &&
+                     (a.logits_row == a.vocab || (GRAD && !p.penalties));
+  // the tile's quotients are exact, and its counts 16 bits, for histories that
+  // are not very long
+  const int64_t w = a.history_width;
+  const bool countable = !p.penalties ||
+                         (a.history_row == w && w < (1 << 16) &&
+                          tile_rows_of(a.vocab > kTile ? kTile : a.vocab) * w * w < ((int64_t)1 << 32));
+  const bool flat = a.vocab <= kTile && dense && countable;
   if (flat) {
-    // a multiple of a pack's elements, so that tiles start on packs
-    int64_t rows = kTile / V;
-    if (rows > kTileRows) rows = kTileRows;
-    if (rows > kPack) rows = rows / kPack * kPack;
-    p.tile_rows = (int32_t)rows;
-    p.magic = (uint32_t)((1ull << 32) / V + 1);
-  } else {
-    p.tile_rows = 1;
-    p.tile_cols = kTile;
+    p.tile_rows = tile_rows_of(a.vocab);
+    p.magic_vocab = (uint32_t)((1ull << 32) / (uint32_t)a.vocab + 1);
+    p.magic_words = (uint32_t)((1ull << 32) / (uint32_t)((a.vocab + 31) / 32) + 1);
+    if (p.penalties) p.magic_width = (uint32_t)((1ull << 32) / (uint32_t)a.history_width + 1);
   }
-  int pack = kPack;
-  auto fits = [&](int v) {
-    const size_t bytes = (size_t)v * T::kBytes;
-    const bool tail = flat ? (p.tile_rows * V) % v == 0 && (a.rows * V) % v == 0
-                           : V % v == 0 && p.out_row % v == 0 &&
-                                 (GRAD ? p.dout_row : a.logits_row) % v == 0;
-    return tail && aligned_to(GRAD ? p.dout : a.logits, bytes) && aligned_to(p.out, bytes);
-  };
-  while (pack > 1 && !fits(pack)) pack /= 2;
-  p.spread = 1;
-  while (p.spread < 64 && p.spread < a.history_width) p.spread *= 2;
-  if (!flat) p.spread = kThreads;
-  switch (pack) {
-    case 8: return launch_tiles<T, (T::kBytes == 2 ? 8 : 4), GRAD>(p, flat, stream);
-    case 4: return launch_tiles<T, 4, GRAD>(p, flat, stream);
-    case 2: return launch_tiles<T, 2, GRAD>(p, flat, stream);
-    default: return launch_tiles<T, 1, GRAD>(p, flat, stream);
-  }
+  if (a.mask_count == 0) p.a.mask_kind = LOGITS_MASK_NONE;  // a table without rows bans nothing
+  p.past = a.rows * a.vocab * T::kBytes > kPastBytes;
+  // a pack has to fit into the array (rows one after another) or the row
+  constexpr int V = 16 / T::kBytes;
+  if ((flat ? a.rows * a.vocab : a.vocab) >= V) return launch<T, V, GRAD>(p, flat, dbias, stream);
+  return launch<T, 1, GRAD>(p, flat, dbias, stream);
 }
 
 template <bool GRAD>
-hipError_t any_type(const LogitsArgs& p, hipStream_t stream) {
+hipError_t any_type(const LogitsArgs& p, float* dbias, hipStream_t stream) {
   switch (p.a.dtype) {
-    case POLICY_F32: return tiles<F32, GRAD>(p, stream);
-    case POLICY_BF16: return tiles<BF16, GRAD>(p, stream);
-    default: return tiles<F16, GRAD>(p, stream);
+    case POLICY_F32: return shape<F32, GRAD>(p, dbias, stream);
+    case POLICY_BF16: return shape<BF16, GRAD>(p, dbias, stream);
+    default: return shape<F16, GRAD>(p, dbias, stream);
   }
+}
+
+__global__ __launch_bounds__(kThreads) void clear_kernel(float* p, int32_t n) {
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i < n) p[i] = 0.0f;
 }
 
 }  // namespace
@@ -251,8 +655,10 @@ hipError_t logits_forward_launch(const logits_args& a, void* out, int64_t out_ro
   p.a = a;
   p.out = out;
   p.out_row = out_row;
-  p.penalties = !neutral(a);
-  return any_type<false>(p, stream);
+  p.penalties = a.history && a.history_width > 0 &&
+                (a.repetition_rows || a.presence_rows || a.frequency_rows || a.repetition != 1.0f ||
+                 a.presence != 0.0f || a.frequency != 0.0f);
+  return any_type<false>(p, nullptr, stream);
 }
 
 bool logits_gradient_reads_logits(const logits_args& a) {
@@ -260,48 +666,36 @@ bool logits_gradient_reads_logits(const logits_args& a) {
 }
 
 int64_t logits_workspace_bytes(int64_t rows, int32_t vocab) {
-  return bias_runs(rows) * (int64_t)vocab * 4;
+  if (rows == 0 || vocab == 0) return 0;
+  int64_t groups = run_groups(rows, vocab, true);
+  if (vocab <= kTile && flat_groups(rows, vocab) > groups) groups = flat_groups(rows, vocab);
+  return groups * vocab * 4;
 }
 
 hipError_t logits_backward_launch(const logits_args& a, const void* dout, int64_t dout_row,
                                   void* dlogits, int64_t dlogits_row, float* dbias,
                                   void* workspace, hipStream_t stream) {
   if (a.vocab == 0) return hipSuccess;
+  if (a.rows == 0) {
+    if (!dbias) return hipSuccess;
+    hipLaunchKernelGGL(clear_kernel, dim3((unsigned)(((int64_t)a.vocab + 255) / 256)),
+                       dim3(kThreads), 0, stream, dbias, a.vocab);
+    return hipGetLastError();
+  }
+  if (!dbias && !dlogits) return hipSuccess;
   LogitsArgs p{};
   p.a = a;
   p.dout = dout;
   p.dout_row = dout_row;
   p.out = dlogits;
   p.out_row = dlogits_row;
-  p.penalties = logits_gradient_reads_logits(a);
-  hipError_t e = hipSuccess;
-  if (dbias) {
-    // before dlogits, which may replace dout
-    if (a.rows == 0) {
-      hipLaunchKernelGGL(clear_kernel, dim3((unsigned)(((int64_t)a.vocab + 255) / 256)),
-                         dim3(kThreads), 0, stream, dbias, (int64_t)a.vocab);
-      return hipGetLastError();
-    }
-    const int64_t runs = bias_runs(a.rows), run_rows = (a.rows + runs - 1) / runs;
-    float* partial = static_cast<float*>(workspace);
-    const dim3 grid((unsigned)(((int64_t)a.vocab + 63) / 64), (unsigned)runs);
-    switch (a.dtype) {
-      case POLICY_F32:
-        hipLaunchKernelGGL(bias_run_kernel<F32>, grid, dim3(kThreads), 0, stream, p, partial, run_rows);
-        break;
-      case POLICY_BF16:
-        hipLaunchKernelGGL(bias_run_kernel<BF16>, grid, dim3(kThreads), 0, stream, p, partial, run_rows);
-        break;
-      default:
-        hipLaunchKernelGGL(bias_run_kernel<F16>, grid, dim3(kThreads), 0, stream, p, partial, run_rows);
-    }
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(bias_join_kernel, dim3((unsigned)(((int64_t)a.vocab + 255) / 256)),
-                       dim3(kThreads), 0, stream, partial, (int32_t)runs, a.vocab, dbias);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  if (a.rows == 0 || !dlogits) return hipSuccess;
-  return any_type<true>(p, stream);
+  p.partial = dbias ? static_cast<float*>(workspace) : nullptr;
+  // without dlogits the factor is not needed
+  p.penalties = dlogits && logits_gradient_reads_logits(a);
+  // a line of 64 bytes holds 16 to 32 logits: with a token in most lines,
+  // loading the marked logits one by one would fetch every line anyway
+  p.dense = p.penalties && (int64_t)a.history_width * 16 >= a.vocab;
+  return any_type<true>(p, dbias, stream);
 }
 
 }  // namespace rl

@@ -77,24 +77,36 @@ def declare(lib):
         getattr(lib, name).restype = i64 if name.endswith("_workspace") else C.c_int
 
 
-def _call(fn, *args):
-    from . import _check
-    _check(fn(*args))
+_loaded = None
 
 
 def _lib():
-    from . import load_library
-    return load_library()
+    global _loaded
+    if _loaded is None:
+        from . import load_library
+        _loaded = load_library()
+    return _loaded
+
+
+def _call(fn, *args):
+    rc = fn(*args)
+    if rc != 0:
+        from . import _check
+        _check(rc)
+
+
+# the raw stream handle without building a stream object, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _here(name, *tensors):
     """The current device's stream; every tensor must live on that device."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"{name}: every tensor must be on the current device, cuda:{dev} "
                              f"(got {t.device})")
-    return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream().cuda_stream
 
 
 def _element(name, t):

@@ -237,3 +237,20 @@ def test_captured_training_pass(rx, R, V):
             torch.cuda.synchronize()
             for x, y in zip(out, want):
                 assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("V", [45, 3000])
+def test_extreme_repetition(rx, V):
+    """Repetitions near the ends of fp32: the quotient is the division's."""
+    rho = torch.tensor([1e-45, 1e-39, 1e-30, 0.3, 7.0, 1e30, 1e38, 3e38], device="cuda")
+    z = torch.randn(8, V, device="cuda") * torch.tensor([1e-44, 1e-38, 1e-9, 1, 1, 1e9, 1e38, 3e38],
+                                                        device="cuda")[:, None]
+    h = torch.arange(40, dtype=torch.int32, device="cuda").repeat(8, 1)
+    got = rx.shape_logits(z, history=h, repetition=rho)
+    want = z.clone()
+    want[:, :40] = torch.where(z > 0, z / rho[:, None], z * rho[:, None])[:, :40]
+    d, r = got.cpu().double().numpy(), want.cpu().double().numpy()
+    assert (np.isfinite(d) == np.isfinite(r)).all()
+    m = np.isfinite(r)
+    # two roundings of a quotient at most, or of the smallest values
+    assert (np.abs(d[m] - r[m]) <= 2 * ref.U * np.abs(r[m]) + 2.0 ** -149).all()
