@@ -13,9 +13,9 @@
 // the packs has no branch per element.
 //
 // The gradient needs a logit only where a token occurred (its sign picks the
-// factor).  Short rows load all of them; long ones load the marked logits
-// alone, or, where the history is so dense that nearly every line of the row
-// holds one, whole packs ahead of time.
+// factor).  Short rows load all of them, as nearly every line holds one; in
+// long ones the history's entries load theirs and leave the sign beside the
+// mark.
 // dbias is summed by the pass that forms dlogits: a thread's packs cover the
 // same columns in every tile, so it adds up its own columns in registers
 // over all tiles it takes, and one more kernel joins the workgroups' sums in
@@ -31,7 +31,9 @@ constexpr int kThreads = 256;
 constexpr int kTile = 2048;      // elements of a tile of whole rows, at most
 constexpr int kTileRows = 128;   // its rows, at most
 constexpr int kRunPacks = 2;     // packs per thread of a run of columns
-constexpr int kFlatGroups = 2048;
+// workgroups of a launch over tiles: what is resident at once on 256 compute
+// units (the forward pass holds 76 registers a thread, the gradient 64)
+constexpr int kForwardGroups = 1536, kGradientGroups = 2048;
 constexpr int kBiasGroups = 2048;  // about, of runs in all
 constexpr float kBanned = -__builtin_inff();
 
@@ -46,7 +48,6 @@ struct LogitsArgs {
   uint32_t magic_words;  // for one by the words of a row of bits
   uint32_t magic_width;  // for one by history_width
   bool penalties;        // the history matters
-  bool dense;            // gradient: logits are loaded whole
   bool past;             // the output is stored past the caches
 };
 
@@ -123,25 +124,97 @@ __device__ __forceinline__ void write_words(uint32_t* p, const uint32_t (&w)[N])
   }
 }
 
-// A cell of a tile whose token occurred: its logit penalised, or its gradient
-// scaled.
+// The new value of a tile's cell whose token occurred: its logit penalised, or
+// its gradient scaled.
 template <bool GRAD>
-__device__ __forceinline__ void replace(uint32_t* val, const uint32_t* count, const uint32_t* pos,
-                                        const Terms& t, int32_t c) {
-  float f = __uint_as_float(val[c]);
-  if (GRAD)
-    f = (pos[c >> 5] >> (c & 31)) & 1u ? divide(f, t.rho, t.inv) : f * t.rho;
-  else
-    f = penalise(f, t, (count[c >> 1] >> ((c & 1) << 4)) & 0xffffu);
-  val[c] = __float_as_uint(f);
+__device__ __forceinline__ float replaced(const uint32_t* val, const uint32_t* count,
+                                          const uint32_t* pos, const Terms& t, int32_t c) {
+  const float f = __uint_as_float(val[c]);
+  if (GRAD) return (pos[c >> 5] >> (c & 31)) & 1u ? divide(f, t.rho, t.inv) : f * t.rho;
+  return penalise(f, t, (count[c >> 1] >> ((c & 1) << 4)) & 0xffffu);
 }
 
 // ------------------------------------------------------- tiles of whole rows
+constexpr int kAhead = 4;  // history entries a thread loads before it uses the first
+
+// What a workgroup needs of a tile, loaded while the one before is worked on.
+template <class T, int V, bool GRAD>
+struct RowsTile {
+  static constexpr int kPacks = kTile / (kThreads * V);
+  Pack<T, V> x[kPacks], z[GRAD ? kPacks : 1];
+  int32_t token[kAhead];
+  int32_t len;
+  float rho, alpha, beta;
+  uint32_t word;  // a mask of bits: this thread's word of the tile's masks,
+  bool named;     // if it has one
+};
+
+// A mask of bits gives every thread at most one word of a tile's masks (128
+// rows of at most 32 logits, or 2048 / vocab rows of more): word j of row r.
+struct MaskWord {
+  int32_t r, j;
+};
+__device__ __forceinline__ MaskWord mask_word(const LogitsArgs& p) {
+  const uint32_t W = (uint32_t)(p.a.vocab + 31) >> 5;
+  const int32_t r = (int32_t)quotient(threadIdx.x, W, p.magic_words);
+  return MaskWord{r, (int32_t)(threadIdx.x - r * W)};
+}
+// The mask row of that row; -1: everything is allowed.  Loaded two tiles
+// ahead, as the word's address waits for it.
+__device__ __forceinline__ int32_t mask_row_ahead(const LogitsArgs& p, int64_t r0, MaskWord m) {
+  const logits_args& a = p.a;
+  if (a.mask_kind != LOGITS_MASK_BITS) return -1;
+  const int64_t r = min(r0 + m.r, a.rows - 1);
+  // (one row per row of logits: mask_count, and so r, is below 2^31)
+  return a.mask_rows ? a.mask_rows[r] : (a.mask_count == 1 ? 0 : (int32_t)r);
+}
+
+// Elements from a tile's first row to the array's end, as far as a pack reaches.
+template <int V>
+__device__ __forceinline__ int32_t tile_reach(const logits_args& a, int64_t r0) {
+  return (int32_t)min((int64_t)(kTile + V), (a.rows - r0) * a.vocab);
+}
+
+// Every load before the first wait: no load behind a branch of its lanes.
+template <class T, int V, bool GRAD>
+__device__ __forceinline__ void load_tile(const LogitsArgs& p, int64_t r0, MaskWord m, int32_t mrow,
+                                          RowsTile<T, V, GRAD>& q) {
+  using raw = typename T::raw;
+  const logits_args& a = p.a;
+  const int tid = threadIdx.x;
+  const int32_t rows = (int32_t)min((int64_t)p.tile_rows, a.rows - r0);
+  const int32_t reach = tile_reach<V>(a, r0);
+  if (p.penalties) {
+    const int64_t r = r0 + min(tid, rows - 1);
+    q.len = a.history_len ? a.history_len[r] : a.history_width;
+    q.rho = a.repetition_rows ? a.repetition_rows[r] : a.repetition;
+    q.alpha = a.presence_rows ? a.presence_rows[r] : a.presence;
+    q.beta = a.frequency_rows ? a.frequency_rows[r] : a.frequency;
+    const int32_t* h = a.history + r0 * a.history_width;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      q.token[j] = h[min(j * kThreads + tid, rows * a.history_width - 1)];
+  }
+  if (a.mask_kind == LOGITS_MASK_BITS) {
+    q.named = m.r < rows && mrow >= 0 && mrow < a.mask_count;
+    q.word = static_cast<const uint32_t*>(a.mask)[q.named ? (int64_t)mrow * a.mask_row + m.j : 0];
+  }
+  const raw* in = static_cast<const raw*>(GRAD ? p.dout : a.logits) + r0 * a.vocab;
+#pragma unroll
+  for (int k = 0; k < q.kPacks; ++k)
+    q.x[k] = load_inside<T, V>(in, (k * kThreads + tid) * V, reach);
+  if (GRAD && p.penalties) {
+    const raw* z = static_cast<const raw*>(a.logits) + r0 * a.vocab;
+#pragma unroll
+    for (int k = 0; k < q.kPacks; ++k)
+      q.z[GRAD ? k : 0] = load_inside<T, V>(z, (k * kThreads + tid) * V, reach);
+  }
+}
+
 template <class T, int V, bool GRAD>
 __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
   using raw = typename T::raw;
   constexpr int kPacks = kTile / (kThreads * V);
-  constexpr int kAhead = 4;  // history entries loaded before the first is used
   __shared__ alignas(16) uint32_t s_val[kTile];  // the tile's values (fp32), penalised in place
   __shared__ alignas(16) uint32_t s_count[kTile / 2];  // two 16-bit counts a word
   __shared__ uint32_t s_ban[kTile / 32 + 1];     // a bit per element: not allowed
@@ -166,47 +239,30 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
         col[k][i] = a.bias[e - quotient(e, (uint32_t)vocab, p.magic_vocab) * vocab];
       }
     }
+  RowsTile<T, V, GRAD> next;
+  const MaskWord m = mask_word(p);
+  const int64_t first = (int64_t)blockIdx.x * p.tile_rows, step = (int64_t)gridDim.x * p.tile_rows;
+  load_tile<T, V, GRAD>(p, first, m, mask_row_ahead(p, first, m), next);
+  int32_t mrow = mask_row_ahead(p, first + step, m);
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int64_t r0 = tile * p.tile_rows;
     const int32_t rows = (int32_t)min((int64_t)p.tile_rows, a.rows - r0);
     const int32_t n = rows * vocab;
-    const raw* in = static_cast<const raw*>(GRAD ? p.dout : a.logits) + r0 * vocab;
-    const raw* z0 = static_cast<const raw*>(a.logits) + r0 * vocab;
     raw* out = static_cast<raw*>(p.out) + r0 * vocab;
     const int32_t* h = p.penalties ? a.history + r0 * width : nullptr;
     const int32_t entries = p.penalties ? rows * width : 0;
-    // elements from the tile's start to the array's end, as far as a pack reaches
-    const int32_t reach = (int32_t)min((int64_t)(kTile + V), (a.rows - r0) * vocab);
-    // Every load that waits for nothing, before the first wait.
-    int32_t len = 0;
-    float rho = 1.0f, alpha = 0.0f, beta = 0.0f;
-    if (p.penalties) {
-      const int64_t r = r0 + min(tid, rows - 1);
-      len = a.history_len ? a.history_len[r] : width;
-      rho = a.repetition_rows ? a.repetition_rows[r] : a.repetition;
-      alpha = a.presence_rows ? a.presence_rows[r] : a.presence;
-      beta = a.frequency_rows ? a.frequency_rows[r] : a.frequency;
-    }
-    Pack<T, V> x[kPacks], z[GRAD ? kPacks : 1];
-    int32_t token[kAhead];
-#pragma unroll
-    for (int k = 0; k < kPacks; ++k)
-      x[k] = load_inside<T, V>(in, (k * kThreads + tid) * V, reach);
-    if (GRAD && p.penalties) {
-#pragma unroll
-      for (int k = 0; k < kPacks; ++k)
-        z[GRAD ? k : 0] = load_inside<T, V>(z0, (k * kThreads + tid) * V, reach);
-    }
-    if (p.penalties) {
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) token[j] = h[min(j * kThreads + tid, entries - 1)];
+    const int32_t reach = tile_reach<V>(a, r0);
+    RowsTile<T, V, GRAD> q = next;
+    if (tile + gridDim.x < tiles) {
+      load_tile<T, V, GRAD>(p, r0 + step, m, mrow, next);
+      mrow = mask_row_ahead(p, r0 + 2 * step, m);
     }
     if (masked || p.penalties) {
       __syncthreads();  // the previous tile's words are read
       if (p.penalties) {
         if (tid < rows) {
-          s_terms[tid] = terms_of(rho, alpha, beta);
-          s_len[tid] = min(max(len, 0), width);
+          s_terms[tid] = terms_of(q.rho, q.alpha, q.beta);
+          s_len[tid] = min(max(q.len, 0), width);
         }
         for (int i = tid * 4; i < kTile / 2; i += kThreads * 4)
           *reinterpret_cast<uint4*>(&s_count[i]) = make_uint4(0, 0, 0, 0);
@@ -216,16 +272,10 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
       __syncthreads();
       if (a.mask_kind == LOGITS_MASK_BITS) {
         // a row's words are shifted to the row's place among the tile's bits
-        const int32_t W = (vocab + 31) >> 5;
-        for (int32_t i = tid; i < rows * W; i += kThreads) {
-          const int32_t r = (int32_t)quotient((uint32_t)i, (uint32_t)W, p.magic_words);
-          const int32_t j = i - r * W;
-          const int64_t at = mask_offset(a, r0 + r);
-          if (at < 0) continue;
-          uint32_t ban = ~static_cast<const uint32_t*>(a.mask)[at + j];
-          const int32_t left = vocab - 32 * j;
-          if (left < 32) ban &= (1u << left) - 1u;
-          const int32_t bit = r * vocab + 32 * j, sh = bit & 31;
+        if (q.named) {
+          const int32_t left = vocab - 32 * m.j;
+          const uint32_t ban = ~q.word & (left < 32 ? (1u << left) - 1u : ~0u);
+          const int32_t bit = m.r * vocab + 32 * m.j, sh = bit & 31;
           atomicOr(&s_ban[bit >> 5], ban << sh);
           if (sh) atomicOr(&s_ban[(bit >> 5) + 1], ban >> (32 - sh));
         }
@@ -249,15 +299,15 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
       for (int k = 0; k < kPacks; ++k) {
         const int32_t e = (k * kThreads + tid) * V;
         if (e >= n) continue;
-        settle<T, V>(x[k], e, reach);
+        settle<T, V>(q.x[k], e, reach);
         uint32_t word[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) word[i] = __float_as_uint(T::widen(x[k].v[i]));
+        for (int i = 0; i < V; ++i) word[i] = __float_as_uint(T::widen(q.x[k].v[i]));
         write_words<V>(s_val + e, word);
         if (GRAD) {
-          settle<T, V>(z[GRAD ? k : 0], e, reach);
+          settle<T, V>(q.z[GRAD ? k : 0], e, reach);
           float g[V];
-          widen_pack<T, V>(z[GRAD ? k : 0], g);
+          widen_pack<T, V>(q.z[GRAD ? k : 0], g);
           uint32_t bits = 0;
 #pragma unroll
           for (int i = 0; i < V; ++i) bits |= (g[i] > 0.0f ? 1u : 0u) << i;
@@ -267,30 +317,42 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
       // Count the tokens; the entry that counts a token first owns it and,
       // once all are counted, replaces the token's value.
       for (int32_t e0 = 0; e0 < entries; e0 += kAhead * kThreads) {
-        int32_t cell[kAhead], row[kAhead];
         if (e0 > 0) {
 #pragma unroll
           for (int j = 0; j < kAhead; ++j)
-            token[j] = h[min(e0 + j * kThreads + tid, entries - 1)];
+            q.token[j] = h[min(e0 + j * kThreads + tid, entries - 1)];
+        }
+        // entries that do not count add 0, each thread's to a word of its own:
+        // no branches, so the LDS works on all of them at once
+        int32_t row[kAhead], cell[kAhead];
+        uint32_t old[kAhead];
+        bool owner[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const int32_t e = min(e0 + j * kThreads + tid, entries - 1);
+          row[j] = (int32_t)quotient((uint32_t)e, (uint32_t)width, p.magic_width);
+          cell[j] = e - row[j] * width;
+          old[j] = (uint32_t)s_len[row[j]];
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-          const int32_t e = e0 + j * kThreads + tid;
-          cell[j] = -1;
-          if (e < entries) {
-            row[j] = (int32_t)quotient((uint32_t)e, (uint32_t)width, p.magic_width);
-            if (e - row[j] * width < s_len[row[j]] && token[j] >= 0 && token[j] < vocab) {
-              const int32_t c = row[j] * vocab + token[j], sh = (c & 1) << 4;
-              const uint32_t old = atomicAdd(&s_count[c >> 1], 1u << sh);
-              if (((old >> sh) & 0xffffu) == 0u) cell[j] = c;
-            }
-          }
+          owner[j] = e0 + j * kThreads + tid < entries && cell[j] < (int32_t)old[j] &&
+                     q.token[j] >= 0 && q.token[j] < vocab;
+          cell[j] = owner[j] ? row[j] * vocab + q.token[j] : 2 * tid;
+          old[j] = atomicAdd(&s_count[cell[j] >> 1], owner[j] ? 1u << ((cell[j] & 1) << 4) : 0u);
         }
         if (entries <= kAhead * kThreads) {
-          __syncthreads();
 #pragma unroll
           for (int j = 0; j < kAhead; ++j)
-            if (cell[j] >= 0) replace<GRAD>(s_val, s_count, s_pos, s_terms[row[j]], cell[j]);
+            owner[j] = owner[j] && ((old[j] >> ((cell[j] & 1) << 4)) & 0xffffu) == 0u;
+          __syncthreads();
+          float f[kAhead];
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j)
+            f[j] = replaced<GRAD>(s_val, s_count, s_pos, s_terms[row[j]], cell[j]);
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j)
+            if (owner[j]) s_val[cell[j]] = __float_as_uint(f[j]);
         }
       }
       if (entries > kAhead * kThreads) {
@@ -299,7 +361,7 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
         for (int32_t c = tid; c < n; c += kThreads)
           if ((s_count[c >> 1] >> ((c & 1) << 4)) & 0xffffu) {
             const int32_t r = (int32_t)quotient((uint32_t)c, (uint32_t)vocab, p.magic_vocab);
-            replace<GRAD>(s_val, s_count, s_pos, s_terms[r], c);
+            s_val[c] = __float_as_uint(replaced<GRAD>(s_val, s_count, s_pos, s_terms[r], c));
           }
       }
     }
@@ -315,8 +377,8 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] = __uint_as_float(word[i]);
       } else {
-        settle<T, V>(x[k], e, reach);
-        widen_pack<T, V>(x[k], f);
+        settle<T, V>(q.x[k], e, reach);
+        widen_pack<T, V>(q.x[k], f);
       }
       const uint32_t ban = masked ? s_ban[e >> 5] >> (e & 31) : 0u;
       if (!GRAD && a.bias && a.bias_row == 0) {
@@ -337,7 +399,7 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
       }
       if (GRAD && p.partial) {
         float g[V];
-        widen_pack<T, V>(x[k], g);
+        widen_pack<T, V>(q.x[k], g);
 #pragma unroll
         for (int i = 0; i < V; ++i)
           col[k][i] += e + i < n && !((ban >> i) & 1u) ? g[i] : 0.0f;
@@ -432,15 +494,10 @@ __global__ __launch_bounds__(kThreads) void logits_runs_kernel(LogitsArgs p) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) token[j] = h[min(j * kThreads + tid, a.history_width - 1)];
     }
-    Pack<T, V> x[kRunPacks], z[GRAD ? kRunPacks : 1];
+    Pack<T, V> x[kRunPacks];
 #pragma unroll
     for (int k = 0; k < kRunPacks; ++k)
       x[k] = load_inside<T, V>(in, (k * kThreads + tid) * V, rest);
-    if (GRAD && p.dense) {
-#pragma unroll
-      for (int k = 0; k < kRunPacks; ++k)
-        z[GRAD ? k : 0] = load_inside<T, V>(z0, (k * kThreads + tid) * V, rest);
-    }
     constexpr int B = V < 4 ? V : 4;  // bias elements of an access
     Pack<F32, B> bias[GRAD ? 1 : kRunPacks][V / B];
     if (!GRAD && a.bias) {
@@ -477,10 +534,21 @@ __global__ __launch_bounds__(kThreads) void logits_runs_kernel(LogitsArgs p) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) token[j] = h[min(i0 + j * kThreads, len - 1)];
         }
+        bool here[4];
+        raw z[GRAD ? 4 : 1];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (i0 + j * kThreads < len && token[j] >= c0 && token[j] - c0 < n)
+        for (int j = 0; j < 4; ++j) {
+          here[j] = i0 + j * kThreads < len && token[j] >= c0 && token[j] - c0 < n;
+          if (GRAD) z[GRAD ? j : 0] = here[j] ? z0[token[j] - c0] : raw{};
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (!here[j]) continue;
+          if (GRAD)
+            atomicOr(&s_count[token[j] - c0], T::widen(z[GRAD ? j : 0]) > 0.0f ? 3u : 1u);
+          else
             atomicAdd(&s_count[token[j] - c0], 1u);
+        }
       }
       __syncthreads();
     }
@@ -503,15 +571,11 @@ __global__ __launch_bounds__(kThreads) void logits_runs_kernel(LogitsArgs p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) any |= c[i];
         if (any) {
-          if (GRAD && p.dense) settle<T, V>(z[GRAD ? k : 0], e, rest);
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             if (!c[i]) continue;
             if (GRAD) {
-              if ((ok >> i) & 1u) {
-                const float zi = T::widen(p.dense ? z[GRAD ? k : 0].v[i] : z0[e + i]);
-                f[i] = zi > 0.0f ? divide(f[i], t.rho, t.inv) : f[i] * t.rho;
-              }
+              f[i] = c[i] & 2u ? divide(f[i], t.rho, t.inv) : f[i] * t.rho;
             } else {
               f[i] = penalise(f[i], t, c[i]);
             }
@@ -570,9 +634,10 @@ int32_t tile_rows_of(int32_t vocab) {
   return rows < kTileRows ? rows : kTileRows;
 }
 // Workgroups along the rows: dbias is summed over as many partial sums.
-int64_t flat_groups(int64_t rows, int32_t vocab) {
+int64_t flat_groups(int64_t rows, int32_t vocab, bool gradient) {
   const int64_t tiles = (rows + tile_rows_of(vocab) - 1) / tile_rows_of(vocab);
-  return tiles < kFlatGroups ? tiles : kFlatGroups;
+  const int64_t most = gradient ? kGradientGroups : kForwardGroups;
+  return tiles < most ? tiles : most;
 }
 int64_t run_groups(int64_t rows, int32_t vocab, bool bias) {
   // with dbias few groups of many rows, as each adds a row of partial sums to
@@ -587,7 +652,7 @@ hipError_t launch(LogitsArgs p, bool flat, float* dbias, hipStream_t stream) {
   const logits_args& a = p.a;
   int64_t groups;
   if (flat) {
-    groups = flat_groups(a.rows, a.vocab);
+    groups = flat_groups(a.rows, a.vocab, GRAD);
     hipLaunchKernelGGL((logits_rows_kernel<T, V, GRAD>), dim3((unsigned)groups), dim3(kThreads), 0,
                        stream, p);
   } else {
@@ -668,7 +733,8 @@ bool logits_gradient_reads_logits(const logits_args& a) {
 int64_t logits_workspace_bytes(int64_t rows, int32_t vocab) {
   if (rows == 0 || vocab == 0) return 0;
   int64_t groups = run_groups(rows, vocab, true);
-  if (vocab <= kTile && flat_groups(rows, vocab) > groups) groups = flat_groups(rows, vocab);
+  if (vocab <= kTile && flat_groups(rows, vocab, true) > groups)
+    groups = flat_groups(rows, vocab, true);
   return groups * vocab * 4;
 }
 
@@ -692,9 +758,6 @@ hipError_t logits_backward_launch(const logits_args& a, const void* dout, int64_
   p.partial = dbias ? static_cast<float*>(workspace) : nullptr;
   // without dlogits the factor is not needed
   p.penalties = dlogits && logits_gradient_reads_logits(a);
-  // a line of 64 bytes holds 16 to 32 logits: with a token in most lines,
-  // loading the marked logits one by one would fetch every line anyway
-  p.dense = p.penalties && (int64_t)a.history_width * 16 >= a.vocab;
   return any_type<true>(p, dbias, stream);
 }
 
