@@ -62,10 +62,15 @@ template <class T, int V>
 __device__ __forceinline__ void store_pack(typename T::raw* p, const Pack<T, V>& x, bool past) {
   if constexpr (V * T::kBytes == 16) {
     const quad_value q = __builtin_bit_cast(quad_value, x);
-    if (past)
+    if (past) {
+      // (the empty statements keep the compiler from merging the two stores
+      // into one, which would drop the hint)
+      asm volatile("" ::: "memory");
       __builtin_nontemporal_store((quad)q, reinterpret_cast<quad*>(p));
-    else
+      asm volatile("" ::: "memory");
+    } else {
       *reinterpret_cast<quad*>(p) = q;
+    }
   } else {
     store_pack<T, V>(p, x);
   }

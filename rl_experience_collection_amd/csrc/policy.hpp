@@ -38,7 +38,7 @@ struct EmbedBackward {
   float scale;
 };
 hipError_t embed_forward_launch(const EmbedForward& a, hipStream_t stream);
-int64_t embed_workspace_bytes(int64_t vocab, int32_t width, int64_t count);
+int64_t embed_workspace_bytes(int32_t dtype, int64_t vocab, int32_t width, int64_t count);
 hipError_t embed_backward_launch(const EmbedBackward& a, hipStream_t stream);
 
 hipError_t logits_forward_launch(const logits_args& a, void* out, int64_t out_row,

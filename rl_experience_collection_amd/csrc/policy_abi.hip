@@ -67,9 +67,7 @@ int check_strides(const char* who, const char* name, int64_t step, int64_t row) 
   return ROLLOUT_OK;
 }
 
-int check_recur_workspace(const char* who, int32_t steps, int32_t rows, int32_t width, int32_t dtype,
-                          const void* workspace, int64_t bytes) {
-  const int64_t need = rl::recur_workspace_bytes(steps, rows, width, dtype);
+int check_workspace(const char* who, int64_t need, const void* workspace, int64_t bytes) {
   if (need == 0) return ROLLOUT_OK;
   if (!workspace || bytes < need)
     return fail(ROLLOUT_EINVAL, "%s: workspace of %lld bytes needed, %lld given", who,
@@ -173,8 +171,8 @@ int recur_forward(const recur_args* a, void* hip_stream) {
     RL_CHECK(check_buffer(who, "x", a->x, eb));
     RL_CHECK(check_buffer(who, "gate", a->gate, eb));
     RL_CHECK(check_buffer(who, "h", a->h, eb));
-    RL_CHECK(check_recur_workspace(who, a->steps, a->rows, a->width, a->dtype, a->workspace,
-                                   a->workspace_bytes));
+    RL_CHECK(check_workspace(who, rl::recur_workspace_bytes(a->steps, a->rows, a->width, a->dtype),
+                             a->workspace, a->workspace_bytes));
   }
   return launched(rl::recur_forward_launch(*a, static_cast<hipStream_t>(hip_stream)), who);
 }
@@ -204,8 +202,8 @@ int recur_backward(const recur_grad_args* a, void* hip_stream) {
     RL_CHECK(check_buffer(who, "dh", a->dh, eb));
     RL_CHECK(check_buffer(who, "dx", a->dx, eb));
     RL_CHECK(check_buffer(who, "dgate", a->dgate, eb));
-    RL_CHECK(check_recur_workspace(who, a->steps, a->rows, a->width, a->dtype, a->workspace,
-                                   a->workspace_bytes));
+    RL_CHECK(check_workspace(who, rl::recur_workspace_bytes(a->steps, a->rows, a->width, a->dtype),
+                             a->workspace, a->workspace_bytes));
   }
   return launched(rl::recur_backward_launch(*a, static_cast<hipStream_t>(hip_stream)), who);
 }
@@ -253,7 +251,7 @@ int embed_forward(int32_t dtype, const void* weight, int64_t vocab, int32_t widt
 
 int64_t embed_workspace(int32_t dtype, int64_t vocab, int32_t width, int64_t count) {
   RL_CHECK(check_embed_sizes("embed_workspace", dtype, vocab, width, count));
-  return vocab == 0 || width == 0 ? 0 : rl::embed_workspace_bytes(vocab, width, count);
+  return rl::embed_workspace_bytes(dtype, vocab, width, count);
 }
 
 int embed_backward(int32_t dtype, const void* dout, int64_t dout_row, const void* index,
@@ -271,11 +269,8 @@ int embed_backward(int32_t dtype, const void* dout, int64_t dout_row, const void
   }
   RL_CHECK(check_buffer(who, "dweight", dweight, eb));
   RL_CHECK(check_rows(who, "dweight", dweight_row, width));
-  const int64_t need = rl::embed_workspace_bytes(vocab, width, count);
-  if (!workspace || workspace_bytes < need)
-    return fail(ROLLOUT_EINVAL, "%s: workspace of %lld bytes needed, %lld given", who,
-                (long long)need, workspace ? (long long)workspace_bytes : 0LL);
-  RL_CHECK(check_buffer(who, "workspace", workspace, 16));
+  RL_CHECK(check_workspace(who, rl::embed_workspace_bytes(dtype, vocab, width, count), workspace,
+                           workspace_bytes));
   rl::EmbedBackward a{dout, index, dweight, workspace, vocab, count, dout_row, dweight_row,
                       dtype, width, index_bytes, scale};
   return launched(rl::embed_backward_launch(a, static_cast<hipStream_t>(hip_stream)), who);
@@ -311,11 +306,8 @@ int logits_backward(const logits_args* a, const void* dout, int64_t dout_row, vo
     RL_CHECK(check_optional(who, "dlogits", dlogits, eb));
     if (dlogits) RL_CHECK(check_rows(who, "dlogits", dlogits_row, a->vocab));
     if (dbias) {
-      const int64_t need = rl::logits_workspace_bytes(a->rows, a->vocab);
-      if (!workspace || workspace_bytes < need)
-        return fail(ROLLOUT_EINVAL, "%s: workspace of %lld bytes needed, %lld given", who,
-                    (long long)need, workspace ? (long long)workspace_bytes : 0LL);
-      RL_CHECK(check_buffer(who, "workspace", workspace, 16));
+      RL_CHECK(check_workspace(who, rl::logits_workspace_bytes(a->rows, a->vocab), workspace,
+                               workspace_bytes));
     }
   }
   return launched(rl::logits_backward_launch(*a, dout, dout_row, dlogits, dlogits_row, dbias,

@@ -47,7 +47,8 @@ def inputs(M, V, D, name, seed, spread="even", out_of_range=0.05):
 
 SIZES = [(1, 1, 1), (3, 2, 5), (64, 45, 128), (65, 1, 8), (255, 511, 6), (256, 512, 4),
          (257, 513, 33), (2047, 45, 3), (2049, 45, 16), (5000, 3, 40), (3, 70000, 2),
-         (9000, 262145, 1), (700, 300, 1000)]
+         (9000, 262145, 1), (700, 300, 1000), (511, 40, 9), (512, 31, 500), (513, 33, 511), (1030, 70, 257),
+         (600, 600, 15), (1500, 20, 520)]
 
 
 @pytest.mark.parametrize("name", ["f32", "bf16", "f16"])

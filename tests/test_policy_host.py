@@ -157,11 +157,11 @@ def test_embed_c_refusals(rx):
         assert text in rx.rollout_last_error(), (kw, rx.rollout_last_error())
     assert fwd(count=0) == OK and fwd(D=0) == OK
 
-    size = lib.embed_workspace(0, 5, 4, 3)
+    size = lib.embed_workspace(0, 5, 4, 3000)
     assert size > 0 and lib.embed_workspace(0, 5, 4, -3) == EINVAL
     assert lib.embed_workspace(0, 0, 4, 3) == 0
 
-    def bwd(dtype=0, dout=64, drow=4, index=64, ib=4, count=3, V=5, D=4, dw=64, wrow=4, ws=64, size=size):
+    def bwd(dtype=0, dout=64, drow=4, index=64, ib=4, count=3000, V=5, D=4, dw=64, wrow=4, ws=64, size=size):
         return lib.embed_backward(dtype, dout, drow, index, ib, count, V, D, 1.0, dw, wrow, ws, size, None)
 
     for kw, text in [(dict(dout=None), "dout is NULL"), (dict(drow=3), "dout are 3 apart"),
