@@ -92,6 +92,53 @@ __device__ __forceinline__ Pack<T, V> narrow_pack(const float (&f)[V]) {
   return x;
 }
 
+// The same at an address that all lanes share plus an offset of each in bytes:
+// one scalar and one 32-bit register, no arithmetic per lane.  (The empty
+// statement keeps the compiler from adding the offset first and the step to
+// every lane's 64-bit sum instead.)
+#define RL_GLOBAL __attribute__((address_space(1)))
+typedef quad RL_GLOBAL* global_quad;
+__device__ __forceinline__ RL_GLOBAL char* shared_address(const void* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  uint64_t a = (uint64_t)hi << 32 | lo;
+  asm("" : "+s"(a));
+  return reinterpret_cast<RL_GLOBAL char*>(a);
+}
+template <class T, int V>
+__device__ __forceinline__ Pack<T, V> load_pack_at(const void* base, uint32_t off) {
+  RL_GLOBAL char* p = shared_address(base) + off;
+  if constexpr (V * T::kBytes == 16) {
+    return __builtin_bit_cast(Pack<T, V>, (quad_value)*reinterpret_cast<global_quad>(p));
+  } else if constexpr (V * T::kBytes == 8) {
+    typedef uint32_t two_value __attribute__((ext_vector_type(2)));
+    typedef uint32_t two __attribute__((ext_vector_type(2), aligned(2)));
+    return __builtin_bit_cast(Pack<T, V>, (two_value)*reinterpret_cast<two RL_GLOBAL*>(p));
+  } else if constexpr (V * T::kBytes == 4) {
+    typedef uint32_t one __attribute__((aligned(2)));
+    return __builtin_bit_cast(Pack<T, V>, (uint32_t)*reinterpret_cast<one RL_GLOBAL*>(p));
+  } else {
+    return __builtin_bit_cast(Pack<T, V>, *reinterpret_cast<uint16_t RL_GLOBAL*>(p));
+  }
+}
+template <class T, int V>
+__device__ __forceinline__ void store_pack_at(void* base, uint32_t off, const Pack<T, V>& x) {
+  RL_GLOBAL char* p = shared_address(base) + off;
+  if constexpr (V * T::kBytes == 16) {
+    *reinterpret_cast<global_quad>(p) = __builtin_bit_cast(quad_value, x);
+  } else if constexpr (V * T::kBytes == 8) {
+    typedef uint32_t two_value __attribute__((ext_vector_type(2)));
+    typedef uint32_t two __attribute__((ext_vector_type(2), aligned(2)));
+    *reinterpret_cast<two RL_GLOBAL*>(p) = __builtin_bit_cast(two_value, x);
+  } else if constexpr (V * T::kBytes == 4) {
+    typedef uint32_t one __attribute__((aligned(2)));
+    *reinterpret_cast<one RL_GLOBAL*>(p) = __builtin_bit_cast(uint32_t, x);
+  } else {
+    *reinterpret_cast<uint16_t RL_GLOBAL*>(p) = __builtin_bit_cast(uint16_t, x);
+  }
+}
+
 // Elements e .. e + V - 1 of an array of n >= V: the access is moved back to
 // lie inside the array (load_inside), and the elements that exist are put in
 // their places when they are used (settle), so that the load sits behind no

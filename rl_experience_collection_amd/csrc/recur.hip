@@ -9,16 +9,28 @@
 // so that the map then selects B instead of multiplying a possibly infinite
 // or NaN state by zero.
 //
-// A workgroup of 8 waves owns a column of 64 lanes x V channels and walks
-// time in tiles of 8 slots, one slot of S steps per wave.  A wave loads its
-// slot into registers, folds it into its map, and leaves the map in LDS;
-// after one barrier every wave folds the maps before its own onto the
-// tile's carry, replays its slot from registers and stores it.  So each
-// element is read and written once.  Where the columns are too few to fill
-// the chip, time is also cut into chunks: a first launch writes every
-// chunk's map to the workspace, and the main launch starts each chunk from
-// the fold of the maps before it.  That reads x and gate twice.  The order
-// of every fold depends on the sizes alone: results are deterministic.
+// A workgroup of 8 (chained: 16) waves owns a column of 64 lanes x V channels and
+// takes time in tiles, one slot of S steps per wave.  A wave loads its slot
+// into registers, folds it into its map, and leaves the map in LDS; after one
+// barrier every wave folds the maps before its own onto the state that enters
+// the tile, replays its slot from registers and stores it.  So each element is
+// read and written once.
+//
+// Where the columns alone fill the chip a workgroup walks all tiles of its
+// column.  Where they are few (CHAIN) every tile has a workgroup of its own,
+// taken in order from a ticket, and the states pass between them: a tile
+// publishes its map, waits until one of the 16 tiles before it has published
+// a state (a map with a done is one) and all nearer ones their maps, folds
+// these onto it, oldest first, and publishes the state that leaves it.
+// Every published map is one 64-bit word, stored and polled by device-coherent
+// relaxed atomics, so no fence is needed; a kernel marks the words as empty
+// first.  Each wait is on a workgroup with an earlier ticket, which
+// runs already and publishes its map without waiting, so every wait ends; a
+// wait that reached its bound all the same would leave NaN, never a wrong
+// number.  A state is the same expression wherever the walk found its start:
+// results do not depend on timing.
+#include <type_traits>
+
 #include "elem.hpp"
 #include "policy.hpp"
 
@@ -26,9 +38,11 @@ namespace rl {
 
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kSlot = 8;                  // steps per wave and tile
-constexpr int kTile = kWaves * kSlot;     // steps per tile
+// Waves of a workgroup and steps per wave and tile (a slot's values stay in
+// registers).  A chained tile is as long as a workgroup's registers allow: each
+// costs a walk, and the walks of a column follow each other.
+constexpr int waves_of(bool chained) { return chained ? 16 : 8; }
+constexpr int slot_steps(bool back, bool chained) { return chained && !back ? 16 : 8; }
 constexpr float kReset = -0.0f;
 
 struct Map {
@@ -56,10 +70,9 @@ __device__ __forceinline__ Map chain(Map first, Map second) {
 // by a difference.  E is 2^(hi + lo), hi + lo the product |g| log2(e) in two
 // parts.
 __device__ __forceinline__ void sigmoids(float g, float& a, float& keep) {
-  float m = __builtin_fabsf(g);
-  m = m > 200.0f ? 200.0f : m;  // (a NaN passes)
+  const float m = __builtin_elementwise_minimum(__builtin_fabsf(g), 200.0f);  // (a NaN stays)
   const float hi = m * -1.44269502f;
-  const float lo = __builtin_fmaf(m, -1.44269502f, -hi) + m * -1.92596300e-8f;
+  const float lo = __builtin_fmaf(m, -1.92596300e-8f, __builtin_fmaf(m, -1.44269502f, -hi));
   float E = __builtin_amdgcn_exp2f(hi);
   E = __builtin_fmaf(E * lo, 0.693147182f, E);
   const float r = __builtin_amdgcn_rcpf(1.0f + E);
@@ -70,10 +83,10 @@ __device__ __forceinline__ void sigmoids(float g, float& a, float& keep) {
 
 struct RecurArgs {
   int32_t L, N, D;
-  int32_t units;     // N * (D / V): lanes with work
-  int32_t per_row;   // D / V
-  int32_t chunk;     // steps per chunk (a multiple of kTile)
-  int32_t chunks;
+  int32_t units;     // N * ceil(D / V): lanes with work
+  int32_t per_row;   // ceil(D / V)
+  int32_t columns;
+  uint32_t tiles;    // chained: tiles of all columns
   int64_t x_step, x_row, g_step, g_row, h_step, h_row;
   int64_t dh_step, dh_row, dx_step, dx_row, dg_step, dg_row;
   const void *x, *gate, *h, *dh;
@@ -82,323 +95,526 @@ struct RecurArgs {
   const uint8_t* dones;
   void *out, *dx, *dg;
   float* last;         // h_last / dh0
-  Map* maps;           // [chunks][units][V]
+  uint32_t* ticket;    // chained: the next tile
+  uint64_t* words;     // chained: [tiles][units][V] published maps
 };
 
-// The carry into chunk `q` of a column: the maps of chunks [lo, hi) folded
-// onto `c`, in the order lo, lo+1, ... (forward) or hi-1, hi-2, ...
-// (backward).  Each wave folds a run of chunks; the runs are joined in LDS.
-template <int V, bool BACK>
-__device__ __forceinline__ void fold_chunks(const RecurArgs& p, int lo, int hi, int32_t u, int w,
-                                            int lane, Map (&s)[kWaves][64][V], float (&c)[V]) {
-  const int count = hi - lo;
-  const int per = (count + kWaves - 1) / kWaves;
-  Map m[V];
+// One of the strided arrays as a column sees it: the address of its first
+// row (the same for the workgroup) and this lane's offset from there.  With
+// 32-bit offsets an access needs no arithmetic per lane.
+template <class T, int V, bool OFF32>
+struct Lane {
+  char* base;
+  typename std::conditional<OFF32, uint32_t, int64_t>::type off;
+  int64_t step;
+  __device__ __forceinline__ Lane(const void* p, int64_t step_, int64_t row, int32_t n0, int32_t n,
+                                  int32_t d)
+      : base(const_cast<char*>(static_cast<const char*>(p)) + n0 * row * T::kBytes),
+        off((((int64_t)(n - n0) * row) + d) * T::kBytes),
+        step(step_ * T::kBytes) {}
+  __device__ __forceinline__ Pack<T, V> load(int32_t t) const {
+    if constexpr (OFF32)
+      return load_pack_at<T, V>(base + t * step, off);
+    else
+      return load_pack<T, V>(reinterpret_cast<const typename T::raw*>(base + t * step + off));
+  }
+  __device__ __forceinline__ void store(int32_t t, const Pack<T, V>& x) const {
+    if constexpr (OFF32)
+      store_pack_at<T, V>(base + t * step, off, x);
+    else
+      store_pack<T, V>(reinterpret_cast<typename T::raw*>(base + t * step + off), x);
+  }
+};
+
+constexpr int kWalk = 16;              // tiles looked back over at most
+constexpr uint32_t kPolls = 1u << 24;  // of a wait, at most
+
+// A published word is a map: its slope below, its b above.  A state is the
+// map that forgets and gives the state.  A slope of these bits is one not yet
+// published: published slopes that are no numbers all have the same bits,
+// others.
+constexpr uint32_t kNothing = 0xffffffffu;
+
+__device__ __forceinline__ void put_map(uint64_t* p, Map m) {
+  const float a = m.a == m.a ? m.a : __builtin_nanf("");
+  __hip_atomic_store(p, (uint64_t)__float_as_uint(a) | (uint64_t)__float_as_uint(m.b) << 32,
+                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ Map get_map(const uint64_t* p) {
+  const uint64_t w = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return Map{__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
+}
+
+// The next tile of a chained workgroup, in the order of the scan, and its
+// column; false when all are taken.
+struct Chained {
+  int32_t order, column;
+  __device__ __forceinline__ bool take(const RecurArgs& p) {
+    __shared__ uint32_t s_ticket;
+    if (threadIdx.x == 0)
+      s_ticket = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();  // (and the tile before is done with its LDS)
+    const uint32_t k = __builtin_amdgcn_readfirstlane(s_ticket);
+    order = (int32_t)(k / (uint32_t)p.columns);
+    column = (int32_t)(k % (uint32_t)p.columns);
+    return k < p.tiles;
+  }
+};
+
+// What a workgroup of a chained scan keeps in LDS besides its slots' maps.
+template <int V>
+struct ChainLds {
+  Map before[kWalk][64][V];  // the maps of the tiles before
+  float state[64][V];        // that enters this tile
+  int32_t walk;              // tiles to look at; 0: the state is there
+};
+
+// The tiles before tile `o` that have to be looked at, as far as one of their
+// words tells: polled by wave 0 until a state and all nearer maps are out.
+// `sample` is that word of tile o; `left` the polls that remain.
+__device__ __forceinline__ int32_t poll_chain(const uint64_t* sample, int64_t stride, int32_t o, int lane,
+                                              uint32_t& left) {
+  const uint64_t* at = sample - (int64_t)min(min(lane, kWalk - 1) + 1, o) * stride;
+  for (;;) {
+    const float a = get_map(at).a;
+    const uint64_t out = __ballot(__float_as_uint(a) != kNothing), state = __ballot(is_reset(a));
+    const int nearest = state ? __builtin_ctzll(state) : 64;
+    // (lanes past the walk repeat its end)
+    if (nearest < kWalk && (~out & ((2ull << nearest) - 1)) == 0) return nearest + 1;
+    if (left == 0) return kWalk;
+    --left;
+    __builtin_amdgcn_s_sleep(1);
+  }
+}
+
+// The state that enters tile `o` (in the order of the scan), for every wave:
+// `c` is the state that enters the scan and becomes that.
+template <int V, int W>
+__device__ __forceinline__ void enter_tile(const RecurArgs& p, int32_t o, int32_t u, bool active, int w,
+                                           int lane, const float (&sa)[W][64][V],
+                                           const float (&sb)[W][64][V], ChainLds<V>& s,
+                                           float (&c)[V]) {
+  const int64_t stride = (int64_t)p.units * V;  // words of a tile
+  uint64_t* mine = p.words + o * stride + (int64_t)u * V;
+  Map t[V];
+  if (w == 0) {
+    // the tile's map
+#pragma unroll
+    for (int v = 0; v < V; ++v) t[v] = Map{sa[0][lane][v], sb[0][lane][v]};
+#pragma unroll
+    for (int j = 1; j < W; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) t[v] = chain(t[v], Map{sa[j][lane][v], sb[j][lane][v]});
+    if (o > 0 && active) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) put_map(mine + v, t[v]);
+    }
+  }
+  if (o > 0) {
+    uint32_t left = kPolls;
+    for (;;) {
+      if (w == 0) {
+        // the word of the column's first unit stands for all
+        const int32_t u0 = __builtin_amdgcn_readfirstlane(u);
+        const int32_t walk = poll_chain(p.words + o * stride + (int64_t)u0 * V, stride, o, lane, left);
+        if (lane == 0) s.walk = walk;
+      }
+      __syncthreads();
+      const int32_t walk = __builtin_amdgcn_readfirstlane(s.walk);
+#pragma unroll
+      for (int k = 0; k < kWalk / W; ++k) {
+        const int back = w + k * W;  // tiles in between
+        if (back >= walk) continue;
+        const uint64_t* at = mine - (int64_t)min(back + 1, o) * stride;
+#pragma unroll
+        for (int v = 0; v < V; ++v) s.before[back][lane][v] = get_map(at + v);
+      }
+      __syncthreads();
+      if (w == 0) {
+        // from the oldest to the nearest: a state starts anew, a gap ends it
+        bool ready = true;
+        float x[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          x[v] = 0.0f;
+          bool known = false;
+          for (int k = walk - 1; k >= 0; --k) {
+            const Map m = s.before[k][lane][v];
+            known = is_reset(m.a) || (known && __float_as_uint(m.a) != kNothing);
+            x[v] = apply(m, x[v]);
+          }
+          ready = ready && known;
+        }
+        const bool done = __all(ready || !active);
+        if (done || left == 0) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) s.state[lane][v] = done ? x[v] : __builtin_nanf("");
+        } else {
+          --left;
+        }
+        if (lane == 0 && (done || left == 0)) s.walk = 0;
+      }
+      __syncthreads();
+      if (__builtin_amdgcn_readfirstlane(s.walk) == 0) break;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v] = s.state[lane][v];
+  }
+  if (w == 0 && active) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (o == 0 || !is_reset(t[v].a)) put_map(mine + v, Map{kReset, apply(t[v], c[v])});
+  }
+}
+
+// Joins the tile's slots: `c` is the state that enters the tile, and then the
+// one that leaves it; `h` becomes the state that enters this wave's slot.
+// Without a done in the tile the maps are plain.
+template <int V, int W, bool FORGETS>
+__device__ __forceinline__ void join_slots(const float (&sa)[W][64][V],
+                                           const float (&sb)[W][64][V], int w, int lane,
+                                           float (&c)[V], float (&h)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = c[v];
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    const bool mine = j == w;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const Map m{sa[j][lane][v], sb[j][lane][v]};
+      if (mine) h[v] = c[v];
+      c[v] = FORGETS ? apply(m, c[v]) : __builtin_fmaf(m.a, c[v], m.b);
+    }
+  }
+}
+
+// Where a workgroup and its lane stand.
+struct Place {
+  int lane, w;
+  int32_t u, n0, n, d;
+  bool active;
+  int64_t cell;
+  template <int V>
+  static __device__ __forceinline__ Place of(const RecurArgs& p, int32_t column) {
+    Place s;
+    s.lane = (int)threadIdx.x & 63;
+    s.w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int32_t first = column * 64;
+    s.active = first + s.lane < p.units;
+    s.u = s.active ? first + s.lane : p.units - 1;  // idle lanes read a valid element
+    s.n0 = first / p.per_row;
+    s.n = s.u / p.per_row;
+    // a row's last unit is moved back to end with it: where D is no multiple
+    // of V it repeats channels of the one before, with the same results
+    s.d = min((s.u - s.n * p.per_row) * V, p.D - V);
+    s.cell = (int64_t)s.n * p.D + s.d;
+    return s;
+  }
+};
+
+// The dones that cut this slot's steps, bit i for step t(i): the state that
+// enters step t is cut where dones[t - 1] is set.
+template <int S, bool BACK>
+__device__ __forceinline__ uint32_t load_dones(const RecurArgs& p, int32_t n, int32_t from, int32_t tb,
+                                               int32_t te) {
+  uint8_t db[S];
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    const int32_t t = BACK ? from - i : from + i;
+    const uint8_t* row = p.dones + (int64_t)(max(min(max(t, tb), te - 1), 1) - 1) * p.N;
+    db[i] = *reinterpret_cast<uint8_t RL_GLOBAL*>(shared_address(row) + (uint32_t)n);
+  }
+  uint32_t done = 0;
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    const int32_t t = BACK ? from - i : from + i;
+    done |= (t > 0 && t >= tb && t < te && db[i] ? 1u : 0u) << i;
+  }
+  return done;
+}
+
+// A slot's map, of steps a h + b.
+template <int V, int S, bool CUT>
+__device__ __forceinline__ void fold_forward(const float (&a)[S][V], const float (&b)[S][V],
+                                             uint32_t done, Map (&m)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) m[v] = Map{a[0][v], b[0][v]};
+#pragma unroll
+  for (int i = 1; i < S; ++i)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float nb = __builtin_fmaf(a[i][v], m[v].b, b[i][v]);
+      m[v].b = CUT && ((done >> i) & 1u) ? b[i][v] : nb;
+      m[v].a *= a[i][v];
+    }
+#pragma unroll
+  for (int v = 0; v < V; ++v) m[v].a = stored_slope(m[v].a, CUT && done != 0);
+}
+
+template <class T, int V, bool SIG, bool CHAIN, bool OFF32>
+__global__ __launch_bounds__(64 * waves_of(CHAIN)) void recur_forward_kernel(const RecurArgs p) {
+  using raw = typename T::raw;
+  constexpr int W = waves_of(CHAIN), S = slot_steps(false, CHAIN), kTile = S * W;
+  __shared__ typename std::conditional<CHAIN, ChainLds<V>, char>::type s_chain;
+  constexpr int kBufs = CHAIN ? 1 : 2;
+  __shared__ alignas(16) float s_a[kBufs][W][64][V], s_b[kBufs][W][64][V];
+  __shared__ uint32_t s_cut[kBufs][W];
+  Chained tile{0, (int32_t)blockIdx.x};
+  do {
+    if (CHAIN && !tile.take(p)) break;
+    const Place at = Place::of<V>(p, tile.column);
+    const int lane = at.lane, w = at.w;
+    const Lane<T, V, OFF32> x(p.x, p.x_step, p.x_row, at.n0, at.n, at.d);
+    const Lane<T, V, OFF32> gate(p.gate, p.g_step, p.g_row, at.n0, at.n, at.d);
+    const Lane<T, V, OFF32> out(p.out, p.h_step, p.h_row, at.n0, at.n, at.d);
+    const int32_t tb = CHAIN ? tile.order * kTile : 0, te = CHAIN ? min(p.L, tb + kTile) : p.L;
+
+    float c[V];  // the state that enters the tile
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v] = p.start ? p.start[at.cell + v] : 0.0f;
+
+    int buf = 0;
+    for (int32_t t0 = tb; t0 < te; t0 += kTile, buf = (buf + 1) % kBufs) {
+      const int32_t ts = t0 + w * S;
+      Pack<T, V> xr[S], gr[S];
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        const int32_t t = min(ts + i, te - 1);  // steps past the end: loaded, not used
+        xr[i] = x.load(t);
+        gr[i] = gate.load(t);
+      }
+      const uint32_t done = p.dones ? load_dones<S, false>(p, at.n, ts, tb, te) : 0u;
+      float a[S][V], b[S][V];
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        float xf[V], gf[V];
+        widen_pack<T, V>(xr[i], xf);
+        widen_pack<T, V>(gr[i], gf);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (SIG) {
+            float keep;
+            sigmoids(gf[v], a[i][v], keep);
+            b[i][v] = keep * xf[v];
+          } else {
+            a[i][v] = gf[v];
+            b[i][v] = xf[v];
+          }
+        }
+      }
+      if (ts + S > te) {
+        // steps past the end leave the state as it is
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+          if (ts + i >= te)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              a[i][v] = 1.0f;
+              b[i][v] = 0.0f;
+            }
+      }
+      const bool cut = __ballot(done != 0) != 0;  // (of the wave)
+      Map m[V];
+      if (cut)
+        fold_forward<V, S, true>(a, b, done, m);
+      else
+        fold_forward<V, S, false>(a, b, done, m);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        s_a[buf][w][lane][v] = m[v].a;
+        s_b[buf][w][lane][v] = m[v].b;
+      }
+      if (lane == 0) s_cut[buf][w] = cut;
+      __syncthreads();
+      if constexpr (CHAIN)
+        enter_tile<V, W>(p, tile.order, at.u, at.active, w, lane, s_a[buf], s_b[buf], s_chain, c);
+      uint32_t cuts = 0;
+#pragma unroll
+      for (int j = 0; j < W; ++j) cuts |= s_cut[buf][j];
+      float h[V];
+      if (__builtin_amdgcn_readfirstlane(cuts))
+        join_slots<V, W, true>(s_a[buf], s_b[buf], w, lane, c, h);
+      else
+        join_slots<V, W, false>(s_a[buf], s_b[buf], w, lane, c, h);
+      auto replay = [&](auto cuts_here) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          if (ts + i >= te) break;
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float nh = __builtin_fmaf(a[i][v], h[v], b[i][v]);
+            h[v] = cuts_here.value && ((done >> i) & 1u) ? b[i][v] : nh;
+          }
+          if (at.active) out.store(ts + i, narrow_pack<T, V>(h));
+        }
+      };
+      if (cut)
+        replay(std::true_type{});
+      else
+        replay(std::false_type{});
+      // h is the state of the slot's last step
+      if (p.last && at.active && ts < p.L && ts + S >= p.L && te == p.L) {
+        const bool end = p.dones && p.dones[(int64_t)(p.L - 1) * p.N + at.n];
+#pragma unroll
+        for (int v = 0; v < V; ++v) p.last[at.cell + v] = end ? 0.0f : h[v];
+      }
+    }
+  } while (CHAIN);
+}
+
+// A slot's map backwards, of steps a (dh + G).
+template <int V, int S, bool CUT>
+__device__ __forceinline__ void fold_backward(const float (&a)[S][V], const float (&dh)[S][V],
+                                              uint32_t done, Map (&m)[V]) {
 #pragma unroll
   for (int v = 0; v < V; ++v) m[v] = Map{1.0f, 0.0f};
-  const int first = w * per, last = min(count, first + per);
-#pragma unroll 4
-  for (int j = first; j < last; ++j) {
-    const int q = BACK ? hi - 1 - j : lo + j;
-    const Map* e = p.maps + ((int64_t)q * p.units + u) * V;
 #pragma unroll
-    for (int v = 0; v < V; ++v) m[v] = chain(m[v], e[v]);
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) s[w][lane][v] = m[v];
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kWaves; ++j)
-#pragma unroll
-    for (int v = 0; v < V; ++v) c[v] = apply(s[j][lane][v], c[v]);
-}
-
-// MAPS: only the chunks' maps are formed (the first launch of a cut scan).
-template <class T, int V, bool SIG, bool MAPS>
-__global__ __launch_bounds__(64 * kWaves) void recur_forward_kernel(const RecurArgs p) {
-  using raw = typename T::raw;
-  __shared__ Map s_map[2][kWaves][64][V];
-  const int lane = (int)threadIdx.x & 63;
-  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int q = (int)blockIdx.y;
-  const int32_t u0 = (int32_t)blockIdx.x * 64 + lane;
-  const bool active = u0 < p.units;
-  const int32_t u = active ? u0 : p.units - 1;  // idle lanes read a valid element
-  const int32_t n = u / p.per_row;
-  const int32_t d = (u - n * p.per_row) * V;
-  const raw* x = static_cast<const raw*>(p.x) + n * p.x_row + d;
-  const raw* gate = static_cast<const raw*>(p.gate) + n * p.g_row + d;
-  raw* out = static_cast<raw*>(p.out) + n * p.h_row + d;
-  const int64_t cell = (int64_t)n * p.D + d;
-  const int32_t tb = q * p.chunk, te = min(p.L, tb + p.chunk);
-
-  float c[V];  // state entering the tile (MAPS: the map's b so far, ca its slope)
-  float ca[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    c[v] = 0.0f;
-    ca[v] = 1.0f;
-  }
-  if (!MAPS) {
-    if (p.start)
-#pragma unroll
-      for (int v = 0; v < V; ++v) c[v] = p.start[cell + v];
-    if (q > 0) {
-      fold_chunks<V, false>(p, 0, q, u, w, lane, s_map[1], c);
-    }
-  }
-
-  int buf = 0;
-  for (int32_t t0 = tb; t0 < te; t0 += kTile, buf ^= 1) {
-    const int32_t ts = t0 + w * kSlot;
-    Pack<T, V> xr[kSlot], gr[kSlot];
-    uint32_t done = 0;
-#pragma unroll
-    for (int i = 0; i < kSlot; ++i) {
-      const int32_t t = min(ts + i, te - 1);  // steps past the end: loaded, not used
-      xr[i] = load_pack<T, V>(x + t * p.x_step);
-      gr[i] = load_pack<T, V>(gate + t * p.g_step);
-    }
-    if (p.dones) {
-      uint8_t db[kSlot];
-#pragma unroll
-      for (int i = 0; i < kSlot; ++i) {
-        const int32_t t = max(min(ts + i, te - 1), 1);
-        db[i] = p.dones[(int64_t)(t - 1) * p.N + n];
-      }
-#pragma unroll
-      for (int i = 0; i < kSlot; ++i) done |= (ts + i > 0 && db[i] ? 1u : 0u) << i;
-    }
-    float a[kSlot][V], b[kSlot][V];
-    Map m[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) m[v] = Map{1.0f, 0.0f};
-    uint32_t forgets = 0;
-#pragma unroll
-    for (int i = 0; i < kSlot; ++i) {
-      float xf[V], gf[V];
-      widen_pack<T, V>(xr[i], xf);
-      widen_pack<T, V>(gr[i], gf);
-      const bool in = ts + i < te;
-      const bool cut = (done >> i) & 1u;
-      forgets |= in && cut;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (SIG) {
-          float keep;
-          sigmoids(gf[v], a[i][v], keep);
-          b[i][v] = keep * xf[v];
-        } else {
-          a[i][v] = gf[v];
-          b[i][v] = xf[v];
-        }
-        const float nb = cut ? b[i][v] : __builtin_fmaf(a[i][v], m[v].b, b[i][v]);
-        m[v].b = in ? nb : m[v].b;
-        m[v].a = in ? m[v].a * a[i][v] : m[v].a;
-      }
-    }
+  for (int i = 0; i < S; ++i)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      m[v].a = stored_slope(m[v].a, forgets != 0);
-      s_map[buf][w][lane][v] = m[v];
-    }
-    __syncthreads();
-    if (MAPS) {
-#pragma unroll
-      for (int j = 0; j < kWaves; ++j)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const Map r = chain(Map{ca[v], c[v]}, s_map[buf][j][lane][v]);
-          ca[v] = r.a;
-          c[v] = r.b;
-        }
-      continue;
-    }
-    float h[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kWaves; ++j) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (j == w) h[v] = c[v];
-        c[v] = apply(s_map[buf][j][lane][v], c[v]);
-      }
+      const float nb = a[i][v] * (dh[i][v] + m[v].b);
+      m[v].b = CUT && ((done >> i) & 1u) ? 0.0f : nb;
+      m[v].a *= a[i][v];
     }
 #pragma unroll
-    for (int i = 0; i < kSlot; ++i) {
-      if (ts + i >= te) break;
-      const bool cut = (done >> i) & 1u;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        h[v] = cut ? b[i][v] : __builtin_fmaf(a[i][v], h[v], b[i][v]);
-      if (active) store_pack<T, V>(out + (ts + i) * p.h_step, narrow_pack<T, V>(h));
-      if (ts + i == p.L - 1 && p.last && active) {
-        const bool end = p.dones && p.dones[(int64_t)(p.L - 1) * p.N + n];
-#pragma unroll
-        for (int v = 0; v < V; ++v) p.last[cell + v] = end ? 0.0f : h[v];
-      }
-    }
-  }
-  if (MAPS && active && w == 0) {
-    Map* e = p.maps + ((int64_t)q * p.units + u) * V;
-#pragma unroll
-    for (int v = 0; v < V; ++v) e[v] = Map{ca[v], c[v]};
-  }
+  for (int v = 0; v < V; ++v) m[v].a = stored_slope(m[v].a, CUT && done != 0);
 }
 
-template <class T, int V, bool SIG, bool MAPS>
-__global__ __launch_bounds__(64 * kWaves) void recur_backward_kernel(const RecurArgs p) {
+template <class T, int V, bool SIG, bool CHAIN, bool OFF32>
+__global__ __launch_bounds__(64 * waves_of(CHAIN)) void recur_backward_kernel(const RecurArgs p) {
   using raw = typename T::raw;
-  __shared__ Map s_map[2][kWaves][64][V];
-  const int lane = (int)threadIdx.x & 63;
-  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int q = (int)blockIdx.y + (MAPS ? 1 : 0);  // the first chunk's map is not needed
-  const int32_t u0 = (int32_t)blockIdx.x * 64 + lane;
-  const bool active = u0 < p.units;
-  const int32_t u = active ? u0 : p.units - 1;
-  const int32_t n = u / p.per_row;
-  const int32_t d = (u - n * p.per_row) * V;
-  const raw* x = static_cast<const raw*>(p.x) + n * p.x_row + d;
-  const raw* gate = static_cast<const raw*>(p.gate) + n * p.g_row + d;
-  const raw* hs = static_cast<const raw*>(p.h) + n * p.h_row + d;
-  const raw* dh = static_cast<const raw*>(p.dh) + n * p.dh_row + d;
-  raw* dx = static_cast<raw*>(p.dx) + n * p.dx_row + d;
-  raw* dg = static_cast<raw*>(p.dg) + n * p.dg_row + d;
-  const int64_t cell = (int64_t)n * p.D + d;
-  const int32_t tb = q * p.chunk, te = min(p.L, tb + p.chunk);
+  constexpr int W = waves_of(CHAIN), S = slot_steps(true, CHAIN), kTile = S * W;
+  __shared__ typename std::conditional<CHAIN, ChainLds<V>, char>::type s_chain;
+  constexpr int kBufs = CHAIN ? 1 : 2;
+  __shared__ alignas(16) float s_a[kBufs][W][64][V], s_b[kBufs][W][64][V];
+  __shared__ uint32_t s_cut[kBufs][W];
+  Chained tile{0, (int32_t)blockIdx.x};
+  do {
+    if (CHAIN && !tile.take(p)) break;
+    const Place at = Place::of<V>(p, tile.column);
+    const int lane = at.lane, w = at.w;
+    const Lane<T, V, OFF32> x(p.x, p.x_step, p.x_row, at.n0, at.n, at.d);
+    const Lane<T, V, OFF32> gate(p.gate, p.g_step, p.g_row, at.n0, at.n, at.d);
+    const Lane<T, V, OFF32> hs(p.h, p.h_step, p.h_row, at.n0, at.n, at.d);
+    const Lane<T, V, OFF32> dh(p.dh, p.dh_step, p.dh_row, at.n0, at.n, at.d);
+    const Lane<T, V, OFF32> dx(p.dx, p.dx_step, p.dx_row, at.n0, at.n, at.d);
+    const Lane<T, V, OFF32> dg(p.dg, p.dg_step, p.dg_row, at.n0, at.n, at.d);
+    // chained tiles are counted from the end, the last of them in time whole
+    const int32_t te = CHAIN ? p.L - tile.order * kTile : p.L, tb = CHAIN ? max(0, te - kTile) : 0;
 
-  float c[V], ca[V];
+    float c[V];  // G of the step after the tile
+    const bool end = p.dones && p.dones[(int64_t)(p.L - 1) * p.N + at.n];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    c[v] = 0.0f;
-    ca[v] = 1.0f;
-  }
-  if (!MAPS) {
-    if (p.start && !(p.dones && p.dones[(int64_t)(p.L - 1) * p.N + n]))
-#pragma unroll
-      for (int v = 0; v < V; ++v) c[v] = p.start[cell + v];
-    if (q < p.chunks - 1) {
-      fold_chunks<V, true>(p, q + 1, p.chunks, u, w, lane, s_map[1], c);
-    }
-  }
+    for (int v = 0; v < V; ++v) c[v] = p.start && !end ? p.start[at.cell + v] : 0.0f;
 
-  int buf = 0;
-  for (int32_t t1 = te; t1 > tb; t1 -= kTile, buf ^= 1) {
-    const int32_t top = t1 - 1 - w * kSlot;  // this wave's latest step
-    Pack<T, V> gr[kSlot], dr[kSlot], xr[MAPS ? 1 : kSlot], hr[MAPS ? 1 : kSlot];
-    uint32_t done = 0;
+    int buf = 0;
+    for (int32_t t1 = te; t1 > tb; t1 -= kTile, buf = (buf + 1) % kBufs) {
+      const int32_t top = t1 - 1 - w * S;  // this wave's latest step
+      Pack<T, V> gr[S], dr[S], xr[SIG ? S : 1], hr[S];
 #pragma unroll
-    for (int i = 0; i < kSlot; ++i) {
-      const int32_t t = max(top - i, tb);
-      gr[i] = load_pack<T, V>(gate + t * p.g_step);
-      dr[i] = load_pack<T, V>(dh + t * p.dh_step);
-      if (!MAPS) {
-        if (SIG) xr[i] = load_pack<T, V>(x + t * p.x_step);
-        hr[i] = load_pack<T, V>(hs + max(t - 1, 0) * p.h_step);
+      for (int i = 0; i < S; ++i) {
+        const int32_t t = max(top - i, tb);
+        gr[i] = gate.load(t);
+        dr[i] = dh.load(t);
       }
-    }
-    if (p.dones) {
-      uint8_t db[kSlot];
+      const uint32_t done = p.dones ? load_dones<S, true>(p, at.n, top, tb, te) : 0u;
 #pragma unroll
-      for (int i = 0; i < kSlot; ++i)
-        db[i] = p.dones[(int64_t)(max(max(top - i, tb), 1) - 1) * p.N + n];
-#pragma unroll
-      for (int i = 0; i < kSlot; ++i) done |= (top - i > 0 && db[i] ? 1u : 0u) << i;
-    }
-    float a[kSlot][V], k[kSlot][V];
-    Map m[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) m[v] = Map{1.0f, 0.0f};
-    uint32_t forgets = 0;
-#pragma unroll
-    for (int i = 0; i < kSlot; ++i) {
-      float gf[V], df[V];
-      widen_pack<T, V>(gr[i], gf);
-      widen_pack<T, V>(dr[i], df);
-      const bool in = top - i >= tb;
-      const bool cut = (done >> i) & 1u;
-      forgets |= in && cut;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (SIG)
-          sigmoids(gf[v], a[i][v], k[i][v]);
-        else
-          a[i][v] = gf[v];
-        const float nb = cut ? 0.0f : a[i][v] * (df[v] + m[v].b);
-        m[v].b = in ? nb : m[v].b;
-        m[v].a = in ? m[v].a * a[i][v] : m[v].a;
+      for (int i = 0; i < S; ++i) {
+        const int32_t t = max(top - i, tb);
+        if (SIG) xr[SIG ? i : 0] = x.load(t);
+        hr[i] = hs.load(max(t - 1, 0));
       }
-    }
+      float a[S][V], k[SIG ? S : 1][V], df[S][V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      m[v].a = stored_slope(m[v].a, forgets != 0);
-      s_map[buf][w][lane][v] = m[v];
-    }
-    __syncthreads();
-    if (MAPS) {
-#pragma unroll
-      for (int j = 0; j < kWaves; ++j)
+      for (int i = 0; i < S; ++i) {
+        float gf[V];
+        widen_pack<T, V>(gr[i], gf);
+        widen_pack<T, V>(dr[i], df[i]);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const Map r = chain(Map{ca[v], c[v]}, s_map[buf][j][lane][v]);
-          ca[v] = r.a;
-          c[v] = r.b;
+          if (SIG)
+            sigmoids(gf[v], a[i][v], k[SIG ? i : 0][v]);
+          else
+            a[i][v] = gf[v];
         }
-      continue;
-    }
-    float G[V];
+      }
+      if (top - S + 1 < tb) {
+        // steps before the tile leave the carry as it is
 #pragma unroll
-    for (int v = 0; v < V; ++v) G[v] = 0.0f;
+        for (int i = 0; i < S; ++i)
+          if (top - i < tb)
 #pragma unroll
-    for (int j = 0; j < kWaves; ++j) {
+            for (int v = 0; v < V; ++v) {
+              a[i][v] = 1.0f;
+              df[i][v] = 0.0f;
+            }
+      }
+      const bool cut = __ballot(done != 0) != 0;
+      Map m[V];
+      if (cut)
+        fold_backward<V, S, true>(a, df, done, m);
+      else
+        fold_backward<V, S, false>(a, df, done, m);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (j == w) G[v] = c[v];
-        c[v] = apply(s_map[buf][j][lane][v], c[v]);
+        s_a[buf][w][lane][v] = m[v].a;
+        s_b[buf][w][lane][v] = m[v].b;
+      }
+      if (lane == 0) s_cut[buf][w] = cut;
+      __syncthreads();
+      if constexpr (CHAIN)
+        enter_tile<V, W>(p, tile.order, at.u, at.active, w, lane, s_a[buf], s_b[buf], s_chain, c);
+      uint32_t cuts = 0;
+#pragma unroll
+      for (int j = 0; j < W; ++j) cuts |= s_cut[buf][j];
+      float G[V];
+      if (__builtin_amdgcn_readfirstlane(cuts))
+        join_slots<V, W, true>(s_a[buf], s_b[buf], w, lane, c, G);
+      else
+        join_slots<V, W, false>(s_a[buf], s_b[buf], w, lane, c, G);
+      auto replay = [&](auto cuts_here) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          const int32_t t = top - i;
+          if (t < tb) break;
+          const bool drop = cuts_here.value && ((done >> i) & 1u);
+          float hf[V], xf[V], ox[V], og[V];
+          widen_pack<T, V>(hr[i], hf);
+          if (SIG) widen_pack<T, V>(xr[SIG ? i : 0], xf);
+          if (t == 0) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) hf[v] = p.h0 ? p.h0[at.cell + v] : 0.0f;
+          }
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float del = df[i][v] + G[v];
+            const float prev = drop ? 0.0f : hf[v];
+            if (SIG) {
+              ox[v] = k[SIG ? i : 0][v] * del;
+              og[v] = a[i][v] * ox[v] * (prev - xf[v]);
+            } else {
+              ox[v] = del;
+              og[v] = drop ? 0.0f : del * prev;
+            }
+            G[v] = drop ? 0.0f : a[i][v] * del;
+          }
+          if (at.active) {
+            dx.store(t, narrow_pack<T, V>(ox));
+            dg.store(t, narrow_pack<T, V>(og));
+          }
+        }
+      };
+      if (cut)
+        replay(std::true_type{});
+      else
+        replay(std::false_type{});
+      // G is that of the slot's earliest step
+      if (p.last && at.active && top >= 0 && top - S < 0 && tb == 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) p.last[at.cell + v] = G[v];
       }
     }
-#pragma unroll
-    for (int i = 0; i < kSlot; ++i) {
-      const int32_t t = top - i;
-      if (t < tb) break;
-      const bool cut = (done >> i) & 1u;
-      float df[V], hf[V], xf[V], ox[V], og[V];
-      widen_pack<T, V>(dr[i], df);
-      widen_pack<T, V>(hr[MAPS ? 0 : i], hf);
-      if (SIG) widen_pack<T, V>(xr[MAPS ? 0 : i], xf);
-      if (t == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) hf[v] = p.h0 ? p.h0[cell + v] : 0.0f;
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float del = df[v] + G[v];
-        const float prev = cut ? 0.0f : hf[v];
-        if (SIG) {
-          ox[v] = k[i][v] * del;
-          og[v] = a[i][v] * ox[v] * (prev - xf[v]);
-        } else {
-          ox[v] = del;
-          og[v] = cut ? 0.0f : del * prev;
-        }
-        G[v] = cut ? 0.0f : a[i][v] * del;
-      }
-      if (active) {
-        store_pack<T, V>(dx + t * p.dx_step, narrow_pack<T, V>(ox));
-        store_pack<T, V>(dg + t * p.dg_step, narrow_pack<T, V>(og));
-        if (t == 0 && p.last) {
-#pragma unroll
-          for (int v = 0; v < V; ++v) p.last[cell + v] = G[v];
-        }
-      }
-    }
-  }
-  if (MAPS && active && w == 0) {
-    Map* e = p.maps + ((int64_t)q * p.units + u) * V;
-#pragma unroll
-    for (int v = 0; v < V; ++v) e[v] = Map{ca[v], c[v]};
-  }
+  } while (CHAIN);
 }
 
 template <class T, int V>
@@ -446,83 +662,112 @@ hipError_t copy_state(const float* from, float* to, int64_t n, hipStream_t strea
   return hipGetLastError();
 }
 
-// Workgroups a launch should have before time is cut into chunks.
-constexpr int64_t kWantGroups = 512;
-
-// Chunks of time: one where the columns alone give the chip enough
-// workgroups, else enough for kWantGroups, each of at least four tiles.
-void cut(int32_t L, int64_t units, int32_t* chunk, int32_t* chunks) {
-  const int64_t columns = units > 0 ? (units + 63) / 64 : 1;
-  int64_t k = (kWantGroups + columns - 1) / columns;
-  const int64_t most = L / (4 * kTile);
-  if (k > most) k = most;
-  if (columns >= kWantGroups / 2 || k <= 1) {
-    *chunk = L;
-    *chunks = 1;
-    return;
-  }
-  int64_t steps = (L + k - 1) / k;
-  steps = (steps + kTile - 1) / kTile * kTile;
-  *chunk = (int32_t)steps;
-  *chunks = (int32_t)((L + steps - 1) / steps);
+// Before a chained scan: the ticket at 0, every word empty.
+__global__ __launch_bounds__(256) void empty_chain_kernel(uint32_t* ticket, uint64_t* words, int64_t n) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    words[i] = kNothing;
 }
 
-bool strides_even(int64_t a, int64_t b) { return ((a | b) & 1) == 0; }
+// Columns that give the chip enough workgroups, each walking all of time.
+constexpr int64_t kWantColumns = 512;
 
-template <class T, int V, bool SIG, bool BACK>
-hipError_t launch(RecurArgs p, hipStream_t stream) {
-  p.per_row = p.D / V;
+int64_t per_row_of(int32_t D, int v) { return (D + v - 1) / v; }
+
+// Channels of a lane: as many as leave the launch enough columns.
+int lane_channels(int32_t N, int32_t D, int32_t dtype) {
+  for (int v = dtype == POLICY_F32 ? 2 : 4; v > 1; v /= 2)
+    if (D >= v && (N * per_row_of(D, v) + 63) / 64 >= kWantColumns) return v;
+  return D >= 2 && dtype != POLICY_F32 ? 2 : 1;
+}
+
+// Tiles of a chained scan, or 0 where the columns are enough, or time too short.
+int32_t chained_tiles(int32_t L, int64_t units, bool back) {
+  const int32_t tile = waves_of(true) * slot_steps(back, true);
+  const int64_t columns = (units + 63) / 64;
+  return columns >= kWantColumns / 2 || L <= 2 * tile ? 0 : (L + tile - 1) / tile;
+}
+// Workspace: a ticket, then the words.
+constexpr size_t kTicketBytes = 256;
+int64_t chained_bytes(int32_t tiles, int64_t units, int v) {
+  return tiles ? (int64_t)kTicketBytes + tiles * units * v * 8 : 0;
+}
+
+template <class T, int V, bool SIG, bool BACK, bool OFF32>
+hipError_t launch(RecurArgs p, void* workspace, hipStream_t stream) {
+  p.per_row = (int32_t)per_row_of(p.D, V);
   p.units = p.N * p.per_row;
-  cut(p.L, p.units, &p.chunk, &p.chunks);
-  const unsigned columns = (unsigned)((p.units + 63) / 64);
-  if (p.chunks > 1) {
-    const dim3 grid(columns, (unsigned)(p.chunks - 1));
-    if (BACK)
-      hipLaunchKernelGGL((recur_backward_kernel<T, V, SIG, true>), grid, dim3(64 * kWaves), 0,
-                         stream, p);
-    else
-      hipLaunchKernelGGL((recur_forward_kernel<T, V, SIG, true>), grid, dim3(64 * kWaves), 0,
-                         stream, p);
+  p.columns = (p.units + 63) / 64;
+  const int32_t tiles = chained_tiles(p.L, p.units, BACK);
+  if constexpr (V <= 2) if (tiles) {  // (wider lanes only where columns are plenty)
+    p.ticket = static_cast<uint32_t*>(workspace);
+    p.words = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + kTicketBytes);
+    const int64_t words = tiles * (int64_t)p.units * V, blocks = (words + 255) / 256;
+    hipLaunchKernelGGL(empty_chain_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0,
+                       stream, p.ticket, p.words, words);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    p.tiles = (uint32_t)tiles * (uint32_t)p.columns;
+    const dim3 grid(p.tiles < (1u << 21) ? p.tiles : 1u << 21), threads(64 * waves_of(true));
+    if constexpr (BACK)
+      hipLaunchKernelGGL((recur_backward_kernel<T, V, SIG, true, OFF32>), grid, threads, 0, stream, p);
+    else
+      hipLaunchKernelGGL((recur_forward_kernel<T, V, SIG, true, OFF32>), grid, threads, 0, stream, p);
+    return hipGetLastError();
   }
-  const dim3 grid(columns, (unsigned)p.chunks);
-  if (BACK)
-    hipLaunchKernelGGL((recur_backward_kernel<T, V, SIG, false>), grid, dim3(64 * kWaves), 0,
-                       stream, p);
+  const dim3 grid((unsigned)p.columns), threads(64 * waves_of(false));
+  if constexpr (BACK)
+    hipLaunchKernelGGL((recur_backward_kernel<T, V, SIG, false, OFF32>), grid, threads, 0, stream, p);
   else
-    hipLaunchKernelGGL((recur_forward_kernel<T, V, SIG, false>), grid, dim3(64 * kWaves), 0,
-                       stream, p);
+    hipLaunchKernelGGL((recur_forward_kernel<T, V, SIG, false, OFF32>), grid, threads, 0, stream, p);
   return hipGetLastError();
 }
 
-template <class T, bool BACK>
-hipError_t pick(const RecurArgs& p, bool sig, bool pairs, hipStream_t stream) {
-  if (pairs)
-    return sig ? launch<T, 2, true, BACK>(p, stream) : launch<T, 2, false, BACK>(p, stream);
-  return sig ? launch<T, 1, true, BACK>(p, stream) : launch<T, 1, false, BACK>(p, stream);
+template <class T, bool SIG, bool BACK>
+hipError_t pick(const RecurArgs& p, int32_t dtype, void* ws, hipStream_t stream) {
+  const int v = lane_channels(p.N, p.D, dtype);
+  // a column's rows, seen from its first, within 32-bit offsets
+  int64_t row = p.x_row;
+  for (int64_t r : {p.g_row, p.h_row, p.dh_row, p.dx_row, p.dg_row}) row = r > row ? r : row;
+  const int64_t rows = 64 / per_row_of(p.D, v) + 1;
+  if (row > (((int64_t)1 << 31) / T::kBytes - p.D) / rows) {
+    if (v == 1) return launch<T, 1, SIG, BACK, false>(p, ws, stream);
+    return launch<T, 2, SIG, BACK, false>(p, ws, stream);
+  }
+  switch (v) {
+    case 4: if constexpr (T::kBytes == 2) return launch<T, 4, SIG, BACK, true>(p, ws, stream);
+    case 2: return launch<T, 2, SIG, BACK, true>(p, ws, stream);
+    default: return launch<T, 1, SIG, BACK, true>(p, ws, stream);
+  }
 }
 
 template <bool BACK>
-hipError_t pick_type(const RecurArgs& p, int32_t dtype, bool sig, bool pairs, hipStream_t stream) {
+hipError_t pick_type(const RecurArgs& p, int32_t dtype, bool sig, void* ws, hipStream_t stream) {
   switch (dtype) {
-    case POLICY_F32: return pick<F32, BACK>(p, sig, pairs, stream);
-    case POLICY_BF16: return pick<BF16, BACK>(p, sig, pairs, stream);
-    default: return pick<F16, BACK>(p, sig, pairs, stream);
+    case POLICY_F32:
+      return sig ? pick<F32, true, BACK>(p, dtype, ws, stream)
+                 : pick<F32, false, BACK>(p, dtype, ws, stream);
+    case POLICY_BF16:
+      return sig ? pick<BF16, true, BACK>(p, dtype, ws, stream)
+                 : pick<BF16, false, BACK>(p, dtype, ws, stream);
+    default:
+      return sig ? pick<F16, true, BACK>(p, dtype, ws, stream)
+                 : pick<F16, false, BACK>(p, dtype, ws, stream);
   }
 }
 
 }  // namespace
 
 int64_t recur_workspace_bytes(int32_t L, int32_t N, int32_t D, int32_t dtype) {
-  (void)dtype;
   int64_t most = 0;
-  for (int v = 1; v <= 2; ++v) {
-    if (D % v) continue;
-    int32_t chunk, chunks;
-    cut(L, (int64_t)N * (D / v), &chunk, &chunks);
-    const int64_t bytes = chunks > 1 ? (int64_t)chunks * N * D * (int64_t)sizeof(Map) : 0;
-    if (bytes > most) most = bytes;
+  if ((int64_t)N * D == 0) return 0;
+  for (int v = 1; v <= 4; v *= 2) {  // whichever the strides allow, in both directions
+    if (D < v) continue;
+    const int64_t units = N * per_row_of(D, v);
+    for (const bool back : {false, true}) {
+      const int64_t bytes = chained_bytes(chained_tiles(L, units, back), units, v);
+      if (bytes > most) most = bytes;
+    }
   }
   return most;
 }
@@ -547,12 +792,7 @@ hipError_t recur_forward_launch(const recur_args& a, hipStream_t stream) {
   p.dones = a.dones;
   p.out = a.h;
   p.last = a.h_last;
-  p.maps = static_cast<Map*>(a.workspace);
-  const size_t two = a.dtype == POLICY_F32 ? 8 : 4;
-  const bool pairs = a.width % 2 == 0 && strides_even(a.x_step, a.x_row) &&
-                     strides_even(a.gate_step, a.gate_row) && strides_even(a.h_step, a.h_row) &&
-                     aligned_to(a.x, two) && aligned_to(a.gate, two) && aligned_to(a.h, two);
-  return pick_type<false>(p, a.dtype, a.form == RECUR_SIGMOID, pairs, stream);
+  return pick_type<false>(p, a.dtype, a.form == RECUR_SIGMOID, a.workspace, stream);
 }
 
 hipError_t recur_backward_launch(const recur_grad_args& a, hipStream_t stream) {
@@ -585,16 +825,7 @@ hipError_t recur_backward_launch(const recur_grad_args& a, hipStream_t stream) {
   p.dx = a.dx;
   p.dg = a.dgate;
   p.last = a.dh0;
-  p.maps = static_cast<Map*>(a.workspace);
-  const bool sig = a.form == RECUR_SIGMOID;
-  const size_t two = a.dtype == POLICY_F32 ? 8 : 4;
-  const bool pairs =
-      a.width % 2 == 0 && (!sig || (strides_even(a.x_step, a.x_row) && aligned_to(a.x, two))) &&
-      strides_even(a.gate_step, a.gate_row) && strides_even(a.h_step, a.h_row) &&
-      strides_even(a.dh_step, a.dh_row) && strides_even(a.dx_step, a.dx_row) &&
-      strides_even(a.dgate_step, a.dgate_row) && aligned_to(a.gate, two) && aligned_to(a.h, two) &&
-      aligned_to(a.dh, two) && aligned_to(a.dx, two) && aligned_to(a.dgate, two);
-  return pick_type<true>(p, a.dtype, sig, pairs, stream);
+  return pick_type<true>(p, a.dtype, a.form == RECUR_SIGMOID, a.workspace, stream);
 }
 
 hipError_t recur_step_launch(int32_t N, int32_t D, int32_t dtype, int32_t form, const void* x,
