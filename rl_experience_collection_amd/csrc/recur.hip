@@ -66,19 +66,22 @@ __device__ __forceinline__ Map chain(Map first, Map second) {
 }
 
 // sigmoid(g) and sigmoid(-g), each to within a few fp32 roundings: with
-// E = exp(-|g|) they are 1 / (1 + E) and E / (1 + E), so neither is formed
-// by a difference.  E is 2^(hi + lo), hi + lo the product |g| log2(e) in two
-// parts.
+// E = exp(-g) they are 1 / (1 + E) and E / (1 + E), so neither is formed by a
+// difference.  E is 2^hi (1 + lo ln 2) with hi the rounded product -g log2(e)
+// and lo what the rounding took off; the product's constant itself is off by
+// 1.3e-8 |g| relative to E.  A large g leaves E = 0.  A g below -126 ln 2 is
+// held there, where the reciprocal is 2^-126, the smallest it forms; taking
+// that off makes sigmoid(g) 0 beyond and changes no larger one by more.
 __device__ __forceinline__ void sigmoids(float g, float& a, float& keep) {
-  const float m = __builtin_elementwise_minimum(__builtin_fabsf(g), 200.0f);  // (a NaN stays)
+  // (a NaN passes both)
+  const float m = __builtin_elementwise_maximum(__builtin_elementwise_minimum(g, 200.0f), -87.3365402f);
   const float hi = m * -1.44269502f;
-  const float lo = __builtin_fmaf(m, -1.92596300e-8f, __builtin_fmaf(m, -1.44269502f, -hi));
+  const float lo = __builtin_fmaf(m, -1.44269502f, -hi);
   float E = __builtin_amdgcn_exp2f(hi);
   E = __builtin_fmaf(E * lo, 0.693147182f, E);
-  const float r = __builtin_amdgcn_rcpf(1.0f + E);
-  const float s = E * r;
-  a = g >= 0.0f ? r : s;
-  keep = g >= 0.0f ? s : r;
+  a = __builtin_amdgcn_rcpf(1.0f + E);
+  keep = E * a;
+  a -= 0x1p-126f;
 }
 
 struct RecurArgs {
@@ -268,22 +271,31 @@ __device__ __forceinline__ void enter_tile(const RecurArgs& p, int32_t o, int32_
 }
 
 // Joins the tile's slots: `c` is the state that enters the tile, and then the
-// one that leaves it; `h` becomes the state that enters this wave's slot.
-// Without a done in the tile the maps are plain.
-template <int V, int W, bool FORGETS>
-__device__ __forceinline__ void join_slots(const float (&sa)[W][64][V],
-                                           const float (&sb)[W][64][V], int w, int lane,
-                                           float (&c)[V], float (&h)[V]) {
-#pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = c[v];
+// one that leaves it; `h` becomes the state that enters this wave's slot.  Bit
+// j of `cuts`: slot j holds a done in some lane.  The choices are the same for
+// the whole wave and stay branches (the empty statements keep them so): as
+// selects they would cost as much as the sums.
+template <int V, int W>
+__device__ __forceinline__ void join_slots(const float (&sa)[W][64][V], const float (&sb)[W][64][V],
+                                           uint32_t cuts, int w, int lane, float (&c)[V],
+                                           float (&h)[V]) {
 #pragma unroll
   for (int j = 0; j < W; ++j) {
-    const bool mine = j == w;
+    Map m[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const Map m{sa[j][lane][v], sb[j][lane][v]};
-      if (mine) h[v] = c[v];
-      c[v] = FORGETS ? apply(m, c[v]) : __builtin_fmaf(m.a, c[v], m.b);
+    for (int v = 0; v < V; ++v) m[v] = Map{sa[j][lane][v], sb[j][lane][v]};
+    if (j == w) {
+      asm volatile("");
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = c[v];
+    }
+    if ((cuts >> j) & 1u) {
+      asm volatile("");
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v] = apply(m[v], c[v]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v] = __builtin_fmaf(m[v].a, c[v], m[v].b);
     }
   }
 }
@@ -428,14 +440,9 @@ __global__ __launch_bounds__(64 * waves_of(CHAIN)) void recur_forward_kernel(con
       __syncthreads();
       if constexpr (CHAIN)
         enter_tile<V, W>(p, tile.order, at.u, at.active, w, lane, s_a[buf], s_b[buf], s_chain, c);
-      uint32_t cuts = 0;
-#pragma unroll
-      for (int j = 0; j < W; ++j) cuts |= s_cut[buf][j];
+      const uint32_t cuts = (uint32_t)__ballot(s_cut[buf][lane % W] != 0);
       float h[V];
-      if (__builtin_amdgcn_readfirstlane(cuts))
-        join_slots<V, W, true>(s_a[buf], s_b[buf], w, lane, c, h);
-      else
-        join_slots<V, W, false>(s_a[buf], s_b[buf], w, lane, c, h);
+      join_slots<V, W>(s_a[buf], s_b[buf], cuts, w, lane, c, h);
       auto replay = [&](auto cuts_here) {
 #pragma unroll
         for (int i = 0; i < S; ++i) {
@@ -564,14 +571,9 @@ __global__ __launch_bounds__(64 * waves_of(CHAIN)) void recur_backward_kernel(co
       __syncthreads();
       if constexpr (CHAIN)
         enter_tile<V, W>(p, tile.order, at.u, at.active, w, lane, s_a[buf], s_b[buf], s_chain, c);
-      uint32_t cuts = 0;
-#pragma unroll
-      for (int j = 0; j < W; ++j) cuts |= s_cut[buf][j];
+      const uint32_t cuts = (uint32_t)__ballot(s_cut[buf][lane % W] != 0);
       float G[V];
-      if (__builtin_amdgcn_readfirstlane(cuts))
-        join_slots<V, W, true>(s_a[buf], s_b[buf], w, lane, c, G);
-      else
-        join_slots<V, W, false>(s_a[buf], s_b[buf], w, lane, c, G);
+      join_slots<V, W>(s_a[buf], s_b[buf], cuts, w, lane, c, G);
       auto replay = [&](auto cuts_here) {
 #pragma unroll
         for (int i = 0; i < S; ++i) {
