@@ -634,5 +634,7 @@ def __getattr__(name):
     # torch is imported only with the first function that needs it
     if name in _POLICY:
         from . import policy
-        return getattr(policy, name)
+        for n in _POLICY:
+            globals()[n] = getattr(policy, n)
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
