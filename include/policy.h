@@ -51,7 +51,7 @@ typedef enum { POLICY_F32 = 0, POLICY_BF16 = 1, POLICY_F16 = 2 } policy_dtype;
 typedef enum { RECUR_LINEAR = 0, RECUR_SIGMOID = 1 } recur_form;
 
 typedef struct {
-  int32_t steps, rows, width; /* L, N, D >= 0; N * D < 2^29 */
+  int32_t steps, rows, width; /* L, N, D >= 0; L <= 2^30, N * D < 2^28 */
   int32_t dtype;              /* policy_dtype */
   int32_t form;               /* recur_form */
   int64_t x_step, x_row;      /* strides in elements */

@@ -423,21 +423,26 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(SumArgs a) {
 
 // ------------------------------------------------------------- few indices
 constexpr int kFewMost = 512;  // indices
-constexpr int kFewRows = 32;   // rows of the vocabulary per workgroup
+
+// Rows of the vocabulary per workgroup: one, as long as the grid stays small.
+int32_t few_rows(int64_t vocab) {
+  const int64_t rows = vocab >> 13;
+  return (int32_t)(rows < 1 ? 1 : rows < 32 ? rows : 32);
+}
 
 // The named places among this workgroup's rows are listed in LDS in order;
 // each thread takes packs of the rows and adds the places of its row.
 template <class T, int V>
 __global__ __launch_bounds__(kThreads) void embed_few_kernel(EmbedBackward a, int32_t per_row,
-                                                             bool past) {
+                                                             int32_t block_rows, bool past) {
   using raw = typename T::raw;
   __shared__ uint32_t s_list[kFewMost];  // row << 16 | position
   __shared__ uint32_t s_wave[kThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int64_t blocks = (a.vocab + kFewRows - 1) / kFewRows;
+  const int64_t blocks = (a.vocab + block_rows - 1) / block_rows;
   for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {
-    const int64_t v0 = block * kFewRows;
-    const int32_t rows = (int32_t)min((int64_t)kFewRows, a.vocab - v0);
+    const int64_t v0 = block * block_rows;
+    const int32_t rows = (int32_t)min((int64_t)block_rows, a.vocab - v0);
     int32_t n = 0;
     for (int32_t i0 = 0; i0 < (int32_t)a.count; i0 += kThreads) {
       const int32_t i = i0 + tid;
@@ -462,13 +467,23 @@ __global__ __launch_bounds__(kThreads) void embed_few_kernel(EmbedBackward a, in
       float acc[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-      for (int32_t j = 0; j < n; ++j) {
-        const uint32_t e = s_list[j];
-        if ((int32_t)(e >> 16) != r) continue;
-        float f[V];
-        widen_pack<T, V>(load_pack<T, V>(dout + (int64_t)(e & 0xffffu) * a.dout_row), f);
+      for (int32_t j0 = 0; j0 < n; j0 += kAhead) {
+        // (other rows' places are loaded too and not added: they are near)
+        uint32_t e[kAhead];
+        Pack<T, V> d[kAhead];
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += f[i];
+        for (int j = 0; j < kAhead; ++j) {
+          e[j] = s_list[min(j0 + j, n - 1)];
+          d[j] = load_pack<T, V>(dout + (int64_t)(e[j] & 0xffffu) * a.dout_row);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const bool add = j0 + j < n && (int32_t)(e[j] >> 16) == r;
+          float f[V];
+          widen_pack<T, V>(d[j], f);
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] += add ? f[i] : 0.0f;
+        }
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] *= a.scale;
@@ -552,8 +567,9 @@ hipError_t backward(const EmbedBackward& a, hipStream_t stream) {
   const int32_t per_row = (a.width + V - 1) / V;
   const bool past = a.vocab * a.width * T::kBytes > kPastBytes;
   if (a.count <= kFewMost) {
-    hipLaunchKernelGGL((embed_few_kernel<T, V>), dim3(capped((a.vocab + kFewRows - 1) / kFewRows)),
-                       dim3(kThreads), 0, stream, a, per_row, past);
+    const int32_t rows = few_rows(a.vocab);
+    hipLaunchKernelGGL((embed_few_kernel<T, V>), dim3(capped((a.vocab + rows - 1) / rows)),
+                       dim3(kThreads), 0, stream, a, per_row, rows, past);
     return hipGetLastError();
   }
   const SortPlan plan = sort_plan(a.vocab, a.count);

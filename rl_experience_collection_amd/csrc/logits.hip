@@ -134,11 +134,47 @@ __device__ __forceinline__ float replaced(const uint32_t* val, const uint32_t* c
   return penalise(f, t, (count[c >> 1] >> ((c & 1) << 4)) & 0xffffu);
 }
 
+// The mask of the V columns from c0 + e, as loaded: a byte of bits, or V bytes
+// (moved back like load_inside).
+template <int V, int MASK>
+__device__ __forceinline__ uint64_t load_mask(const logits_args& a, int64_t at, int32_t c0, int32_t e,
+                                              int32_t n) {
+  const uint8_t* m = static_cast<const uint8_t*>(a.mask);
+  if constexpr (MASK == LOGITS_MASK_BITS) {
+    return m[at * 4 + ((c0 + min(e, n - 1)) >> 3)];
+  } else if constexpr (V == 8) {
+    typedef uint64_t eight __attribute__((aligned(1)));
+    return *reinterpret_cast<const eight*>(m + at + c0 + min(e, n - V));
+  } else if constexpr (V == 4) {
+    typedef uint32_t four __attribute__((aligned(1)));
+    return *reinterpret_cast<const four*>(m + at + c0 + min(e, n - V));
+  } else {
+    return m[at + c0 + min(e, n - V)];
+  }
+}
+// Bit i: column c0 + e + i is allowed.
+template <int V, int MASK>
+__device__ __forceinline__ uint32_t mask_bits(uint64_t raw, int32_t c0, int32_t e, int32_t n) {
+  if constexpr (MASK == LOGITS_MASK_BITS) {
+    return (uint32_t)raw >> ((c0 + e) & 7);
+  } else {
+    const int32_t back = e - (n - V);
+    if (back > 0) raw >>= 8 * back;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) bits |= ((raw >> (8 * i)) & 0xffu ? 1u : 0u) << i;
+    return bits;
+  }
+}
+
 // ------------------------------------------------------- tiles of whole rows
 constexpr int kAhead = 4;  // history entries a thread loads before it uses the first
 
+// FLAT_MASK: a byte of mask per logit, one after another like them, is read
+// like them; other masks become bits in LDS.
+//
 // What a workgroup needs of a tile, loaded while the one before is worked on.
-template <class T, int V, bool GRAD>
+template <class T, int V, bool GRAD, bool FLAT_MASK>
 struct RowsTile {
   static constexpr int kPacks = kTile / (kThreads * V);
   Pack<T, V> x[kPacks], z[GRAD ? kPacks : 1];
@@ -147,6 +183,7 @@ struct RowsTile {
   float rho, alpha, beta;
   uint32_t word;  // a mask of bits: this thread's word of the tile's masks,
   bool named;     // if it has one
+  uint64_t mask[FLAT_MASK ? kPacks : 1];  // the packs' bytes of the mask
 };
 
 // A mask of bits gives every thread at most one word of a tile's masks (128
@@ -176,9 +213,9 @@ __device__ __forceinline__ int32_t tile_reach(const logits_args& a, int64_t r0) 
 }
 
 // Every load before the first wait: no load behind a branch of its lanes.
-template <class T, int V, bool GRAD>
+template <class T, int V, bool GRAD, bool FLAT_MASK>
 __device__ __forceinline__ void load_tile(const LogitsArgs& p, int64_t r0, MaskWord m, int32_t mrow,
-                                          RowsTile<T, V, GRAD>& q) {
+                                          RowsTile<T, V, GRAD, FLAT_MASK>& q) {
   using raw = typename T::raw;
   const logits_args& a = p.a;
   const int tid = threadIdx.x;
@@ -199,6 +236,11 @@ __device__ __forceinline__ void load_tile(const LogitsArgs& p, int64_t r0, MaskW
     q.named = m.r < rows && mrow >= 0 && mrow < a.mask_count;
     q.word = static_cast<const uint32_t*>(a.mask)[q.named ? (int64_t)mrow * a.mask_row + m.j : 0];
   }
+  if (FLAT_MASK) {
+#pragma unroll
+    for (int k = 0; k < q.kPacks; ++k)
+      q.mask[FLAT_MASK ? k : 0] = load_mask<V, LOGITS_MASK_BYTES>(a, r0 * a.vocab, 0, (k * kThreads + tid) * V, reach);
+  }
   const raw* in = static_cast<const raw*>(GRAD ? p.dout : a.logits) + r0 * a.vocab;
 #pragma unroll
   for (int k = 0; k < q.kPacks; ++k)
@@ -211,7 +253,7 @@ __device__ __forceinline__ void load_tile(const LogitsArgs& p, int64_t r0, MaskW
   }
 }
 
-template <class T, int V, bool GRAD>
+template <class T, int V, bool GRAD, bool FLAT_MASK>
 __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
   using raw = typename T::raw;
   constexpr int kPacks = kTile / (kThreads * V);
@@ -224,7 +266,7 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
   const logits_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63;
   const int32_t vocab = a.vocab, width = a.history_width;
-  const bool masked = a.mask_kind != LOGITS_MASK_NONE;
+  const bool masked = a.mask_kind != LOGITS_MASK_NONE && !FLAT_MASK;  // by bits in LDS
   const int64_t tiles = (a.rows + p.tile_rows - 1) / p.tile_rows;
   // per element of the thread's packs, whose columns are the same in every
   // tile: the running sums of dbias (gradient) or a bias that all rows share
@@ -239,10 +281,10 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
         col[k][i] = a.bias[e - quotient(e, (uint32_t)vocab, p.magic_vocab) * vocab];
       }
     }
-  RowsTile<T, V, GRAD> next;
+  RowsTile<T, V, GRAD, FLAT_MASK> next;
   const MaskWord m = mask_word(p);
   const int64_t first = (int64_t)blockIdx.x * p.tile_rows, step = (int64_t)gridDim.x * p.tile_rows;
-  load_tile<T, V, GRAD>(p, first, m, mask_row_ahead(p, first, m), next);
+  load_tile<T, V, GRAD, FLAT_MASK>(p, first, m, mask_row_ahead(p, first, m), next);
   int32_t mrow = mask_row_ahead(p, first + step, m);
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int64_t r0 = tile * p.tile_rows;
@@ -252,9 +294,9 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
     const int32_t* h = p.penalties ? a.history + r0 * width : nullptr;
     const int32_t entries = p.penalties ? rows * width : 0;
     const int32_t reach = tile_reach<V>(a, r0);
-    RowsTile<T, V, GRAD> q = next;
+    RowsTile<T, V, GRAD, FLAT_MASK> q = next;
     if (tile + gridDim.x < tiles) {
-      load_tile<T, V, GRAD>(p, r0 + step, m, mrow, next);
+      load_tile<T, V, GRAD, FLAT_MASK>(p, r0 + step, m, mrow, next);
       mrow = mask_row_ahead(p, r0 + 2 * step, m);
     }
     if (masked || p.penalties) {
@@ -380,7 +422,8 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
         settle<T, V>(q.x[k], e, reach);
         widen_pack<T, V>(q.x[k], f);
       }
-      const uint32_t ban = masked ? s_ban[e >> 5] >> (e & 31) : 0u;
+      uint32_t ban = masked ? s_ban[e >> 5] >> (e & 31) : 0u;
+      if (FLAT_MASK) ban = ~mask_bits<V, LOGITS_MASK_BYTES>(q.mask[FLAT_MASK ? k : 0], 0, e, reach);
       if (!GRAD && a.bias && a.bias_row == 0) {
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] += col[k][i];
@@ -426,39 +469,6 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
 }
 
 // ------------------------------------------------ runs of columns of one row
-// The mask of the V columns from c0 + e, as loaded: a byte of bits, or V bytes
-// (moved back like load_inside).
-template <int V, int MASK>
-__device__ __forceinline__ uint64_t load_mask(const logits_args& a, int64_t at, int32_t c0, int32_t e,
-                                              int32_t n) {
-  const uint8_t* m = static_cast<const uint8_t*>(a.mask);
-  if constexpr (MASK == LOGITS_MASK_BITS) {
-    return m[at * 4 + ((c0 + min(e, n - 1)) >> 3)];
-  } else if constexpr (V == 8) {
-    typedef uint64_t eight __attribute__((aligned(1)));
-    return *reinterpret_cast<const eight*>(m + at + c0 + min(e, n - V));
-  } else if constexpr (V == 4) {
-    typedef uint32_t four __attribute__((aligned(1)));
-    return *reinterpret_cast<const four*>(m + at + c0 + min(e, n - V));
-  } else {
-    return m[at + c0 + min(e, n - V)];
-  }
-}
-// Bit i: column c0 + e + i is allowed.
-template <int V, int MASK>
-__device__ __forceinline__ uint32_t mask_bits(uint64_t raw, int32_t c0, int32_t e, int32_t n) {
-  if constexpr (MASK == LOGITS_MASK_BITS) {
-    return (uint32_t)raw >> ((c0 + e) & 7);
-  } else {
-    const int32_t back = e - (n - V);
-    if (back > 0) raw >>= 8 * back;
-    uint32_t bits = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) bits |= ((raw >> (8 * i)) & 0xffu ? 1u : 0u) << i;
-    return bits;
-  }
-}
-
 template <class T, int V, bool GRAD, int MASK>
 __global__ __launch_bounds__(kThreads) void logits_runs_kernel(LogitsArgs p) {
   using raw = typename T::raw;
@@ -653,8 +663,10 @@ hipError_t launch(LogitsArgs p, bool flat, float* dbias, hipStream_t stream) {
   int64_t groups;
   if (flat) {
     groups = flat_groups(a.rows, a.vocab, GRAD);
-    hipLaunchKernelGGL((logits_rows_kernel<T, V, GRAD>), dim3((unsigned)groups), dim3(kThreads), 0,
-                       stream, p);
+    const bool flat_mask = a.mask_kind == LOGITS_MASK_BYTES && !a.mask_rows &&
+                           a.mask_count == a.rows && (a.mask_row == a.vocab || a.rows == 1);
+    auto kernel = flat_mask ? logits_rows_kernel<T, V, GRAD, true> : logits_rows_kernel<T, V, GRAD, false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kThreads), 0, stream, p);
   } else {
     constexpr int kRun = kThreads * V * kRunPacks;
     groups = run_groups(a.rows, a.vocab, dbias != nullptr);

@@ -48,8 +48,10 @@ int check_recur_sizes(const char* who, int32_t steps, int32_t rows, int32_t widt
   if (steps < 0 || rows < 0 || width < 0)
     return fail(ROLLOUT_EINVAL, "%s: negative size (steps %d, rows %d, width %d)", who, steps, rows,
                 width);
-  if ((int64_t)rows * width >= (int64_t)1 << 29)
-    return fail(ROLLOUT_EINVAL, "%s: rows * width must be below 2^29 (got %d * %d)", who, rows, width);
+  if (steps > 1 << 30)
+    return fail(ROLLOUT_EINVAL, "%s: steps must be at most 2^30 (got %d)", who, steps);
+  if ((int64_t)rows * width >= (int64_t)1 << 28)
+    return fail(ROLLOUT_EINVAL, "%s: rows * width must be below 2^28 (got %d * %d)", who, rows, width);
   if (!known_dtype(dtype)) return fail(ROLLOUT_EINVAL, "%s: unknown dtype %d", who, dtype);
   return ROLLOUT_OK;
 }

@@ -188,3 +188,10 @@ def test_two_streams_at_once(rx):
     torch.cuda.synchronize()
     for k, g in enumerate(got):
         assert torch.equal(g, want[k % 2])
+
+
+@pytest.mark.parametrize("spread", ["even", "skew", "one"])
+@pytest.mark.parametrize("M,V,D", [(300, 8191, 9), (512, 8192, 40), (511, 16384, 6), (77, 40000, 24),
+                                   (512, 270000, 4)])
+def test_few_indices_in_a_large_vocabulary(rx, M, V, D, spread):
+    check(rx, *inputs(M, V, D, "bf16", M + V, spread), "bf16")

@@ -53,7 +53,8 @@ def _recur_args(policy, **kw):
 
 @pytest.mark.parametrize("change,text", [
     (dict(steps=-1), "negative size"), (dict(rows=-2), "negative size"),
-    (dict(rows=1 << 20, width=1 << 11), "2\\^29"), (dict(dtype=3), "dtype"), (dict(form=2), "form"),
+    (dict(rows=1 << 14, width=1 << 14), "2\\^28"),
+    (dict(steps=(1 << 30) + 1), "2\\^30"), (dict(dtype=3), "dtype"), (dict(form=2), "form"),
     (dict(x=None), "x is NULL"), (dict(gate=None), "gate is NULL"), (dict(h=None), "h is NULL"),
     (dict(x=66), "aligned"), (dict(dtype=1, gate=65), "aligned"), (dict(h0=2), "h0 is not aligned"),
     (dict(x_step=-6), "stride"), (dict(h_row=-1), "stride"),
