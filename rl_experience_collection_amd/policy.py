@@ -120,14 +120,13 @@ def _ptr(t):
 
 
 def _exact(name, t, dtype, shape):
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous()):
         return
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _flags(name, t, shape):
@@ -153,8 +152,12 @@ def _unit(name, t, axes):
     return t.stride()[:-1]
 
 
+def _wants_grad(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
 def _no_grad(name, *tensors):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+    if _wants_grad(*tensors):
         raise ValueError(f"{name} records no gradient: call it under torch.no_grad()")
 
 
@@ -163,20 +166,16 @@ def _workspace(like, bytes_):
 
 
 # ---------------------------------------------------------------- recurrence
-def _recur_forward(x, gate, h0, dones, form, h_last=True):
+def _recur_forward(x, gate, h0, dones, form):
     L, N, D = x.shape
     lib, stream = _lib(), _here("recurrence", x, gate, h0, dones)
     h = torch.empty_like(x)
-    last = torch.empty((N, D), dtype=torch.float32, device=x.device) if h_last else None
-    a = RecurArgs(steps=L, rows=N, width=D, dtype=_DTYPES[x.dtype], form=form)
-    a.x_step, a.x_row = _unit("x", x, 3)
-    a.gate_step, a.gate_row = _unit("gate", gate, 3)
-    a.h_step, a.h_row = h.stride()[:2]
-    a.x, a.gate, a.h0, a.dones = _ptr(x), _ptr(gate), _ptr(h0), _ptr(dones)
-    a.h, a.h_last = _ptr(h), _ptr(last)
-    a.workspace_bytes = lib.recur_workspace(L, N, D, a.dtype)
-    ws = _workspace(x, max(0, a.workspace_bytes))
-    a.workspace = _ptr(ws)
+    last = torch.empty((N, D), dtype=torch.float32, device=x.device)
+    dt = _DTYPES[x.dtype]
+    size = lib.recur_workspace(L, N, D, dt)
+    ws = _workspace(x, size)
+    a = RecurArgs(L, N, D, dt, form, *x.stride()[:2], *gate.stride()[:2], *h.stride()[:2],
+                  _ptr(x), _ptr(gate), _ptr(h0), _ptr(dones), _ptr(h), _ptr(last), _ptr(ws), size)
     _call(lib.recur_forward, C.byref(a), stream)
     return h, last
 
@@ -186,19 +185,13 @@ def _recur_backward(x, gate, h, h0, dones, dh, dh_last, form, want_dh0):
     lib, stream = _lib(), _here("recurrence", x, gate, h, h0, dones, dh, dh_last)
     dx, dgate = torch.empty_like(h), torch.empty_like(gate)
     dh0 = torch.empty((N, D), dtype=torch.float32, device=gate.device) if want_dh0 else None
-    a = RecurGradArgs(steps=L, rows=N, width=D, dtype=_DTYPES[gate.dtype], form=form)
-    if x is not None:
-        a.x_step, a.x_row = x.stride()[:2]
-    a.gate_step, a.gate_row = gate.stride()[:2]
-    a.h_step, a.h_row = h.stride()[:2]
-    a.dh_step, a.dh_row = dh.stride()[:2]
-    a.dx_step, a.dx_row = dx.stride()[:2]
-    a.dgate_step, a.dgate_row = dgate.stride()[:2]
-    a.x, a.gate, a.h, a.h0, a.dones = _ptr(x), _ptr(gate), _ptr(h), _ptr(h0), _ptr(dones)
-    a.dh, a.dh_last, a.dx, a.dgate, a.dh0 = _ptr(dh), _ptr(dh_last), _ptr(dx), _ptr(dgate), _ptr(dh0)
-    a.workspace_bytes = lib.recur_workspace(L, N, D, a.dtype)
-    ws = _workspace(gate, max(0, a.workspace_bytes))
-    a.workspace = _ptr(ws)
+    dt = _DTYPES[gate.dtype]
+    size = lib.recur_workspace(L, N, D, dt)
+    ws = _workspace(gate, size)
+    a = RecurGradArgs(L, N, D, dt, form, *(x.stride()[:2] if x is not None else (0, 0)),
+                      *gate.stride()[:2], *h.stride()[:2], *dh.stride()[:2], *dx.stride()[:2],
+                      *dgate.stride()[:2], _ptr(x), _ptr(gate), _ptr(h), _ptr(h0), _ptr(dones),
+                      _ptr(dh), _ptr(dh_last), _ptr(dx), _ptr(dgate), _ptr(dh0), _ptr(ws), size)
     _call(lib.recur_backward, C.byref(a), stream)
     return dx, dgate, dh0
 
@@ -248,6 +241,8 @@ def recurrence(x, gate, h0=None, dones=None, form: str = "sigmoid"):
     _unit("gate", gate, 3)
     _exact("h0", h0, torch.float32, (N, D))
     dones = _flags("dones", dones, (L, N))
+    if not _wants_grad(x, gate, h0):
+        return _recur_forward(x, gate, h0, dones, f)
     return _Recurrence.apply(x, gate, h0, dones, f)
 
 
@@ -280,18 +275,21 @@ def recurrence_step(x, gate, state, resets=None, form: str = "sigmoid", out_stat
 _INDEX_BYTES = {torch.int32: 4, torch.int64: 8}
 
 
+def _embed_forward(weight, index, scale):
+    V, D = weight.shape
+    stream = _here("embed", weight, index)
+    out = torch.empty(index.shape + (D,), dtype=weight.dtype, device=weight.device)
+    _call(_lib().embed_forward, _DTYPES[weight.dtype], _ptr(weight), V, D, max(D, weight.stride(0)),
+          _ptr(index), _INDEX_BYTES[index.dtype], index.numel(), scale, _ptr(out), D, stream)
+    return out
+
+
 class _Embed(torch.autograd.Function):
     @staticmethod
     def forward(ctx, weight, index, scale):
-        V, D = weight.shape
-        stream = _here("embed", weight, index)
-        out = torch.empty(tuple(index.shape) + (D,), dtype=weight.dtype, device=weight.device)
-        _call(_lib().embed_forward, _DTYPES[weight.dtype], _ptr(weight), V, D,
-              max(D, weight.stride(0)), _ptr(index), _INDEX_BYTES[index.dtype], index.numel(), scale,
-              _ptr(out), D, stream)
         ctx.save_for_backward(index)
-        ctx.vocab, ctx.scale = V, scale
-        return out
+        ctx.vocab, ctx.scale = weight.shape[0], scale
+        return _embed_forward(weight, index, scale)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -325,48 +323,52 @@ def embed(weight, index, scale: float = 1.0):
         raise ValueError(f"index must be int32 or int64, got {index.dtype}")
     if not index.is_contiguous():
         raise ValueError("index must be contiguous")
+    if not _wants_grad(weight):
+        return _embed_forward(weight, index, float(scale))
     return _Embed.apply(weight, index, float(scale))
 
 
 # -------------------------------------------------------------------- logits
 def _logits_args(logits, bias, history, history_len, penalties, mask, mask_rows):
-    """The C struct; every tensor has been checked."""
+    """The C struct; every tensor has been checked.  penalties: repetition,
+    presence, frequency, each a number or a tensor."""
     V = logits.shape[-1]
-    a = LogitsArgs(vocab=V, dtype=_DTYPES[logits.dtype], history_width=0, mask_kind=0,
-                   repetition=1.0, presence=0.0, frequency=0.0)
-    a.rows = logits.numel() // V if V else 0
-    a.logits = _ptr(logits)
-    a.logits_row = logits.stride(0) if logits.dim() == 2 and logits.shape[0] > 1 else V
-    if bias is not None:
-        a.bias, a.bias_row = _ptr(bias), V if bias.dim() > 1 else 0
-    if history is not None:
-        a.history, a.history_row, a.history_width = _ptr(history), history.shape[-1], history.shape[-1]
-        a.history_len = _ptr(history_len)
-    for name, value in penalties:
-        if isinstance(value, torch.Tensor):
-            setattr(a, name + "_rows", _ptr(value))
+    row = logits.stride(0) if logits.dim() == 2 and logits.shape[0] > 1 else V
+    H = 0 if history is None else history.shape[-1]
+    scalars, rows = [1.0, 0.0, 0.0], [None, None, None]
+    for i, p in enumerate(penalties):
+        if isinstance(p, torch.Tensor):
+            rows[i] = p.data_ptr()
         else:
-            setattr(a, name, value)
+            scalars[i] = p
+    kind, mask_row, mask_count = LOGITS_MASK_NONE, 0, 0
     if mask is not None:
-        a.mask, a.mask_row = _ptr(mask), mask.shape[-1]
-        a.mask_kind = LOGITS_MASK_BITS if mask.dtype == torch.int32 else LOGITS_MASK_BYTES
-        a.mask_count = mask.numel() // mask.shape[-1] if mask.shape[-1] else 0
-        a.mask_rows = _ptr(mask_rows)
-    return a
+        kind = LOGITS_MASK_BITS if mask.dtype is torch.int32 else LOGITS_MASK_BYTES
+        mask_row = mask.shape[-1]
+        mask_count = mask.numel() // mask_row if mask_row else 0
+    return LogitsArgs(logits.numel() // V if V else 0, V, _DTYPES[logits.dtype], _ptr(logits), row,
+                      _ptr(bias), V if bias is not None and bias.dim() > 1 else 0, _ptr(history), H,
+                      _ptr(history_len), H, kind, *scalars, *rows, _ptr(mask), mask_row, mask_count,
+                      _ptr(mask_rows))
+
+
+def _logits_forward(logits, bias, history, history_len, penalties, mask, mask_rows, out):
+    stream = _here("shape_logits", logits, bias, history, history_len, mask, mask_rows, out,
+                   *[p for p in penalties if isinstance(p, torch.Tensor)])
+    a = _logits_args(logits, bias, history, history_len, penalties, mask, mask_rows)
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    out_row = out.stride(0) if out.dim() == 2 and out.shape[0] > 1 else a.vocab
+    _call(_lib().logits_forward, C.byref(a), _ptr(out), out_row, stream)
+    return out
 
 
 class _ShapeLogits(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, bias, history, history_len, penalties, mask, mask_rows, out):
-        rows = [v for _, v in penalties if isinstance(v, torch.Tensor)]
-        stream = _here("shape_logits", logits, bias, history, history_len, mask, mask_rows, out, *rows)
-        a = _logits_args(logits, bias, history, history_len, penalties, mask, mask_rows)
-        if out is None:
-            out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        out_row = out.stride(0) if out.dim() == 2 and out.shape[0] > 1 else a.vocab
-        _call(_lib().logits_forward, C.byref(a), _ptr(out), out_row, stream)
+    def forward(ctx, logits, bias, history, history_len, penalties, mask, mask_rows):
+        out = _logits_forward(logits, bias, history, history_len, penalties, mask, mask_rows, None)
         # of the penalties only the repetition scales the gradient
-        rep = penalties[0][1]
+        rep = penalties[0]
         ctx.repetition = None if isinstance(rep, torch.Tensor) else rep
         if history is None or ctx.repetition == 1.0:
             logits, history, history_len = None, None, None
@@ -382,7 +384,7 @@ class _ShapeLogits(torch.autograd.Function):
         V = dout.shape[-1]
         dout = dout.contiguous()
         a = _logits_args(dout if logits is None else logits, None, history, history_len,
-                         (("repetition", ctx.repetition if rep is None else rep),), mask, mask_rows)
+                         (ctx.repetition if rep is None else rep,), mask, mask_rows)
         dlogits = torch.empty_like(dout) if ctx.needs_input_grad[0] else None
         dbias = torch.empty(V, dtype=torch.float32, device=dout.device) \
             if ctx.needs_input_grad[1] else None
@@ -390,7 +392,7 @@ class _ShapeLogits(torch.autograd.Function):
         ws = _workspace(dout, size)
         _call(lib.logits_backward, C.byref(a), _ptr(dout), V, _ptr(dlogits), V, _ptr(dbias), _ptr(ws),
               size, stream)
-        return dlogits, dbias, None, None, None, None, None, None
+        return dlogits, dbias, None, None, None, None, None
 
 
 def _per_row(name, value, lead):
@@ -420,7 +422,7 @@ def shape_logits(logits, bias=None, history=None, history_len=None, repetition=1
     _element("logits", logits)
     if logits.dim() < 1:
         raise ValueError("logits must be [..., V]")
-    V, lead = logits.shape[-1], tuple(logits.shape[:-1])
+    V, lead = logits.shape[-1], logits.shape[:-1]
     if not logits.is_contiguous():
         _unit("logits", logits, 2)
         if logits.stride(0) < V:
@@ -435,9 +437,8 @@ def shape_logits(logits, bias=None, history=None, history_len=None, repetition=1
         _exact("history_len", history_len, torch.int32, lead)
     elif history_len is not None:
         raise ValueError("history_len needs a history")
-    penalties = (("repetition", _per_row("repetition", repetition, lead)),
-                 ("presence", _per_row("presence", presence, lead)),
-                 ("frequency", _per_row("frequency", frequency, lead)))
+    penalties = (_per_row("repetition", repetition, lead), _per_row("presence", presence, lead),
+                 _per_row("frequency", frequency, lead))
     if mask is not None:
         if mask.dtype == torch.bool:
             mask = mask.view(torch.uint8)
@@ -450,8 +451,8 @@ def shape_logits(logits, bias=None, history=None, history_len=None, repetition=1
             raise ValueError("mask must be contiguous")
         if mask_rows is not None:
             _exact("mask_rows", mask_rows, torch.int32, lead)
-        elif mask.numel() != width and tuple(mask.shape[:-1]) != lead:
-            raise ValueError(f"mask must have one row or rows {lead}, got shape {tuple(mask.shape)}")
+        elif mask.numel() != width and mask.shape[:-1] != lead:
+            raise ValueError(f"mask must have one row or rows {tuple(lead)}, got shape {tuple(mask.shape)}")
     elif mask_rows is not None:
         raise ValueError("mask_rows needs a mask")
     if out is not None:
@@ -462,7 +463,6 @@ def shape_logits(logits, bias=None, history=None, history_len=None, repetition=1
             _unit("out", out, 2)
             if out.stride(0) < V:
                 raise ValueError("out's rows must not overlap")
-        with torch.no_grad():
-            _ShapeLogits.apply(logits, bias, history, history_len, penalties, mask, mask_rows, out)
-        return out
-    return _ShapeLogits.apply(logits, bias, history, history_len, penalties, mask, mask_rows, None)
+    if out is not None or not _wants_grad(logits, bias):
+        return _logits_forward(logits, bias, history, history_len, penalties, mask, mask_rows, out)
+    return _ShapeLogits.apply(logits, bias, history, history_len, penalties, mask, mask_rows)
