@@ -195,3 +195,12 @@ def test_two_streams_at_once(rx):
                                    (512, 270000, 4)])
 def test_few_indices_in_a_large_vocabulary(rx, M, V, D, spread):
     check(rx, *inputs(M, V, D, "bf16", M + V, spread), "bf16")
+
+
+def test_wide_indices_that_name_no_row(rx):
+    """64-bit indices whose low words alone would name one."""
+    w, _, dout = inputs(6, 9, 8, "f32", 2)
+    idx = torch.tensor([3, 2 ** 32 + 3, -2 ** 32 + 3, 3 - 2 ** 63, 8, 2 ** 62])
+    check(rx, w, idx, dout, "f32")
+    big = idx.repeat(200)
+    check(rx, w, big, dout.repeat(200, 1), "f32")

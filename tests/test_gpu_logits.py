@@ -254,3 +254,27 @@ def test_extreme_repetition(rx, V):
     m = np.isfinite(r)
     # two roundings of a quotient at most, or of the smallest values
     assert (np.abs(d[m] - r[m]) <= 2 * ref.U * np.abs(r[m]) + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("R,V", [(96_000_000, 45), (135_000, 32003)])
+def test_far_offsets(rx, R, V):
+    """More than 2^32 logits: the first and the last rows give the bits of the
+    same rows on their own, the gradient included."""
+    z = torch.empty(R, V, dtype=torch.bfloat16, device="cuda")
+    step = R // 8
+    for lo in range(0, R, step):
+        z[lo:lo + step].normal_()
+    a, _ = inputs(8, V, 4, "bf16", 3, "table")
+    c = {k: v.cuda() for k, v in a.items()}
+    kw = dict(bias=c["bias"], history=c["history"][:1].expand(R, 4).contiguous(), repetition=1.25,
+              frequency=0.25, mask=c["mask"], mask_rows=torch.arange(R, dtype=torch.int32, device="cuda") % 5)
+    leaf = z.requires_grad_()
+    out = rx.shape_logits(leaf, **kw)
+    g, = torch.autograd.grad(out, leaf, out.detach().clamp(min=-1))
+    for rows in (slice(0, 1000), slice(R - 1000, R)):
+        few = dict(kw, history=kw["history"][rows].contiguous(), mask_rows=kw["mask_rows"][rows].contiguous())
+        one = z.detach()[rows].clone().requires_grad_()
+        want = rx.shape_logits(one, **few)
+        assert torch.equal(out.detach()[rows], want.detach())
+        gw, = torch.autograd.grad(want, one, want.detach().clamp(min=-1))
+        assert torch.equal(g[rows], gw)

@@ -301,3 +301,45 @@ def test_captured_training_pass(rx, L, N, D):
             torch.cuda.synchronize()
             for a, b in zip(out, want):
                 assert torch.equal(a, b)
+
+
+def test_far_offsets(rx):
+    """Rows more than 2^32 bytes apart and steps past 2^32 elements: each row
+    gives the bits of the same row on its own."""
+    N, L, D = 2, 4_400_000, 512
+    x = torch.empty(N, L, D, dtype=torch.bfloat16, device="cuda")
+    gate = torch.empty(N, L, D, dtype=torch.bfloat16, device="cuda")
+    for n in range(N):
+        for lo in range(0, L, 1_100_000):
+            x[n, lo:lo + 1_100_000].normal_()
+            gate[n, lo:lo + 1_100_000].normal_(2.0)
+    h, last = rx.recurrence(x.transpose(0, 1), gate.transpose(0, 1))
+    assert h.transpose(0, 1).is_contiguous()
+    for n in range(N):
+        one, one_last = rx.recurrence(x[n][:, None], gate[n][:, None])
+        assert torch.equal(one_last[0], last[n])
+        for lo in range(0, L, 1_100_000):
+            assert torch.equal(one[lo:lo + 1_100_000, 0], h[lo:lo + 1_100_000, n])
+        del one
+
+
+def test_tensors_elsewhere_are_refused(rx):
+    x = torch.zeros(3, 2, 4)
+    with pytest.raises(ValueError, match="device"):
+        rx.recurrence(x, x)
+    with pytest.raises(ValueError, match="device"):
+        rx.recurrence(x.cuda(), x.cuda(), dones=torch.zeros(3, 2, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="device"):
+        rx.recurrence_step(x[0], x[0], x[0])
+    with pytest.raises(ValueError, match="device"):
+        rx.embed(x[0].cuda(), torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="device"):
+        rx.shape_logits(x, repetition=torch.ones(3, 2, device="cuda"))
+
+
+def test_second_gradients_are_refused(rx):
+    x = torch.randn(3, 2, 4, device="cuda", requires_grad=True)
+    h, _ = rx.recurrence(x, x)
+    g, = torch.autograd.grad(h.sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(g.sum(), x)
