@@ -31,9 +31,15 @@ constexpr int kThreads = 256;
 constexpr int kTile = 2048;      // elements of a tile of whole rows, at most
 constexpr int kTileRows = 128;   // its rows, at most
 constexpr int kRunPacks = 2;     // packs per thread of a run of columns
-// workgroups of a launch over tiles: what is resident at once on 256 compute
-// units (the forward pass holds 76 registers a thread, the gradient 64)
-constexpr int kForwardGroups = 1536, kGradientGroups = 2048;
+// Workgroups of a launch over tiles: what is resident at once on 256 compute
+// units.  The kernel is held to 128 registers a thread (4 waves a SIMD): the
+// 4,096,000 x 45 training pass takes 884 us so, 960 us with the 150 that the
+// compiler takes by itself and 978 us at 96, where it spills.
+constexpr int kTileWaves = 4;
+constexpr int kTileGroups = 256 * kTileWaves;
+// (96 registers: the 4096 x 32003 training pass takes 344 us, 359 us at the
+// compiler's 104, 492 us at 80, where it spills)
+constexpr int kRunWaves = 5;
 constexpr int kBiasGroups = 2048;  // about, of runs in all
 constexpr float kBanned = -__builtin_inff();
 
@@ -170,11 +176,12 @@ __device__ __forceinline__ uint32_t mask_bits(uint64_t raw, int32_t c0, int32_t 
 // ------------------------------------------------------- tiles of whole rows
 constexpr int kAhead = 4;  // history entries a thread loads before it uses the first
 
-// FLAT_MASK: a byte of mask per logit, one after another like them, is read
-// like them; other masks become bits in LDS.
-//
+// How a tile takes its mask: bits and bytes become bits of the tile in LDS; a
+// byte per logit, one after another like them, is read like them.
+enum MaskMode { kNoMask, kBitMask, kByteMask, kFlatMask };
+
 // What a workgroup needs of a tile, loaded while the one before is worked on.
-template <class T, int V, bool GRAD, bool FLAT_MASK>
+template <class T, int V, bool GRAD, int MODE>
 struct RowsTile {
   static constexpr int kPacks = kTile / (kThreads * V);
   Pack<T, V> x[kPacks], z[GRAD ? kPacks : 1];
@@ -183,7 +190,7 @@ struct RowsTile {
   float rho, alpha, beta;
   uint32_t word;  // a mask of bits: this thread's word of the tile's masks,
   bool named;     // if it has one
-  uint64_t mask[FLAT_MASK ? kPacks : 1];  // the packs' bytes of the mask
+  uint64_t mask[MODE == kFlatMask ? kPacks : 1];  // the packs' bytes of the mask
 };
 
 // A mask of bits gives every thread at most one word of a tile's masks (128
@@ -200,7 +207,6 @@ __device__ __forceinline__ MaskWord mask_word(const LogitsArgs& p) {
 // ahead, as the word's address waits for it.
 __device__ __forceinline__ int32_t mask_row_ahead(const LogitsArgs& p, int64_t r0, MaskWord m) {
   const logits_args& a = p.a;
-  if (a.mask_kind != LOGITS_MASK_BITS) return -1;
   const int64_t r = min(r0 + m.r, a.rows - 1);
   // (one row per row of logits: mask_count, and so r, is below 2^31)
   return a.mask_rows ? a.mask_rows[r] : (a.mask_count == 1 ? 0 : (int32_t)r);
@@ -213,9 +219,9 @@ __device__ __forceinline__ int32_t tile_reach(const logits_args& a, int64_t r0) 
 }
 
 // Every load before the first wait: no load behind a branch of its lanes.
-template <class T, int V, bool GRAD, bool FLAT_MASK>
+template <class T, int V, bool GRAD, int MODE>
 __device__ __forceinline__ void load_tile(const LogitsArgs& p, int64_t r0, MaskWord m, int32_t mrow,
-                                          RowsTile<T, V, GRAD, FLAT_MASK>& q) {
+                                          RowsTile<T, V, GRAD, MODE>& q) {
   using raw = typename T::raw;
   const logits_args& a = p.a;
   const int tid = threadIdx.x;
@@ -232,14 +238,14 @@ __device__ __forceinline__ void load_tile(const LogitsArgs& p, int64_t r0, MaskW
     for (int j = 0; j < kAhead; ++j)
       q.token[j] = h[min(j * kThreads + tid, rows * a.history_width - 1)];
   }
-  if (a.mask_kind == LOGITS_MASK_BITS) {
+  if (MODE == kBitMask) {
     q.named = m.r < rows && mrow >= 0 && mrow < a.mask_count;
     q.word = static_cast<const uint32_t*>(a.mask)[q.named ? (int64_t)mrow * a.mask_row + m.j : 0];
   }
-  if (FLAT_MASK) {
+  if (MODE == kFlatMask) {
 #pragma unroll
     for (int k = 0; k < q.kPacks; ++k)
-      q.mask[FLAT_MASK ? k : 0] = load_mask<V, LOGITS_MASK_BYTES>(a, r0 * a.vocab, 0, (k * kThreads + tid) * V, reach);
+      q.mask[MODE == kFlatMask ? k : 0] = load_mask<V, LOGITS_MASK_BYTES>(a, r0 * a.vocab, 0, (k * kThreads + tid) * V, reach);
   }
   const raw* in = static_cast<const raw*>(GRAD ? p.dout : a.logits) + r0 * a.vocab;
 #pragma unroll
@@ -253,8 +259,8 @@ __device__ __forceinline__ void load_tile(const LogitsArgs& p, int64_t r0, MaskW
   }
 }
 
-template <class T, int V, bool GRAD, bool FLAT_MASK>
-__global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
+template <class T, int V, bool GRAD, int MODE>
+__global__ __launch_bounds__(kThreads, kTileWaves) void logits_rows_kernel(LogitsArgs p) {
   using raw = typename T::raw;
   constexpr int kPacks = kTile / (kThreads * V);
   __shared__ alignas(16) uint32_t s_val[kTile];  // the tile's values (fp32), penalised in place
@@ -266,7 +272,7 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
   const logits_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63;
   const int32_t vocab = a.vocab, width = a.history_width;
-  const bool masked = a.mask_kind != LOGITS_MASK_NONE && !FLAT_MASK;  // by bits in LDS
+  constexpr bool masked = MODE == kBitMask || MODE == kByteMask;  // by bits in LDS
   const int64_t tiles = (a.rows + p.tile_rows - 1) / p.tile_rows;
   // per element of the thread's packs, whose columns are the same in every
   // tile: the running sums of dbias (gradient) or a bias that all rows share
@@ -281,11 +287,12 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
         col[k][i] = a.bias[e - quotient(e, (uint32_t)vocab, p.magic_vocab) * vocab];
       }
     }
-  RowsTile<T, V, GRAD, FLAT_MASK> next;
-  const MaskWord m = mask_word(p);
+  RowsTile<T, V, GRAD, MODE> next;
+  MaskWord m{0, 0};
+  if (MODE == kBitMask) m = mask_word(p);
   const int64_t first = (int64_t)blockIdx.x * p.tile_rows, step = (int64_t)gridDim.x * p.tile_rows;
-  load_tile<T, V, GRAD, FLAT_MASK>(p, first, m, mask_row_ahead(p, first, m), next);
-  int32_t mrow = mask_row_ahead(p, first + step, m);
+  load_tile<T, V, GRAD, MODE>(p, first, m, MODE == kBitMask ? mask_row_ahead(p, first, m) : -1, next);
+  int32_t mrow = MODE == kBitMask ? mask_row_ahead(p, first + step, m) : -1;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int64_t r0 = tile * p.tile_rows;
     const int32_t rows = (int32_t)min((int64_t)p.tile_rows, a.rows - r0);
@@ -294,10 +301,10 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
     const int32_t* h = p.penalties ? a.history + r0 * width : nullptr;
     const int32_t entries = p.penalties ? rows * width : 0;
     const int32_t reach = tile_reach<V>(a, r0);
-    RowsTile<T, V, GRAD, FLAT_MASK> q = next;
+    RowsTile<T, V, GRAD, MODE> q = next;
     if (tile + gridDim.x < tiles) {
-      load_tile<T, V, GRAD, FLAT_MASK>(p, r0 + step, m, mrow, next);
-      mrow = mask_row_ahead(p, r0 + 2 * step, m);
+      load_tile<T, V, GRAD, MODE>(p, r0 + step, m, mrow, next);
+      if (MODE == kBitMask) mrow = mask_row_ahead(p, r0 + 2 * step, m);
     }
     if (masked || p.penalties) {
       __syncthreads();  // the previous tile's words are read
@@ -312,7 +319,7 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
       }
       if (masked && tid < kTile / 32 + 1) s_ban[tid] = 0u;
       __syncthreads();
-      if (a.mask_kind == LOGITS_MASK_BITS) {
+      if (MODE == kBitMask) {
         // a row's words are shifted to the row's place among the tile's bits
         if (q.named) {
           const int32_t left = vocab - 32 * m.j;
@@ -321,8 +328,7 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
           atomicOr(&s_ban[bit >> 5], ban << sh);
           if (sh) atomicOr(&s_ban[(bit >> 5) + 1], ban >> (32 - sh));
         }
-      } else if (masked) {
-#pragma unroll 4
+      } else if (MODE == kByteMask) {
         for (int32_t e = tid; e < kTile; e += kThreads) {
           bool ban = false;
           if (e < n) {
@@ -423,7 +429,7 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
         widen_pack<T, V>(q.x[k], f);
       }
       uint32_t ban = masked ? s_ban[e >> 5] >> (e & 31) : 0u;
-      if (FLAT_MASK) ban = ~mask_bits<V, LOGITS_MASK_BYTES>(q.mask[FLAT_MASK ? k : 0], 0, e, reach);
+      if (MODE == kFlatMask) ban = ~mask_bits<V, LOGITS_MASK_BYTES>(q.mask[MODE == kFlatMask ? k : 0], 0, e, reach);
       if (!GRAD && a.bias && a.bias_row == 0) {
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] += col[k][i];
@@ -470,7 +476,7 @@ __global__ __launch_bounds__(kThreads) void logits_rows_kernel(LogitsArgs p) {
 
 // ------------------------------------------------ runs of columns of one row
 template <class T, int V, bool GRAD, int MASK>
-__global__ __launch_bounds__(kThreads) void logits_runs_kernel(LogitsArgs p) {
+__global__ __launch_bounds__(kThreads, kRunWaves) void logits_runs_kernel(LogitsArgs p) {
   using raw = typename T::raw;
   constexpr int kRun = kThreads * V * kRunPacks;
   __shared__ alignas(16) uint32_t s_count[kRun];
@@ -644,10 +650,9 @@ int32_t tile_rows_of(int32_t vocab) {
   return rows < kTileRows ? rows : kTileRows;
 }
 // Workgroups along the rows: dbias is summed over as many partial sums.
-int64_t flat_groups(int64_t rows, int32_t vocab, bool gradient) {
+int64_t flat_groups(int64_t rows, int32_t vocab) {
   const int64_t tiles = (rows + tile_rows_of(vocab) - 1) / tile_rows_of(vocab);
-  const int64_t most = gradient ? kGradientGroups : kForwardGroups;
-  return tiles < most ? tiles : most;
+  return tiles < kTileGroups ? tiles : kTileGroups;
 }
 int64_t run_groups(int64_t rows, int32_t vocab, bool bias) {
   // with dbias few groups of many rows, as each adds a row of partial sums to
@@ -662,10 +667,13 @@ hipError_t launch(LogitsArgs p, bool flat, float* dbias, hipStream_t stream) {
   const logits_args& a = p.a;
   int64_t groups;
   if (flat) {
-    groups = flat_groups(a.rows, a.vocab, GRAD);
+    groups = flat_groups(a.rows, a.vocab);
     const bool flat_mask = a.mask_kind == LOGITS_MASK_BYTES && !a.mask_rows &&
                            a.mask_count == a.rows && (a.mask_row == a.vocab || a.rows == 1);
-    auto kernel = flat_mask ? logits_rows_kernel<T, V, GRAD, true> : logits_rows_kernel<T, V, GRAD, false>;
+    auto kernel = flat_mask                            ? logits_rows_kernel<T, V, GRAD, kFlatMask>
+                  : a.mask_kind == LOGITS_MASK_BITS  ? logits_rows_kernel<T, V, GRAD, kBitMask>
+                  : a.mask_kind == LOGITS_MASK_BYTES ? logits_rows_kernel<T, V, GRAD, kByteMask>
+                                                     : logits_rows_kernel<T, V, GRAD, kNoMask>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kThreads), 0, stream, p);
   } else {
     constexpr int kRun = kThreads * V * kRunPacks;
@@ -745,8 +753,8 @@ bool logits_gradient_reads_logits(const logits_args& a) {
 int64_t logits_workspace_bytes(int64_t rows, int32_t vocab) {
   if (rows == 0 || vocab == 0) return 0;
   int64_t groups = run_groups(rows, vocab, true);
-  if (vocab <= kTile && flat_groups(rows, vocab, true) > groups)
-    groups = flat_groups(rows, vocab, true);
+  if (vocab <= kTile && flat_groups(rows, vocab) > groups)
+    groups = flat_groups(rows, vocab);
   return groups * vocab * 4;
 }
 
