@@ -24,11 +24,17 @@
 // these onto it, oldest first, and publishes the state that leaves it.
 // Every published map is one 64-bit word, stored and polled by device-coherent
 // relaxed atomics, so no fence is needed; a kernel marks the words as empty
-// first.  Each wait is on a workgroup with an earlier ticket, which
-// runs already and publishes its map without waiting, so every wait ends; a
-// wait that reached its bound all the same would leave NaN, never a wrong
-// number.  A state is the same expression wherever the walk found its start:
-// results do not depend on timing.
+// first.  Each wait is on workgroups with earlier tickets, which run already
+// and wait on earlier ones only, so every wait ends; a wait that reached its
+// bound all the same would leave NaN, never a wrong number.  A state is the
+// same expression wherever the walk found its start: results do not depend on
+// timing.
+//
+// Linear gates may be larger than 1, and a product of them infinite where the
+// states are not (those of a padded row are zero).  A slot whose slope is no
+// finite number is not folded: its workgroup takes that tile's slots one after
+// another, step by step; a chained tile whose slope is none publishes no map,
+// only the state that leaves it.
 #include <type_traits>
 
 #include "elem.hpp"
@@ -58,6 +64,8 @@ __device__ __forceinline__ bool is_reset(float a) { return __float_as_uint(a) ==
 __device__ __forceinline__ float stored_slope(float a, bool reset) {
   return reset ? kReset : a + 0.0f;
 }
+// Not a finite number.
+__device__ __forceinline__ bool is_wild(float a) { return !(__builtin_fabsf(a) < __builtin_inff()); }
 __device__ __forceinline__ float apply(Map m, float h) {
   return is_reset(m.a) ? m.b : __builtin_fmaf(m.a, h, m.b);
 }
@@ -195,15 +203,18 @@ __device__ __forceinline__ int32_t poll_chain(const uint64_t* sample, int64_t st
 }
 
 // The state that enters tile `o` (in the order of the scan), for every wave:
-// `c` is the state that enters the scan and becomes that.
-template <int V, int W>
-__device__ __forceinline__ void enter_tile(const RecurArgs& p, int32_t o, int32_t u, bool active, int w,
-                                           int lane, const float (&sa)[W][64][V],
+// `c` is the state that enters the scan and becomes that.  `wild`: a slot's
+// slope is no finite number.  Wave 0 learns whether it has to publish the state
+// that leaves the tile itself, later: a tile with an infinite slope has no map.
+template <bool SIG, int V, int W>
+__device__ __forceinline__ bool enter_tile(const RecurArgs& p, int32_t o, int32_t u, bool active, int w,
+                                           int lane, bool wild, const float (&sa)[W][64][V],
                                            const float (&sb)[W][64][V], ChainLds<V>& s,
                                            float (&c)[V]) {
   const int64_t stride = (int64_t)p.units * V;  // words of a tile
   uint64_t* mine = p.words + o * stride + (int64_t)u * V;
   Map t[V];
+  bool held = false;
   if (w == 0) {
     // the tile's map
 #pragma unroll
@@ -212,7 +223,13 @@ __device__ __forceinline__ void enter_tile(const RecurArgs& p, int32_t o, int32_
     for (int j = 1; j < W; ++j)
 #pragma unroll
       for (int v = 0; v < V; ++v) t[v] = chain(t[v], Map{sa[j][lane][v], sb[j][lane][v]});
-    if (o > 0 && active) {
+    if constexpr (!SIG) {
+      bool any = wild;
+#pragma unroll
+      for (int v = 0; v < V; ++v) any = any || is_wild(t[v].a);
+      held = __ballot(any) != 0;
+    }
+    if (o > 0 && active && !held) {
 #pragma unroll
       for (int v = 0; v < V; ++v) put_map(mine + v, t[v]);
     }
@@ -267,11 +284,22 @@ __device__ __forceinline__ void enter_tile(const RecurArgs& p, int32_t o, int32_
 #pragma unroll
     for (int v = 0; v < V; ++v) c[v] = s.state[lane][v];
   }
-  if (w == 0 && active) {
+  if (w == 0 && active && !held) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (o == 0 || !is_reset(t[v].a)) put_map(mine + v, Map{kReset, apply(t[v], c[v])});
   }
+  return held;
+}
+
+// The state that leaves tile `o`, for those after it (wave 0).
+template <int V>
+__device__ __forceinline__ void put_state(const RecurArgs& p, int32_t o, int32_t u, bool active,
+                                          const float (&c)[V]) {
+  if (!active) return;
+  uint64_t* mine = p.words + (o * (int64_t)p.units + u) * V;
+#pragma unroll
+  for (int v = 0; v < V; ++v) put_map(mine + v, Map{kReset, c[v]});
 }
 
 // Joins the tile's slots: `c` is the state that enters the tile, and then the
@@ -303,6 +331,30 @@ __device__ __forceinline__ void join_slots(const float (&sa)[W][64][V], const fl
     }
   }
 }
+
+// The same where a slot has no map: one after another each wave runs its slot
+// on the state and hands it on.
+template <int V, int W, class Run>
+__device__ __forceinline__ void join_wild(float (&hand)[64][V], int w, int lane, float (&c)[V],
+                                          float (&h)[V], Run run) {
+  for (int j = 0; j < W; ++j) {
+    if (j == w) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = c[v];
+      run(c);
+#pragma unroll
+      for (int v = 0; v < V; ++v) hand[lane][v] = c[v];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v] = hand[lane][v];
+    __syncthreads();
+  }
+}
+
+// What a slot tells of itself besides its maps: a done in some lane, a slope
+// that is no finite number.
+constexpr uint32_t kCut = 1, kWild = 2;
 
 // Where a workgroup and its lane stand.
 struct Place {
@@ -374,7 +426,7 @@ __global__ __launch_bounds__(64 * waves_of(CHAIN)) void recur_forward_kernel(con
   __shared__ typename std::conditional<CHAIN, ChainLds<V>, char>::type s_chain;
   constexpr int kBufs = CHAIN ? 1 : 2;
   __shared__ alignas(16) float s_a[kBufs][W][64][V], s_b[kBufs][W][64][V];
-  __shared__ uint32_t s_cut[kBufs][W];
+  __shared__ uint32_t s_note[kBufs][W];
   Chained tile{0, (int32_t)blockIdx.x};
   do {
     if (CHAIN && !tile.take(p)) break;
@@ -440,13 +492,37 @@ __global__ __launch_bounds__(64 * waves_of(CHAIN)) void recur_forward_kernel(con
         s_a[buf][w][lane][v] = m[v].a;
         s_b[buf][w][lane][v] = m[v].b;
       }
-      if (lane == 0) s_cut[buf][w] = cut;
+      uint32_t note = cut ? kCut : 0u;
+      if constexpr (!SIG) {
+        bool wild = false;
+#pragma unroll
+        for (int v = 0; v < V; ++v) wild = wild || is_wild(m[v].a);
+        if (__ballot(wild)) note |= kWild;
+      }
+      if (lane == 0) s_note[buf][w] = note;
       __syncthreads();
+      const uint32_t notes = s_note[buf][lane % W];
+      const uint32_t cuts = (uint32_t)__ballot((notes & kCut) != 0);
+      const bool wild = !SIG && __ballot((notes & kWild) != 0) != 0;
+      bool held = false;
       if constexpr (CHAIN)
-        enter_tile<V, W>(p, tile.order, at.u, at.active, w, lane, s_a[buf], s_b[buf], s_chain, c);
-      const uint32_t cuts = (uint32_t)__ballot(s_cut[buf][lane % W] != 0);
+        held = enter_tile<SIG, V, W>(p, tile.order, at.u, at.active, w, lane, wild, s_a[buf], s_b[buf],
+                                     s_chain, c);
       float h[V];
-      join_slots<V, W>(s_a[buf], s_b[buf], cuts, w, lane, c, h);
+      if (wild) {
+        join_wild<V, W>(s_a[buf][0], w, lane, c, h, [&](float (&s)[V]) {
+#pragma unroll
+          for (int i = 0; i < S; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+              s[v] = (done >> i) & 1u ? b[i][v] : __builtin_fmaf(a[i][v], s[v], b[i][v]);
+        });
+      } else {
+        join_slots<V, W>(s_a[buf], s_b[buf], cuts, w, lane, c, h);
+      }
+      if constexpr (CHAIN && !SIG) {
+        if (held) put_state<V>(p, tile.order, at.u, at.active, c);
+      }
       auto replay = [&](auto cuts_here) {
 #pragma unroll
         for (int i = 0; i < S; ++i) {
@@ -498,7 +574,7 @@ __global__ __launch_bounds__(64 * waves_of(CHAIN)) void recur_backward_kernel(co
   __shared__ typename std::conditional<CHAIN, ChainLds<V>, char>::type s_chain;
   constexpr int kBufs = CHAIN ? 1 : 2;
   __shared__ alignas(16) float s_a[kBufs][W][64][V], s_b[kBufs][W][64][V];
-  __shared__ uint32_t s_cut[kBufs][W];
+  __shared__ uint32_t s_note[kBufs][W];
   Chained tile{0, (int32_t)blockIdx.x};
   do {
     if (CHAIN && !tile.take(p)) break;
@@ -571,13 +647,37 @@ __global__ __launch_bounds__(64 * waves_of(CHAIN)) void recur_backward_kernel(co
         s_a[buf][w][lane][v] = m[v].a;
         s_b[buf][w][lane][v] = m[v].b;
       }
-      if (lane == 0) s_cut[buf][w] = cut;
+      uint32_t note = cut ? kCut : 0u;
+      if constexpr (!SIG) {
+        bool wild = false;
+#pragma unroll
+        for (int v = 0; v < V; ++v) wild = wild || is_wild(m[v].a);
+        if (__ballot(wild)) note |= kWild;
+      }
+      if (lane == 0) s_note[buf][w] = note;
       __syncthreads();
+      const uint32_t notes = s_note[buf][lane % W];
+      const uint32_t cuts = (uint32_t)__ballot((notes & kCut) != 0);
+      const bool wild = !SIG && __ballot((notes & kWild) != 0) != 0;
+      bool held = false;
       if constexpr (CHAIN)
-        enter_tile<V, W>(p, tile.order, at.u, at.active, w, lane, s_a[buf], s_b[buf], s_chain, c);
-      const uint32_t cuts = (uint32_t)__ballot(s_cut[buf][lane % W] != 0);
+        held = enter_tile<SIG, V, W>(p, tile.order, at.u, at.active, w, lane, wild, s_a[buf], s_b[buf],
+                                     s_chain, c);
       float G[V];
-      join_slots<V, W>(s_a[buf], s_b[buf], cuts, w, lane, c, G);
+      if (wild) {
+        join_wild<V, W>(s_a[buf][0], w, lane, c, G, [&](float (&s)[V]) {
+#pragma unroll
+          for (int i = 0; i < S; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+              s[v] = (done >> i) & 1u ? 0.0f : a[i][v] * (df[i][v] + s[v]);
+        });
+      } else {
+        join_slots<V, W>(s_a[buf], s_b[buf], cuts, w, lane, c, G);
+      }
+      if constexpr (CHAIN && !SIG) {
+        if (held) put_state<V>(p, tile.order, at.u, at.active, c);
+      }
       auto replay = [&](auto cuts_here) {
 #pragma unroll
         for (int i = 0; i < S; ++i) {

@@ -167,6 +167,28 @@ def test_extreme_gates(rx):
     check(rx, i, "f32", True)
 
 
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("L,lo,hi,gate", [(40, 16, 24, 2e5), (1300, 16, 24, 2e5), (1300, 520, 776, 1.5)])
+def test_gates_whose_product_overflows(rx, L, lo, hi, gate, name):
+    """Linear gates above 1 from step lo to hi, 1 elsewhere; their product is
+    no fp32 number, the states are: all zero, tiny before the growth, zero
+    until it is over, cut by a done in its middle."""
+    i = inputs(L, 4, 65, name, False, 0.0, 17)
+    i["gate"] = torch.ones_like(i["gate"])
+    i["gate"][lo:hi] = gate
+    i["dones"] = torch.zeros(L, 4, dtype=torch.uint8)
+    i["dones"][(lo + hi) // 2, 3] = 1
+    i["x"][:, [0, 1, 3]] = 0
+    i["dh"][:, [0, 1, 3]] = 0
+    i["x"][:hi, 2] = 0
+    i["dh"][lo:, 2] = 0
+    for k in ("h0", "dl"):
+        i[k][[0, 2]] = 0
+        i[k][[1, 3]] = torch.sign(i[k][[1, 3]]) * 1e-36
+    h, _ = check(rx, i, name, False)
+    assert (h[:, 0] == 0).all() and (h[-1, 1].abs() > 0).all()
+
+
 def test_a_gate_that_is_not_a_number_reaches_its_channel_only(rx):
     i = inputs(30, 2, 4, "f32", True, 0.0, 13)
     c = {k: v.cuda() for k, v in i.items() if v is not None}
