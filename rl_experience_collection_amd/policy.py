@@ -5,9 +5,14 @@
     shape_logits                    penalties, bias and mask on logits
 
 `embed`, `recurrence` and `shape_logits` take part in torch's autograd; their
-gradients run in the library's kernels too.  Calls run on torch's current stream, on the current
-device, where their tensors must live; outputs and workspaces come from
-torch's allocator, so captured graphs keep their own.
+gradients run in the library's kernels too.  Calls run on torch's current
+stream, on the current device, where their tensors must live; outputs and
+workspaces come from torch's allocator, so captured graphs keep their own.
+
+A backward pass that is captured into a graph asks for its gradients with
+torch.autograd.grad, or is captured when no eager graph of the same leaves is
+alive: torch accumulates into a leaf's .grad on the stream on which the leaf was
+first used, and to wait for that stream inside a capture ends the process.
 """
 from __future__ import annotations
 
@@ -165,11 +170,20 @@ def _workspace(like, bytes_):
     return torch.empty(bytes_, dtype=torch.uint8, device=like.device) if bytes_ else None
 
 
+def _like(t):
+    """An empty tensor of t's shape, in its layout where that leaves the last
+    dimension contiguous (of overlapping windows torch derives one that does not)."""
+    e = torch.empty_like(t)
+    if t.shape[-1] > 1 and e.stride(-1) != 1:
+        e = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return e
+
+
 # ---------------------------------------------------------------- recurrence
 def _recur_forward(x, gate, h0, dones, form):
     L, N, D = x.shape
     lib, stream = _lib(), _here("recurrence", x, gate, h0, dones)
-    h = torch.empty_like(x)
+    h = _like(x)
     last = torch.empty((N, D), dtype=torch.float32, device=x.device)
     dt = _DTYPES[x.dtype]
     size = lib.recur_workspace(L, N, D, dt)
@@ -183,7 +197,7 @@ def _recur_forward(x, gate, h0, dones, form):
 def _recur_backward(x, gate, h, h0, dones, dh, dh_last, form, want_dh0):
     L, N, D = gate.shape
     lib, stream = _lib(), _here("recurrence", x, gate, h, h0, dones, dh, dh_last)
-    dx, dgate = torch.empty_like(h), torch.empty_like(gate)
+    dx, dgate = _like(h), _like(gate)
     dh0 = torch.empty((N, D), dtype=torch.float32, device=gate.device) if want_dh0 else None
     dt = _DTYPES[gate.dtype]
     size = lib.recur_workspace(L, N, D, dt)

@@ -108,6 +108,19 @@ def test_strides(rx, L, name):
     check(rx, rep, name, True, dict(dh=i["dh"][:1, :1].cuda().expand(L, 3, 12)))
 
 
+@pytest.mark.parametrize("L,N,D", [(3, 1, 8), (40, 2, 70), (1300, 1, 12)])
+def test_overlapping_windows(rx, L, N, D):
+    """x and gate slide over one sequence a step at a time: two axes share a
+    stride, of an input's elements several are the same."""
+    i = inputs(L, N, D, "f32", True, 0.1, 18)
+    windows = {}
+    for k in ("x", "gate"):
+        seq = torch.randn(L + N + D, generator=torch.Generator().manual_seed(19))
+        i[k] = seq.as_strided((L, N, D), (1, 1, 1)).clone()
+        windows[k] = seq.cuda().as_strided((L, N, D), (1, 1, 1))
+    check(rx, i, "f32", True, windows)
+
+
 def test_gradient_of_a_broadcast_gate_is_the_sum(rx):
     i = inputs(40, 6, 8, "f32", True, 0.1, 10)
     one = i["gate"][:, :1].cuda().requires_grad_()
