@@ -1,7 +1,7 @@
 // Penalties, bias and mask on logits, and their gradient (include/policy.h).
 //
-// Two shapes.  Rows of at most 2048 logits that lie one after another are
-// taken several at a time: a tile is a run of whole rows addressed as one
+// Two shapes.  Many short rows (a quarter of a run of columns at most) that lie
+// one after another are taken several at a time: a tile is a run of whole rows addressed as one
 // array.  Longer (or strided) rows are cut into runs of columns, one row at a
 // time.  In both a thread owns fixed 16-byte packs of the tile, loads them
 // first, and while they are on their way the workgroup counts the history's
@@ -40,7 +40,7 @@ constexpr int kTileGroups = 256 * kTileWaves;
 // (96 registers: the 4096 x 32003 training pass takes 344 us, 359 us at the
 // compiler's 104, 492 us at 80, where it spills)
 constexpr int kRunWaves = 5;
-constexpr int kBiasGroups = 2048;  // about, of runs in all
+constexpr int kBiasGroups = 1024;  // about, of runs in all, with dbias
 constexpr float kBanned = -__builtin_inff();
 
 struct LogitsArgs {
@@ -644,6 +644,16 @@ __global__ __launch_bounds__(1024) void bias_join_kernel(const float* partial, i
   }
 }
 
+// The longest rows taken several at a time, a quarter of a run of columns.
+// 32,768 rows of bf16 with a history of 64 (forward, gradient): 63 and 78 us at
+// 900 logits, as runs 75 and 89; at 1100 115 and 137, as runs 77 and 87.  fp32:
+// 36 and 47 us at 500, as runs 50 and 68; at 700 62 and 90, as runs 52 and 85.
+int32_t flat_most(int32_t dtype) { return dtype == POLICY_F32 ? 512 : 1024; }
+// As many rows are taken one at a time whatever their length, which spreads
+// them over more of the chip: 512 rows of 45 fp32 logits take 4.2 and 7.4 us so,
+// 7.9 and 9.9 as tiles; 2048 take 6.0 and 13.9, 8.0 and 10.4 as tiles.
+constexpr int64_t kFewRows = 512;
+
 // Rows of a tile of whole rows.
 int32_t tile_rows_of(int32_t vocab) {
   const int32_t rows = kTile / vocab;
@@ -656,7 +666,8 @@ int64_t flat_groups(int64_t rows, int32_t vocab) {
 }
 int64_t run_groups(int64_t rows, int32_t vocab, bool bias) {
   // with dbias few groups of many rows, as each adds a row of partial sums to
-  // the traffic, but enough to fill the chip
+  // the traffic, but enough to fill the chip: the gradient of 4096 x 32,003 bf16
+  // takes 151 us with 1024 groups in all, 166 with 2048, 169 with 768
   const int64_t runs = (vocab + 4095) / 4096;
   const int64_t most = bias ? (kBiasGroups + runs - 1) / runs : 65535;
   return rows < most ? rows : most;
@@ -701,8 +712,8 @@ hipError_t shape(LogitsArgs p, float* dbias, hipStream_t stream) {
   const int64_t w = a.history_width;
   const bool countable = !p.penalties ||
                          (a.history_row == w && w < (1 << 16) &&
-                          tile_rows_of(a.vocab > kTile ? kTile : a.vocab) * w * w < ((int64_t)1 << 32));
-  const bool flat = a.vocab <= kTile && dense && countable;
+                          tile_rows_of(a.vocab < kTile ? a.vocab : kTile) * w * w < ((int64_t)1 << 32));
+  const bool flat = a.vocab <= flat_most(a.dtype) && a.rows > kFewRows && dense && countable;
   if (flat) {
     p.tile_rows = tile_rows_of(a.vocab);
     p.magic_vocab = (uint32_t)((1ull << 32) / (uint32_t)a.vocab + 1);
@@ -753,7 +764,7 @@ bool logits_gradient_reads_logits(const logits_args& a) {
 int64_t logits_workspace_bytes(int64_t rows, int32_t vocab) {
   if (rows == 0 || vocab == 0) return 0;
   int64_t groups = run_groups(rows, vocab, true);
-  if (vocab <= kTile && flat_groups(rows, vocab) > groups)
+  if (vocab <= flat_most(POLICY_BF16) && flat_groups(rows, vocab) > groups)
     groups = flat_groups(rows, vocab);
   return groups * vocab * 4;
 }

@@ -99,6 +99,29 @@ def test_matches_the_formula(rx, R, V, H, mask, name):
     check(rx, *inputs(R, V, H, name, R + V + H, mask), name)
 
 
+@pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("mask", ["none", "bytes", "bits", "shared", "table"])
+@pytest.mark.parametrize("R,V,H", [(512, 45, 20), (513, 45, 20), (1200, 45, 20), (2600, 33, 300), (600, 512, 9),
+                                   (601, 513, 9), (520, 1024, 70), (530, 1025, 4), (9000, 1, 3), (700, 257, 0)])
+def test_many_rows(rx, R, V, H, mask, name):
+    check(rx, *inputs(R, V, H, name, R + V + H, mask), name)
+
+
+def test_many_rows_in_place_and_masked(rx):
+    """Tiles of many rows: written over their own input; what a masked place
+    holds does not matter; each argument left out."""
+    a, allowed = inputs(700, 45, 20, "f32", 12, "bits")
+    c = {k: v.cuda() for k, v in a.items()}
+    want = rx.shape_logits(**c)
+    z = torch.where(torch.from_numpy(allowed).cuda(), c["logits"], float("nan"))
+    out = rx.shape_logits(**dict(c, logits=z), out=z)
+    assert out is z and torch.equal(z, want)
+    for drop in ("bias", "history_len", "repetition", "presence", "frequency", "mask"):
+        check(rx, {k: v for k, v in a.items() if k != drop}, None if drop == "mask" else allowed, "f32")
+    b = dict(a, bias=torch.randn(700, 45))
+    check(rx, b, allowed, "f32")
+
+
 @pytest.mark.parametrize("drop", ["bias", "history_len", "repetition", "presence", "frequency"])
 def test_each_argument_alone(rx, drop):
     a, allowed = inputs(40, 45, 20, "f32", 5, "bits")
@@ -207,7 +230,7 @@ def test_rows_between_the_outputs_are_left_alone(rx):
             assert torch.equal(t[:7, :V], z) and (t[7] == 7).all() and (t[:, V:] == 7).all()
 
 
-@pytest.mark.parametrize("R,V", [(200, 45), (3, 9000)])
+@pytest.mark.parametrize("R,V", [(200, 45), (3, 9000), (2000, 45)])
 def test_captured_training_pass(rx, R, V):
     data = [{k: v.cuda() for k, v in inputs(R, V, 9, "bf16", s, "table")[0].items()} for s in (1, 2, 3)]
     buf = {k: v.clone() for k, v in data[0].items()}
