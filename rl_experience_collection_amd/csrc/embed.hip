@@ -6,7 +6,7 @@
 // pack moved back to the row's end: it repeats elements of the one before
 // with the same values.  (The same goes for the gradient below.)
 //
-// The gradient sums the rows of dout that share an index.  Few indices (512 at
+// The gradient sums the rows of dout that share an index.  Few indices (1024 at
 // most) take one launch: every workgroup owns a few rows of the vocabulary and
 // reads all indices.  More are sorted: a stable radix sort of the positions by
 // index with digits of at most 9 bits, two launches a digit (counts, then
@@ -56,6 +56,9 @@ __device__ __forceinline__ uint32_t key_at(const void* p, int32_t bytes, int64_t
 }
 
 // --------------------------------------------------------------- the lookup
+// Bound by memory: 65,536 of 131,072 rows of 1024 bf16 in 41 us (203 MB, 4.9
+// TB/s), 262,147 of 50,021 rows of 500 fp16 in 72 us (277 MB written as the
+// lines of rows of 1000 bytes, 109 MB read).
 constexpr int kPacks = 4;  // packs per thread
 
 template <class T, int V>
@@ -370,7 +373,9 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(SumArgs a,
 // Clears the rows without an index and joins the partial sums of those that
 // cross pieces.  SPLIT threads share a pack of a row: each adds a run of its
 // partial sums, and the runs are added in order.  One where the vocabulary
-// alone fills the chip, else 8: a small vocabulary has many sums a row.
+// alone fills the chip, else 8: a small vocabulary has many sums a row (the
+// gradient of 64,000 rows into 45 x 128 fp32 takes 23.6 us so, 27.6 with one;
+// that of 262,144 into 8192 x 256 86 us with one, 96 with 8).
 template <class T, int V, int SPLIT>
 __global__ __launch_bounds__(kThreads) void embed_join_kernel(SumArgs a) {
   using raw = typename T::raw;
@@ -422,32 +427,50 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(SumArgs a) {
 }
 
 // ------------------------------------------------------------- few indices
-constexpr int kFewMost = 512;  // indices
+// Indices, at most.  1000 spread over a vocabulary of 45 x 128 fp32 take 5.8 us
+// in this one launch, 15.8 sorted (50,021 x 500 bf16: 28 and 40); 1000 times
+// the same index 28 and 17.5.  2000 take as long either way at 50,021 x 500.
+constexpr int kFewMost = 1024;
+constexpr int kFewRows = 32;    // rows of the vocabulary per workgroup, at most
+constexpr int kFewParts = 8;    // threads that share a pack of a row
+constexpr int kFewPacks = kThreads / kFewParts;  // packs of a row per workgroup
 
-// Rows of the vocabulary per workgroup: one, as long as the grid stays small.
-int32_t few_rows(int64_t vocab) {
-  const int64_t rows = vocab >> 13;
-  return (int32_t)(rows < 1 ? 1 : rows < 32 ? rows : 32);
+// One row per workgroup, as long as the grid stays small.
+int32_t few_rows(int64_t vocab, int64_t chunks) {
+  const int64_t rows = (vocab * chunks) >> 13;
+  return (int32_t)(rows < 1 ? 1 : rows < kFewRows ? rows : kFewRows);
 }
 
-// The named places among this workgroup's rows are listed in LDS in order;
-// each thread takes packs of the rows and adds the places of its row.
+// The places of the indices among this workgroup's rows are listed in LDS, by
+// row and in order.  The rows that have none are cleared.  Of the others one
+// after another is summed: each part takes a run of its places, and the parts
+// are added in order, so that one index repeated is not one thread's work.
 template <class T, int V>
 __global__ __launch_bounds__(kThreads) void embed_few_kernel(EmbedBackward a, int32_t per_row,
                                                              int32_t block_rows, bool past) {
   using raw = typename T::raw;
-  __shared__ uint32_t s_list[kFewMost];  // row << 16 | position
+  __shared__ uint32_t s_list[kFewMost];    // row << 16 | position, in order of position
+  __shared__ uint16_t s_place[kFewMost];   // positions by row
   __shared__ uint32_t s_wave[kThreads / 64];
+  __shared__ uint32_t s_end[kFewRows];     // counts of the rows, then ends of their places
+  __shared__ float s_sum[kFewParts][kFewPacks][V];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int64_t blocks = (a.vocab + block_rows - 1) / block_rows;
+  const int part = tid / kFewPacks, here = tid % kFewPacks;
+  const int32_t count = (int32_t)a.count;
+  const int64_t chunks = (per_row + kFewPacks - 1) / kFewPacks;
+  const int64_t blocks = (a.vocab + block_rows - 1) / block_rows * chunks;
   for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {
-    const int64_t v0 = block * block_rows;
+    const int64_t v0 = block / chunks * block_rows;
     const int32_t rows = (int32_t)min((int64_t)block_rows, a.vocab - v0);
+    const int32_t c0 = (int32_t)(block % chunks) * kFewPacks;
+    const int32_t packs = min(per_row - c0, kFewPacks);
+    if (tid < kFewRows) s_end[tid] = 0u;
+    __syncthreads();
     int32_t n = 0;
-    for (int32_t i0 = 0; i0 < (int32_t)a.count; i0 += kThreads) {
+    for (int32_t i0 = 0; i0 < count; i0 += kThreads) {
       const int32_t i = i0 + tid;
-      const int64_t v = (int64_t)key_at(a.index, a.index_bytes, a.vocab, min(i, (int32_t)a.count - 1)) - v0;
-      const bool mine = i < a.count && v >= 0 && v < rows;
+      const int64_t v = (int64_t)key_at(a.index, a.index_bytes, a.vocab, min(i, count - 1)) - v0;
+      const bool mine = i < count && v >= 0 && v < rows;
       const uint64_t m = __ballot(mine);
       __syncthreads();
       if (lane == 0) s_wave[w] = (uint32_t)__popcll(m);
@@ -457,45 +480,95 @@ __global__ __launch_bounds__(kThreads) void embed_few_kernel(EmbedBackward a, in
         if (j < w) at += s_wave[j];
         n += s_wave[j];
       }
-      if (mine) s_list[at] = (uint32_t)v << 16 | (uint32_t)i;
+      if (mine) {
+        s_list[at] = (uint32_t)v << 16 | (uint32_t)i;
+        atomicAdd(&s_end[v], 1u);
+      }
     }
     __syncthreads();
-    for (int32_t g = tid; g < rows * per_row; g += kThreads) {
-      const int32_t r = g / per_row;
-      const int32_t col = min((g - r * per_row) * V, a.width - V);
-      const raw* dout = static_cast<const raw*>(a.dout) + col;
+    if (n > 0 && w == 0) {
+      // ends of the rows' places; then, 64 entries at a time, each to its row's
+      // next place (s_end counts up from the row's first)
+      const uint32_t mine = lane < kFewRows ? s_end[lane] : 0u;
+      uint32_t end = mine;
+#pragma unroll
+      for (int d = 1; d < kFewRows; d <<= 1) {
+        const uint32_t y = __shfl_up(end, d, 64);
+        if (lane >= d) end += y;
+      }
+      if (lane < kFewRows) s_end[lane] = end - mine;
+      for (int32_t i0 = 0; i0 < n; i0 += 64) {
+        const bool in = i0 + lane < n;
+        const uint32_t e = s_list[min(i0 + lane, n - 1)], row = e >> 16;
+        uint64_t same = __ballot(in);
+#pragma unroll
+        for (int b = 1; b < kFewRows; b <<= 1) {
+          const uint64_t ones = __ballot((row & b) != 0);
+          same &= row & b ? ones : ~ones;
+        }
+        if (!in) continue;
+        const int earlier = __popcll(same & ((1ull << lane) - 1));
+        // every lane of a row reads its cursor before the first of them moves it
+        const uint32_t place = s_end[row] + earlier;
+        if (earlier == 0) s_end[row] = place + __popcll(same);
+        s_place[place] = (uint16_t)e;
+      }
+    }
+    __syncthreads();
+    auto first_of = [&](int32_t r) { return r ? (int32_t)s_end[r - 1] : 0; };
+    for (int32_t g = tid; g < rows * packs; g += kThreads) {
+      const int32_t r = g / packs;
+      if (first_of(r) != (int32_t)s_end[r]) continue;
+      const int32_t col = min((c0 + g - r * packs) * V, a.width - V);
+      const float zero[V] = {};
+      store_pack<T, V>(static_cast<raw*>(a.dweight) + (v0 + r) * a.dweight_row + col,
+                       narrow_pack<T, V>(zero), past);
+    }
+    const int32_t col = min((c0 + min(here, packs - 1)) * V, a.width - V);
+    const raw* dout = static_cast<const raw*>(a.dout) + col;
+    for (int32_t r = 0; r < rows && n > 0; ++r) {
+      const int32_t lo = first_of(r), hi = (int32_t)s_end[r];
+      if (lo == hi) continue;  // (the same for all threads)
+      const int32_t per = (hi - lo + kFewParts - 1) / kFewParts;
+      const int32_t from = min(hi, lo + part * per), to = min(hi, from + per);
       float acc[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-      for (int32_t j0 = 0; j0 < n; j0 += kAhead) {
-        // (other rows' places are loaded too and not added: they are near)
-        uint32_t e[kAhead];
+      for (int32_t j0 = from; j0 < to; j0 += kAhead) {
         Pack<T, V> d[kAhead];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          e[j] = s_list[min(j0 + j, n - 1)];
-          d[j] = load_pack<T, V>(dout + (int64_t)(e[j] & 0xffffu) * a.dout_row);
-        }
+        for (int j = 0; j < kAhead; ++j)
+          d[j] = load_pack<T, V>(dout + (int64_t)s_place[min(j0 + j, to - 1)] * a.dout_row);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-          const bool add = j0 + j < n && (int32_t)(e[j] >> 16) == r;
+          if (j0 + j >= to) break;
           float f[V];
           widen_pack<T, V>(d[j], f);
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[i] += add ? f[i] : 0.0f;
+          for (int i = 0; i < V; ++i) acc[i] += f[i];
         }
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] *= a.scale;
-      store_pack<T, V>(static_cast<raw*>(a.dweight) + (v0 + r) * a.dweight_row + col,
-                       narrow_pack<T, V>(acc), past);
+      for (int i = 0; i < V; ++i) s_sum[part][here][i] = acc[i];
+      __syncthreads();
+      if (part == 0 && here < packs) {
+        for (int j = 1; j < kFewParts; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] += s_sum[j][here][i];
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] *= a.scale;
+        store_pack<T, V>(static_cast<raw*>(a.dweight) + (v0 + r) * a.dweight_row + col,
+                         narrow_pack<T, V>(acc), past);
+      }
+      __syncthreads();
     }
     __syncthreads();
   }
 }
 
 // Entries of the sorted list per piece: about 2^17 threads in all, but pieces
-// long enough that partial sums stay a small part of the traffic.
+// long enough that partial sums stay a small part of the traffic.  (2^16 and
+// 2^18 threads: within 3% at every size tried, 45 x 32 to 131,072 x 1024.)
 int32_t piece_length(int64_t count, int64_t per_row) {
   int64_t piece = (count * per_row) >> 17;
   piece = (piece + 15) / 16 * 16;
@@ -567,8 +640,9 @@ hipError_t backward(const EmbedBackward& a, hipStream_t stream) {
   const int32_t per_row = (a.width + V - 1) / V;
   const bool past = a.vocab * a.width * T::kBytes > kPastBytes;
   if (a.count <= kFewMost) {
-    const int32_t rows = few_rows(a.vocab);
-    hipLaunchKernelGGL((embed_few_kernel<T, V>), dim3(capped((a.vocab + rows - 1) / rows)),
+    const int64_t chunks = (per_row + kFewPacks - 1) / kFewPacks;
+    const int32_t rows = few_rows(a.vocab, chunks);
+    hipLaunchKernelGGL((embed_few_kernel<T, V>), dim3(capped((a.vocab + rows - 1) / rows * chunks)),
                        dim3(kThreads), 0, stream, a, per_row, rows, past);
     return hipGetLastError();
   }
@@ -617,7 +691,9 @@ hipError_t backward(const EmbedBackward& a, hipStream_t stream) {
   s.pieces = (int32_t)((a.count + s.piece - 1) / s.piece);
   s.scale = a.scale;
   s.past = past;
-  // at least half the lanes of a wave have a pack of their own
+  // at least half the lanes of a wave have a pack of their own (262,144 rows of
+  // 1024 bf16 into 512: 143 us so, 148 otherwise; 64,000 of 32 fp32 into 45:
+  // 21.9 and 20.6)
   if (per_row > 32) {
     const int64_t waves = (int64_t)s.pieces * ((per_row + 63) / 64);
     hipLaunchKernelGGL((embed_sum_kernel<T, V, true>), dim3(capped((waves + 3) / 4)), dim3(kThreads), 0,

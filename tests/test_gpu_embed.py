@@ -204,3 +204,18 @@ def test_wide_indices_that_name_no_row(rx):
     check(rx, w, idx, dout, "f32")
     big = idx.repeat(200)
     check(rx, w, big, dout.repeat(200, 1), "f32")
+
+
+@pytest.mark.parametrize("spread", ["even", "skew", "one"])
+@pytest.mark.parametrize("M,V,D", [(1023, 45, 128), (1024, 45, 129), (1025, 45, 128), (1000, 3, 700), (1024, 300000, 9),
+                                   (640, 20000, 300), (900, 33, 1)])
+def test_about_a_thousand_indices(rx, M, V, D, spread):
+    check(rx, *inputs(M, V, D, "f32", M + D, spread), "f32")
+    check(rx, *inputs(M, V, D, "bf16", M + D, spread, out_of_range=0.0), "bf16")
+
+
+def test_indices_of_neighbouring_rows(rx):
+    """All of them within the rows that one workgroup owns, in mixed order."""
+    w, idx, dout = inputs(1024, 270000, 40, "f32", 4)
+    idx = torch.randint(5 * 32 - 3, 6 * 32 + 3, (1024,), generator=torch.Generator().manual_seed(5)).int()
+    check(rx, w, idx, dout, "f32")
