@@ -24,9 +24,9 @@ def sigmoid(g):
 
 
 # Roundings of one step, each at most u of the step's magnitudes: the
-# sigmoid (its exponent's two-part product 2, exp2 2, 1 + E 1, reciprocal 2,
-# product 1) 8, b's product 1, the fused multiply-add 1; the map's slope takes
-# the same 8 and a product; joining the maps of slots, tiles and chunks adds
+# sigmoid (its exponent's product and what it rounds off 2, exp2 2, 1 + E 1,
+# reciprocal 2, product 1) 8, b's product 1, the fused multiply-add 1; the map's
+# slope takes the same 8 and a product; joining the maps of slots and tiles adds
 # at most 2 per 8 steps.  12 covers a step.
 STEP = 12
 

@@ -73,6 +73,14 @@ def test_matches_the_formula(rx, L, N, D, sig, name):
     check(rx, inputs(L, N, D, name, sig, 0.05, L * 31 + D), name, sig)
 
 
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("sig", [False, True])
+@pytest.mark.parametrize("L,N,D", [(128, 2, 5), (130, 2, 5), (256, 1, 9), (257, 1, 9), (385, 3, 33), (20, 256, 128),
+                                   (300, 129, 63)])
+def test_borders_of_the_tiles(rx, L, N, D, sig, name):
+    check(rx, inputs(L, N, D, name, sig, 0.02, L + D), name, sig)
+
+
 @pytest.mark.parametrize("p_done", [0.0, 0.5, 1.0])
 @pytest.mark.parametrize("L,N,D", [(70, 3, 10), (1100, 2, 6)])
 def test_dones(rx, L, N, D, p_done):
