@@ -40,6 +40,10 @@ constexpr int kTileGroups = 256 * kTileWaves;
 // (96 registers: the 4096 x 32003 training pass takes 344 us, 359 us at the
 // compiler's 104, 492 us at 80, where it spills)
 constexpr int kRunWaves = 5;
+// Workgroups of a launch over runs, about: four times what is resident, so that
+// a bias is loaded once for many rows.  4096 x 32,003 bf16 forward takes 110 us
+// so, 124 with a workgroup a row; 32,768 x 4000 98 and 123.
+constexpr int kRunGroups = 5120;
 constexpr int kBiasGroups = 1024;  // about, of runs in all, with dbias
 constexpr float kBanned = -__builtin_inff();
 
@@ -489,6 +493,28 @@ __global__ __launch_bounds__(kThreads, kRunWaves) void logits_runs_kernel(Logits
   const int32_t rest = a.vocab - c0;
   // the running sums of dbias of the thread's columns
   float col[kRunPacks][V] = {};
+  // their bias, as loaded; one that all rows share is loaded once
+  constexpr int B = V < 4 ? V : 4;  // elements of an access
+  Pack<F32, B> bias[GRAD ? 1 : kRunPacks][V / B];
+  auto load_bias = [&](int64_t r) {
+    const uint32_t* b = reinterpret_cast<const uint32_t*>(a.bias) + r * a.bias_row + c0;
+#pragma unroll
+    for (int k = 0; k < kRunPacks; ++k)
+#pragma unroll
+      for (int j = 0; j < V / B; ++j)
+        bias[GRAD ? 0 : k][j] = load_inside<F32, B>(b, (k * kThreads + tid) * V + j * B, rest);
+  };
+  auto settle_bias = [&]() {
+#pragma unroll
+    for (int k = 0; k < kRunPacks; ++k)
+#pragma unroll
+      for (int j = 0; j < V / B; ++j)
+        settle<F32, B>(bias[GRAD ? 0 : k][j], (k * kThreads + tid) * V + j * B, rest);
+  };
+  if (!GRAD && a.bias && !a.bias_row) {
+    load_bias(0);
+    settle_bias();
+  }
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
     const raw* in = GRAD ? static_cast<const raw*>(p.dout) + r * p.dout_row + c0
                          : static_cast<const raw*>(a.logits) + r * a.logits_row + c0;
@@ -514,16 +540,7 @@ __global__ __launch_bounds__(kThreads, kRunWaves) void logits_runs_kernel(Logits
 #pragma unroll
     for (int k = 0; k < kRunPacks; ++k)
       x[k] = load_inside<T, V>(in, (k * kThreads + tid) * V, rest);
-    constexpr int B = V < 4 ? V : 4;  // bias elements of an access
-    Pack<F32, B> bias[GRAD ? 1 : kRunPacks][V / B];
-    if (!GRAD && a.bias) {
-      const uint32_t* b = reinterpret_cast<const uint32_t*>(a.bias) + r * a.bias_row + c0;
-#pragma unroll
-      for (int k = 0; k < kRunPacks; ++k)
-#pragma unroll
-        for (int j = 0; j < V / B; ++j)
-          bias[GRAD ? 0 : k][j] = load_inside<F32, B>(b, (k * kThreads + tid) * V + j * B, rest);
-    }
+    if (!GRAD && a.bias && a.bias_row) load_bias(r);
     uint64_t mraw[kRunPacks] = {};
     bool free_row = true;  // everything is allowed
     if (MASK != LOGITS_MASK_NONE) {
@@ -568,6 +585,7 @@ __global__ __launch_bounds__(kThreads, kRunWaves) void logits_runs_kernel(Logits
       }
       __syncthreads();
     }
+    if (!GRAD && a.bias && a.bias_row) settle_bias();
 #pragma unroll
     for (int k = 0; k < kRunPacks; ++k) {
       const int32_t e = (k * kThreads + tid) * V;
@@ -601,8 +619,7 @@ __global__ __launch_bounds__(kThreads, kRunWaves) void logits_runs_kernel(Logits
       if (!GRAD && a.bias) {
 #pragma unroll
         for (int j = 0; j < V / B; ++j) {
-          Pack<F32, B>& b = bias[GRAD ? 0 : k][j];
-          settle<F32, B>(b, e + j * B, rest);
+          const Pack<F32, B>& b = bias[GRAD ? 0 : k][j];
 #pragma unroll
           for (int i = 0; i < B; ++i) f[j * B + i] += F32::widen(b.v[i]);
         }
@@ -646,12 +663,12 @@ __global__ __launch_bounds__(1024) void bias_join_kernel(const float* partial, i
 
 // The longest rows taken several at a time, a quarter of a run of columns.
 // 32,768 rows of bf16 with a history of 64 (forward, gradient): 63 and 78 us at
-// 900 logits, as runs 75 and 89; at 1100 115 and 137, as runs 77 and 87.  fp32:
-// 36 and 47 us at 500, as runs 50 and 68; at 700 62 and 90, as runs 52 and 85.
+// 900 logits, as runs 67 and 88; at 1100 115 and 137, as runs 65 and 85.  fp32:
+// 36 and 47 us at 500, as runs 44 and 66; at 700 62 and 90, as runs 45 and 82.
 int32_t flat_most(int32_t dtype) { return dtype == POLICY_F32 ? 512 : 1024; }
 // As many rows are taken one at a time whatever their length, which spreads
 // them over more of the chip: 512 rows of 45 fp32 logits take 4.2 and 7.4 us so,
-// 7.9 and 9.9 as tiles; 2048 take 6.0 and 13.9, 8.0 and 10.4 as tiles.
+// 7.9 and 9.9 as tiles; 8192 take 14 and 21, 8.3 and 11 as tiles.
 constexpr int64_t kFewRows = 512;
 
 // Rows of a tile of whole rows.
@@ -669,7 +686,7 @@ int64_t run_groups(int64_t rows, int32_t vocab, bool bias) {
   // the traffic, but enough to fill the chip: the gradient of 4096 x 32,003 bf16
   // takes 151 us with 1024 groups in all, 166 with 2048, 169 with 768
   const int64_t runs = (vocab + 4095) / 4096;
-  const int64_t most = bias ? (kBiasGroups + runs - 1) / runs : 65535;
+  const int64_t most = ((bias ? kBiasGroups : kRunGroups) + runs - 1) / runs;
   return rows < most ? rows : most;
 }
 
