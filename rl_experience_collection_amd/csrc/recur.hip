@@ -9,7 +9,7 @@
 // so that the map then selects B instead of multiplying a possibly infinite
 // or NaN state by zero.
 //
-// A workgroup of 8 (chained: 16) waves owns a column of 64 lanes x V channels and
+// A workgroup of W waves (8, or 16 where it is alone on its compute unit) owns a column of 64 lanes x V channels and
 // takes time in tiles, one slot of S steps per wave.  A wave loads its slot
 // into registers, folds it into its map, and leaves the map in LDS; after one
 // barrier every wave folds the maps before its own onto the state that enters
@@ -44,12 +44,10 @@ namespace rl {
 
 namespace {
 
-// Waves of a workgroup and steps per wave and tile (a slot's values stay in
-// registers).  A chained tile is as long as a workgroup's registers allow: each
+// Steps per wave and tile (a slot's values stay in registers).  A chained tile is as long as a workgroup's registers allow: each
 // costs a walk, and the walks of a column follow each other.  Backward, lanes
 // of two channels take 4 steps: a 1024 x 500 x 64 bf16 pass 98 us against 110
 // with 8, 4096 x 64 x 128 fp32 169 against 183; lanes of one or four 8.
-constexpr int waves_of(bool chained) { return chained ? 16 : 8; }
 constexpr int slot_steps(int v, bool back, bool chained) {
   return chained ? (back ? 8 : 16) : back && v == 2 ? 4 : 8;
 }
@@ -421,12 +419,12 @@ __device__ __forceinline__ void fold_forward(const float (&a)[S][V], const float
 
 // Bound by memory where the columns fill the chip: 500 x 8192 x 64 bf16 in 320
 // us (1.58 GB at 4.9 TB/s), 500 x 128 x 128 fp32, whose 256 columns give each
-// compute unit one workgroup, in 28 (98 MB at 3.6 TB/s).  Chained, by the states'
+// compute unit one workgroup, in FWD1.  Chained, by the states'
 // way from tile to tile: 65,537 x 2 x 1000 fp16 in 260 us (786 MB at 3.0 TB/s).
-template <class T, int V, bool SIG, bool CHAIN, bool OFF32>
-__global__ __launch_bounds__(64 * waves_of(CHAIN)) void recur_forward_kernel(const RecurArgs p) {
+template <class T, int V, bool SIG, bool CHAIN, bool OFF32, int W>
+__global__ __launch_bounds__(64 * W) void recur_forward_kernel(const RecurArgs p) {
   using raw = typename T::raw;
-  constexpr int W = waves_of(CHAIN), S = slot_steps(V, false, CHAIN), kTile = S * W;
+  constexpr int S = slot_steps(V, false, CHAIN), kTile = S * W;
   __shared__ typename std::conditional<CHAIN, ChainLds<V>, char>::type s_chain;
   constexpr int kBufs = CHAIN ? 1 : 2;
   __shared__ alignas(16) float s_a[kBufs][W][64][V], s_b[kBufs][W][64][V];
@@ -572,11 +570,11 @@ __device__ __forceinline__ void fold_backward(const float (&a)[S][V], const floa
 }
 
 // Bound like the forward pass: 500 x 8192 x 64 bf16 in 638 us (3.15 GB at 4.9
-// TB/s), 500 x 128 x 128 fp32 with linear gates in 40 (164 MB at 4.1 TB/s).
-template <class T, int V, bool SIG, bool CHAIN, bool OFF32>
-__global__ __launch_bounds__(64 * waves_of(CHAIN)) void recur_backward_kernel(const RecurArgs p) {
+// TB/s), 500 x 128 x 128 fp32 with linear gates in BWD1.
+template <class T, int V, bool SIG, bool CHAIN, bool OFF32, int W>
+__global__ __launch_bounds__(64 * W) void recur_backward_kernel(const RecurArgs p) {
   using raw = typename T::raw;
-  constexpr int W = waves_of(CHAIN), S = slot_steps(V, true, CHAIN), kTile = S * W;
+  constexpr int S = slot_steps(V, true, CHAIN), kTile = S * W;
   __shared__ typename std::conditional<CHAIN, ChainLds<V>, char>::type s_chain;
   constexpr int kBufs = CHAIN ? 1 : 2;
   __shared__ alignas(16) float s_a[kBufs][W][64][V], s_b[kBufs][W][64][V];
@@ -787,6 +785,14 @@ __global__ __launch_bounds__(256) void empty_chain_kernel(uint32_t* ticket, uint
 // take 164 us so, chained 103; 256 take 182, chained 210.
 constexpr int64_t kWantColumns = 256;
 
+// Waves of a workgroup that has a compute unit to itself.  (Lanes of 8 bytes
+// have enough loads on their way from 8: 500 x 256 x 128 fp32 takes 35 + 77 us
+// so, 37 + 82 from 16.  Lanes of 4: 8192 x 128 x 256 bf16 369 + 749 us from 8,
+// 339 + 647 from 16; with more workgroups, 500 x 200 x 128 fp32, 30 + 67 and
+// 38 + 69; within a tile of 8 waves, 30 x 128 x 128 fp32, 5.0 + 6.8 and 6.8 +
+// 8.4.)
+constexpr int kManyWaves = 16, kFewWaves = 8;
+
 int64_t per_row_of(int32_t D, int v) { return (D + v - 1) / v; }
 
 // Channels of a lane: as many as leave the launch enough columns.  4096 x 256 x
@@ -802,7 +808,7 @@ int lane_channels(int32_t N, int32_t D, int32_t dtype) {
 // the whole time.  400 x 4 x 128 fp32 forward: 12.6 us as two tiles, 16.2 in one
 // workgroup's walk.
 int32_t chained_tiles(int32_t L, int64_t units, bool back) {
-  const int32_t tile = waves_of(true) * slot_steps(1, back, true);
+  const int32_t tile = kManyWaves * slot_steps(1, back, true);
   const int64_t columns = (units + 63) / 64;
   return columns >= kWantColumns || L <= tile ? 0 : (L + tile - 1) / tile;
 }
@@ -810,6 +816,15 @@ int32_t chained_tiles(int32_t L, int64_t units, bool back) {
 constexpr size_t kTicketBytes = 256;
 int64_t chained_bytes(int32_t tiles, int64_t units, int v) {
   return tiles ? (int64_t)kTicketBytes + tiles * units * v * 8 : 0;
+}
+
+template <class T, int V, bool SIG, bool BACK, bool CHAIN, bool OFF32, int W>
+hipError_t start(const RecurArgs& p, dim3 grid, hipStream_t stream) {
+  if constexpr (BACK)
+    hipLaunchKernelGGL((recur_backward_kernel<T, V, SIG, CHAIN, OFF32, W>), grid, dim3(64 * W), 0, stream, p);
+  else
+    hipLaunchKernelGGL((recur_forward_kernel<T, V, SIG, CHAIN, OFF32, W>), grid, dim3(64 * W), 0, stream, p);
+  return hipGetLastError();
 }
 
 template <class T, int V, bool SIG, bool BACK, bool OFF32>
@@ -827,19 +842,14 @@ hipError_t launch(RecurArgs p, void* workspace, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     p.tiles = (uint32_t)tiles * (uint32_t)p.columns;
-    const dim3 grid(p.tiles < (1u << 21) ? p.tiles : 1u << 21), threads(64 * waves_of(true));
-    if constexpr (BACK)
-      hipLaunchKernelGGL((recur_backward_kernel<T, V, SIG, true, OFF32>), grid, threads, 0, stream, p);
-    else
-      hipLaunchKernelGGL((recur_forward_kernel<T, V, SIG, true, OFF32>), grid, threads, 0, stream, p);
-    return hipGetLastError();
+    const dim3 grid(p.tiles < (1u << 21) ? p.tiles : 1u << 21);
+    return start<T, V, SIG, BACK, true, OFF32, kManyWaves>(p, grid, stream);
   }
-  const dim3 grid((unsigned)p.columns), threads(64 * waves_of(false));
-  if constexpr (BACK)
-    hipLaunchKernelGGL((recur_backward_kernel<T, V, SIG, false, OFF32>), grid, threads, 0, stream, p);
-  else
-    hipLaunchKernelGGL((recur_forward_kernel<T, V, SIG, false, OFF32>), grid, threads, 0, stream, p);
-  return hipGetLastError();
+  const dim3 grid((unsigned)p.columns);
+  if constexpr (V * T::kBytes <= 4)
+    if (p.columns <= kWantColumns && p.L > kFewWaves * slot_steps(V, BACK, false))
+      return start<T, V, SIG, BACK, false, OFF32, kManyWaves>(p, grid, stream);
+  return start<T, V, SIG, BACK, false, OFF32, kFewWaves>(p, grid, stream);
 }
 
 template <class T, bool SIG, bool BACK>
