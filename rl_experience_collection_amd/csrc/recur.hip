@@ -417,9 +417,9 @@ __device__ __forceinline__ void fold_forward(const float (&a)[S][V], const float
   for (int v = 0; v < V; ++v) m[v].a = stored_slope(m[v].a, CUT && done != 0);
 }
 
-// Bound by memory where the columns fill the chip: 500 x 8192 x 64 bf16 in 320
-// us (1.58 GB at 4.9 TB/s), 500 x 128 x 128 fp32, whose 256 columns give each
-// compute unit one workgroup, in FWD1.  Chained, by the states'
+// Bound by memory where the columns fill the chip: 500 x 8192 x 64 bf16 in 318
+// us (1.58 GB at 5.0 TB/s); 500 x 128 x 128 fp32, whose 256 columns give each
+// compute unit one workgroup, in 25 (98 MB at 3.9 TB/s).  Chained, by the states'
 // way from tile to tile: 65,537 x 2 x 1000 fp16 in 260 us (786 MB at 3.0 TB/s).
 template <class T, int V, bool SIG, bool CHAIN, bool OFF32, int W>
 __global__ __launch_bounds__(64 * W) void recur_forward_kernel(const RecurArgs p) {
@@ -569,8 +569,8 @@ __device__ __forceinline__ void fold_backward(const float (&a)[S][V], const floa
   for (int v = 0; v < V; ++v) m[v].a = stored_slope(m[v].a, CUT && done != 0);
 }
 
-// Bound like the forward pass: 500 x 8192 x 64 bf16 in 638 us (3.15 GB at 4.9
-// TB/s), 500 x 128 x 128 fp32 with linear gates in BWD1.
+// Bound like the forward pass: 500 x 8192 x 64 bf16 in 641 us (3.15 GB at 4.9
+// TB/s), 500 x 128 x 128 fp32 with linear gates in 36 (164 MB at 4.5 TB/s).
 template <class T, int V, bool SIG, bool CHAIN, bool OFF32, int W>
 __global__ __launch_bounds__(64 * W) void recur_backward_kernel(const RecurArgs p) {
   using raw = typename T::raw;

@@ -114,6 +114,23 @@ def _here(name, *tensors):
     return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream().cuda_stream
 
 
+def _there(t):
+    """The stream of a backward pass: it runs on the device of its gradients,
+    where the forward call's tensors are known to live."""
+    return _raw_stream(t.get_device()) if _raw_stream else torch.cuda.current_stream().cuda_stream
+
+
+def _first_order(backward):
+    """A backward pass whose results have no gradient.  torch's own guard for
+    that costs a third of a small pass's time on the host, and is needed only
+    where a graph over the gradients is asked for."""
+    guarded = torch.autograd.function.once_differentiable(backward)
+
+    def run(ctx, *grads):
+        return (guarded if torch.is_grad_enabled() else backward)(ctx, *grads)
+    return staticmethod(run)
+
+
 def _element(name, t):
     if t.dtype not in _DTYPES:
         raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
@@ -196,7 +213,7 @@ def _recur_forward(x, gate, h0, dones, form):
 
 def _recur_backward(x, gate, h, h0, dones, dh, dh_last, form, want_dh0):
     L, N, D = gate.shape
-    lib, stream = _lib(), _here("recurrence", x, gate, h, h0, dones, dh, dh_last)
+    lib, stream = _lib(), _there(dh)
     dx, dgate = _like(h), _like(gate)
     dh0 = torch.empty((N, D), dtype=torch.float32, device=gate.device) if want_dh0 else None
     dt = _DTYPES[gate.dtype]
@@ -219,8 +236,7 @@ class _Recurrence(torch.autograd.Function):
         ctx.set_materialize_grads(False)
         return h, last
 
-    @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_first_order
     def backward(ctx, dh, dh_last):
         x, gate, h, h0, dones = ctx.saved_tensors
         if dh is None and dh_last is None:
@@ -302,22 +318,22 @@ class _Embed(torch.autograd.Function):
     @staticmethod
     def forward(ctx, weight, index, scale):
         ctx.save_for_backward(index)
-        ctx.vocab, ctx.scale = weight.shape[0], scale
+        V, D = weight.shape
+        dt, count = _DTYPES[weight.dtype], index.numel()
+        ctx.sizes = V, D, dt, count, scale, _lib().embed_workspace(dt, V, D, count)
         return _embed_forward(weight, index, scale)
 
-    @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_first_order
     def backward(ctx, dout):
         index, = ctx.saved_tensors
-        V, D, count = ctx.vocab, dout.shape[-1], index.numel()
-        lib, stream = _lib(), _here("embed", dout, index)
-        dout = dout.contiguous()
-        dweight = torch.empty((V, D), dtype=dout.dtype, device=dout.device)
-        dt = _DTYPES[dout.dtype]
-        size = lib.embed_workspace(dt, V, D, count)
+        V, D, dt, count, scale, size = ctx.sizes
+        if not dout.is_contiguous():
+            dout = dout.contiguous()
+        dweight = dout.new_empty((V, D))
         ws = _workspace(dout, size)
-        _call(lib.embed_backward, dt, _ptr(dout), D, _ptr(index), _INDEX_BYTES[index.dtype], count,
-              V, D, ctx.scale, _ptr(dweight), D, _ptr(ws), size, stream)
+        _call(_lib().embed_backward, dt, dout.data_ptr(), D, index.data_ptr(),
+              _INDEX_BYTES[index.dtype], count, V, D, scale, dweight.data_ptr(), D, _ptr(ws), size,
+              _there(dout))
         return dweight, None, None
 
 
@@ -390,11 +406,10 @@ class _ShapeLogits(torch.autograd.Function):
                               rep if ctx.repetition is None else None)
         return out
 
-    @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_first_order
     def backward(ctx, dout):
         logits, history, history_len, mask, mask_rows, rep = ctx.saved_tensors
-        lib, stream = _lib(), _here("shape_logits", dout, logits, mask)
+        lib, stream = _lib(), _there(dout)
         V = dout.shape[-1]
         dout = dout.contiguous()
         a = _logits_args(dout if logits is None else logits, None, history, history_len,
