@@ -366,6 +366,26 @@ def test_far_offsets(rx):
         del one
 
 
+def test_far_offsets_backward(rx):
+    N, L, D = 2, 4_400_000, 512
+    x, gate, dh = (torch.empty(N, L, D, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    for n in range(N):
+        for lo in range(0, L, 1_100_000):
+            x[n, lo:lo + 1_100_000].normal_()
+            gate[n, lo:lo + 1_100_000].normal_(2.0)
+            dh[n, lo:lo + 1_100_000].normal_()
+    leaves = [t.transpose(0, 1).requires_grad_() for t in (x, gate)]
+    h, _ = rx.recurrence(*leaves)
+    dx, dg = torch.autograd.grad(h, leaves, dh.transpose(0, 1))
+    del h
+    for n in range(N):
+        one = [t[n][:, None].detach().requires_grad_() for t in (x, gate)]
+        h, _ = rx.recurrence(*one)
+        for whole, own in zip((dx, dg), torch.autograd.grad(h, one, dh[n][:, None])):
+            for lo in range(0, L, 1_100_000):
+                assert torch.equal(own[lo:lo + 1_100_000, 0], whole[lo:lo + 1_100_000, n])
+
+
 def test_tensors_elsewhere_are_refused(rx):
     x = torch.zeros(3, 2, 4)
     with pytest.raises(ValueError, match="device"):
