@@ -32,9 +32,10 @@
 //
 // Linear gates may be larger than 1, and a product of them infinite where the
 // states are not (those of a padded row are zero).  A slot whose slope is no
-// finite number is not folded: its workgroup takes that tile's slots one after
-// another, step by step; a chained tile whose slope is none publishes no map,
-// only the state that leaves it.
+// finite number for a channel has no map there: its wave runs it step by step on
+// the state that enters it, once the slots before have passed.  A chained tile
+// publishes no map of such a channel, only the state that leaves it.  Other
+// channels and episodes keep their results to the bit.
 #include <type_traits>
 
 #include "elem.hpp"
@@ -201,18 +202,28 @@ __device__ __forceinline__ int32_t poll_chain(const uint64_t* sample, int64_t st
 }
 
 // The state that enters tile `o` (in the order of the scan), for every wave:
-// `c` is the state that enters the scan and becomes that.  `wild`: a slot's
-// slope is no finite number.  Wave 0 learns whether it has to publish the state
-// that leaves the tile itself, later: a tile with an infinite slope has no map.
+// `c` is the state that enters the scan and becomes that.  Wave 0 learns whether
+// it has to publish the state that leaves the tile itself, later, for some
+// channel: one with a slope that is no finite number (`wild`: of a slot).
 template <bool SIG, int V, int W>
-__device__ __forceinline__ bool enter_tile(const RecurArgs& p, int32_t o, int32_t u, bool active, int w,
-                                           int lane, bool wild, const float (&sa)[W][64][V],
-                                           const float (&sb)[W][64][V], ChainLds<V>& s,
-                                           float (&c)[V]) {
+__device__ __forceinline__ bool enter_tile(const RecurArgs& p, int32_t o, int32_t u, bool active,
+                                               int w, int lane, bool wild,
+                                               const float (&sa)[W][64][V],
+                                               const float (&sb)[W][64][V], ChainLds<V>& s,
+                                               float (&c)[V]) {
   const int64_t stride = (int64_t)p.units * V;  // words of a tile
   uint64_t* mine = p.words + o * stride + (int64_t)u * V;
   Map t[V];
   bool held = false;
+  // (a slot's own slope too: one before a done does not show in the tile's)
+  auto without_map = [&](float a, int v) {
+    bool none = is_wild(a);
+    if (wild) {
+#pragma unroll 1
+      for (int j = 0; j < W; ++j) none = none || is_wild(sa[j][lane][v]);
+    }
+    return none;
+  };
   if (w == 0) {
     // the tile's map
 #pragma unroll
@@ -221,15 +232,16 @@ __device__ __forceinline__ bool enter_tile(const RecurArgs& p, int32_t o, int32_
     for (int j = 1; j < W; ++j)
 #pragma unroll
       for (int v = 0; v < V; ++v) t[v] = chain(t[v], Map{sa[j][lane][v], sb[j][lane][v]});
-    if constexpr (!SIG) {
+    if (!SIG) {
       bool any = wild;
 #pragma unroll
       for (int v = 0; v < V; ++v) any = any || is_wild(t[v].a);
       held = __ballot(any) != 0;
     }
-    if (o > 0 && active && !held) {
+    if (o > 0 && active) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) put_map(mine + v, t[v]);
+      for (int v = 0; v < V; ++v)
+        if (!held || !without_map(t[v].a, v)) put_map(mine + v, t[v]);
     }
   }
   if (o > 0) {
@@ -282,22 +294,24 @@ __device__ __forceinline__ bool enter_tile(const RecurArgs& p, int32_t o, int32_
 #pragma unroll
     for (int v = 0; v < V; ++v) c[v] = s.state[lane][v];
   }
-  if (w == 0 && active && !held) {
+  if (w == 0 && active) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (o == 0 || !is_reset(t[v].a)) put_map(mine + v, Map{kReset, apply(t[v], c[v])});
+      if ((o == 0 || !is_reset(t[v].a)) && (!held || !without_map(t[v].a, v)))
+        put_map(mine + v, Map{kReset, apply(t[v], c[v])});
   }
   return held;
 }
 
-// The state that leaves tile `o`, for those after it (wave 0).
+// The state that leaves tile `o`, where wave 0 has published nothing yet.
 template <int V>
-__device__ __forceinline__ void put_state(const RecurArgs& p, int32_t o, int32_t u, bool active,
-                                          const float (&c)[V]) {
+__device__ __forceinline__ void put_held(const RecurArgs& p, int32_t o, int32_t u, bool active,
+                                         const float (&c)[V]) {
   if (!active) return;
   uint64_t* mine = p.words + (o * (int64_t)p.units + u) * V;
 #pragma unroll
-  for (int v = 0; v < V; ++v) put_map(mine + v, Map{kReset, c[v]});
+  for (int v = 0; v < V; ++v)
+    if (__float_as_uint(get_map(mine + v).a) == kNothing) put_map(mine + v, Map{kReset, c[v]});
 }
 
 // Joins the tile's slots: `c` is the state that enters the tile, and then the
@@ -330,23 +344,29 @@ __device__ __forceinline__ void join_slots(const float (&sa)[W][64][V], const fl
   }
 }
 
-// The same where a slot has no map: one after another each wave runs its slot
-// on the state and hands it on.
+// The same where some channel's slots have no maps: one after another each wave
+// runs its slot on the state that enters it (run: h -> the state that leaves),
+// for those channels, and leaves the result in the place of the map's b.
 template <int V, int W, class Run>
-__device__ __forceinline__ void join_wild(float (&hand)[64][V], int w, int lane, float (&c)[V],
-                                          float (&h)[V], Run run) {
+__device__ __forceinline__ void join_wild(const float (&sa)[W][64][V], float (&sb)[W][64][V], int w,
+                                          int lane, float (&c)[V], float (&h)[V], Run run) {
+#pragma unroll 1
   for (int j = 0; j < W; ++j) {
     if (j == w) {
+      float step[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = c[v];
-      run(c);
+      for (int v = 0; v < V; ++v) h[v] = step[v] = c[v];
+      run(step);
 #pragma unroll
-      for (int v = 0; v < V; ++v) hand[lane][v] = c[v];
+      for (int v = 0; v < V; ++v)
+        if (is_wild(sa[j][lane][v])) sb[j][lane][v] = step[v];
     }
     __syncthreads();
 #pragma unroll
-    for (int v = 0; v < V; ++v) c[v] = hand[lane][v];
-    __syncthreads();
+    for (int v = 0; v < V; ++v) {
+      const Map m = Map{sa[j][lane][v], sb[j][lane][v]};
+      c[v] = is_wild(m.a) ? m.b : apply(m, c[v]);
+    }
   }
 }
 
@@ -512,7 +532,7 @@ __global__ __launch_bounds__(64 * W) void recur_forward_kernel(const RecurArgs p
                                      s_chain, c);
       float h[V];
       if (wild) {
-        join_wild<V, W>(s_a[buf][0], w, lane, c, h, [&](float (&s)[V]) {
+        join_wild<V, W>(s_a[buf], s_b[buf], w, lane, c, h, [&](float (&s)[V]) {
 #pragma unroll
           for (int i = 0; i < S; ++i)
 #pragma unroll
@@ -523,7 +543,7 @@ __global__ __launch_bounds__(64 * W) void recur_forward_kernel(const RecurArgs p
         join_slots<V, W>(s_a[buf], s_b[buf], cuts, w, lane, c, h);
       }
       if constexpr (CHAIN && !SIG) {
-        if (held) put_state<V>(p, tile.order, at.u, at.active, c);
+        if (held) put_held<V>(p, tile.order, at.u, at.active, c);
       }
       auto replay = [&](auto cuts_here) {
 #pragma unroll
@@ -669,7 +689,7 @@ __global__ __launch_bounds__(64 * W) void recur_backward_kernel(const RecurArgs 
                                      s_chain, c);
       float G[V];
       if (wild) {
-        join_wild<V, W>(s_a[buf][0], w, lane, c, G, [&](float (&s)[V]) {
+        join_wild<V, W>(s_a[buf], s_b[buf], w, lane, c, G, [&](float (&s)[V]) {
 #pragma unroll
           for (int i = 0; i < S; ++i)
 #pragma unroll
@@ -680,7 +700,7 @@ __global__ __launch_bounds__(64 * W) void recur_backward_kernel(const RecurArgs 
         join_slots<V, W>(s_a[buf], s_b[buf], cuts, w, lane, c, G);
       }
       if constexpr (CHAIN && !SIG) {
-        if (held) put_state<V>(p, tile.order, at.u, at.active, c);
+        if (held) put_held<V>(p, tile.order, at.u, at.active, c);
       }
       auto replay = [&](auto cuts_here) {
 #pragma unroll

@@ -221,6 +221,36 @@ def test_a_gate_that_is_not_a_number_reaches_its_channel_only(rx):
     assert torch.equal(h, hb)
 
 
+@pytest.mark.parametrize("L", [40, 1300])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 3e38])
+def test_a_linear_gate_that_overflows_reaches_its_channel_only(rx, L, bad):
+    """Three gates of one channel in a row, then a done: the other channels and
+    the episodes behind the done keep their bits, gradients included."""
+    i = inputs(L, 2, 70, "f32", False, 0.0, 20)
+    i["dones"] = torch.zeros(L, 2, dtype=torch.uint8)
+    i["dones"][20, 1] = 1
+    c = {k: v.cuda() for k, v in i.items()}
+
+    def run(gate):
+        leaves = [c["x"].clone().requires_grad_(), gate.clone().requires_grad_(),
+                  c["h0"].clone().requires_grad_()]
+        out = rx.recurrence(*leaves, c["dones"], form="linear")
+        return list(out) + list(torch.autograd.grad(out, leaves, (c["dh"], c["dl"])))
+
+    clean = run(c["gate"])
+    gate = c["gate"].clone()
+    gate[12:15, 1, 2] = bad
+    got = run(gate)
+    assert not torch.isfinite(got[0][14:21, 1, 2]).any()
+    for t in (got, clean):
+        t[0][12:21, 1, 2] = 0  # h
+        t[2][:15, 1, 2] = 0    # dx
+        t[3][:21, 1, 2] = 0    # dgate
+        t[4][1, 2] = 0         # dh0
+    for a, b in zip(got, clean):
+        assert torch.equal(a, b)
+
+
 def test_cut_rollouts_compose(rx):
     i = inputs(300, 4, 6, "f32", True, 0.05, 14)
     c = {k: v.cuda() for k, v in i.items()}
