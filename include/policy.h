@@ -72,8 +72,11 @@ typedef struct {
  *   d_t = dh_t + G_{t+1},   G_t = a_t m_t d_t,   dh0 = G_0,
  *   RECUR_LINEAR   dx_t = d_t,            dgate_t = d_t m_t h_{t-1}
  *   RECUR_SIGMOID  dx_t = (1 - a_t) d_t,  dgate_t = a_t (1 - a_t) d_t (m_t h_{t-1} - x_t)
- * h is the forward call's output (in its dtype).  x is read only in the
- * sigmoid form. */
+ * h is the forward call's output, read in fp32 and in the linear form; the
+ * sigmoid form of the 16-bit types takes the states in fp32 instead (`kept`
+ * below), because a state that follows its input makes h_{t-1} - x_t a
+ * difference of near numbers, which a rounded h would leave few digits of.
+ * x is read only in the sigmoid form. */
 typedef struct {
   int32_t steps, rows, width;
   int32_t dtype;
@@ -86,7 +89,7 @@ typedef struct {
   int64_t dgate_step, dgate_row;
   const void *x; /* may be NULL in the linear form */
   const void *gate;
-  const void *h;
+  const void *h; /* may be NULL in the sigmoid form of the 16-bit types */
   const float *h0;      /* NULL: zero */
   const uint8_t *dones; /* NULL: none */
   const void *dh;
@@ -99,8 +102,10 @@ typedef struct {
 } recur_grad_args;
 
 /* Workspace in bytes of recur_forward and of recur_backward for these sizes
- * (the same for both; 0 for most), or a negative ROLLOUT_E* code. */
+ * (the same for both; 0 for most in fp32), or a negative ROLLOUT_E* code. */
 int64_t recur_workspace(int32_t steps, int32_t rows, int32_t width, int32_t dtype);
+/* The same of recur_forward_kept and recur_backward_kept. */
+int64_t recur_kept_workspace(int32_t steps, int32_t rows, int32_t width, int32_t dtype);
 
 /* L, N or D of 0 is a no-op, except that L = 0 copies h0 to h_last (and
  * dh_last to dh0).  Errors: ROLLOUT_EINVAL (NULL or misaligned buffer,
@@ -108,6 +113,14 @@ int64_t recur_workspace(int32_t steps, int32_t rows, int32_t width, int32_t dtyp
  * ROLLOUT_EHIP. */
 int recur_forward(const recur_args *args, void *hip_stream);
 int recur_backward(const recur_grad_args *args, void *hip_stream);
+/* The same two for a training pass.  `kept` [ceil(L / 8)][N][D] f32 holds the
+ * states that enter the steps 0, 8, 16, ... (before a done cuts them): the
+ * first call writes it, the second, of the same x, gate, h0 and dones, takes
+ * the states from there.  Only the sigmoid form of the 16-bit types uses it;
+ * otherwise it may be NULL and the calls are the two above.  recur_backward
+ * itself forms the states again, from x and gate. */
+int recur_forward_kept(const recur_args *args, float *kept, void *hip_stream);
+int recur_backward_kept(const recur_grad_args *args, const float *kept, void *hip_stream);
 
 /* One step, for acting: h = a m state + b with m = 0 where resets[n] is not 0
  * (the episode ended before this step), new_state the same value unrounded.

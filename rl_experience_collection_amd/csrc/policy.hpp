@@ -12,9 +12,15 @@ namespace rl {
 // Sets the calling thread's rollout_last_error() text; returns `code`.
 int set_error(int code, const char* text);
 
-int64_t recur_workspace_bytes(int32_t L, int32_t N, int32_t D, int32_t dtype);
-hipError_t recur_forward_launch(const recur_args& a, hipStream_t stream);
-hipError_t recur_backward_launch(const recur_grad_args& a, hipStream_t stream);
+// Whether the gradient takes the states from `kept`, not from h.
+bool recur_keeps(int32_t dtype, int32_t form);
+int64_t recur_kept_floats(int32_t L, int32_t N, int32_t D);
+// The chained scans' words; without kept states the gradient's workspace
+// holds those as well, first.
+int64_t recur_chain_bytes(int32_t L, int32_t N, int32_t D);
+// kept: NULL where they are not wanted.
+hipError_t recur_forward_launch(const recur_args& a, float* kept, hipStream_t stream);
+hipError_t recur_backward_launch(const recur_grad_args& a, const float* kept, hipStream_t stream);
 hipError_t recur_step_launch(int32_t N, int32_t D, int32_t dtype, int32_t form, const void* x,
                              int64_t x_row, const void* gate, int64_t gate_row,
                              const float* state, const uint8_t* resets, void* h, int64_t h_row,

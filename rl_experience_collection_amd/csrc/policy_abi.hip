@@ -77,6 +77,94 @@ int check_workspace(const char* who, int64_t need, const void* workspace, int64_
   return check_buffer(who, "workspace", workspace, 16);
 }
 
+// Of a gradient that forms the states again.
+int64_t states_bytes(int32_t steps, int32_t rows, int32_t width) {
+  return (rl::recur_kept_floats(steps, rows, width) * 4 + 255) / 256 * 256;
+}
+
+int forward_scan(const char* who, const recur_args* a, float* kept, bool keep, void* hip_stream) {
+  if (!a) return fail(ROLLOUT_EINVAL, "%s: arguments are NULL", who);
+  RL_CHECK(check_recur_sizes(who, a->steps, a->rows, a->width, a->dtype));
+  RL_CHECK(check_form(who, a->form));
+  if (a->rows == 0 || a->width == 0) return ROLLOUT_OK;
+  RL_CHECK(check_optional(who, "h0", a->h0, 4));
+  RL_CHECK(check_optional(who, "h_last", a->h_last, 4));
+  keep = keep && rl::recur_keeps(a->dtype, a->form);
+  if (a->steps > 0) {
+    const size_t eb = element_bytes(a->dtype);
+    RL_CHECK(check_strides(who, "x", a->x_step, a->x_row));
+    RL_CHECK(check_strides(who, "gate", a->gate_step, a->gate_row));
+    RL_CHECK(check_strides(who, "h", a->h_step, a->h_row));
+    RL_CHECK(check_buffer(who, "x", a->x, eb));
+    RL_CHECK(check_buffer(who, "gate", a->gate, eb));
+    RL_CHECK(check_buffer(who, "h", a->h, eb));
+    if (keep) RL_CHECK(check_buffer(who, "kept", kept, 4));
+    RL_CHECK(check_workspace(who, rl::recur_chain_bytes(a->steps, a->rows, a->width), a->workspace,
+                             a->workspace_bytes));
+  }
+  return launched(
+      rl::recur_forward_launch(*a, keep ? kept : nullptr, static_cast<hipStream_t>(hip_stream)), who);
+}
+
+int backward_scan(const char* who, const recur_grad_args* a, const float* kept, bool keep,
+                  void* hip_stream) {
+  if (!a) return fail(ROLLOUT_EINVAL, "%s: arguments are NULL", who);
+  RL_CHECK(check_recur_sizes(who, a->steps, a->rows, a->width, a->dtype));
+  RL_CHECK(check_form(who, a->form));
+  if (a->rows == 0 || a->width == 0) return ROLLOUT_OK;
+  RL_CHECK(check_optional(who, "h0", a->h0, 4));
+  RL_CHECK(check_optional(who, "dh_last", a->dh_last, 4));
+  RL_CHECK(check_optional(who, "dh0", a->dh0, 4));
+  const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  if (a->steps == 0) return launched(rl::recur_backward_launch(*a, nullptr, stream), who);
+  const size_t eb = element_bytes(a->dtype);
+  const bool states = rl::recur_keeps(a->dtype, a->form);
+  if (a->form == RECUR_SIGMOID) {
+    RL_CHECK(check_strides(who, "x", a->x_step, a->x_row));
+    RL_CHECK(check_buffer(who, "x", a->x, eb));
+  }
+  RL_CHECK(check_strides(who, "gate", a->gate_step, a->gate_row));
+  RL_CHECK(check_strides(who, "dh", a->dh_step, a->dh_row));
+  RL_CHECK(check_strides(who, "dx", a->dx_step, a->dx_row));
+  RL_CHECK(check_strides(who, "dgate", a->dgate_step, a->dgate_row));
+  RL_CHECK(check_buffer(who, "gate", a->gate, eb));
+  if (!states) {
+    RL_CHECK(check_strides(who, "h", a->h_step, a->h_row));
+    RL_CHECK(check_buffer(who, "h", a->h, eb));
+  }
+  RL_CHECK(check_buffer(who, "dh", a->dh, eb));
+  RL_CHECK(check_buffer(who, "dx", a->dx, eb));
+  RL_CHECK(check_buffer(who, "dgate", a->dgate, eb));
+  if (states && keep) RL_CHECK(check_buffer(who, "kept", kept, 4));
+  const int64_t chain = rl::recur_chain_bytes(a->steps, a->rows, a->width);
+  const int64_t again = states && !keep ? states_bytes(a->steps, a->rows, a->width) : 0;
+  RL_CHECK(check_workspace(who, again + chain, a->workspace, a->workspace_bytes));
+  if (!again) return launched(rl::recur_backward_launch(*a, kept, stream), who);
+  // the states once more, into the workspace
+  float* own = static_cast<float*>(a->workspace);
+  recur_grad_args g = *a;
+  g.workspace = static_cast<char*>(a->workspace) + again;
+  g.workspace_bytes = a->workspace_bytes - again;
+  recur_args f{};
+  f.steps = a->steps;
+  f.rows = a->rows;
+  f.width = a->width;
+  f.dtype = a->dtype;
+  f.form = a->form;
+  f.x_step = a->x_step;
+  f.x_row = a->x_row;
+  f.gate_step = a->gate_step;
+  f.gate_row = a->gate_row;
+  f.x = a->x;
+  f.gate = a->gate;
+  f.h0 = a->h0;
+  f.dones = a->dones;
+  f.workspace = g.workspace;
+  f.workspace_bytes = g.workspace_bytes;
+  RL_CHECK(launched(rl::recur_forward_launch(f, own, stream), who));
+  return launched(rl::recur_backward_launch(g, own, stream), who);
+}
+
 constexpr int32_t kMaxWidth = 1 << 24;
 constexpr int64_t kMaxCount = ((int64_t)1 << 31) - 2;
 
@@ -154,60 +242,27 @@ extern "C" {
 
 int64_t recur_workspace(int32_t steps, int32_t rows, int32_t width, int32_t dtype) {
   RL_CHECK(check_recur_sizes("recur_workspace", steps, rows, width, dtype));
-  return rl::recur_workspace_bytes(steps, rows, width, dtype);
+  if ((int64_t)rows * width == 0) return 0;
+  return rl::recur_chain_bytes(steps, rows, width) +
+         (rl::recur_keeps(dtype, RECUR_SIGMOID) ? states_bytes(steps, rows, width) : 0);
+}
+
+int64_t recur_kept_workspace(int32_t steps, int32_t rows, int32_t width, int32_t dtype) {
+  RL_CHECK(check_recur_sizes("recur_kept_workspace", steps, rows, width, dtype));
+  return rl::recur_chain_bytes(steps, rows, width);
 }
 
 int recur_forward(const recur_args* a, void* hip_stream) {
-  const char* who = "recur_forward";
-  if (!a) return fail(ROLLOUT_EINVAL, "%s: arguments are NULL", who);
-  RL_CHECK(check_recur_sizes(who, a->steps, a->rows, a->width, a->dtype));
-  RL_CHECK(check_form(who, a->form));
-  if (a->rows == 0 || a->width == 0) return ROLLOUT_OK;
-  RL_CHECK(check_optional(who, "h0", a->h0, 4));
-  RL_CHECK(check_optional(who, "h_last", a->h_last, 4));
-  if (a->steps > 0) {
-    const size_t eb = element_bytes(a->dtype);
-    RL_CHECK(check_strides(who, "x", a->x_step, a->x_row));
-    RL_CHECK(check_strides(who, "gate", a->gate_step, a->gate_row));
-    RL_CHECK(check_strides(who, "h", a->h_step, a->h_row));
-    RL_CHECK(check_buffer(who, "x", a->x, eb));
-    RL_CHECK(check_buffer(who, "gate", a->gate, eb));
-    RL_CHECK(check_buffer(who, "h", a->h, eb));
-    RL_CHECK(check_workspace(who, rl::recur_workspace_bytes(a->steps, a->rows, a->width, a->dtype),
-                             a->workspace, a->workspace_bytes));
-  }
-  return launched(rl::recur_forward_launch(*a, static_cast<hipStream_t>(hip_stream)), who);
+  return forward_scan("recur_forward", a, nullptr, false, hip_stream);
 }
-
 int recur_backward(const recur_grad_args* a, void* hip_stream) {
-  const char* who = "recur_backward";
-  if (!a) return fail(ROLLOUT_EINVAL, "%s: arguments are NULL", who);
-  RL_CHECK(check_recur_sizes(who, a->steps, a->rows, a->width, a->dtype));
-  RL_CHECK(check_form(who, a->form));
-  if (a->rows == 0 || a->width == 0) return ROLLOUT_OK;
-  RL_CHECK(check_optional(who, "h0", a->h0, 4));
-  RL_CHECK(check_optional(who, "dh_last", a->dh_last, 4));
-  RL_CHECK(check_optional(who, "dh0", a->dh0, 4));
-  if (a->steps > 0) {
-    const size_t eb = element_bytes(a->dtype);
-    if (a->form == RECUR_SIGMOID) {
-      RL_CHECK(check_strides(who, "x", a->x_step, a->x_row));
-      RL_CHECK(check_buffer(who, "x", a->x, eb));
-    }
-    RL_CHECK(check_strides(who, "gate", a->gate_step, a->gate_row));
-    RL_CHECK(check_strides(who, "h", a->h_step, a->h_row));
-    RL_CHECK(check_strides(who, "dh", a->dh_step, a->dh_row));
-    RL_CHECK(check_strides(who, "dx", a->dx_step, a->dx_row));
-    RL_CHECK(check_strides(who, "dgate", a->dgate_step, a->dgate_row));
-    RL_CHECK(check_buffer(who, "gate", a->gate, eb));
-    RL_CHECK(check_buffer(who, "h", a->h, eb));
-    RL_CHECK(check_buffer(who, "dh", a->dh, eb));
-    RL_CHECK(check_buffer(who, "dx", a->dx, eb));
-    RL_CHECK(check_buffer(who, "dgate", a->dgate, eb));
-    RL_CHECK(check_workspace(who, rl::recur_workspace_bytes(a->steps, a->rows, a->width, a->dtype),
-                             a->workspace, a->workspace_bytes));
-  }
-  return launched(rl::recur_backward_launch(*a, static_cast<hipStream_t>(hip_stream)), who);
+  return backward_scan("recur_backward", a, nullptr, false, hip_stream);
+}
+int recur_forward_kept(const recur_args* a, float* kept, void* hip_stream) {
+  return forward_scan("recur_forward_kept", a, kept, true, hip_stream);
+}
+int recur_backward_kept(const recur_grad_args* a, const float* kept, void* hip_stream) {
+  return backward_scan("recur_backward_kept", a, kept, true, hip_stream);
 }
 
 int recur_step(int32_t rows, int32_t width, int32_t dtype, int32_t form, const void* x,

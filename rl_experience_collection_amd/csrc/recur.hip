@@ -49,9 +49,21 @@ namespace {
 // costs a walk, and the walks of a column follow each other.  Backward, lanes
 // of two channels take 4 steps: a 1024 x 500 x 64 bf16 pass 98 us against 110
 // with 8, 4096 x 64 x 128 fp32 169 against 183; lanes of one or four 8.
-constexpr int slot_steps(int v, bool back, bool chained) {
-  return chained ? (back ? 8 : 16) : back && v == 2 ? 4 : 8;
+// A gradient on kept states takes the steps between two of them.
+constexpr int slot_steps(int v, bool back, bool chained, bool kept) {
+  return chained ? (back ? 8 : 16) : back && v == 2 && !kept ? 4 : 8;
 }
+// Steps between two states that are kept for the gradient.  dgate's factor
+// h_{t-1} - x_t of the sigmoid form is a difference of near numbers where the
+// state follows its input; from an h of 16 bits it keeps few digits or none
+// (inputs of a constant and 1% noise: dgate off by 16% in bf16).  So the forward
+// pass keeps every eighth state in fp32, a quarter of what h takes, and the
+// gradient runs from there through x and gate, which it has in registers, and
+// reads no h: both passes of 500 x 8192 x 64 bf16 take 884 us, from h 941 (500 x
+// 128 x 128 56 and 55, 500 x 1024 x 64 119 and 130).
+constexpr int kKeep = 8;
+template <class T, bool SIG>
+constexpr bool kKeeps = SIG && T::kBytes == 2;
 constexpr float kReset = -0.0f;
 
 struct Map {
@@ -109,6 +121,7 @@ struct RecurArgs {
   const uint8_t* dones;
   void *out, *dx, *dg;
   float* last;         // h_last / dh0
+  float* kept;         // [ceil(L / 8)][N][D] states, or NULL (forward)
   uint32_t* ticket;    // chained: the next tile
   uint64_t* words;     // chained: [tiles][units][V] published maps
 };
@@ -444,7 +457,9 @@ __device__ __forceinline__ void fold_forward(const float (&a)[S][V], const float
 template <class T, int V, bool SIG, bool CHAIN, bool OFF32, int W>
 __global__ __launch_bounds__(64 * W) void recur_forward_kernel(const RecurArgs p) {
   using raw = typename T::raw;
-  constexpr int S = slot_steps(V, false, CHAIN), kTile = S * W;
+  constexpr bool KEEPS = kKeeps<T, SIG>;
+  constexpr int S = slot_steps(V, false, CHAIN, KEEPS), kTile = S * W;
+  static_assert(S % kKeep == 0, "a slot begins at a kept state");
   __shared__ typename std::conditional<CHAIN, ChainLds<V>, char>::type s_chain;
   constexpr int kBufs = CHAIN ? 1 : 2;
   __shared__ alignas(16) float s_a[kBufs][W][64][V], s_b[kBufs][W][64][V];
@@ -549,12 +564,16 @@ __global__ __launch_bounds__(64 * W) void recur_forward_kernel(const RecurArgs p
 #pragma unroll
         for (int i = 0; i < S; ++i) {
           if (ts + i >= te) break;
+          if (KEEPS && i % kKeep == 0 && p.kept && at.active)
+            store_pack<F32, V>(reinterpret_cast<uint32_t*>(p.kept) +
+                                   (int64_t)((ts + i) / kKeep) * p.N * p.D + at.cell,
+                               narrow_pack<F32, V>(h));
 #pragma unroll
           for (int v = 0; v < V; ++v) {
             const float nh = __builtin_fmaf(a[i][v], h[v], b[i][v]);
             h[v] = cuts_here.value && ((done >> i) & 1u) ? b[i][v] : nh;
           }
-          if (at.active) out.store(ts + i, narrow_pack<T, V>(h));
+          if (at.active && (!KEEPS || p.out)) out.store(ts + i, narrow_pack<T, V>(h));
         }
       };
       if (cut)
@@ -594,7 +613,9 @@ __device__ __forceinline__ void fold_backward(const float (&a)[S][V], const floa
 template <class T, int V, bool SIG, bool CHAIN, bool OFF32, int W>
 __global__ __launch_bounds__(64 * W) void recur_backward_kernel(const RecurArgs p) {
   using raw = typename T::raw;
-  constexpr int S = slot_steps(V, true, CHAIN), kTile = S * W;
+  constexpr bool KEEPS = kKeeps<T, SIG>;
+  constexpr int S = slot_steps(V, true, CHAIN, KEEPS), kTile = S * W;
+  static_assert(!KEEPS || S == kKeep, "a slot is the steps from a kept state to the next");
   __shared__ typename std::conditional<CHAIN, ChainLds<V>, char>::type s_chain;
   constexpr int kBufs = CHAIN ? 1 : 2;
   __shared__ alignas(16) float s_a[kBufs][W][64][V], s_b[kBufs][W][64][V];
@@ -610,8 +631,12 @@ __global__ __launch_bounds__(64 * W) void recur_backward_kernel(const RecurArgs 
     const Lane<T, V, OFF32> dh(p.dh, p.dh_step, p.dh_row, at.n0, at.n, at.d);
     const Lane<T, V, OFF32> dx(p.dx, p.dx_step, p.dx_row, at.n0, at.n, at.d);
     const Lane<T, V, OFF32> dg(p.dg, p.dg_step, p.dg_row, at.n0, at.n, at.d);
-    // chained tiles are counted from the end, the last of them in time whole
-    const int32_t te = CHAIN ? p.L - tile.order * kTile : p.L, tb = CHAIN ? max(0, te - kTile) : 0;
+    // Chained tiles are counted from the end, the last of them in time whole;
+    // with kept states tiles begin at a multiple of their length, the last of
+    // them in time may be short.
+    const int32_t whole = KEEPS ? (p.L + kTile - 1) / kTile * kTile : p.L;
+    const int32_t tt = CHAIN ? whole - tile.order * kTile : whole, te = min(tt, p.L);
+    const int32_t tb = CHAIN ? max(0, tt - kTile) : 0;
 
     float c[V];  // G of the step after the tile
     const bool end = p.dones && p.dones[(int64_t)(p.L - 1) * p.N + at.n];
@@ -619,22 +644,27 @@ __global__ __launch_bounds__(64 * W) void recur_backward_kernel(const RecurArgs 
     for (int v = 0; v < V; ++v) c[v] = p.start && !end ? p.start[at.cell + v] : 0.0f;
 
     int buf = 0;
-    for (int32_t t1 = te; t1 > tb; t1 -= kTile, buf = (buf + 1) % kBufs) {
+    for (int32_t t1 = tt; t1 > tb; t1 -= kTile, buf = (buf + 1) % kBufs) {
       const int32_t top = t1 - 1 - w * S;  // this wave's latest step
-      Pack<T, V> gr[S], dr[S], xr[SIG ? S : 1], hr[S];
+      auto inside = [&](int32_t t) { return KEEPS ? min(t, te - 1) : max(t, tb); };
+      Pack<T, V> gr[S], dr[S], xr[SIG ? S : 1], hr[KEEPS ? 1 : S];
+      Pack<F32, V> kr;
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        const int32_t t = max(top - i, tb);
+        const int32_t t = inside(top - i);
         gr[i] = gate.load(t);
         dr[i] = dh.load(t);
       }
       const uint32_t done = p.dones ? load_dones<S, true>(p, at.n, top, tb, te) : 0u;
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        const int32_t t = max(top - i, tb);
+        const int32_t t = inside(top - i);
         if (SIG) xr[SIG ? i : 0] = x.load(t);
-        hr[i] = hs.load(max(t - 1, 0));
+        if (!KEEPS) hr[KEEPS ? 0 : i] = hs.load(max(t - 1, 0));
       }
+      if constexpr (KEEPS)
+        kr = load_pack<F32, V>(reinterpret_cast<const uint32_t*>(p.kept) +
+                               (int64_t)(inside(top - S + 1) / kKeep) * p.N * p.D + at.cell);
       float a[S][V], k[SIG ? S : 1][V], df[S][V];
 #pragma unroll
       for (int i = 0; i < S; ++i) {
@@ -649,11 +679,30 @@ __global__ __launch_bounds__(64 * W) void recur_backward_kernel(const RecurArgs 
             a[i][v] = gf[v];
         }
       }
-      if (top - S + 1 < tb) {
-        // steps before the tile leave the carry as it is
+      // the state that enters each step, less its input
+      float q[KEEPS ? S : 1][V];
+      if constexpr (KEEPS) {
+        float s[V];
+        widen_pack<F32, V>(kr, s);
+#pragma unroll
+        for (int i = S - 1; i >= 0; --i) {
+          float xf[V];
+          widen_pack<T, V>(xr[i], xf);
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const bool drop = (done >> i) & 1u;
+            const float b = k[i][v] * xf[v];
+            q[i][v] = (drop ? 0.0f : s[v]) - xf[v];
+            const float ns = __builtin_fmaf(a[i][v], s[v], b);
+            s[v] = drop ? b : ns;
+          }
+        }
+      }
+      if (KEEPS ? top >= te : top - S + 1 < tb) {
+        // steps outside the tile leave the carry as it is
 #pragma unroll
         for (int i = 0; i < S; ++i)
-          if (top - i < tb)
+          if (KEEPS ? top - i >= te : top - i < tb)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
               a[i][v] = 1.0f;
@@ -706,22 +755,25 @@ __global__ __launch_bounds__(64 * W) void recur_backward_kernel(const RecurArgs 
 #pragma unroll
         for (int i = 0; i < S; ++i) {
           const int32_t t = top - i;
-          if (t < tb) break;
+          if (KEEPS ? t >= te : t < tb) {
+            if (KEEPS) continue;
+            break;
+          }
           const bool drop = cuts_here.value && ((done >> i) & 1u);
           float hf[V], xf[V], ox[V], og[V];
-          widen_pack<T, V>(hr[i], hf);
-          if (SIG) widen_pack<T, V>(xr[SIG ? i : 0], xf);
-          if (t == 0) {
+          if (!KEEPS) widen_pack<T, V>(hr[KEEPS ? 0 : i], hf);
+          if (SIG && !KEEPS) widen_pack<T, V>(xr[SIG ? i : 0], xf);
+          if (!KEEPS && t == 0) {
 #pragma unroll
             for (int v = 0; v < V; ++v) hf[v] = p.h0 ? p.h0[at.cell + v] : 0.0f;
           }
 #pragma unroll
           for (int v = 0; v < V; ++v) {
             const float del = df[i][v] + G[v];
-            const float prev = drop ? 0.0f : hf[v];
+            const float prev = KEEPS || drop ? 0.0f : hf[v];
             if (SIG) {
               ox[v] = k[SIG ? i : 0][v] * del;
-              og[v] = a[i][v] * ox[v] * (prev - xf[v]);
+              og[v] = a[i][v] * ox[v] * (KEEPS ? q[KEEPS ? i : 0][v] : prev - xf[v]);
             } else {
               ox[v] = del;
               og[v] = drop ? 0.0f : del * prev;
@@ -828,7 +880,7 @@ int lane_channels(int32_t N, int32_t D, int32_t dtype) {
 // the whole time.  400 x 4 x 128 fp32 forward: 12.6 us as two tiles, 16.2 in one
 // workgroup's walk.
 int32_t chained_tiles(int32_t L, int64_t units, bool back) {
-  const int32_t tile = kManyWaves * slot_steps(1, back, true);
+  const int32_t tile = kManyWaves * slot_steps(1, back, true, false);
   const int64_t columns = (units + 63) / 64;
   return columns >= kWantColumns || L <= tile ? 0 : (L + tile - 1) / tile;
 }
@@ -867,7 +919,7 @@ hipError_t launch(RecurArgs p, void* workspace, hipStream_t stream) {
   }
   const dim3 grid((unsigned)p.columns);
   if constexpr (V * T::kBytes <= 4)
-    if (p.columns <= kWantColumns && p.L > kFewWaves * slot_steps(V, BACK, false))
+    if (p.columns <= kWantColumns && p.L > kFewWaves * slot_steps(V, BACK, false, kKeeps<T, SIG>))
       return start<T, V, SIG, BACK, false, OFF32, kManyWaves>(p, grid, stream);
   return start<T, V, SIG, BACK, false, OFF32, kFewWaves>(p, grid, stream);
 }
@@ -907,7 +959,15 @@ hipError_t pick_type(const RecurArgs& p, int32_t dtype, bool sig, void* ws, hipS
 
 }  // namespace
 
-int64_t recur_workspace_bytes(int32_t L, int32_t N, int32_t D, int32_t dtype) {
+bool recur_keeps(int32_t dtype, int32_t form) {
+  return dtype != POLICY_F32 && form == RECUR_SIGMOID;
+}
+
+int64_t recur_kept_floats(int32_t L, int32_t N, int32_t D) {
+  return ((int64_t)L + kKeep - 1) / kKeep * N * D;
+}
+
+int64_t recur_chain_bytes(int32_t L, int32_t N, int32_t D) {
   int64_t most = 0;
   if ((int64_t)N * D == 0) return 0;
   for (int v = 1; v <= 4; v *= 2) {  // whichever the strides allow, in both directions
@@ -921,7 +981,7 @@ int64_t recur_workspace_bytes(int32_t L, int32_t N, int32_t D, int32_t dtype) {
   return most;
 }
 
-hipError_t recur_forward_launch(const recur_args& a, hipStream_t stream) {
+hipError_t recur_forward_launch(const recur_args& a, float* kept, hipStream_t stream) {
   const int64_t cells = (int64_t)a.rows * a.width;
   if (cells == 0) return hipSuccess;
   if (a.steps == 0) return copy_state(a.h0, a.h_last, cells, stream);
@@ -940,11 +1000,12 @@ hipError_t recur_forward_launch(const recur_args& a, hipStream_t stream) {
   p.start = a.h0;
   p.dones = a.dones;
   p.out = a.h;
+  p.kept = kept;
   p.last = a.h_last;
   return pick_type<false>(p, a.dtype, a.form == RECUR_SIGMOID, a.workspace, stream);
 }
 
-hipError_t recur_backward_launch(const recur_grad_args& a, hipStream_t stream) {
+hipError_t recur_backward_launch(const recur_grad_args& a, const float* kept, hipStream_t stream) {
   const int64_t cells = (int64_t)a.rows * a.width;
   if (cells == 0) return hipSuccess;
   if (a.steps == 0) return copy_state(a.dh_last, a.dh0, cells, stream);
@@ -967,6 +1028,7 @@ hipError_t recur_backward_launch(const recur_grad_args& a, hipStream_t stream) {
   p.x = a.x;
   p.gate = a.gate;
   p.h = a.h;
+  p.kept = const_cast<float*>(kept);
   p.dh = a.dh;
   p.start = a.dh_last;
   p.h0 = a.h0;

@@ -23,7 +23,8 @@ import torch
 POLICY_F32, POLICY_BF16, POLICY_F16 = 0, 1, 2
 RECUR_LINEAR, RECUR_SIGMOID = 0, 1
 LOGITS_MASK_NONE, LOGITS_MASK_BYTES, LOGITS_MASK_BITS = 0, 1, 2
-EXPORTED = ("recur_workspace", "recur_forward", "recur_backward", "recur_step",
+EXPORTED = ("recur_workspace", "recur_kept_workspace", "recur_forward", "recur_backward",
+            "recur_forward_kept", "recur_backward_kept", "recur_step",
             "embed_forward", "embed_workspace", "embed_backward",
             "logits_forward", "logits_workspace", "logits_backward")
 
@@ -67,9 +68,11 @@ class LogitsArgs(C.Structure):
 def declare(lib):
     """Argument types of the entry points of include/policy.h."""
     vp, i32, i64 = C.c_void_p, C.c_int32, C.c_int64
-    lib.recur_workspace.argtypes = [i32, i32, i32, i32]
+    lib.recur_workspace.argtypes = lib.recur_kept_workspace.argtypes = [i32, i32, i32, i32]
     lib.recur_forward.argtypes = [C.POINTER(RecurArgs), vp]
     lib.recur_backward.argtypes = [C.POINTER(RecurGradArgs), vp]
+    lib.recur_forward_kept.argtypes = [C.POINTER(RecurArgs), vp, vp]
+    lib.recur_backward_kept.argtypes = [C.POINTER(RecurGradArgs), vp, vp]
     lib.recur_step.argtypes = [i32, i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp]
     lib.embed_forward.argtypes = [i32, vp, i64, i32, i64, vp, i32, i64, C.c_float, vp, i64, vp]
     lib.embed_workspace.argtypes = [i32, i64, i32, i64]
@@ -197,56 +200,64 @@ def _like(t):
 
 
 # ---------------------------------------------------------------- recurrence
-def _recur_forward(x, gate, h0, dones, form):
+def _recur_forward(x, gate, h0, dones, form, kept=None):
     L, N, D = x.shape
     lib, stream = _lib(), _here("recurrence", x, gate, h0, dones)
     h = _like(x)
     last = torch.empty((N, D), dtype=torch.float32, device=x.device)
     dt = _DTYPES[x.dtype]
-    size = lib.recur_workspace(L, N, D, dt)
+    size = lib.recur_kept_workspace(L, N, D, dt)
     ws = _workspace(x, size)
     a = RecurArgs(L, N, D, dt, form, *x.stride()[:2], *gate.stride()[:2], *h.stride()[:2],
                   _ptr(x), _ptr(gate), _ptr(h0), _ptr(dones), _ptr(h), _ptr(last), _ptr(ws), size)
-    _call(lib.recur_forward, C.byref(a), stream)
+    if kept is None:
+        _call(lib.recur_forward, C.byref(a), stream)
+    else:
+        _call(lib.recur_forward_kept, C.byref(a), _ptr(kept), stream)
     return h, last
 
 
-def _recur_backward(x, gate, h, h0, dones, dh, dh_last, form, want_dh0):
+def _recur_backward(x, gate, h, kept, h0, dones, dh, dh_last, form, want_dh0):
     L, N, D = gate.shape
     lib, stream = _lib(), _there(dh)
-    dx, dgate = _like(h), _like(gate)
+    dx, dgate = _like(x if h is None else h), _like(gate)
     dh0 = torch.empty((N, D), dtype=torch.float32, device=gate.device) if want_dh0 else None
     dt = _DTYPES[gate.dtype]
-    size = lib.recur_workspace(L, N, D, dt)
+    size = lib.recur_kept_workspace(L, N, D, dt)
     ws = _workspace(gate, size)
     a = RecurGradArgs(L, N, D, dt, form, *(x.stride()[:2] if x is not None else (0, 0)),
-                      *gate.stride()[:2], *h.stride()[:2], *dh.stride()[:2], *dx.stride()[:2],
-                      *dgate.stride()[:2], _ptr(x), _ptr(gate), _ptr(h), _ptr(h0), _ptr(dones),
-                      _ptr(dh), _ptr(dh_last), _ptr(dx), _ptr(dgate), _ptr(dh0), _ptr(ws), size)
-    _call(lib.recur_backward, C.byref(a), stream)
+                      *gate.stride()[:2], *(h.stride()[:2] if h is not None else (0, 0)),
+                      *dh.stride()[:2], *dx.stride()[:2], *dgate.stride()[:2],
+                      _ptr(x), _ptr(gate), _ptr(h), _ptr(h0), _ptr(dones), _ptr(dh), _ptr(dh_last), _ptr(dx), _ptr(dgate), _ptr(dh0), _ptr(ws), size)
+    _call(lib.recur_backward_kept, C.byref(a), _ptr(kept), stream)
     return dx, dgate, dh0
 
 
 class _Recurrence(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gate, h0, dones, form):
-        h, last = _recur_forward(x, gate, h0, dones, form)
-        ctx.save_for_backward(x if form == RECUR_SIGMOID else None, gate, h, h0, dones)
+        # the gradient takes the states of 16-bit sigmoid gates from `kept`, not from h
+        kept = None
+        if form == RECUR_SIGMOID and x.dtype != torch.float32:
+            kept = torch.empty(((x.shape[0] + 7) // 8,) + x.shape[1:], dtype=torch.float32, device=x.device)
+        h, last = _recur_forward(x, gate, h0, dones, form, kept)
+        ctx.save_for_backward(x if form == RECUR_SIGMOID else None, gate, h if kept is None else None, kept,
+                              h0, dones)
         ctx.form = form
         ctx.set_materialize_grads(False)
         return h, last
 
     @_first_order
     def backward(ctx, dh, dh_last):
-        x, gate, h, h0, dones = ctx.saved_tensors
+        x, gate, h, kept, h0, dones = ctx.saved_tensors
         if dh is None and dh_last is None:
             return None, None, None, None, None
-        dh = torch.zeros_like(h) if dh is None else dh
+        dh = torch.zeros(gate.shape, dtype=gate.dtype, device=gate.device) if dh is None else dh
         if dh.shape[-1] > 1 and dh.stride(-1) != 1:
             dh = dh.contiguous()
         if dh_last is not None:
             dh_last = dh_last.contiguous()
-        dx, dgate, dh0 = _recur_backward(x, gate, h, h0, dones, dh, dh_last, ctx.form,
+        dx, dgate, dh0 = _recur_backward(x, gate, h, kept, h0, dones, dh, dh_last, ctx.form,
                                          h0 is not None and ctx.needs_input_grad[2])
         return dx, dgate, dh0, None, None
 
