@@ -41,7 +41,10 @@ typedef enum { POLICY_F32 = 0, POLICY_BF16 = 1, POLICY_F16 = 2 } policy_dtype;
  * dones are a collection's, so the state that follows a finished episode is
  * zero, and a rollout cut in two gives the whole's results when the second
  * part starts from the first part's h_last.  m selects: a NaN or infinity of
- * a finished episode does not reach the next one.
+ * a finished episode does not reach the next one.  Products of linear gates may
+ * leave fp32's range: the states are those of the steps one by one all the same,
+ * to fp32 roundings.  Of a state that sigmoid gates shrink below 2^-126 of
+ * itself, what is left is lost.
  *
  * x, gate, h, dh, dx and dgate are [L][N][D] of one dtype, element (t, n, d)
  * at t * step + n * row + d with the strides given for each; the output

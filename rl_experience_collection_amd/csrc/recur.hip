@@ -30,12 +30,17 @@
 // same expression wherever the walk found its start: results do not depend on
 // timing.
 //
-// Linear gates may be larger than 1, and a product of them infinite where the
-// states are not (those of a padded row are zero).  A slot whose slope is no
-// finite number for a channel has no map there: its wave runs it step by step on
-// the state that enters it, once the slots before have passed.  A chained tile
-// publishes no map of such a channel, only the state that leaves it.  Other
-// channels and episodes keep their results to the bit.
+// Linear gates may be larger than 1, and their products leave fp32's range
+// where the states do not.  A slot whose slope or b is no finite number for a
+// channel has no map there; one whose slope fell below 2^-126 on the way
+// (faint) has one only for states so small beside b that what the slope has
+// lost is below b's rounding.  Without a map the slot's wave runs it step by
+// step on the state that enters it, once the slots before have passed.  A
+// chained tile publishes no map of such a channel, or a faint one, and a walk
+// that cannot use it waits for the state that leaves the tile.  Other channels
+// and episodes keep their results to the bit.  (Sigmoid gates are at most 1: no
+// product grows again, and what a faint slope loses stays below 2^-126 of the
+// state it multiplies.)
 #include <type_traits>
 
 #include "elem.hpp"
@@ -71,23 +76,46 @@ struct Map {
 };
 
 __device__ __forceinline__ bool is_reset(float a) { return __float_as_uint(a) == 0x80000000u; }
-// A product of slopes in its stored form: +0 for either zero, -0 after a done.
+// Below 2^-126 a product of slopes is faint: it has lost digits, if not all.
+constexpr float kFaint = 0x1p-149f;
+__device__ __forceinline__ bool is_faint(float a) {
+  return (__float_as_uint(a) & 0x7fffffffu) - 1u < 0x007fffffu;
+}
+// A product of slopes in its stored form: -0 after a done; of linear gates +0
+// for either zero; of sigmoid gates never zero, so that an infinite state
+// stays infinite.
+template <bool SIG>
 __device__ __forceinline__ float stored_slope(float a, bool reset) {
-  return reset ? kReset : a + 0.0f;
+  return reset ? kReset : SIG ? __builtin_elementwise_maximum(a, kFaint) : a + 0.0f;
 }
 // Not a finite number.
 __device__ __forceinline__ bool is_wild(float a) { return !(__builtin_fabsf(a) < __builtin_inff()); }
 __device__ __forceinline__ float apply(Map m, float h) {
   return is_reset(m.a) ? m.b : __builtin_fmaf(m.a, h, m.b);
 }
-// first, then second
+// first, then second, where no product of linear slopes becomes faint
+template <bool SIG>
 __device__ __forceinline__ Map chain(Map first, Map second) {
   Map r;
-  r.a = stored_slope(first.a * second.a, is_reset(first.a) || is_reset(second.a));
+  r.a = stored_slope<SIG>(first.a * second.a, is_reset(first.a) || is_reset(second.a));
   r.b = apply(second, first.b);
   return r;
 }
-
+// The linear slope f, then s.  A faint one stays so while nothing above 1
+// follows; after that it is no number.
+__device__ __forceinline__ float slope_times(float f, float s) {
+  const float p = f * s;
+  if (f == 0.0f || s == 0.0f) return p;
+  const bool ff = is_faint(f), sf = is_faint(s);
+  if (ff || sf) return __builtin_fabsf(ff ? s : f) <= 1.0f ? kFaint : __builtin_nanf("");
+  return is_faint(p) || p == 0.0f ? kFaint : p;
+}
+// Whether the map says nothing of what becomes of h.
+template <bool SIG>
+__device__ __forceinline__ bool is_lost(Map m, float h) {
+  return !SIG && (is_wild(m.a) ||
+                  (is_faint(m.a) && __builtin_fabsf(h) > 0x1p99f * __builtin_fabsf(m.b)));
+}
 // sigmoid(g) and sigmoid(-g), each to within a few fp32 roundings: with
 // E = exp(-g) they are 1 / (1 + E) and E / (1 + E), so neither is formed by a
 // difference.  E is 2^hi (1 + lo ln 2) with hi the rounded product -g log2(e)
@@ -217,44 +245,68 @@ __device__ __forceinline__ int32_t poll_chain(const uint64_t* sample, int64_t st
 // The state that enters tile `o` (in the order of the scan), for every wave:
 // `c` is the state that enters the scan and becomes that.  Wave 0 learns whether
 // it has to publish the state that leaves the tile itself, later, for some
-// channel: one with a slope that is no finite number (`wild`: of a slot).
+// channel: one that the tile's map does not take there.  `odd`: a slot has no
+// map, or a faint one.
 template <bool SIG, int V, int W>
 __device__ __forceinline__ bool enter_tile(const RecurArgs& p, int32_t o, int32_t u, bool active,
-                                               int w, int lane, bool wild,
+                                               int w, int lane, bool odd,
                                                const float (&sa)[W][64][V],
                                                const float (&sb)[W][64][V], ChainLds<V>& s,
                                                float (&c)[V]) {
   const int64_t stride = (int64_t)p.units * V;  // words of a tile
   uint64_t* mine = p.words + o * stride + (int64_t)u * V;
   Map t[V];
-  bool held = false;
-  // (a slot's own slope too: one before a done does not show in the tile's)
-  auto without_map = [&](float a, int v) {
-    bool none = is_wild(a);
-    if (wild) {
-#pragma unroll 1
-      for (int j = 0; j < W; ++j) none = none || is_wild(sa[j][lane][v]);
-    }
-    return none;
-  };
+  bool none[V];  // no map
   if (w == 0) {
     // the tile's map
 #pragma unroll
-    for (int v = 0; v < V; ++v) t[v] = Map{sa[0][lane][v], sb[0][lane][v]};
+    for (int v = 0; v < V; ++v) {
+      t[v] = Map{sa[0][lane][v], sb[0][lane][v]};
+      none[v] = false;
+    }
+    float high = 0.0f;
 #pragma unroll
     for (int j = 1; j < W; ++j)
 #pragma unroll
-      for (int v = 0; v < V; ++v) t[v] = chain(t[v], Map{sa[j][lane][v], sb[j][lane][v]});
-    if (!SIG) {
-      bool any = wild;
+      for (int v = 0; v < V; ++v) {
+        const Map m = Map{sa[j][lane][v], sb[j][lane][v]};
+        t[v] = chain<SIG>(t[v], m);
+        if (!SIG) high = __builtin_fmaxf(high, __builtin_fabsf(m.a));
+      }
+    if constexpr (!SIG) {
+      // With slopes of at most 1 a product is at its least at the end; else, and
+      // where that is faint, the slopes are gone through with care.  (All later
+      // tiles wait for this: 4096 x 16 x 128 bf16 takes 22 us so, 21 without the
+      // check and 32 where every slope is gone through.)
+      bool again = odd || high > 1.0f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) any = any || is_wild(t[v].a);
-      held = __ballot(any) != 0;
+      for (int v = 0; v < V; ++v)
+        again = again || (!is_reset(t[v].a) && (__builtin_fabsf(t[v].a) < 0x1p-126f || is_wild(t[v].b)));
+      if (__ballot(again)) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          t[v] = Map{sa[0][lane][v], sb[0][lane][v]};
+          none[v] = is_wild(t[v].a);
+        }
+#pragma unroll 1
+        for (int j = 1; j < W; ++j)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const Map m = Map{sa[j][lane][v], sb[j][lane][v]};
+            const bool cut = is_reset(t[v].a) || is_reset(m.a);
+            // (a done forgets what went wrong before it)
+            none[v] = !is_reset(m.a) && (none[v] || is_lost<SIG>(m, t[v].b));
+            t[v] = Map{stored_slope<SIG>(slope_times(t[v].a, m.a), cut), apply(m, t[v].b)};
+          }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          none[v] = none[v] || (!is_reset(t[v].a) && (is_wild(t[v].a) || is_wild(t[v].b)));
+      }
     }
     if (o > 0 && active) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (!held || !without_map(t[v].a, v)) put_map(mine + v, t[v]);
+        if (!none[v]) put_map(mine + v, t[v]);
     }
   }
   if (o > 0) {
@@ -287,7 +339,8 @@ __device__ __forceinline__ bool enter_tile(const RecurArgs& p, int32_t o, int32_
           bool known = false;
           for (int k = walk - 1; k >= 0; --k) {
             const Map m = s.before[k][lane][v];
-            known = is_reset(m.a) || (known && __float_as_uint(m.a) != kNothing);
+            known = is_reset(m.a) ||
+                    (known && __float_as_uint(m.a) != kNothing && !is_lost<SIG>(m, x[v]));
             x[v] = apply(m, x[v]);
           }
           ready = ready && known;
@@ -307,16 +360,21 @@ __device__ __forceinline__ bool enter_tile(const RecurArgs& p, int32_t o, int32_
 #pragma unroll
     for (int v = 0; v < V; ++v) c[v] = s.state[lane][v];
   }
-  if (w == 0 && active) {
+  bool held = false;
+  if (w == 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if ((o == 0 || !is_reset(t[v].a)) && (!held || !without_map(t[v].a, v)))
-        put_map(mine + v, Map{kReset, apply(t[v], c[v])});
+    for (int v = 0; v < V; ++v) {
+      if (!none[v] && o > 0 && is_reset(t[v].a)) continue;  // its map was its state
+      const bool later = none[v] || is_lost<SIG>(t[v], c[v]);
+      held = held || later;
+      if (active && !later) put_map(mine + v, Map{kReset, apply(t[v], c[v])});
+    }
+    held = !SIG && __ballot(held) != 0;
   }
   return held;
 }
 
-// The state that leaves tile `o`, where wave 0 has published nothing yet.
+// The state that leaves tile `o`, where wave 0 has published no state yet.
 template <int V>
 __device__ __forceinline__ void put_held(const RecurArgs& p, int32_t o, int32_t u, bool active,
                                          const float (&c)[V]) {
@@ -324,7 +382,7 @@ __device__ __forceinline__ void put_held(const RecurArgs& p, int32_t o, int32_t 
   uint64_t* mine = p.words + (o * (int64_t)p.units + u) * V;
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    if (__float_as_uint(get_map(mine + v).a) == kNothing) put_map(mine + v, Map{kReset, c[v]});
+    if (!is_reset(get_map(mine + v).a)) put_map(mine + v, Map{kReset, c[v]});
 }
 
 // Joins the tile's slots: `c` is the state that enters the tile, and then the
@@ -357,35 +415,85 @@ __device__ __forceinline__ void join_slots(const float (&sa)[W][64][V], const fl
   }
 }
 
-// The same where some channel's slots have no maps: one after another each wave
-// runs its slot on the state that enters it (run: h -> the state that leaves),
-// for those channels, and leaves the result in the place of the map's b.
+// The same where some slot has no map for a channel, or a faint one.  A slot
+// that needs it is run by its wave on the state that enters it, for those
+// channels (run: h -> the state that leaves), and leaves the result in the place
+// of the map's b.  All waves hold the same states and maps here, so they agree
+// on which slots those are.
 template <int V, int W, class Run>
-__device__ __forceinline__ void join_wild(const float (&sa)[W][64][V], float (&sb)[W][64][V], int w,
-                                          int lane, float (&c)[V], float (&h)[V], Run run) {
+__device__ __forceinline__ void join_odd(const float (&sa)[W][64][V], float (&sb)[W][64][V], int w,
+                                         int lane, float (&c)[V], float (&h)[V], Run run) {
 #pragma unroll 1
   for (int j = 0; j < W; ++j) {
-    if (j == w) {
-      float step[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = step[v] = c[v];
-      run(step);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (is_wild(sa[j][lane][v])) sb[j][lane][v] = step[v];
-    }
-    __syncthreads();
+    Map m[V];
+    bool lost[V], any = false;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const Map m = Map{sa[j][lane][v], sb[j][lane][v]};
-      c[v] = is_wild(m.a) ? m.b : apply(m, c[v]);
+      m[v] = Map{sa[j][lane][v], sb[j][lane][v]};
+      lost[v] = is_lost<false>(m[v], c[v]);
+      any = any || lost[v];
+    }
+    if (j == w) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = c[v];
+    }
+    if (__ballot(any)) {
+      __syncthreads();  // every wave has the slot's maps
+      if (j == w) {
+        float step[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) step[v] = c[v];
+        run(step);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (lost[v]) sb[j][lane][v] = step[v];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v] = lost[v] ? sb[j][lane][v] : apply(m[v], c[v]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v] = apply(m[v], c[v]);
     }
   }
 }
 
-// What a slot tells of itself besides its maps: a done in some lane, a slope
-// that is no finite number.
-constexpr uint32_t kCut = 1, kWild = 2;
+// What a slot tells of itself besides its maps: a done in some lane; no map, or
+// a faint one, of some channel.
+constexpr uint32_t kCut = 1, kOdd = 2;
+
+// The stored slope of a slot's steps from their product `a`.  `low`: the least
+// magnitude on the way (linear gates); the steps are gone through with care only
+// where it left the normal numbers.  A b that is no finite number leaves no map.
+template <int S, int V, bool SIG>
+__device__ __forceinline__ void settle_slopes(const float (&a)[S][V], const float (&low)[V], bool cut,
+                                              Map (&m)[V]) {
+  if constexpr (!SIG) {
+    bool again = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) again = again || low[v] < 0x1p-126f;
+    if (__ballot(again)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        m[v].a = a[0][v];
+#pragma unroll
+        for (int i = 1; i < S; ++i) m[v].a = slope_times(m[v].a, a[i][v]);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (is_wild(m[v].b)) m[v].a = __builtin_nanf("");
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) m[v].a = stored_slope<SIG>(m[v].a, cut);
+}
+template <int V>
+__device__ __forceinline__ bool is_odd(const Map (&m)[V]) {
+  bool odd = false;
+#pragma unroll
+  for (int v = 0; v < V; ++v) odd = odd || is_wild(m[v].a) || is_faint(m[v].a);
+  return odd;
+}
 
 // Where a workgroup and its lane stand.
 struct Place {
@@ -433,11 +541,15 @@ __device__ __forceinline__ uint32_t load_dones(const RecurArgs& p, int32_t n, in
 }
 
 // A slot's map, of steps a h + b.
-template <int V, int S, bool CUT>
+template <int V, int S, bool SIG, bool CUT>
 __device__ __forceinline__ void fold_forward(const float (&a)[S][V], const float (&b)[S][V],
                                              uint32_t done, Map (&m)[V]) {
+  float low[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) m[v] = Map{a[0][v], b[0][v]};
+  for (int v = 0; v < V; ++v) {
+    m[v] = Map{a[0][v], b[0][v]};
+    low[v] = __builtin_fabsf(a[0][v]);
+  }
 #pragma unroll
   for (int i = 1; i < S; ++i)
 #pragma unroll
@@ -445,9 +557,9 @@ __device__ __forceinline__ void fold_forward(const float (&a)[S][V], const float
       const float nb = __builtin_fmaf(a[i][v], m[v].b, b[i][v]);
       m[v].b = CUT && ((done >> i) & 1u) ? b[i][v] : nb;
       m[v].a *= a[i][v];
+      if (!SIG) low[v] = __builtin_fminf(low[v], __builtin_fabsf(m[v].a));
     }
-#pragma unroll
-  for (int v = 0; v < V; ++v) m[v].a = stored_slope(m[v].a, CUT && done != 0);
+  settle_slopes<S, V, SIG>(a, low, CUT && done != 0, m);
 }
 
 // Bound by memory where the columns fill the chip: 500 x 8192 x 64 bf16 in 318
@@ -521,9 +633,9 @@ __global__ __launch_bounds__(64 * W) void recur_forward_kernel(const RecurArgs p
       const bool cut = __ballot(done != 0) != 0;  // (of the wave)
       Map m[V];
       if (cut)
-        fold_forward<V, S, true>(a, b, done, m);
+        fold_forward<V, S, SIG, true>(a, b, done, m);
       else
-        fold_forward<V, S, false>(a, b, done, m);
+        fold_forward<V, S, SIG, false>(a, b, done, m);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         s_a[buf][w][lane][v] = m[v].a;
@@ -531,23 +643,20 @@ __global__ __launch_bounds__(64 * W) void recur_forward_kernel(const RecurArgs p
       }
       uint32_t note = cut ? kCut : 0u;
       if constexpr (!SIG) {
-        bool wild = false;
-#pragma unroll
-        for (int v = 0; v < V; ++v) wild = wild || is_wild(m[v].a);
-        if (__ballot(wild)) note |= kWild;
+        if (__ballot(is_odd<V>(m))) note |= kOdd;
       }
       if (lane == 0) s_note[buf][w] = note;
       __syncthreads();
       const uint32_t notes = s_note[buf][lane % W];
       const uint32_t cuts = (uint32_t)__ballot((notes & kCut) != 0);
-      const bool wild = !SIG && __ballot((notes & kWild) != 0) != 0;
+      const bool odd = !SIG && __ballot((notes & kOdd) != 0) != 0;
       bool held = false;
       if constexpr (CHAIN)
-        held = enter_tile<SIG, V, W>(p, tile.order, at.u, at.active, w, lane, wild, s_a[buf], s_b[buf],
+        held = enter_tile<SIG, V, W>(p, tile.order, at.u, at.active, w, lane, odd, s_a[buf], s_b[buf],
                                      s_chain, c);
       float h[V];
-      if (wild) {
-        join_wild<V, W>(s_a[buf], s_b[buf], w, lane, c, h, [&](float (&s)[V]) {
+      if (odd) {
+        join_odd<V, W>(s_a[buf], s_b[buf], w, lane, c, h, [&](float (&s)[V]) {
 #pragma unroll
           for (int i = 0; i < S; ++i)
 #pragma unroll
@@ -591,11 +700,15 @@ __global__ __launch_bounds__(64 * W) void recur_forward_kernel(const RecurArgs p
 }
 
 // A slot's map backwards, of steps a (dh + G).
-template <int V, int S, bool CUT>
+template <int V, int S, bool SIG, bool CUT>
 __device__ __forceinline__ void fold_backward(const float (&a)[S][V], const float (&dh)[S][V],
                                               uint32_t done, Map (&m)[V]) {
+  float low[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) m[v] = Map{1.0f, 0.0f};
+  for (int v = 0; v < V; ++v) {
+    m[v] = Map{1.0f, 0.0f};
+    low[v] = 1.0f;
+  }
 #pragma unroll
   for (int i = 0; i < S; ++i)
 #pragma unroll
@@ -603,9 +716,9 @@ __device__ __forceinline__ void fold_backward(const float (&a)[S][V], const floa
       const float nb = a[i][v] * (dh[i][v] + m[v].b);
       m[v].b = CUT && ((done >> i) & 1u) ? 0.0f : nb;
       m[v].a *= a[i][v];
+      if (!SIG) low[v] = __builtin_fminf(low[v], __builtin_fabsf(m[v].a));
     }
-#pragma unroll
-  for (int v = 0; v < V; ++v) m[v].a = stored_slope(m[v].a, CUT && done != 0);
+  settle_slopes<S, V, SIG>(a, low, CUT && done != 0, m);
 }
 
 // Bound like the forward pass: 500 x 8192 x 64 bf16 in 641 us (3.15 GB at 4.9
@@ -712,9 +825,9 @@ __global__ __launch_bounds__(64 * W) void recur_backward_kernel(const RecurArgs 
       const bool cut = __ballot(done != 0) != 0;
       Map m[V];
       if (cut)
-        fold_backward<V, S, true>(a, df, done, m);
+        fold_backward<V, S, SIG, true>(a, df, done, m);
       else
-        fold_backward<V, S, false>(a, df, done, m);
+        fold_backward<V, S, SIG, false>(a, df, done, m);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         s_a[buf][w][lane][v] = m[v].a;
@@ -722,23 +835,20 @@ __global__ __launch_bounds__(64 * W) void recur_backward_kernel(const RecurArgs 
       }
       uint32_t note = cut ? kCut : 0u;
       if constexpr (!SIG) {
-        bool wild = false;
-#pragma unroll
-        for (int v = 0; v < V; ++v) wild = wild || is_wild(m[v].a);
-        if (__ballot(wild)) note |= kWild;
+        if (__ballot(is_odd<V>(m))) note |= kOdd;
       }
       if (lane == 0) s_note[buf][w] = note;
       __syncthreads();
       const uint32_t notes = s_note[buf][lane % W];
       const uint32_t cuts = (uint32_t)__ballot((notes & kCut) != 0);
-      const bool wild = !SIG && __ballot((notes & kWild) != 0) != 0;
+      const bool odd = !SIG && __ballot((notes & kOdd) != 0) != 0;
       bool held = false;
       if constexpr (CHAIN)
-        held = enter_tile<SIG, V, W>(p, tile.order, at.u, at.active, w, lane, wild, s_a[buf], s_b[buf],
+        held = enter_tile<SIG, V, W>(p, tile.order, at.u, at.active, w, lane, odd, s_a[buf], s_b[buf],
                                      s_chain, c);
       float G[V];
-      if (wild) {
-        join_wild<V, W>(s_a[buf], s_b[buf], w, lane, c, G, [&](float (&s)[V]) {
+      if (odd) {
+        join_odd<V, W>(s_a[buf], s_b[buf], w, lane, c, G, [&](float (&s)[V]) {
 #pragma unroll
           for (int i = 0; i < S; ++i)
 #pragma unroll
