@@ -45,6 +45,7 @@
 
 #include "elem.hpp"
 #include "policy.hpp"
+#include "wait.hpp"
 
 namespace rl {
 
@@ -236,8 +237,7 @@ __device__ __forceinline__ int32_t poll_chain(const uint64_t* sample, int64_t st
     const int nearest = state ? __builtin_ctzll(state) : 64;
     // (lanes past the walk repeat its end)
     if (nearest < kWalk && (~out & ((2ull << nearest) - 1)) == 0) return nearest + 1;
-    if (left == 0) return kWalk;
-    --left;
+    if (wait_over(false, left)) return kWalk;
     __builtin_amdgcn_s_sleep(1);
   }
 }
@@ -346,13 +346,11 @@ __device__ __forceinline__ bool enter_tile(const RecurArgs& p, int32_t o, int32_
           ready = ready && known;
         }
         const bool done = __all(ready || !active);
-        if (done || left == 0) {
+        if (wait_over(done, left)) {
 #pragma unroll
           for (int v = 0; v < V; ++v) s.state[lane][v] = done ? x[v] : __builtin_nanf("");
-        } else {
-          --left;
+          if (lane == 0) s.walk = 0;
         }
-        if (lane == 0 && (done || left == 0)) s.walk = 0;
       }
       __syncthreads();
       if (__builtin_amdgcn_readfirstlane(s.walk) == 0) break;
