@@ -29,6 +29,13 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Orders a wave's accesses to LDS: what its lanes read before is read before
+// any of them writes after.  The LDS takes a wave's accesses in order, so this
+// costs nothing; it holds the compiler to that order.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 // Quotient of n by d for n * d < 2^32 (magic = floor(2^32 / d) + 1, d > 1).
 __device__ __forceinline__ uint32_t quotient(uint32_t n, uint32_t d, uint32_t magic) {
   return d == 1 ? n : __umulhi(n, magic);
@@ -246,13 +253,17 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_place_kernel(SortPass p)
         const uint64_t ones = __ballot((digit >> b) & 1u);
         same &= ((digit >> b) & 1u) ? ones : ~ones;
       }
-      if (!in) continue;
       const int earlier = __popcll(same & ((1ull << lane) - 1));
-      // every lane of a digit reads its cursor before the first of them moves it
+      // every lane of a digit reads its cursor before the first of them moves
+      // it, and that before the next round reads it
       const uint32_t place = s_cursor[w][digit] + earlier;
-      if (earlier == 0) s_cursor[w][digit] = place + __popcll(same);
-      p.keys_out[place] = key[j];
-      p.pos_out[place] = pos[j];
+      wave_order();
+      if (in && earlier == 0) s_cursor[w][digit] = place + __popcll(same);
+      wave_order();
+      if (in) {
+        p.keys_out[place] = key[j];
+        p.pos_out[place] = pos[j];
+      }
     }
   }
 }
@@ -497,6 +508,7 @@ __global__ __launch_bounds__(kThreads) void embed_few_kernel(EmbedBackward a, in
         if (lane >= d) end += y;
       }
       if (lane < kFewRows) s_end[lane] = end - mine;
+      wave_order();
       for (int32_t i0 = 0; i0 < n; i0 += 64) {
         const bool in = i0 + lane < n;
         const uint32_t e = s_list[min(i0 + lane, n - 1)], row = e >> 16;
@@ -506,12 +518,14 @@ __global__ __launch_bounds__(kThreads) void embed_few_kernel(EmbedBackward a, in
           const uint64_t ones = __ballot((row & b) != 0);
           same &= row & b ? ones : ~ones;
         }
-        if (!in) continue;
         const int earlier = __popcll(same & ((1ull << lane) - 1));
-        // every lane of a row reads its cursor before the first of them moves it
+        // every lane of a row reads its cursor before the first of them moves
+        // it, and that before the next round reads it
         const uint32_t place = s_end[row] + earlier;
-        if (earlier == 0) s_end[row] = place + __popcll(same);
-        s_place[place] = (uint16_t)e;
+        wave_order();
+        if (in && earlier == 0) s_end[row] = place + __popcll(same);
+        wave_order();
+        if (in) s_place[place] = (uint16_t)e;
       }
     }
     __syncthreads();
