@@ -5,7 +5,8 @@
     shape_logits                    penalties, bias and mask on logits
 
 `embed`, `recurrence` and `shape_logits` take part in torch's autograd; their
-gradients run in the library's kernels too.  Calls run on torch's current
+gradients run in the library's kernels too.  Forward-mode derivatives and the
+transforms of torch.func are refused.  Calls run on torch's current
 stream, on the current device, where their tensors must live; outputs and
 workspaces come from torch's allocator, so captured graphs keep their own.
 
@@ -19,6 +20,7 @@ from __future__ import annotations
 import ctypes as C
 
 import torch
+import torch.autograd.forward_ad as _forward_ad
 
 POLICY_F32, POLICY_BF16, POLICY_F16 = 0, 1, 2
 RECUR_LINEAR, RECUR_SIGMOID = 0, 1
@@ -130,6 +132,7 @@ def _first_order(backward):
     guarded = torch.autograd.function.once_differentiable(backward)
 
     def run(ctx, *grads):
+        _no_tangent("a backward pass", *grads)
         return (guarded if torch.is_grad_enabled() else backward)(ctx, *grads)
     return staticmethod(run)
 
@@ -184,6 +187,16 @@ def _wants_grad(*tensors):
 def _no_grad(name, *tensors):
     if _wants_grad(*tensors):
         raise ValueError(f"{name} records no gradient: call it under torch.no_grad()")
+
+
+def _no_tangent(name, *tensors):
+    """Refuses a forward-mode derivative: a dual tensor asks for no gradient,
+    and its tangent would be dropped without a word."""
+    if _forward_ad._current_level < 0:
+        return
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and _forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"{name} has no forward-mode derivative")
 
 
 def _workspace(like, bytes_):
@@ -271,6 +284,7 @@ def recurrence(x, gate, h0=None, dones=None, form: str = "sigmoid"):
     dtype, h_last [N, D] is float32 and starts the next rollout.  Gradients
     flow to x, gate and h0."""
     f = _form(form)
+    _no_tangent("recurrence", x, gate, h0)
     _element("x", x)
     if x.dim() != 3:
         raise ValueError(f"x must be [L, N, D], got {tuple(x.shape)}")
@@ -294,6 +308,7 @@ def recurrence_step(x, gate, state, resets=None, form: str = "sigmoid", out_stat
     be `state` itself, to update it in place.  It records no gradient:
     inputs that ask for one are refused unless under torch.no_grad()."""
     f = _form(form)
+    _no_tangent("recurrence_step", x, gate, state, out_state)
     _no_grad("recurrence_step", x, gate, state)
     dt = _element("x", x)
     (x_row,), (gate_row,) = _unit("x", x, 2), _unit("gate", gate, 2)
@@ -354,6 +369,7 @@ def embed(weight, index, scale: float = 1.0):
     of any shape; returns index.shape + [D] in weight's dtype.  An index outside
     [0, V), such as the -1 of an episode's first step, gives zeros.  The
     gradient flows to weight and is dense."""
+    _no_tangent("embed", weight)
     _element("weight", weight)
     if weight.dim() != 2:
         raise ValueError(f"weight must be [V, D], got {tuple(weight.shape)}")
@@ -459,6 +475,7 @@ def shape_logits(logits, bias=None, history=None, history_len=None, repetition=1
     rows chosen by mask_rows [...] int32 (a value that names no row allows
     everything).  out: written instead of a new tensor; may be `logits`.
     Gradients flow to logits and to a bias of shape [V]."""
+    _no_tangent("shape_logits", logits, bias, repetition, presence, frequency, out)
     _element("logits", logits)
     if logits.dim() < 1:
         raise ValueError("logits must be [..., V]")
