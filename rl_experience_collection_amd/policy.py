@@ -199,6 +199,13 @@ def _no_tangent(name, *tensors):
             raise NotImplementedError(f"{name} has no forward-mode derivative")
 
 
+def _written(t):
+    """Tells autograd that the caller's tensor has new values, so that a graph
+    which saved the old ones raises instead of using these."""
+    if not t.is_inference():
+        torch.autograd.graph.increment_version(t)
+
+
 def _workspace(like, bytes_):
     return torch.empty(bytes_, dtype=torch.uint8, device=like.device) if bytes_ else None
 
@@ -324,6 +331,8 @@ def recurrence_step(x, gate, state, resets=None, form: str = "sigmoid", out_stat
     new = torch.empty_like(state) if out_state is None else out_state
     _call(_lib().recur_step, N, D, dt, f, _ptr(x), x_row, _ptr(gate), gate_row, _ptr(state),
           _ptr(resets), _ptr(h), D, _ptr(new), stream)
+    if out_state is not None:
+        _written(out_state)
     return h, new
 
 
@@ -521,5 +530,8 @@ def shape_logits(logits, bias=None, history=None, history_len=None, repetition=1
             if out.stride(0) < V:
                 raise ValueError("out's rows must not overlap")
     if out is not None or not _wants_grad(logits, bias):
-        return _logits_forward(logits, bias, history, history_len, penalties, mask, mask_rows, out)
+        result = _logits_forward(logits, bias, history, history_len, penalties, mask, mask_rows, out)
+        if out is not None:
+            _written(out)
+        return result
     return _ShapeLogits.apply(logits, bias, history, history_len, penalties, mask, mask_rows)
