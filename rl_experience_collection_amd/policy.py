@@ -316,7 +316,7 @@ def recurrence_step(x, gate, state, resets=None, form: str = "sigmoid", out_stat
     inputs that ask for one are refused unless under torch.no_grad()."""
     f = _form(form)
     _no_tangent("recurrence_step", x, gate, state, out_state)
-    _no_grad("recurrence_step", x, gate, state)
+    _no_grad("recurrence_step", x, gate, state, out_state)
     dt = _element("x", x)
     (x_row,), (gate_row,) = _unit("x", x, 2), _unit("gate", gate, 2)
     if gate.dtype != x.dtype or gate.shape != x.shape:
@@ -522,7 +522,7 @@ def shape_logits(logits, bias=None, history=None, history_len=None, repetition=1
     elif mask_rows is not None:
         raise ValueError("mask_rows needs a mask")
     if out is not None:
-        _no_grad("shape_logits with out", logits, bias)
+        _no_grad("shape_logits with out", logits, bias, out)
         if out.dtype != logits.dtype or out.shape != logits.shape:
             raise ValueError("out must have logits' dtype and shape")
         if not out.is_contiguous():

@@ -37,3 +37,14 @@ def test_a_view_shares_its_base(rx, k):
 def test_inference_mode(rx, k):
     with torch.inference_mode():
         into(rx, torch.ones(2, 5))[k]()
+
+
+@pytest.mark.parametrize("k", [0, 1])
+def test_an_output_that_asks_for_a_gradient_is_refused(rx, k):
+    leaf = torch.ones(2, 5, requires_grad=True)
+    with pytest.raises(ValueError, match="no_grad"):
+        into(rx, leaf)[k]()
+    with pytest.raises(ValueError, match="no_grad"):
+        into(rx, leaf * 2)[k]()
+    with torch.no_grad():
+        into(rx, leaf)[k]()
