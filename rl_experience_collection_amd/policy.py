@@ -206,6 +206,30 @@ def _written(t):
         torch.autograd.graph.increment_version(t)
 
 
+def _apart_or_same(name, out, t):
+    """The output is the input itself, or shares no element with it.  Both have
+    the same type and rows of the same width, given apart by their strides."""
+    shift = (out.data_ptr() - t.data_ptr()) // t.element_size()
+    width, rows = t.shape[-1], t.numel() // t.shape[-1] if t.shape[-1] else 0
+    if rows == 0:
+        return
+    strides = [width if u.is_contiguous() else u.stride(0) for u in (t, out)]
+    if (shift == 0 and (rows == 1 or strides[0] == strides[1])) or \
+            shift >= (rows - 1) * strides[0] + width or -shift >= (rows - 1) * strides[1] + width:
+        return
+    # interleaved rows of one buffer: every row lies between two of the other's
+    if strides[0] == strides[1]:
+        shared = not width <= shift % strides[0] <= strides[0] - width
+    else:
+        a, b = torch.arange(rows) * strides[0], torch.arange(rows) * strides[1] + shift
+        k = torch.searchsorted(a, b)
+        shared = bool(((b - a[(k - 1).clamp(min=0)] < width) & (k > 0) |
+                       (a[k.clamp(max=rows - 1)] - b < width) & (k < rows)).any())
+    if not shared:
+        return
+    raise ValueError(f"{name} must be the input itself or not overlap it")
+
+
 def _workspace(like, bytes_):
     return torch.empty(bytes_, dtype=torch.uint8, device=like.device) if bytes_ else None
 
@@ -325,6 +349,8 @@ def recurrence_step(x, gate, state, resets=None, form: str = "sigmoid", out_stat
     N, D = x.shape
     _exact("state", state, torch.float32, (N, D))
     _exact("out_state", out_state, torch.float32, (N, D))
+    if out_state is not None:
+        _apart_or_same("out_state", out_state, state)
     resets = _flags("resets", resets, (N,))
     stream = _here("recurrence_step", x, gate, state, resets, out_state)
     h = torch.empty((N, D), dtype=x.dtype, device=x.device)
@@ -482,7 +508,8 @@ def shape_logits(logits, bias=None, history=None, history_len=None, repetition=1
     [..., V], or int32 [..., ceil(V / 32)] with token v at bit v % 32 of word
     v // 32; one row per row of logits, a single row for all, or any number of
     rows chosen by mask_rows [...] int32 (a value that names no row allows
-    everything).  out: written instead of a new tensor; may be `logits`.
+    everything).  out: written instead of a new tensor; may be `logits`, else
+    it must not overlap it.
     Gradients flow to logits and to a bias of shape [V]."""
     _no_tangent("shape_logits", logits, bias, repetition, presence, frequency, out)
     _element("logits", logits)
@@ -529,6 +556,7 @@ def shape_logits(logits, bias=None, history=None, history_len=None, repetition=1
             _unit("out", out, 2)
             if out.stride(0) < V:
                 raise ValueError("out's rows must not overlap")
+        _apart_or_same("out", out, logits)
     if out is not None or not _wants_grad(logits, bias):
         result = _logits_forward(logits, bias, history, history_len, penalties, mask, mask_rows, out)
         if out is not None:
