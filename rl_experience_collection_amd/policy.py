@@ -489,7 +489,7 @@ class _ShapeLogits(torch.autograd.Function):
 def _per_row(name, value, lead):
     if isinstance(value, torch.Tensor):
         _exact(name, value, torch.float32, lead)
-        if value.requires_grad:
+        if _wants_grad(value):
             raise ValueError(f"{name} takes no gradient")
         return value
     return float(value)
@@ -522,7 +522,7 @@ def shape_logits(logits, bias=None, history=None, history_len=None, repetition=1
             raise ValueError("logits' rows must not overlap")
     if bias is not None:
         _exact("bias", bias, torch.float32, (V,) if bias.dim() == 1 else lead + (V,))
-        if bias.requires_grad and bias.dim() > 1:
+        if bias.dim() > 1 and _wants_grad(bias):
             raise ValueError("only a bias of shape [V] takes a gradient")
     if history is not None:
         H = history.shape[-1] if history.dim() else 0
