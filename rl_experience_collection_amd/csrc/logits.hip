@@ -697,33 +697,34 @@ int64_t run_groups(int64_t rows, int32_t vocab, bool bias) {
   return rows < most ? rows : most;
 }
 
-template <class T, int V, bool GRAD>
-hipError_t launch(LogitsArgs p, bool flat, float* dbias, hipStream_t stream) {
+// The launch over whole rows: its workgroups.
+template <class T, bool GRAD>
+int64_t launch_rows(const LogitsArgs& p, hipStream_t stream) {
+  constexpr int V = 16 / T::kBytes;
   const logits_args& a = p.a;
-  int64_t groups;
-  if (flat) {
-    groups = flat_groups(a.rows, a.vocab);
-    const bool flat_mask = a.mask_kind == LOGITS_MASK_BYTES && !a.mask_rows &&
-                           a.mask_count == a.rows && (a.mask_row == a.vocab || a.rows == 1);
-    auto kernel = flat_mask                            ? logits_rows_kernel<T, V, GRAD, kFlatMask>
-                  : a.mask_kind == LOGITS_MASK_BITS  ? logits_rows_kernel<T, V, GRAD, kBitMask>
-                  : a.mask_kind == LOGITS_MASK_BYTES ? logits_rows_kernel<T, V, GRAD, kByteMask>
-                                                     : logits_rows_kernel<T, V, GRAD, kNoMask>;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kThreads), 0, stream, p);
-  } else {
-    constexpr int kRun = kThreads * V * kRunPacks;
-    groups = run_groups(a.rows, a.vocab, dbias != nullptr);
-    const dim3 grid((unsigned)((a.vocab + kRun - 1) / kRun), (unsigned)groups);
-    auto kernel = a.mask_kind == LOGITS_MASK_BITS    ? logits_runs_kernel<T, V, GRAD, LOGITS_MASK_BITS>
-                  : a.mask_kind == LOGITS_MASK_BYTES ? logits_runs_kernel<T, V, GRAD, LOGITS_MASK_BYTES>
-                                                     : logits_runs_kernel<T, V, GRAD, LOGITS_MASK_NONE>;
-    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, p);
-  }
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !dbias) return e;
-  hipLaunchKernelGGL(bias_join_kernel, dim3((unsigned)(((int64_t)a.vocab + 63) / 64)), dim3(1024), 0,
-                     stream, p.partial, (int32_t)groups, a.vocab, dbias);
-  return hipGetLastError();
+  const int64_t groups = flat_groups(a.rows, a.vocab);
+  const bool flat_mask = a.mask_kind == LOGITS_MASK_BYTES && !a.mask_rows &&
+                         a.mask_count == a.rows && a.mask_row == a.vocab;
+  auto kernel = flat_mask                            ? logits_rows_kernel<T, V, GRAD, kFlatMask>
+                : a.mask_kind == LOGITS_MASK_BITS  ? logits_rows_kernel<T, V, GRAD, kBitMask>
+                : a.mask_kind == LOGITS_MASK_BYTES ? logits_rows_kernel<T, V, GRAD, kByteMask>
+                                                   : logits_rows_kernel<T, V, GRAD, kNoMask>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kThreads), 0, stream, p);
+  return groups;
+}
+
+// The launch over runs of columns: its workgroups along the rows.
+template <class T, int V, bool GRAD>
+int64_t launch_runs(const LogitsArgs& p, bool bias, hipStream_t stream) {
+  constexpr int kRun = kThreads * V * kRunPacks;
+  const logits_args& a = p.a;
+  const int64_t groups = run_groups(a.rows, a.vocab, bias);
+  const dim3 grid((unsigned)((a.vocab + kRun - 1) / kRun), (unsigned)groups);
+  auto kernel = a.mask_kind == LOGITS_MASK_BITS    ? logits_runs_kernel<T, V, GRAD, LOGITS_MASK_BITS>
+                : a.mask_kind == LOGITS_MASK_BYTES ? logits_runs_kernel<T, V, GRAD, LOGITS_MASK_BYTES>
+                                                   : logits_runs_kernel<T, V, GRAD, LOGITS_MASK_NONE>;
+  hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, p);
+  return groups;
 }
 
 template <class T, bool GRAD>
@@ -746,10 +747,16 @@ hipError_t shape(LogitsArgs p, float* dbias, hipStream_t stream) {
   }
   if (a.mask_count == 0) p.a.mask_kind = LOGITS_MASK_NONE;  // a table without rows bans nothing
   p.past = a.rows * a.vocab * T::kBytes > kPastBytes;
-  // a pack has to fit into the array (rows one after another) or the row
+  // a pack has to fit into the row (whole rows are many, so it fits into those)
   constexpr int V = 16 / T::kBytes;
-  if ((flat ? a.rows * a.vocab : a.vocab) >= V) return launch<T, V, GRAD>(p, flat, dbias, stream);
-  return launch<T, 1, GRAD>(p, flat, dbias, stream);
+  const int64_t groups = flat           ? launch_rows<T, GRAD>(p, stream)
+                         : a.vocab >= V ? launch_runs<T, V, GRAD>(p, dbias != nullptr, stream)
+                                        : launch_runs<T, 1, GRAD>(p, dbias != nullptr, stream);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !dbias) return e;
+  hipLaunchKernelGGL(bias_join_kernel, dim3((unsigned)(((int64_t)a.vocab + 63) / 64)), dim3(1024), 0,
+                     stream, p.partial, (int32_t)groups, a.vocab, dbias);
+  return hipGetLastError();
 }
 
 template <bool GRAD>

@@ -566,7 +566,6 @@ __device__ __forceinline__ void fold_forward(const float (&a)[S][V], const float
 // way from tile to tile: 65,537 x 2 x 1000 fp16 in 260 us (786 MB at 3.0 TB/s).
 template <class T, int V, bool SIG, bool CHAIN, bool OFF32, int W>
 __global__ __launch_bounds__(64 * W) void recur_forward_kernel(const RecurArgs p) {
-  using raw = typename T::raw;
   constexpr bool KEEPS = kKeeps<T, SIG>;
   constexpr int S = slot_steps(V, false, CHAIN, KEEPS), kTile = S * W;
   static_assert(S % kKeep == 0, "a slot begins at a kept state");
@@ -723,7 +722,6 @@ __device__ __forceinline__ void fold_backward(const float (&a)[S][V], const floa
 // TB/s), 500 x 128 x 128 fp32 with linear gates in 36 (164 MB at 4.5 TB/s).
 template <class T, int V, bool SIG, bool CHAIN, bool OFF32, int W>
 __global__ __launch_bounds__(64 * W) void recur_backward_kernel(const RecurArgs p) {
-  using raw = typename T::raw;
   constexpr bool KEEPS = kKeeps<T, SIG>;
   constexpr int S = slot_steps(V, true, CHAIN, KEEPS), kTile = S * W;
   static_assert(!KEEPS || S == kKeep, "a slot is the steps from a kept state to the next");
@@ -1013,7 +1011,7 @@ hipError_t launch(RecurArgs p, void* workspace, hipStream_t stream) {
   p.units = p.N * p.per_row;
   p.columns = (p.units + 63) / 64;
   const int32_t tiles = chained_tiles(p.L, p.units, BACK);
-  if constexpr (V <= 2) if (tiles) {  // (wider lanes only where columns are plenty)
+  if constexpr (V * T::kBytes <= 4) if (tiles) {  // (wider lanes only where columns are plenty)
     p.ticket = static_cast<uint32_t*>(workspace);
     p.words = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + kTicketBytes);
     const int64_t words = tiles * (int64_t)p.units * V, blocks = (words + 255) / 256;
