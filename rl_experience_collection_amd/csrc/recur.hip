@@ -32,9 +32,9 @@
 //
 // Linear gates may be larger than 1, and their products leave fp32's range
 // where the states do not.  A slot whose slope or b is no finite number for a
-// channel has no map there; one whose slope fell below 2^-126 on the way
-// (faint) has one only for states so small beside b that what the slope has
-// lost is below b's rounding.  Without a map the slot's wave runs it step by
+// channel has no map there; one whose slope is below 2^-126 (faint) has one only
+// for states so small beside b that what the slope has lost is below b's
+// rounding.  Without a map the slot's wave runs it step by
 // step on the state that enters it, once the slots before have passed.  A
 // chained tile publishes no map of such a channel, or a faint one, and a walk
 // that cannot use it waits for the state that leaves the tile.  Other channels
@@ -94,7 +94,7 @@ __device__ __forceinline__ bool is_wild(float a) { return !(__builtin_fabsf(a) <
 __device__ __forceinline__ float apply(Map m, float h) {
   return is_reset(m.a) ? m.b : __builtin_fmaf(m.a, h, m.b);
 }
-// first, then second, where no product of linear slopes becomes faint
+// first, then second
 template <bool SIG>
 __device__ __forceinline__ Map chain(Map first, Map second) {
   Map r;
@@ -102,21 +102,36 @@ __device__ __forceinline__ Map chain(Map first, Map second) {
   r.b = apply(second, first.b);
   return r;
 }
-// The linear slope f, then s.  A faint one stays so while nothing above 1
-// follows; after that it is no number.
-__device__ __forceinline__ float slope_times(float f, float s) {
-  const float p = f * s;
-  if (f == 0.0f || s == 0.0f) return p;
-  const bool ff = is_faint(f), sf = is_faint(s);
-  if (ff || sf) return __builtin_fabsf(ff ? s : f) <= 1.0f ? kFaint : __builtin_nanf("");
-  return is_faint(p) || p == 0.0f ? kFaint : p;
-}
+// A product of up to 16 linear slopes, its exponent apart: it loses nothing on
+// its way out of fp32's range and back.  A faint slope counts as 2^-126, which
+// it is below.
+struct Product {
+  float m = 1.0f;
+  int32_t e = 0;
+  bool faint = false;
+  __device__ __forceinline__ void times(float s) {
+    m *= __builtin_amdgcn_frexp_mantf(s);
+    e += __builtin_amdgcn_frexp_expf(s);
+  }
+  __device__ __forceinline__ void times_stored(float s) {
+    faint = faint || is_faint(s);
+    times(is_faint(s) ? 0x1p-126f : s);
+  }
+  // 0 only for a slope of zero; no number where it is not known to be faint
+  __device__ __forceinline__ float value() const {
+    const float p = __builtin_amdgcn_ldexpf(m, e);
+    const bool low = __builtin_fabsf(p) <= 0x1p-126f && m != 0.0f;
+    return low ? kFaint : faint && m != 0.0f ? __builtin_nanf("") : p;
+  }
+};
+
 // Whether the map says nothing of what becomes of h.
 template <bool SIG>
 __device__ __forceinline__ bool is_lost(Map m, float h) {
   return !SIG && (is_wild(m.a) ||
                   (is_faint(m.a) && __builtin_fabsf(h) > 0x1p99f * __builtin_fabsf(m.b)));
 }
+
 // sigmoid(g) and sigmoid(-g), each to within a few fp32 roundings: with
 // E = exp(-g) they are 1 / (1 + E) and E / (1 + E), so neither is formed by a
 // difference.  E is 2^hi (1 + lo ln 2) with hi the rounded product -g log2(e)
@@ -264,43 +279,52 @@ __device__ __forceinline__ bool enter_tile(const RecurArgs& p, int32_t o, int32_
       t[v] = Map{sa[0][lane][v], sb[0][lane][v]};
       none[v] = false;
     }
-    float high = 0.0f;
+    if constexpr (SIG) {
 #pragma unroll
-    for (int j = 1; j < W; ++j)
+      for (int j = 1; j < W; ++j)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const Map m = Map{sa[j][lane][v], sb[j][lane][v]};
-        t[v] = chain<SIG>(t[v], m);
-        if (!SIG) high = __builtin_fmaxf(high, __builtin_fabsf(m.a));
-      }
-    if constexpr (!SIG) {
-      // With slopes of at most 1 a product is at its least at the end; else, and
-      // where that is faint, the slopes are gone through with care.  (All later
-      // tiles wait for this: 4096 x 16 x 128 bf16 takes 22 us so, 21 without the
-      // check and 32 where every slope is gone through.)
-      bool again = odd || high > 1.0f;
+        for (int v = 0; v < V; ++v) t[v] = chain<SIG>(t[v], Map{sa[j][lane][v], sb[j][lane][v]});
+    } else {
+      // (All later tiles wait for this: 4096 x 16 x 128 bf16 takes 22 us so, 21
+      // with a plain product.)
+      Product a[V];
+      bool cut[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        again = again || (!is_reset(t[v].a) && (__builtin_fabsf(t[v].a) < 0x1p-126f || is_wild(t[v].b)));
-      if (__ballot(again)) {
+      for (int v = 0; v < V; ++v) cut[v] = is_reset(t[v].a);
+      if (!odd) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[v].times(t[v].a);
+#pragma unroll
+        for (int j = 1; j < W; ++j)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const Map m = Map{sa[j][lane][v], sb[j][lane][v]};
+            cut[v] = cut[v] || is_reset(m.a);
+            a[v].times(m.a);
+            t[v].b = apply(m, t[v].b);
+          }
+      } else {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          t[v] = Map{sa[0][lane][v], sb[0][lane][v]};
           none[v] = is_wild(t[v].a);
+          a[v].times_stored(t[v].a);
         }
 #pragma unroll 1
         for (int j = 1; j < W; ++j)
 #pragma unroll
           for (int v = 0; v < V; ++v) {
             const Map m = Map{sa[j][lane][v], sb[j][lane][v]};
-            const bool cut = is_reset(t[v].a) || is_reset(m.a);
             // (a done forgets what went wrong before it)
             none[v] = !is_reset(m.a) && (none[v] || is_lost<SIG>(m, t[v].b));
-            t[v] = Map{stored_slope<SIG>(slope_times(t[v].a, m.a), cut), apply(m, t[v].b)};
+            cut[v] = cut[v] || is_reset(m.a);
+            a[v].times_stored(m.a);
+            t[v].b = apply(m, t[v].b);
           }
+      }
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          none[v] = none[v] || (!is_reset(t[v].a) && (is_wild(t[v].a) || is_wild(t[v].b)));
+      for (int v = 0; v < V; ++v) {
+        t[v].a = stored_slope<SIG>(a[v].value(), cut[v]);
+        none[v] = none[v] || (!cut[v] && (is_wild(t[v].a) || is_wild(t[v].b)));
       }
     }
     if (o > 0 && active) {
@@ -461,8 +485,8 @@ __device__ __forceinline__ void join_odd(const float (&sa)[W][64][V], float (&sb
 constexpr uint32_t kCut = 1, kOdd = 2;
 
 // The stored slope of a slot's steps from their product `a`.  `low`: the least
-// magnitude on the way (linear gates); the steps are gone through with care only
-// where it left the normal numbers.  A b that is no finite number leaves no map.
+// magnitude on the way (linear gates); where it left the normal numbers the
+// product is formed again.  A b that is no finite number leaves no map.
 template <int S, int V, bool SIG>
 __device__ __forceinline__ void settle_slopes(const float (&a)[S][V], const float (&low)[V], bool cut,
                                               Map (&m)[V]) {
@@ -473,9 +497,10 @@ __device__ __forceinline__ void settle_slopes(const float (&a)[S][V], const floa
     if (__ballot(again)) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        m[v].a = a[0][v];
+        Product p;
 #pragma unroll
-        for (int i = 1; i < S; ++i) m[v].a = slope_times(m[v].a, a[i][v]);
+        for (int i = 0; i < S; ++i) p.times(a[i][v]);
+        if (low[v] < 0x1p-126f) m[v].a = p.value();
       }
     }
 #pragma unroll
