@@ -631,7 +631,7 @@ _POLICY = ("embed", "recurrence", "recurrence_step", "shape_logits")
 
 
 def __getattr__(name):
-    # torch is imported only with the first function that needs it
+    # policy.py imports torch, which a caller of the C names may lack
     if name in _POLICY:
         from . import policy
         for n in _POLICY:

@@ -64,7 +64,7 @@ __device__ __forceinline__ uint32_t key_at(const void* p, int32_t bytes, int64_t
 
 // --------------------------------------------------------------- the lookup
 // Bound by memory: 65,536 of 131,072 rows of 1024 bf16 in 41 us (203 MB, 4.9
-// TB/s), 262,147 of 50,021 rows of 500 fp16 in 72 us (277 MB written as the
+// TB/s), 262,147 of 50,021 rows of 500 fp16 in 71 us (277 MB written as the
 // lines of rows of 1000 bytes, 109 MB read).
 constexpr int kPacks = 4;  // packs per thread
 

@@ -1,9 +1,9 @@
 // Penalties, bias and mask on logits, and their gradient (include/policy.h).
 //
 // Two shapes.  Many short rows (a quarter of a run of columns at most) that lie
-// one after another are taken several at a time: a tile is a run of whole rows addressed as one
-// array.  Longer (or strided) rows are cut into runs of columns, one row at a
-// time.  In both a thread owns fixed 16-byte packs of the tile, loads them
+// one after another are taken several at a time: a tile is a run of whole rows
+// addressed as one array.  Longer (or strided) rows are cut into runs of columns,
+// one row at a time.  In both a thread owns fixed 16-byte packs of the tile, loads them
 // first, and while they are on their way the workgroup counts the history's
 // tokens that fall into the tile in LDS (integer adds: their order does not
 // matter).  In the first shape rows and packs do not line up, and most packs
@@ -32,13 +32,13 @@ constexpr int kTile = 2048;      // elements of a tile of whole rows, at most
 constexpr int kTileRows = 128;   // its rows, at most
 constexpr int kRunPacks = 2;     // packs per thread of a run of columns
 // Workgroups of a launch over tiles: what is resident at once on 256 compute
-// units.  The kernel is held to 128 registers a thread (4 waves a SIMD): the
-// 4,096,000 x 45 training pass takes 884 us so, 960 us with the 150 that the
-// compiler takes by itself and 978 us at 96, where it spills.
+// units.  The kernel is held to 128 registers a thread (4 waves a SIMD): a
+// 4,096,000 x 45 training pass takes 880 us so, 960 with the 150 that the
+// compiler takes by itself and 978 at 96, where it spills.
 constexpr int kTileWaves = 4;
 constexpr int kTileGroups = 256 * kTileWaves;
-// (96 registers: the 4096 x 32003 training pass takes 344 us, 359 us at the
-// compiler's 104, 492 us at 80, where it spills)
+// (96 registers: a 4096 x 32,003 training pass takes 304 us so and with 128, 359
+// with 80, where it spills; 64 x 128,001 forward 13.0, 13.0 and 16.0)
 constexpr int kRunWaves = 5;
 // Workgroups of a launch over runs, about: four times what is resident, so that
 // a bias is loaded once for many rows.  4096 x 32,003 bf16 forward takes 110 us
@@ -263,8 +263,8 @@ __device__ __forceinline__ void load_tile(const LogitsArgs& p, int64_t r0, MaskW
   }
 }
 
-// 4,096,000 x 45 fp32 with bytes of mask and a history of 20 in 415 us (1.9 GB at
-// 4.6 TB/s), the gradient with dbias in 518 (2.6 GB at 5.0): bound by the four
+// 4,096,000 x 45 fp32 with a table of masks and a history of 20 in 419 us (1.9 GB
+// at 4.5 TB/s), the gradient with dbias in 517 (2.6 GB at 5.0): bound by the four
 // barriers of a tile at 4 workgroups a compute unit, and by memory.
 template <class T, int V, bool GRAD, int MODE>
 __global__ __launch_bounds__(kThreads, kTileWaves) void logits_rows_kernel(LogitsArgs p) {
@@ -482,10 +482,11 @@ __global__ __launch_bounds__(kThreads, kTileWaves) void logits_rows_kernel(Logit
 }
 
 // ------------------------------------------------ runs of columns of one row
-// 4096 x 32,003 bf16 with a mask of bits in 130 us (540 MB at 4.2 TB/s), the
-// gradient with dbias in 170 (3.2): bound by memory, whose lines the rows of
+// 4096 x 32,003 bf16 with a mask of bits in 129 us (540 MB at 4.2 TB/s), the
+// gradient with dbias in 169 (3.2): bound by memory, whose lines the rows of
 // 64,006 bytes do not respect, and by the counting's barriers.  64 x 128,001 with
-// a history of 2048 in 12.6: the latency of one round of workgroups.
+// a history of 2048 in 12.6: 2048 workgroups, of which 1280 are resident, so two
+// rounds of loads and counting, each of which reads its row's whole history.
 template <class T, int V, bool GRAD, int MASK>
 __global__ __launch_bounds__(kThreads, kRunWaves) void logits_runs_kernel(LogitsArgs p) {
   using raw = typename T::raw;

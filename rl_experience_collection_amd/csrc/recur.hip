@@ -9,9 +9,9 @@
 // so that the map then selects B instead of multiplying a possibly infinite
 // or NaN state by zero.
 //
-// A workgroup of W waves (8, or 16 where it is alone on its compute unit) owns a column of 64 lanes x V channels and
-// takes time in tiles, one slot of S steps per wave.  A wave loads its slot
-// into registers, folds it into its map, and leaves the map in LDS; after one
+// A workgroup of W waves (8, or 16 where it is alone on its compute unit) owns
+// a column of 64 lanes x V channels and takes time in tiles, one slot of S steps
+// per wave.  A wave loads its slot into registers, folds it into its map, and leaves the map in LDS; after one
 // barrier every wave folds the maps before its own onto the state that enters
 // the tile, replays its slot from registers and stores it.  So each element is
 // read and written once.
@@ -34,9 +34,8 @@
 // where the states do not.  A slot whose slope or b is no finite number for a
 // channel has no map there; one whose slope is below 2^-126 (faint) has one only
 // for states so small beside b that what the slope has lost is below b's
-// rounding.  Without a map the slot's wave runs it step by
-// step on the state that enters it, once the slots before have passed.  A
-// chained tile publishes no map of such a channel, or a faint one, and a walk
+// rounding.  Without a map the slot's wave runs it step by step on the state that
+// enters it, once the slots before have passed.  A chained tile publishes no map of such a channel, or a faint one, and a walk
 // that cannot use it waits for the state that leaves the tile.  Other channels
 // and episodes keep their results to the bit.  (Sigmoid gates are at most 1: no
 // product grows again, and what a faint slope loses stays below 2^-126 of the
@@ -51,11 +50,12 @@ namespace rl {
 
 namespace {
 
-// Steps per wave and tile (a slot's values stay in registers).  A chained tile is as long as a workgroup's registers allow: each
-// costs a walk, and the walks of a column follow each other.  Backward, lanes
-// of two channels take 4 steps: a 1024 x 500 x 64 bf16 pass 98 us against 110
-// with 8, 4096 x 64 x 128 fp32 169 against 183; lanes of one or four 8.
-// A gradient on kept states takes the steps between two of them.
+// Steps per wave and tile (a slot's values stay in registers).  A chained tile is
+// as long as a workgroup's registers allow: each costs a walk, and the walks of
+// a column follow each other.  Backward, lanes of two channels take 4 steps: 64 x
+// 4096 x 128 fp32 159 us with sigmoid gates against 170 with 8 (with linear ones
+// 136 and 133); lanes of one or four 8.  A gradient on kept states takes the
+// steps between two of them.
 constexpr int slot_steps(int v, bool back, bool chained, bool kept) {
   return chained ? (back ? 8 : 16) : back && v == 2 && !kept ? 4 : 8;
 }
@@ -65,7 +65,7 @@ constexpr int slot_steps(int v, bool back, bool chained, bool kept) {
 // (inputs of a constant and 1% noise: dgate off by 16% in bf16).  So the forward
 // pass keeps every eighth state in fp32, a quarter of what h takes, and the
 // gradient runs from there through x and gate, which it has in registers, and
-// reads no h: both passes of 500 x 8192 x 64 bf16 take 884 us, from h 941 (500 x
+// reads no h: both passes of 500 x 8192 x 64 bf16 take 886 us, from h 941 (500 x
 // 128 x 128 56 and 55, 500 x 1024 x 64 119 and 130).
 constexpr int kKeep = 8;
 template <class T, bool SIG>
@@ -586,9 +586,10 @@ __device__ __forceinline__ void fold_forward(const float (&a)[S][V], const float
 }
 
 // Bound by memory where the columns fill the chip: 500 x 8192 x 64 bf16 in 318
-// us (1.58 GB at 5.0 TB/s); 500 x 128 x 128 fp32, whose 256 columns give each
-// compute unit one workgroup, in 25 (98 MB at 3.9 TB/s).  Chained, by the states'
-// way from tile to tile: 65,537 x 2 x 1000 fp16 in 260 us (786 MB at 3.0 TB/s).
+// us (1.58 GB at 5.0 TB/s; 341 with the kept states, 1.71 GB); 500 x 128 x 128
+// fp32, whose 256 columns give each compute unit one workgroup, in 26 (98 MB at
+// 3.7 TB/s).  Chained, by the states' way from tile to tile: 65,537 x 2 x 1000
+// fp16 in 262 us (786 MB at 3.0 TB/s).
 template <class T, int V, bool SIG, bool CHAIN, bool OFF32, int W>
 __global__ __launch_bounds__(64 * W) void recur_forward_kernel(const RecurArgs p) {
   constexpr bool KEEPS = kKeeps<T, SIG>;
@@ -743,7 +744,7 @@ __device__ __forceinline__ void fold_backward(const float (&a)[S][V], const floa
   settle_slopes<S, V, SIG>(a, low, CUT && done != 0, m);
 }
 
-// Bound like the forward pass: 500 x 8192 x 64 bf16 in 641 us (3.15 GB at 4.9
+// Bound like the forward pass: 500 x 8192 x 64 bf16 in 551 us (2.76 GB at 5.0
 // TB/s), 500 x 128 x 128 fp32 with linear gates in 36 (164 MB at 4.5 TB/s).
 template <class T, int V, bool SIG, bool CHAIN, bool OFF32, int W>
 __global__ __launch_bounds__(64 * W) void recur_backward_kernel(const RecurArgs p) {
