@@ -2,47 +2,11 @@
 // the launches.  Nothing is allocated and nothing is kept between calls.
 #include <hip/hip_runtime.h>
 
-#include <cstdarg>
-#include <cstdio>
+#include "checks.hpp"
 
-#include "elem.hpp"
-#include "policy.hpp"
+using namespace rl;
 
 namespace {
-
-int fail(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  std::vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  return rl::set_error(code, buf);
-}
-
-int launched(hipError_t e, const char* what) {
-  return e == hipSuccess ? ROLLOUT_OK : fail(ROLLOUT_EHIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-bool known_dtype(int32_t d) { return d == POLICY_F32 || d == POLICY_BF16 || d == POLICY_F16; }
-size_t element_bytes(int32_t d) { return d == POLICY_F32 ? 4 : 2; }
-
-// A buffer of elements: not NULL and aligned to its element.
-int check_buffer(const char* who, const char* name, const void* p, size_t bytes) {
-  if (!p) return fail(ROLLOUT_EINVAL, "%s: %s is NULL", who, name);
-  if (!rl::aligned_to(p, bytes))
-    return fail(ROLLOUT_EINVAL, "%s: %s is not aligned to its %zu-byte elements", who, name, bytes);
-  return ROLLOUT_OK;
-}
-// The same where NULL is allowed.
-int check_optional(const char* who, const char* name, const void* p, size_t bytes) {
-  return p ? check_buffer(who, name, p, bytes) : ROLLOUT_OK;
-}
-
-#define RL_CHECK(call)   \
-  do {                   \
-    const int _rc = (call); \
-    if (_rc) return _rc; \
-  } while (0)
 
 int check_recur_sizes(const char* who, int32_t steps, int32_t rows, int32_t width, int32_t dtype) {
   if (steps < 0 || rows < 0 || width < 0)
@@ -60,21 +24,6 @@ int check_form(const char* who, int32_t form) {
   if (form != RECUR_LINEAR && form != RECUR_SIGMOID)
     return fail(ROLLOUT_EINVAL, "%s: unknown form %d", who, form);
   return ROLLOUT_OK;
-}
-
-int check_strides(const char* who, const char* name, int64_t step, int64_t row) {
-  if (step < 0 || row < 0)
-    return fail(ROLLOUT_EINVAL, "%s: negative stride of %s (%lld, %lld)", who, name, (long long)step,
-                (long long)row);
-  return ROLLOUT_OK;
-}
-
-int check_workspace(const char* who, int64_t need, const void* workspace, int64_t bytes) {
-  if (need == 0) return ROLLOUT_OK;
-  if (!workspace || bytes < need)
-    return fail(ROLLOUT_EINVAL, "%s: workspace of %lld bytes needed, %lld given", who,
-                (long long)need, workspace ? (long long)bytes : 0LL);
-  return check_buffer(who, "workspace", workspace, 16);
 }
 
 // Of a gradient that forms the states again.
@@ -182,14 +131,6 @@ int check_index(const char* who, const void* index, int32_t bytes) {
   if (bytes != 4 && bytes != 8)
     return fail(ROLLOUT_EINVAL, "%s: index_bytes must be 4 or 8 (got %d)", who, bytes);
   return check_buffer(who, "index", index, (size_t)bytes);
-}
-
-// Rows of at least `width` elements, one after another.
-int check_rows(const char* who, const char* name, int64_t row, int64_t width) {
-  if (row < width)
-    return fail(ROLLOUT_EINVAL, "%s: rows of %s are %lld apart, closer than their width %lld", who,
-                name, (long long)row, (long long)width);
-  return ROLLOUT_OK;
 }
 
 int check_logits(const char* who, const logits_args* a, bool read_logits) {
