@@ -16,7 +16,10 @@ The functions carry the C names:
     (include/per.h).
 The operators of a policy with memory (include/policy.h) are `embed`,
 `recurrence`, `recurrence_step` and `shape_logits` (policy.py); all but the
-step take part in torch's autograd.
+step take part in torch's autograd.  Those of a residual block with a selective
+memory (include/block.h) are `causal_conv`, `causal_conv_step`,
+`selective_scan`, `selective_scan_step`, `residual_norm` and `dropout`
+(block.py); likewise.
 There are also helpers: `alloc_outputs`, `alloc_dqn_outputs` and the `Collector` and
 `DqnCollector` and `PerSampler` convenience classes.
 """
@@ -151,8 +154,9 @@ def load_library(path: str = LIB_PATH):
     except ImportError:
         pass
     else:
-        from . import policy
+        from . import block, policy
         policy.declare(L)
+        block.declare(L)
     _lib = L
     return L
 
@@ -628,13 +632,20 @@ class PerSampler:
 
 # ---------------------------------------------------------- policies with memory
 _POLICY = ("embed", "recurrence", "recurrence_step", "shape_logits")
+_BLOCK = ("causal_conv", "causal_conv_step", "selective_scan", "selective_scan_step", "residual_norm",
+          "dropout")
 
 
 def __getattr__(name):
-    # policy.py imports torch, which a caller of the C names may lack
+    # policy.py and block.py import torch, which a caller of the C names may lack
     if name in _POLICY:
         from . import policy
         for n in _POLICY:
             globals()[n] = getattr(policy, n)
+        return globals()[name]
+    if name in _BLOCK:
+        from . import block
+        for n in _BLOCK:
+            globals()[n] = getattr(block, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

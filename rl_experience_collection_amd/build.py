@@ -9,7 +9,8 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(os.path.dirname(PKG), "_build", "rollout")
 LIB = os.path.join(PKG, "librollout.so")
 SOURCES = ["abi.hip", "pack.hip", "rollout.hip", "value.hip", "gae.hip", "dqn.hip", "per.hip",
-           "policy_abi.hip", "embed.hip", "recur.hip", "logits.hip"]
+           "policy_abi.hip", "embed.hip", "recur.hip", "logits.hip",
+           "block_abi.hip", "conv.hip", "scan.hip", "scan_grad.hip", "norm.hip", "drop.hip", "sums.hip"]
 # measurement kernels used by bench.py only, in a library of their own
 PROBE_LIB = os.path.join(PKG, "libbenchprobes.so")
 PROBE_SOURCES = ["bench_probes.hip"]

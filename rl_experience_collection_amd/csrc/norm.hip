@@ -1,0 +1,503 @@
+// The norms after and before a block, with its gate, dropout, scales and
+// residual between them, and their gradient (include/block.h).
+//
+// A row lies in the registers of a group of threads (8 to 512, 8 or 16
+// elements each), so that it is read once for both norms; the next row's loads
+// are in flight meanwhile.  Sums over a row meet by lane exchanges, beyond a
+// wave in LDS.  The gradient forms the row again from the forward call's
+// inputs and the two stored factors (8 bytes a row), rather than from a
+// stream that was rounded when it was stored, and a thread sums the weights'
+// gradients of its own columns over all rows that it takes.
+#include <algorithm>
+
+#include "block.hpp"
+#include "elem.hpp"
+#include "philox.hpp"
+
+namespace rl {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504f;
+
+struct NormRun {
+  norm_grad_args g;  // forward: g.f alone
+  DropRule rule;
+  void *stream, *normed;  // forward
+  float* stats;
+  int64_t stream_row, normed_row;
+  float inv_width;
+  bool past;      // outputs are stored past the caches
+  float* params;  // gradient: [workgroups][2 or 3][D]
+};
+
+enum GateKind { kNoGate, kRowGate, kChannelGate };
+
+// ------------------------------------------------------------ sums of a row
+template <int CTRL>
+__device__ __forceinline__ float lane_dpp(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
+}
+// Over 8, 16 or 64 lanes; every lane gets it.
+template <int N>
+__device__ __forceinline__ float lanes_sum(float x) {
+  x += lane_dpp<0xB1>(x);   // quad_perm 1, 0, 3, 2
+  x += lane_dpp<0x4E>(x);   // quad_perm 2, 3, 0, 1
+  x += lane_dpp<0x141>(x);  // row_half_mirror
+  if constexpr (N >= 16) x += lane_dpp<0x140>(x);  // row_mirror
+  if constexpr (N == 64) {
+    const int lane = threadIdx.x & 63;
+    x += lane_xor16f(x, lane);
+    x += lane_xor32f(x, lane);
+  }
+  return x;
+}
+
+constexpr int threads_of(int TPR) { return TPR > 256 ? TPR : 256; }
+
+// Sums over the TPR threads of a row.  The two halves of the LDS array are
+// used in turn: a wave that writes one again has passed the barrier of the
+// other, which no wave reaches before it has read the first.
+template <int TPR>
+struct RowSum {
+  int turn = 0;
+  __device__ __forceinline__ float operator()(float x, float (&s)[2][8]) {
+    if constexpr (TPR <= 64) {
+      return lanes_sum<TPR>(x);
+    } else {
+      x = lanes_sum<64>(x);
+      if ((threadIdx.x & 63) == 0) s[turn][threadIdx.x >> 6] = x;
+      __syncthreads();
+      float sum = s[turn][0];
+#pragma unroll
+      for (int i = 1; i < TPR / 64; ++i) sum += s[turn][i];
+      turn ^= 1;
+      return sum;
+    }
+  }
+};
+
+// ---------------------------------------------------------- a thread's share
+// Packs of V elements: start, and how many of its first elements belong to the
+// pack before (a row's last pack is moved back into the row).
+template <class T, int V, int TPR, int K>
+struct Share {
+  int32_t at[K], fresh[K];
+  bool has[K];
+  __device__ __forceinline__ explicit Share(int32_t D) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int32_t e = ((int32_t)(threadIdx.x % TPR) + TPR * i) * V;
+      at[i] = min(e, D - V);
+      fresh[i] = e - at[i];
+      has[i] = e < D;
+    }
+  }
+  using Row = Pack<T, V>[K];
+  __device__ __forceinline__ void load(const void* p, int64_t row, int64_t r, Row& x) const {
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      x[i] = load_pack<T, V>(static_cast<const typename T::raw*>(p) + r * row + at[i]);
+  }
+  __device__ __forceinline__ void store(void* p, int64_t row, int64_t r, const float (&f)[K][V], bool past) const {
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      if (has[i])
+        store_pack<T, V>(static_cast<typename T::raw*>(p) + r * row + at[i], narrow_pack<T, V>(f[i]), past);
+  }
+  __device__ __forceinline__ void weights(const float* w, float (&f)[K][V]) const {
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) f[i][v] = w ? w[at[i] + v] : 1.0f;
+  }
+  // The sum of the products, each element once.
+  __device__ __forceinline__ float dot(const float (&a)[K][V], const float (&b)[K][V]) const {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) sum = v >= fresh[i] ? __builtin_fmaf(a[i][v], b[i][v], sum) : sum;
+    return sum;
+  }
+};
+
+// Which of the V elements from i are kept: bit j for element i + j.
+template <int V>
+__device__ __forceinline__ uint32_t kept_bits(const DropRule& rule, uint64_t seed, uint64_t i) {
+  const uint32_t off = (uint32_t)i & 7;
+  const uint4 d = drop_draws(rule, seed, i >> 3);
+  uint32_t bits = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) bits |= (draw_of(d, j) >= rule.drop ? 1u : 0u) << j;
+  if (off + V > 8) {
+    const uint4 n = drop_draws(rule, seed, (i >> 3) + 1);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bits |= (draw_of(n, j) >= rule.drop ? 1u : 0u) << (8 + j);
+  }
+  return bits >> off;
+}
+
+// act(g) and its slope
+__device__ __forceinline__ void activate(int32_t kind, float g, float& act, float& slope) {
+  if (kind == BLOCK_NONE) {
+    act = g;
+    slope = 1.0f;
+    return;
+  }
+  const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * kLog2e));
+  if (kind == BLOCK_SIGMOID) {
+    act = s;
+    slope = s * (1.0f - s);
+  } else {
+    act = g * s;
+    slope = s * __builtin_fmaf(g, 1.0f - s, 1.0f);
+  }
+}
+
+template <class T, int V, int TPR, int K, int GATE>
+__global__ void __launch_bounds__(threads_of(TPR)) norm_forward_kernel(const NormRun q) {
+  const norm_args& a = q.g.f;
+  constexpr int kRows = threads_of(TPR) / TPR;
+  __shared__ float s_sum[2][8];
+  const Share<T, V, TPR, K> own(a.width);
+  RowSum<TPR> row_sum;
+  const bool branch = a.branch != nullptr, drops = q.rule.drop != 0;
+  const uint64_t seed = q.rule.seed_at ? *q.rule.seed_at : q.rule.seed;
+  float w[K][V], bw[K][V], gc[K][V];
+  own.weights(a.weight, w);
+  own.weights(a.branch_weight, bw);
+  if (GATE == kChannelGate) {
+    own.weights(static_cast<const float*>(a.gate), gc);
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float slope;
+        activate(a.activation, gc[i][v], gc[i][v], slope);
+      }
+  }
+  typename Share<T, V, TPR, K>::Row res, br, ga;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+  const auto fetch = [&](int64_t at) {
+    at = at < a.rows ? at : a.rows - 1;
+    own.load(a.residual, a.residual_row, at, res);
+    if (branch) own.load(a.branch, a.branch_row, at, br);
+    if (GATE == kRowGate) own.load(a.gate, a.gate_row, at, ga);
+  };
+  fetch(r);
+  // (all of a workgroup's threads go round as often: they meet in row_sum)
+  for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.rows; first += step, r += step) {
+    float s[K][V], b[K][V], g[K][V];
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      widen_pack<T, V>(res[i], s[i]);
+      if (branch) widen_pack<T, V>(br[i], b[i]);
+      if (GATE == kRowGate) widen_pack<T, V>(ga[i], g[i]);
+    }
+    if (first + step < a.rows) fetch(r + step);
+    float inv_b = 1.0f;
+    if (branch && a.branch_norm)
+      inv_b = __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum(own.dot(b, b), s_sum), q.inv_width, a.eps));
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      uint32_t kept = ~0u;
+      if (branch && drops) kept = kept_bits<V>(q.rule, seed, (uint64_t)(r * a.width + own.at[i]));
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        s[i][v] *= a.residual_scale;
+        if (!branch) continue;
+        float z = b[i][v] * inv_b * bw[i][v];
+        if (GATE == kChannelGate) z *= gc[i][v];
+        if (GATE == kRowGate) {
+          float act, slope;
+          activate(a.activation, g[i][v], act, slope);
+          z *= act;
+        }
+        if (drops) z = (kept >> v) & 1u ? z * q.rule.scale : 0.0f;
+        s[i][v] = __builtin_fmaf(a.branch_scale, z, s[i][v]);
+      }
+    }
+    const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum(own.dot(s, s), s_sum), q.inv_width, a.eps));
+    if (r < a.rows) {
+      if (q.stream) own.store(q.stream, q.stream_row, r, s, q.past);
+      if (q.normed) {
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v) s[i][v] *= inv * w[i][v];
+        own.store(q.normed, q.normed_row, r, s, q.past);
+      }
+      if (q.stats && threadIdx.x % TPR == 0) {
+        q.stats[2 * r] = inv_b;
+        q.stats[2 * r + 1] = inv;
+      }
+    }
+  }
+}
+
+template <class T, int V, int TPR, int K, int GATE>
+__global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const NormRun q) {
+  const norm_grad_args& p = q.g;
+  const norm_args& a = p.f;
+  constexpr int kThreads = threads_of(TPR), kRows = kThreads / TPR;
+  __shared__ float s_sum[2][8];
+  const Share<T, V, TPR, K> own(a.width);
+  RowSum<TPR> row_sum;
+  const bool branch = a.branch != nullptr, drops = q.rule.drop != 0;
+  const uint64_t seed = q.rule.seed_at ? *q.rule.seed_at : q.rule.seed;
+  float w[K][V], bw[K][V], gc[K][V], gs[K][V];
+  float dw[K][V], dbw[K][V], dgc[K][V];
+  own.weights(a.weight, w);
+  own.weights(a.branch_weight, bw);
+  if (GATE == kChannelGate) own.weights(static_cast<const float*>(a.gate), gc);
+#pragma unroll
+  for (int i = 0; i < K; ++i)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      dw[i][v] = dbw[i][v] = dgc[i][v] = 0.0f;
+      if (GATE == kChannelGate) activate(a.activation, gc[i][v], gc[i][v], gs[i][v]);
+    }
+  typename Share<T, V, TPR, K>::Row res, br, ga, ds, dn;
+  float inv_b_next = 1.0f, inv_next = 1.0f;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+  const auto fetch = [&](int64_t at) {
+    at = at < a.rows ? at : a.rows - 1;
+    own.load(a.residual, a.residual_row, at, res);
+    if (branch) own.load(a.branch, a.branch_row, at, br);
+    if (GATE == kRowGate) own.load(a.gate, a.gate_row, at, ga);
+    if (p.dstream) own.load(p.dstream, p.dstream_row, at, ds);
+    if (p.dnormed) own.load(p.dnormed, p.dnormed_row, at, dn);
+    inv_b_next = p.stats[2 * at];
+    inv_next = p.stats[2 * at + 1];
+  };
+  fetch(r);
+  for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.rows; first += step, r += step) {
+    const bool mine = r < a.rows;
+    const float inv_b = inv_b_next, inv = inv_next;
+    // s: the stream; u: the normed branch; act, slope: of the gate; d: dstream
+    float s[K][V], u[K][V], act[K][V], slope[K][V], d[K][V], e[K][V];
+    uint32_t kept[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      widen_pack<T, V>(res[i], s[i]);
+      if (branch) widen_pack<T, V>(br[i], u[i]);
+      if (GATE == kRowGate) widen_pack<T, V>(ga[i], act[i]);
+      if (p.dstream) widen_pack<T, V>(ds[i], d[i]);
+      if (p.dnormed) widen_pack<T, V>(dn[i], e[i]);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        // (rows past the end repeat the last one: their gradients count 0)
+        if (!p.dstream || !mine) d[i][v] = 0.0f;
+        if (!p.dnormed || !mine) e[i][v] = 0.0f;
+      }
+    }
+    if (first + step < a.rows) fetch(r + step);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      kept[i] = ~0u;
+      if (branch && drops) kept[i] = kept_bits<V>(q.rule, seed, (uint64_t)(r * a.width + own.at[i]));
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        s[i][v] *= a.residual_scale;
+        if (branch) {
+          u[i][v] *= inv_b;
+          float z = u[i][v] * bw[i][v];
+          if (GATE == kRowGate) {
+            activate(a.activation, act[i][v], act[i][v], slope[i][v]);
+            z *= act[i][v];
+          }
+          if (GATE == kChannelGate) z *= gc[i][v];
+          if (drops) z = (kept[i] >> v) & 1u ? z * q.rule.scale : 0.0f;
+          s[i][v] = __builtin_fmaf(a.branch_scale, z, s[i][v]);
+        }
+        s[i][v] *= inv;
+        dw[i][v] = __builtin_fmaf(e[i][v], s[i][v], dw[i][v]);
+        e[i][v] *= w[i][v];
+      }
+    }
+    if (p.dnormed) {
+      const float mean = row_sum(own.dot(e, s), s_sum) * q.inv_width;
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[i][v] = __builtin_fmaf(inv, __builtin_fmaf(-s[i][v], mean, e[i][v]), d[i][v]);
+    }
+    if (p.dresidual && mine) {
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[i][v] = a.residual_scale * d[i][v];
+      own.store(p.dresidual, a.width, r, s, q.past);
+    }
+    if (!branch) continue;
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float dz = a.branch_scale * d[i][v];
+        if (drops) dz = (kept[i] >> v) & 1u ? dz * q.rule.scale : 0.0f;
+        if (GATE == kRowGate) s[i][v] = dz * (u[i][v] * bw[i][v]) * slope[i][v];
+        if (GATE == kChannelGate) dgc[i][v] = __builtin_fmaf(dz * (u[i][v] * bw[i][v]), gs[i][v], dgc[i][v]);
+        const float du = GATE == kRowGate ? dz * act[i][v] : GATE == kChannelGate ? dz * gc[i][v] : dz;
+        dbw[i][v] = __builtin_fmaf(du, u[i][v], dbw[i][v]);
+        e[i][v] = du * bw[i][v];
+      }
+    if (GATE == kRowGate && p.dgate && mine) own.store(p.dgate, a.width, r, s, q.past);
+    if (a.branch_norm) {
+      const float mean = row_sum(own.dot(e, u), s_sum) * q.inv_width;
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) e[i][v] = inv_b * __builtin_fmaf(-u[i][v], mean, e[i][v]);
+    }
+    if (p.dbranch && mine) own.store(p.dbranch, a.width, r, e, q.past);
+  }
+  // the workgroup's sums over its rows, pack by pack
+  __shared__ float s_part[kRows > 1 ? kThreads : 1][V];
+  const auto put = [&](int which, const float(&f)[K][V]) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      float* out = q.params + ((int64_t)blockIdx.x * (GATE == kChannelGate ? 3 : 2) + which) * a.width;
+      if constexpr (kRows == 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (v >= own.fresh[i]) out[own.at[i] + v] = f[i][v];
+      } else {
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; ++v) s_part[threadIdx.x][v] = f[i][v];
+        __syncthreads();
+        for (int32_t c = threadIdx.x; c < TPR * V; c += kThreads) {
+          const int32_t start = (c / V + TPR * i) * V, at = min(start, a.width - V);
+          if (c % V < start - at) continue;
+          float sum = 0.0f;
+          for (int32_t row = 0; row < kRows; ++row) sum += s_part[row * TPR + c / V][c % V];
+          out[at + c % V] = sum;
+        }
+      }
+    }
+  };
+  put(0, dw);
+  put(1, dbw);
+  if (GATE == kChannelGate) put(2, dgc);
+}
+
+// Threads of a row and elements of a thread: the fewest that hold the row.
+struct Shape {
+  int32_t threads, elements;
+};
+Shape shape_of(int32_t D) {
+  return D <= 64     ? Shape{8, 8}
+         : D <= 128  ? Shape{16, 8}
+         : D <= 512  ? Shape{64, 8}
+         : D <= 2048 ? Shape{256, 8}
+         : D <= 4096 ? Shape{512, 8}
+                     : Shape{512, 16};
+}
+// Workgroups: each takes many rows, so that weights are read and their
+// gradients written once for all of them.
+constexpr int64_t kForwardGroups = 256 * 8, kBackwardGroups = 256 * 4;
+uint32_t groups_of(int64_t R, int32_t D, bool grad) {
+  const int32_t rows = std::max(1, 256 / shape_of(D).threads);
+  const int64_t most = grad ? kBackwardGroups : kForwardGroups;
+  return (uint32_t)std::min((R + rows - 1) / rows, most);
+}
+
+template <class T, int V, int TPR, int K, int GATE, bool GRAD>
+void launch(const NormRun& q, hipStream_t stream) {
+  const dim3 grid(groups_of(q.g.f.rows, q.g.f.width, GRAD)), threads(threads_of(TPR));
+  if constexpr (GRAD)
+    norm_backward_kernel<T, V, TPR, K, GATE><<<grid, threads, 0, stream>>>(q);
+  else
+    norm_forward_kernel<T, V, TPR, K, GATE><<<grid, threads, 0, stream>>>(q);
+}
+template <class T, int GATE, bool GRAD>
+void launch_shape(const NormRun& q, hipStream_t stream) {
+  constexpr int V = 16 / T::kBytes, K = 8 / V;
+  const Shape s = shape_of(q.g.f.width);
+  if (q.g.f.width < V) return launch<T, 1, 8, 1, GATE, GRAD>(q, stream);
+  if (s.threads == 8) return launch<T, V, 8, K, GATE, GRAD>(q, stream);
+  if (s.threads == 16) return launch<T, V, 16, K, GATE, GRAD>(q, stream);
+  if (s.threads == 64) return launch<T, V, 64, K, GATE, GRAD>(q, stream);
+  if (s.threads == 256) return launch<T, V, 256, K, GATE, GRAD>(q, stream);
+  if (s.elements == 8) return launch<T, V, 512, K, GATE, GRAD>(q, stream);
+  return launch<T, V, 512, 2 * K, GATE, GRAD>(q, stream);
+}
+template <class T, bool GRAD>
+void launch_gate(const NormRun& q, hipStream_t stream) {
+  const norm_args& a = q.g.f;
+  if (!a.gate || !a.branch) return launch_shape<T, kNoGate, GRAD>(q, stream);
+  if (a.gate_row) return launch_shape<T, kRowGate, GRAD>(q, stream);
+  return launch_shape<T, kChannelGate, GRAD>(q, stream);
+}
+template <bool GRAD>
+void launch_any(const NormRun& q, hipStream_t stream) {
+  if (q.g.f.dtype == POLICY_F32)
+    launch_gate<F32, GRAD>(q, stream);
+  else if (q.g.f.dtype == POLICY_BF16)
+    launch_gate<BF16, GRAD>(q, stream);
+  else
+    launch_gate<F16, GRAD>(q, stream);
+}
+
+int64_t up(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+
+NormRun run_of(const norm_args& a) {
+  NormRun q = {};
+  q.g.f = a;
+  q.rule = drop_rule(a.drop, a.seed, a.seed_at, a.offset);
+  q.inv_width = (float)(1.0 / a.width);
+  q.past = a.rows * a.width * (a.dtype == POLICY_F32 ? 4 : 2) > kPastBytes;
+  return q;
+}
+
+}  // namespace
+
+hipError_t norm_forward_launch(const norm_args& a, void* stream_out, int64_t stream_row,
+                               void* normed, int64_t normed_row, float* stats, hipStream_t stream) {
+  NormRun q = run_of(a);
+  q.stream = stream_out;
+  q.stream_row = stream_row;
+  q.normed = normed;
+  q.normed_row = normed_row;
+  q.stats = stats;
+  launch_any<false>(q, stream);
+  return hipGetLastError();
+}
+
+int64_t norm_workspace_bytes(int64_t R, int32_t D, int32_t dtype) {
+  if (R == 0) return 0;
+  const int64_t groups = groups_of(R, D, true);
+  return up(groups * 3 * D * 4) + up(sums_floats(groups, 3 * D) * 4);
+}
+
+hipError_t norm_backward_launch(const norm_grad_args& g, hipStream_t stream) {
+  const norm_args& a = g.f;
+  const int64_t D = a.width;
+  const bool channel = a.gate && a.gate_row == 0;
+  if (a.rows == 0) {
+    hipError_t e = hipSuccess;
+    if (g.dweight) e = copy_or_clear_launch(nullptr, g.dweight, D * 4, stream);
+    if (e == hipSuccess && g.dbranch_weight) e = copy_or_clear_launch(nullptr, g.dbranch_weight, D * 4, stream);
+    if (e == hipSuccess && channel && g.dgate) e = copy_or_clear_launch(nullptr, g.dgate, D * 4, stream);
+    return e;
+  }
+  NormRun q = run_of(a);
+  q.g = g;
+  q.params = static_cast<float*>(g.workspace);
+  launch_any<true>(q, stream);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !(g.dweight || g.dbranch_weight || (channel && g.dgate))) return e;
+  const int64_t groups = groups_of(a.rows, a.width, true);
+  const int32_t d = a.width, columns = (channel ? 3 : 2) * d;
+  const SumsOut out = {{g.dweight, g.dbranch_weight, channel ? static_cast<float*>(g.dgate) : nullptr},
+                       {d, 2 * d, columns}};
+  return sums_launch(q.params, groups, columns,
+                     reinterpret_cast<float*>(static_cast<char*>(g.workspace) + up(groups * columns * 4)), out,
+                     stream);
+}
+
+}  // namespace rl

@@ -1,0 +1,350 @@
+// Selective state space scan: forward and single step (include/block.h).
+//
+// Per state of a step the scan takes an exponent's product, an exp2 (a
+// quarter-rate instruction), the input's product and two multiply-adds: eight
+// issue slots, beside some sixty per channel and step for softplus, gate and
+// conversions.  At 16 states that, not memory, bounds it.
+#include "scan.hpp"
+
+namespace rl {
+
+namespace {
+
+struct ScanRun {
+  scan_args a;
+  ScanPlan p;
+  ScanSummary sum;
+};
+
+// One unit's x, delta and gate of a lane's channel, as loaded.
+template <class T>
+struct UnitColumns {
+  typename T::raw x[kUnit], d[kUnit], z[kUnit];
+  __device__ __forceinline__ void load(const scan_args& a, const ScanWave& k, int32_t t0, bool gate) {
+    using raw = typename T::raw;
+    const raw* px = static_cast<const raw*>(a.x) + k.n * a.x_row;
+    const raw* pd = static_cast<const raw*>(a.delta) + k.n * a.delta_row;
+    const raw* pz = static_cast<const raw*>(a.gate) + k.n * a.gate_row;
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) {
+      const int32_t t = min(t0 + i, a.steps - 1);
+      x[i] = (px + t * a.x_step)[k.channel];
+      d[i] = (pd + t * a.delta_step)[k.channel];
+      if (gate) z[i] = (pz + t * a.gate_step)[k.channel];
+    }
+  }
+};
+
+// What enters chunk `chunk`: the states that the chunks before leave, one
+// after another.
+__device__ __forceinline__ void enter_chunk(const ScanRun& q, const ScanWave& k, const float (&rate)[4][4],
+                                            float (&h)[4][4]) {
+  const scan_args& a = q.a;
+  const int64_t nd = (int64_t)a.rows * a.width;
+  for (int32_t i = 0; i < k.chunk; ++i) {
+    const bool cut = q.sum.cut[(int64_t)i * a.rows + k.n] != 0;
+    const int64_t at = i * nd + (int64_t)k.n * a.width;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int64_t c = at + k.quad_channel(q.p, r);
+      float own[4];
+      load_states(q.sum.state + c * a.states, k.s0, a.states, own);
+      const float total = q.sum.total[c];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        // (a state of 0 stays 0 under any decay)
+        const float left = h[r][s] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(total * rate[r][s]) * h[r][s];
+        h[r][s] = cut ? own[s] : left + own[s];
+      }
+    }
+  }
+}
+
+// A chunk of the scan.  SUMMARY: from a state of zero, without outputs.
+template <class T, int NB, bool SUMMARY>
+__global__ void __launch_bounds__(64 * NB) scan_forward_kernel(const ScanRun q) {
+  const scan_args& a = q.a;
+  const ScanWave k(q.p, a.rows, a.groups, a.states);
+  __shared__ float s_bc[NB][kUnit][32];
+  __shared__ float s_part[NB > 1 && !SUMMARY ? 2 : 1][NB > 1 && !SUMMARY ? NB : 1][kUnit][64];
+  const int32_t L = a.steps, S = a.states;
+  const int32_t u0 = k.chunk * q.p.chunk_units, u1 = min(u0 + q.p.chunk_units, q.p.units);
+  const bool gated = !SUMMARY && a.gate != nullptr;
+
+  float rate[4][4], h[4][4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int32_t c = k.quad_channel(q.p, r);
+    load_states(a.rate + (int64_t)c * S, k.s0, S, rate[r]);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      rate[r][s] *= kLog2e;
+      h[r][s] = 0.0f;
+    }
+    if (!SUMMARY && a.state) load_states(a.state + ((int64_t)k.n * a.width + c) * S, k.s0, S, h[r]);
+  }
+  if constexpr (!SUMMARY) {
+    if (k.chunk > 0) enter_chunk(q, k, rate, h);
+  }
+  const float bias = a.delta_bias ? a.delta_bias[k.channel] : 0.0f;
+  const float skip = a.skip ? a.skip[k.channel] : 0.0f;
+  float total = 0.0f;
+  uint32_t any_cut = 0;
+
+  UnitInputs<T> in;
+  UnitColumns<T> col;
+  in.load(a, k, u0 * kUnit);
+  col.load(a, k, u0 * kUnit, gated);
+  uint32_t cuts = unit_cuts(a, k, u0 * kUnit);
+  for (int32_t u = u0; u < u1; ++u) {
+    const int32_t t0 = u * kUnit;
+    if constexpr (!SUMMARY) {
+      if (a.kept) {
+        const int64_t at = ((int64_t)u * a.rows + k.n) * a.width;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (k.quad_has(q.p, r)) store_states(a.kept + (at + k.quad_channel(q.p, r)) * S, k.s0, S, h[r]);
+      }
+    }
+    wave_sync();  // (the reads of the unit before)
+    in.put(s_bc[k.w], k.lane);
+    wave_sync();
+    float x[kUnit], dt[kUnit], du[kUnit], z[kUnit], y[kUnit];
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) {
+      x[i] = T::widen(col.x[i]);
+      const float v = T::widen(col.d[i]) + bias;
+      float E;
+      dt[i] = a.softplus ? softplus_of(v, E) : v;
+      du[i] = dt[i] * x[i];
+      if (t0 + i >= L) dt[i] = du[i] = 0.0f;  // past the end: the state stays
+      if (SUMMARY) total += dt[i];
+      if (gated) z[i] = T::widen(col.z[i]);
+    }
+    const uint32_t cut = cuts;
+    any_cut |= cut;
+    if (u + 1 < u1) {
+      in.load(a, k, t0 + kUnit);
+      col.load(a, k, t0 + kUnit, gated);
+      cuts = unit_cuts(a, k, t0 + kUnit);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) {
+      if ((cut >> i) & 1u) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) h[r][s] = 0.0f;
+      }
+      const float4 b4 = *reinterpret_cast<const float4*>(&s_bc[k.w][i][4 * k.j]);
+      const float b[4] = {b4.x, b4.y, b4.z, b4.w};
+      const float dts[4] = {quad_get<0>(dt[i]), quad_get<1>(dt[i]), quad_get<2>(dt[i]), quad_get<3>(dt[i])};
+      const float dus[4] = {quad_get<0>(du[i]), quad_get<1>(du[i]), quad_get<2>(du[i]), quad_get<3>(du[i])};
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          h[r][s] = __builtin_fmaf(__builtin_amdgcn_exp2f(dts[r] * rate[r][s]), h[r][s], dus[r] * b[s]);
+      if constexpr (!SUMMARY) {
+        const float4 c4 = *reinterpret_cast<const float4*>(&s_bc[k.w][i][16 + 4 * k.j]);
+        const float c[4] = {c4.x, c4.y, c4.z, c4.w};
+        float part[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          part[r] = c[0] * h[r][0];
+#pragma unroll
+          for (int s = 1; s < 4; ++s) part[r] = __builtin_fmaf(c[s], h[r][s], part[r]);
+        }
+        y[i] = quad_turn(part, k.lane);
+      }
+    }
+    if constexpr (!SUMMARY) {
+      if constexpr (NB > 1) {
+        float(&buf)[NB][kUnit][64] = s_part[u & 1];
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) buf[k.w][i][k.lane] = y[i];
+        __syncthreads();  // (a wave that is a unit ahead writes the other half)
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) {
+          if (i % NB != k.w) continue;
+          y[i] = buf[0][i][k.lane];
+#pragma unroll
+          for (int v = 1; v < NB; ++v) y[i] += buf[v][i][k.lane];
+        }
+      }
+      typename T::raw* py = static_cast<typename T::raw*>(a.y) + k.n * a.y_row;
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i) {
+        if (NB > 1 && i % NB != k.w) continue;
+        if (t0 + i >= L) continue;
+        float v = __builtin_fmaf(skip, x[i], y[i]);
+        if (gated) v *= z[i] * sigmoid_of(z[i]);
+        if (k.mine) (py + (t0 + i) * a.y_step)[k.channel] = T::narrow(v);
+      }
+    }
+  }
+
+  const int64_t row = (int64_t)k.n * a.width;
+  if constexpr (SUMMARY) {
+    const int64_t at = (int64_t)k.chunk * a.rows * a.width + row;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (k.quad_has(q.p, r)) store_states(q.sum.state + (at + k.quad_channel(q.p, r)) * S, k.s0, S, h[r]);
+    if (k.mine && k.w == 0) q.sum.total[at + k.channel] = total;
+    if (k.block == 0 && k.g == 0 && threadIdx.x == 0)
+      q.sum.cut[(int64_t)k.chunk * a.rows + k.n] = any_cut != 0;
+  } else if (a.new_state && u1 == q.p.units) {
+    const bool ended = a.dones && a.dones[(int64_t)(L - 1) * a.rows + k.n] != 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (ended) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) h[r][s] = 0.0f;
+      }
+      if (k.quad_has(q.p, r))
+        store_states(a.new_state + (row + k.quad_channel(q.p, r)) * S, k.s0, S, h[r]);
+    }
+  }
+}
+
+// One step: a lane takes four states of a channel, `lanes` (a power of two)
+// lanes a channel.  State in, state out, nothing else of size: what it costs
+// is a launch.
+template <class T>
+__global__ void __launch_bounds__(256) scan_step_kernel(const scan_args a, int32_t lanes) {
+  using raw = typename T::raw;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t column = id / lanes;
+  if (column >= (int64_t)a.rows * a.width) return;  // (all of a column's lanes together)
+  const int32_t s0 = 4 * (int32_t)(id % lanes), S = a.states;
+  const int32_t n = (int32_t)(column / a.width), d = (int32_t)(column % a.width);
+  const int32_t g = d / (a.width / a.groups);
+  const float x = T::widen((static_cast<const raw*>(a.x) + n * a.x_row)[d]);
+  const float v = T::widen((static_cast<const raw*>(a.delta) + n * a.delta_row)[d]) +
+                  (a.delta_bias ? a.delta_bias[d] : 0.0f);
+  float E;
+  const float dt = a.softplus ? softplus_of(v, E) : v;
+  float y = 0.0f;
+  if (s0 < S) {
+    float h[4], rate[4];
+    load_states(a.state + column * S, s0, S, h);
+    load_states(a.rate + (int64_t)d * S, s0, S, rate);
+    const raw* b = static_cast<const raw*>(a.b) + n * a.b_row + g * a.b_group;
+    const raw* c = static_cast<const raw*>(a.c) + n * a.c_row + g * a.c_group;
+    const bool cut = a.dones && a.dones[n] != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (s0 + i >= S) continue;
+      const float decay = __builtin_amdgcn_exp2f(dt * (rate[i] * kLog2e));
+      h[i] = __builtin_fmaf(decay, cut ? 0.0f : h[i], (dt * x) * T::widen(b[s0 + i]));
+      y = __builtin_fmaf(T::widen(c[s0 + i]), h[i], y);
+    }
+    store_states(a.new_state + column * S, s0, S, h);
+  }
+  for (int32_t i = 1; i < lanes; i <<= 1) y += __shfl_xor(y, i);
+  if (s0 != 0) return;
+  y = __builtin_fmaf(a.skip ? a.skip[d] : 0.0f, x, y);
+  if (a.gate) {
+    const float z = T::widen((static_cast<const raw*>(a.gate) + n * a.gate_row)[d]);
+    y *= z * sigmoid_of(z);
+  }
+  (static_cast<raw*>(a.y) + n * a.y_row)[d] = T::narrow(y);
+}
+
+template <class T, int NB>
+void launch_forward(const ScanRun& q, hipStream_t stream) {
+  const uint32_t groups = (uint32_t)(q.p.columns * q.p.chunks);
+  // (the last chunk's summary is read by none)
+  if (q.p.chunks > 1)
+    scan_forward_kernel<T, NB, true>
+        <<<dim3((uint32_t)(q.p.columns * (q.p.chunks - 1))), dim3(64 * NB), 0, stream>>>(q);
+  scan_forward_kernel<T, NB, false><<<dim3(groups), dim3(64 * NB), 0, stream>>>(q);
+}
+
+template <class T>
+void launch_states(const ScanRun& q, hipStream_t stream) {
+  switch (q.p.state_blocks) {
+    case 1: return launch_forward<T, 1>(q, stream);
+    case 2: return launch_forward<T, 2>(q, stream);
+    case 3: return launch_forward<T, 3>(q, stream);
+    default: return launch_forward<T, 4>(q, stream);
+  }
+}
+
+}  // namespace
+
+// A chunk has four units at least, and chunks are made until about two waves
+// a SIMD have work (1024 SIMDs); a scan with half of that many columns is not
+// cut, as the second look at its inputs would cost what the cut gains.
+ScanPlan scan_plan(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G, bool grad) {
+  ScanPlan p;
+  p.group_width = D / G;
+  p.blocks = cdiv(p.group_width, 64);
+  p.units = cdiv(L, kUnit);
+  p.state_blocks = cdiv(S, kBlock);
+  p.columns = (int64_t)N * G * p.blocks;
+  const int64_t waves = p.columns * p.state_blocks;
+  p.chunks = 1;
+  p.chunk_units = p.units;
+  if (waves <= 512) {
+    const int64_t wanted = min((int64_t)64, 2048 / waves);
+    p.chunk_units = max(4, cdiv(p.units, (int)wanted));
+    p.chunks = cdiv(p.units, p.chunk_units);
+  }
+  if (p.chunks == 1) p.chunk_units = p.units;
+  return p;
+}
+
+namespace {
+int64_t up(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+}  // namespace
+
+int64_t scan_summary_bytes(const ScanPlan& p, int32_t N, int32_t D, int32_t S) {
+  if (p.chunks == 1) return 0;
+  const int64_t nd = (int64_t)p.chunks * N * D;
+  return up(nd * S * 4) + up(nd * 4) + up((int64_t)p.chunks * N * 4);
+}
+ScanSummary scan_summary(const ScanPlan& p, int32_t N, int32_t D, int32_t S, void* workspace) {
+  const int64_t nd = (int64_t)p.chunks * N * D;
+  char* w = static_cast<char*>(workspace);
+  return ScanSummary{reinterpret_cast<float*>(w), reinterpret_cast<float*>(w + up(nd * S * 4)),
+                     reinterpret_cast<int32_t*>(w + up(nd * S * 4) + up(nd * 4))};
+}
+
+int64_t scan_workspace_bytes(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G) {
+  if (L == 0 || N == 0 || D == 0) return 0;
+  return scan_summary_bytes(scan_plan(L, N, D, S, G, false), N, D, S);
+}
+
+hipError_t scan_forward_launch(const scan_args& a, hipStream_t stream) {
+  const int64_t state_bytes = (int64_t)a.rows * a.width * a.states * 4;
+  if (a.steps == 0)
+    return a.new_state ? copy_or_clear_launch(a.state, a.new_state, state_bytes, stream) : hipSuccess;
+  ScanRun q;
+  q.a = a;
+  q.p = scan_plan(a.steps, a.rows, a.width, a.states, a.groups, false);
+  q.sum = scan_summary(q.p, a.rows, a.width, a.states, a.workspace);
+  if (a.dtype == POLICY_F32)
+    launch_states<F32>(q, stream);
+  else if (a.dtype == POLICY_BF16)
+    launch_states<BF16>(q, stream);
+  else
+    launch_states<F16>(q, stream);
+  return hipGetLastError();
+}
+
+hipError_t scan_step_launch(const scan_args& a, hipStream_t stream) {
+  int32_t lanes = 1;
+  while (4 * lanes < a.states) lanes *= 2;
+  const int64_t threads = (int64_t)a.rows * a.width * lanes;
+  const dim3 grid((uint32_t)((threads + 255) / 256));
+  if (a.dtype == POLICY_F32)
+    scan_step_kernel<F32><<<grid, 256, 0, stream>>>(a, lanes);
+  else if (a.dtype == POLICY_BF16)
+    scan_step_kernel<BF16><<<grid, 256, 0, stream>>>(a, lanes);
+  else
+    scan_step_kernel<F16><<<grid, 256, 0, stream>>>(a, lanes);
+  return hipGetLastError();
+}
+
+}  // namespace rl

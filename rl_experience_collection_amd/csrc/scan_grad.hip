@@ -1,0 +1,530 @@
+// Gradient of the selective state space scan (include/block.h).
+//
+// With v_t = c_t h_t + skip x_t, w_t = dL/dv_t (dy times the gate's silu) and
+// d_t = dL/dh_t,
+//   d_t = c_t w_t + a_{t+1} m_{t+1} d_{t+1},   a_t = exp(D_t rate),
+//   db = sum over channels of d D x,  dc = sum over channels of w h,
+//   q_t = a_t m_t h_{t-1} d_t,  drate = sum D q,
+//   dD = x sum over s of b d + sum over s of rate q,  dx = D sum of b d + skip w.
+// A wave runs its units from the last to the first.  Of a unit it takes the
+// state that enters it from what the forward call kept, forms its eight states
+// again, holding kHeld of them in registers at a time, and goes back over
+// them.  Decays are formed twice (an exp2 costs less than the registers that
+// would hold it).
+#include "scan.hpp"
+
+namespace rl {
+
+namespace {
+
+constexpr int kHeld = 4;  // states of a lane's channels held at a time
+
+struct GradRun {
+  scan_grad_args g;
+  ScanPlan p;
+  ScanSummary sum;
+  float* shared;  // [blocks][L][N][G][state blocks][32]: db and dc of the blocks, or NULL
+  float* params;  // [chunks][N][D S + 2 D]: drate, dskip, ddelta_bias
+};
+
+template <class T>
+struct GradColumns {
+  typename T::raw x[kUnit], d[kUnit], z[kUnit], dy[kUnit];
+  template <bool SUMMARY>
+  __device__ __forceinline__ void load(const scan_grad_args& g, const ScanWave& k, int32_t t0, bool gate) {
+    using raw = typename T::raw;
+    const scan_args& a = g.f;
+    const raw* px = static_cast<const raw*>(a.x) + k.n * a.x_row;
+    const raw* pd = static_cast<const raw*>(a.delta) + k.n * a.delta_row;
+    const raw* pz = static_cast<const raw*>(a.gate) + k.n * a.gate_row;
+    const raw* pg = static_cast<const raw*>(g.dy) + k.n * g.dy_row;
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) {
+      const int32_t t = min(t0 + i, a.steps - 1);
+      if (!SUMMARY) x[i] = (px + t * a.x_step)[k.channel];
+      d[i] = (pd + t * a.delta_step)[k.channel];
+      dy[i] = (pg + t * g.dy_step)[k.channel];
+      if (gate) z[i] = (pz + t * a.gate_step)[k.channel];
+    }
+  }
+};
+
+__device__ __forceinline__ void quad_all(float v, float (&q)[4]) {
+  q[0] = quad_get<0>(v);
+  q[1] = quad_get<1>(v);
+  q[2] = quad_get<2>(v);
+  q[3] = quad_get<3>(v);
+}
+__device__ __forceinline__ void read4(const float* p, float (&v)[4]) {
+  const float4 x = *reinterpret_cast<const float4*>(p);
+  v[0] = x.x;
+  v[1] = x.y;
+  v[2] = x.z;
+  v[3] = x.w;
+}
+
+// What leaves chunk `chunk` backward enters from the chunks after it.
+__device__ __forceinline__ void enter_backward(const GradRun& q, const ScanWave& k,
+                                               const float (&rate)[4][4], float (&G)[4][4]) {
+  const scan_args& a = q.g.f;
+  const int64_t nd = (int64_t)a.rows * a.width;
+  for (int32_t i = q.p.chunks - 1; i > k.chunk; --i) {
+    const bool cut = q.sum.cut[(int64_t)i * a.rows + k.n] != 0;
+    const int64_t at = i * nd + (int64_t)k.n * a.width;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int64_t c = at + k.quad_channel(q.p, r);
+      float own[4];
+      load_states(q.sum.state + c * a.states, k.s0, a.states, own);
+      const float total = q.sum.total[c];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const float left = G[r][s] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(total * rate[r][s]) * G[r][s];
+        G[r][s] = cut ? own[s] : left + own[s];
+      }
+    }
+  }
+}
+
+// Sums over the wave's quads of the four values of b's and c's gradients that
+// every lane holds.  Halving the values at each meeting, lane l ends with one:
+// of b where its bit 5 is 0, else of c, state 2 (bit 4) + (bit 3) of the four
+// of lane l & 3, and a sum over bit 2 still to come.
+__device__ __forceinline__ float meet(const float (&b)[4], const float (&c)[4], int lane) {
+  float w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(b[i]), __float_as_uint(c[i]), false, false);
+    w[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  float v[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(w[i]), __float_as_uint(w[i + 2]), false, false);
+    v[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  const bool up = lane & 8;
+  return (up ? v[1] : v[0]) + from_lane<0x128>(up ? v[0] : v[1]);  // row_ror:8
+}
+// The sum over bit 2 of two steps at once: of the first where bit 2 is 0.
+__device__ __forceinline__ float meet_pair(float first, float second, int lane) {
+  const bool up = lane & 4;
+  const float other = up ? first : second;
+  int x = __builtin_amdgcn_update_dpp(0, __float_as_int(other), 0x104, 0xF, 0x5, true);  // row_shl:4
+  x = __builtin_amdgcn_update_dpp(x, __float_as_int(other), 0x114, 0xF, 0xA, false);     // row_shr:4
+  return (up ? second : first) + __int_as_float(x);
+}
+
+template <class T, int NB, bool SUMMARY>
+__global__ void __launch_bounds__(64 * NB) scan_backward_kernel(const GradRun q) {
+  const scan_grad_args& g = q.g;
+  const scan_args& a = g.f;
+  ScanWave k(q.p, a.rows, a.groups, a.states);
+  if (SUMMARY) ++k.chunk;  // (the first chunk's is read by none)
+  __shared__ float s_bc[NB][kUnit][32];
+  __shared__ float s_part[NB > 1 && !SUMMARY ? 2 : 1][NB > 1 && !SUMMARY ? NB : 1][3][kUnit][64];
+  const int32_t L = a.steps, S = a.states;
+  const int32_t u0 = k.chunk * q.p.chunk_units, u1 = min(u0 + q.p.chunk_units, q.p.units);
+  const bool gated = a.gate != nullptr;
+
+  float rate[4][4], G[4][4], drate[4][4];
+  const bool ended = a.dones && a.dones[(int64_t)(L - 1) * a.rows + k.n] != 0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int32_t c = k.quad_channel(q.p, r);
+    load_states(a.rate + (int64_t)c * S, k.s0, S, rate[r]);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      rate[r][s] *= kLog2e;
+      G[r][s] = drate[r][s] = 0.0f;
+    }
+    // (the last chunk's summary starts from the gradient of new_state itself)
+    if ((!SUMMARY || k.chunk == q.p.chunks - 1) && g.dnew_state && !ended)
+      load_states(g.dnew_state + ((int64_t)k.n * a.width + c) * S, k.s0, S, G[r]);
+  }
+  if constexpr (!SUMMARY) {
+    if (k.chunk < q.p.chunks - 1) {
+      // (the last chunk's summary holds what dnew_state sends)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) G[r][s] = 0.0f;
+      enter_backward(q, k, rate, G);
+    }
+  }
+  const float bias = a.delta_bias ? a.delta_bias[k.channel] : 0.0f;
+  const float skip = a.skip ? a.skip[k.channel] : 0.0f;
+  float total = 0.0f, dskip = 0.0f, dbias = 0.0f;
+  uint32_t any_cut = 0;
+
+  UnitInputs<T> in;
+  GradColumns<T> col;
+  float kept[4][4];
+  const auto fetch = [&](int32_t u) {
+    in.load(a, k, u * kUnit);
+    col.template load<SUMMARY>(g, k, u * kUnit, gated);
+    if constexpr (!SUMMARY) {
+      const int64_t at = ((int64_t)u * a.rows + k.n) * a.width;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        load_states(a.kept + (at + k.quad_channel(q.p, r)) * S, k.s0, S, kept[r]);
+    }
+    return unit_cuts(a, k, u * kUnit);
+  };
+  uint32_t cuts = fetch(u1 - 1);
+  for (int32_t u = u1 - 1; u >= u0; --u) {
+    const int32_t t0 = u * kUnit;
+    wave_sync();
+    in.put(s_bc[k.w], k.lane);
+    wave_sync();
+    // dt: D; w: the gradient of v; sg: D's slope; f: dgate / v
+    float x[kUnit], dt[kUnit], w[kUnit], sg[kUnit], f[kUnit], h[4][4];
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) {
+      const bool past = t0 + i >= L;
+      const float v = T::widen(col.d[i]) + bias;
+      float E;
+      dt[i] = a.softplus ? softplus_of(v, E) : v;
+      sg[i] = a.softplus ? sigmoid_from(v, E) : 1.0f;
+      w[i] = T::widen(col.dy[i]);
+      if (!SUMMARY) x[i] = T::widen(col.x[i]);
+      f[i] = 0.0f;
+      if (gated) {
+        const float z = T::widen(col.z[i]);
+        const float sz = sigmoid_of(z);
+        f[i] = w[i] * sz * __builtin_fmaf(z, 1.0f - sz, 1.0f);
+        w[i] *= z * sz;
+      }
+      if (past) dt[i] = w[i] = 0.0f;  // the gradient of the state passes through
+      if (!k.mine) w[i] = 0.0f;       // (a copy of another channel)
+      if (SUMMARY) total += dt[i];
+    }
+    if constexpr (!SUMMARY) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) h[r][s] = kept[r][s];
+    }
+    const uint32_t cut = cuts;
+    any_cut |= cut;
+    if (u > u0) cuts = fetch(u - 1);
+
+    if constexpr (SUMMARY) {
+#pragma unroll
+      for (int i = kUnit - 1; i >= 0; --i) {
+        float c[4], dts[4], ws[4];
+        read4(&s_bc[k.w][i][16 + 4 * k.j], c);
+        quad_all(dt[i], dts);
+        quad_all(w[i], ws);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            G[r][s] = __builtin_amdgcn_exp2f(dts[r] * rate[r][s]) * __builtin_fmaf(c[s], ws[r], G[r][s]);
+        if ((cut >> i) & 1u) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) G[r][s] = 0.0f;
+        }
+      }
+    } else {
+      // the state after step i from the one before it
+      const auto advance = [&](float(&v)[4][4], int i) {
+        float b[4], dts[4], dus[4];
+        read4(&s_bc[k.w][i][4 * k.j], b);
+        quad_all(dt[i], dts);
+        quad_all(dt[i] * x[i], dus);
+        if ((cut >> i) & 1u) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) v[r][s] = 0.0f;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            v[r][s] = __builtin_fmaf(__builtin_amdgcn_exp2f(dts[r] * rate[r][s]), v[r][s], dus[r] * b[s]);
+      };
+      float y[kUnit], p1[kUnit], p2[kUnit];
+      // A lane's own channel of a step, when the sums over its states are known.
+      const auto finish = [&](int i) {
+        if (t0 + i >= L) return;
+        using raw = typename T::raw;
+        const int64_t t = t0 + i;
+        const float dD = __builtin_fmaf(x[i], p1[i], p2[i] * kLn2);
+        const float dd = dD * sg[i];
+        if (k.mine) {
+          (static_cast<raw*>(g.dx) + t * g.dx_step + k.n * g.dx_row)[k.channel] =
+              T::narrow(__builtin_fmaf(dt[i], p1[i], skip * w[i]));
+          (static_cast<raw*>(g.ddelta) + t * g.ddelta_step + k.n * g.ddelta_row)[k.channel] = T::narrow(dd);
+          if (gated)
+            (static_cast<raw*>(g.dgate) + t * g.dgate_step + k.n * g.dgate_row)[k.channel] =
+                T::narrow(f[i] * __builtin_fmaf(skip, x[i], y[i]));
+          dskip = __builtin_fmaf(w[i], x[i], dskip);
+          dbias += dd;
+        }
+      };
+      float odd = 0.0f;  // the second of a pair of steps
+#pragma unroll
+      for (int part = kUnit / kHeld - 1; part >= 0; --part) {
+        float v[4][4], held[kHeld][4][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) v[r][s] = h[r][s];
+#pragma unroll
+        for (int i = 0; i < part * kHeld; ++i) advance(v, i);
+#pragma unroll
+        for (int m = 0; m < kHeld; ++m) {
+          const int i = part * kHeld + m;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) held[m][r][s] = v[r][s];
+          advance(v, i);
+          if (gated) {
+            float c[4], sums[4];
+            read4(&s_bc[k.w][i][16 + 4 * k.j], c);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              sums[r] = c[0] * v[r][0];
+#pragma unroll
+              for (int s = 1; s < 4; ++s) sums[r] = __builtin_fmaf(c[s], v[r][s], sums[r]);
+            }
+            y[i] = quad_turn(sums, k.lane);
+          }
+        }
+#pragma unroll
+        for (int m = kHeld - 1; m >= 0; --m) {
+          const int i = part * kHeld + m;
+          float b[4], c[4], dts[4], dus[4], ws[4], db[4], dc[4], s1[4], s2[4];
+          read4(&s_bc[k.w][i][4 * k.j], b);
+          read4(&s_bc[k.w][i][16 + 4 * k.j], c);
+          quad_all(dt[i], dts);
+          quad_all(k.mine ? dt[i] * x[i] : 0.0f, dus);
+          quad_all(w[i], ws);
+#pragma unroll
+          for (int s = 0; s < 4; ++s) db[s] = dc[s] = 0.0f;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            s1[r] = s2[r] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              const float after = m == kHeld - 1 ? v[r][s] : held[m < kHeld - 1 ? m + 1 : m][r][s];
+              G[r][s] = __builtin_fmaf(c[s], ws[r], G[r][s]);
+              dc[s] = __builtin_fmaf(ws[r], after, dc[s]);
+              db[s] = __builtin_fmaf(G[r][s], dus[r], db[s]);
+              s1[r] = __builtin_fmaf(G[r][s], b[s], s1[r]);
+            }
+          }
+          if ((cut >> i) & 1u) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+              for (int s = 0; s < 4; ++s) G[r][s] = 0.0f;
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+              for (int s = 0; s < 4; ++s) {
+                G[r][s] *= __builtin_amdgcn_exp2f(dts[r] * rate[r][s]);
+                const float p = G[r][s] * held[m][r][s];
+                s2[r] = __builtin_fmaf(rate[r][s], p, s2[r]);
+                drate[r][s] = __builtin_fmaf(dts[r], p, drate[r][s]);
+              }
+          }
+          p1[i] = quad_turn(s1, k.lane);
+          p2[i] = quad_turn(s2, k.lane);
+          if constexpr (NB == 1) finish(i);
+          const float met = meet(db, dc, k.lane);
+          if (i & 1) {
+            odd = met;
+          } else {
+            const float sum = meet_pair(met, odd, k.lane);
+            const int32_t t = t0 + i + ((k.lane >> 2) & 1);
+            const int s = 4 * k.j + 2 * ((k.lane >> 4) & 1) + ((k.lane >> 3) & 1);
+            const bool is_c = k.lane & 32;
+            if (t < L) {
+              if (q.shared) {
+                const int64_t at = (((int64_t)k.block * L + t) * a.rows + k.n) * a.groups + k.g;
+                q.shared[(at * NB + k.w) * 32 + (is_c ? 16 : 0) + s] = sum;
+              } else if (k.w * kBlock + s < S) {
+                using raw = typename T::raw;
+                raw* p = is_c ? static_cast<raw*>(g.dc) + t * g.dc_step + k.n * g.dc_row + k.g * g.dc_group
+                              : static_cast<raw*>(g.db) + t * g.db_step + k.n * g.db_row + k.g * g.db_group;
+                p[k.w * kBlock + s] = T::narrow(sum);
+              }
+            }
+          }
+        }
+      }
+      if constexpr (NB > 1) {
+        float(&buf)[NB][3][kUnit][64] = s_part[u & 1];
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) {
+          buf[k.w][0][i][k.lane] = gated ? y[i] : 0.0f;
+          buf[k.w][1][i][k.lane] = p1[i];
+          buf[k.w][2][i][k.lane] = p2[i];
+        }
+        __syncthreads();  // (a wave that is a unit ahead writes the other half)
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) {
+          if (i % NB != k.w) continue;
+          y[i] = p1[i] = p2[i] = 0.0f;
+#pragma unroll
+          for (int v = 0; v < NB; ++v) {
+            y[i] += buf[v][0][i][k.lane];
+            p1[i] += buf[v][1][i][k.lane];
+            p2[i] += buf[v][2][i][k.lane];
+          }
+          finish(i);
+        }
+      }
+    }
+  }
+
+  const int64_t row = (int64_t)k.n * a.width;
+  if constexpr (SUMMARY) {
+    const int64_t at = (int64_t)k.chunk * a.rows * a.width + row;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (k.quad_has(q.p, r)) store_states(q.sum.state + (at + k.quad_channel(q.p, r)) * S, k.s0, S, G[r]);
+    if (k.mine && k.w == 0) q.sum.total[at + k.channel] = total;
+    if (k.block == 0 && k.g == 0 && threadIdx.x == 0)
+      q.sum.cut[(int64_t)k.chunk * a.rows + k.n] = any_cut != 0;
+  } else {
+    float* params = q.params + ((int64_t)k.chunk * a.rows + k.n) * ((int64_t)a.width * (S + 2));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (!k.quad_has(q.p, r)) continue;
+      store_states(params + (int64_t)k.quad_channel(q.p, r) * S, k.s0, S, drate[r]);
+      if (u0 == 0 && g.dstate)
+        store_states(g.dstate + (row + k.quad_channel(q.p, r)) * S, k.s0, S, G[r]);
+    }
+    if constexpr (NB > 1) {
+      __syncthreads();
+      s_part[0][k.w][0][0][k.lane] = dskip;
+      s_part[0][k.w][1][0][k.lane] = dbias;
+      __syncthreads();
+      dskip = dbias = 0.0f;
+#pragma unroll
+      for (int v = 0; v < NB; ++v) {
+        dskip += s_part[0][v][0][0][k.lane];
+        dbias += s_part[0][v][1][0][k.lane];
+      }
+    }
+    if (k.mine && k.w == 0) {
+      params[(int64_t)a.width * S + k.channel] = dskip;
+      params[(int64_t)a.width * (S + 1) + k.channel] = dbias;
+    }
+  }
+}
+
+// db and dc: the sums over a group's blocks, rounded.  A thread takes one
+// value of one kind.
+template <class T>
+__global__ void __launch_bounds__(256) scan_shared_kernel(const GradRun q, int64_t total) {
+  const scan_grad_args& g = q.g;
+  const scan_args& a = g.f;
+  const int32_t wide = q.p.state_blocks * 32;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+    const int32_t i = (int32_t)(e % wide);
+    const int64_t row = e / wide;  // (t, n, group)
+    const int32_t s = (i / 32) * kBlock + (i & 15);
+    if (s >= a.states) continue;
+    float sum = 0.0f;
+    for (int32_t b = 0; b < q.p.blocks; ++b) sum += q.shared[(int64_t)b * total + e];
+    const int32_t grp = (int32_t)(row % a.groups);
+    const int64_t tn = row / a.groups;
+    const int64_t n = tn % a.rows, t = tn / a.rows;
+    using raw = typename T::raw;
+    raw* p = i & 16 ? static_cast<raw*>(g.dc) + t * g.dc_step + n * g.dc_row + grp * g.dc_group
+                    : static_cast<raw*>(g.db) + t * g.db_step + n * g.db_row + grp * g.db_group;
+    p[s] = T::narrow(sum);
+  }
+}
+
+template <class T, int NB>
+void launch_backward(const GradRun& q, hipStream_t stream) {
+  if (q.p.chunks > 1)
+    scan_backward_kernel<T, NB, true>
+        <<<dim3((uint32_t)(q.p.columns * (q.p.chunks - 1))), dim3(64 * NB), 0, stream>>>(q);
+  scan_backward_kernel<T, NB, false>
+      <<<dim3((uint32_t)(q.p.columns * q.p.chunks)), dim3(64 * NB), 0, stream>>>(q);
+  if (q.shared) {
+    const int64_t total = (int64_t)q.g.f.steps * q.g.f.rows * q.g.f.groups * NB * 32;
+    const int64_t groups = (total + 255) / 256;
+    scan_shared_kernel<T><<<dim3((uint32_t)(groups < 16384 ? groups : 16384)), 256, 0, stream>>>(q, total);
+  }
+}
+template <class T>
+void launch_states(const GradRun& q, hipStream_t stream) {
+  switch (q.p.state_blocks) {
+    case 1: return launch_backward<T, 1>(q, stream);
+    case 2: return launch_backward<T, 2>(q, stream);
+    case 3: return launch_backward<T, 3>(q, stream);
+    default: return launch_backward<T, 4>(q, stream);
+  }
+}
+
+int64_t up(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+
+// The workspace, in order: summaries, shared sums, sums of the parameters'
+// gradients, scratch to add those up.
+struct Parts {
+  int64_t summary, shared, params, scratch;
+};
+Parts parts_of(const ScanPlan& p, int32_t L, int32_t N, int32_t D, int32_t S, int32_t G) {
+  const int64_t rows = (int64_t)p.chunks * N;
+  Parts b;
+  b.summary = scan_summary_bytes(p, N, D, S);
+  b.shared = p.blocks > 1 ? up((int64_t)p.blocks * L * N * G * p.state_blocks * 32 * 4) : 0;
+  b.params = up(rows * D * (S + 2) * 4);
+  b.scratch = up(sums_floats(rows, D * (S + 2)) * 4);
+  return b;
+}
+
+}  // namespace
+
+int64_t scan_grad_workspace_bytes(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G) {
+  if (L == 0 || N == 0 || D == 0) return 0;
+  const Parts b = parts_of(scan_plan(L, N, D, S, G, true), L, N, D, S, G);
+  return b.summary + b.shared + b.params + b.scratch;
+}
+
+hipError_t scan_backward_launch(const scan_grad_args& g, hipStream_t stream) {
+  const scan_args& a = g.f;
+  const int64_t D = a.width, S = a.states;
+  if (a.steps == 0 || a.rows == 0) {
+    hipError_t e = copy_or_clear_launch(nullptr, g.drate, D * S * 4, stream);
+    if (e == hipSuccess && g.dskip) e = copy_or_clear_launch(nullptr, g.dskip, D * 4, stream);
+    if (e == hipSuccess && g.ddelta_bias) e = copy_or_clear_launch(nullptr, g.ddelta_bias, D * 4, stream);
+    if (e == hipSuccess && g.dstate && a.rows > 0)
+      e = copy_or_clear_launch(g.dnew_state, g.dstate, a.rows * D * S * 4, stream);
+    return e;
+  }
+  GradRun q;
+  q.g = g;
+  q.p = scan_plan(a.steps, a.rows, a.width, a.states, a.groups, true);
+  const Parts b = parts_of(q.p, a.steps, a.rows, a.width, a.states, a.groups);
+  char* w = static_cast<char*>(a.workspace);
+  q.sum = scan_summary(q.p, a.rows, a.width, a.states, w);
+  q.shared = b.shared ? reinterpret_cast<float*>(w + b.summary) : nullptr;
+  q.params = reinterpret_cast<float*>(w + b.summary + b.shared);
+  if (a.dtype == POLICY_F32)
+    launch_states<F32>(q, stream);
+  else if (a.dtype == POLICY_BF16)
+    launch_states<BF16>(q, stream);
+  else
+    launch_states<F16>(q, stream);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int32_t ds = (int32_t)(D * S), d = (int32_t)D;
+  const SumsOut out = {{g.drate, g.dskip, g.ddelta_bias}, {ds, ds + d, ds + 2 * d}};
+  return sums_launch(q.params, (int64_t)q.p.chunks * a.rows, ds + 2 * d,
+                     reinterpret_cast<float*>(w + b.summary + b.shared + b.params), out, stream);
+}
+
+}  // namespace rl

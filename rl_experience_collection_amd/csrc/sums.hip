@@ -1,0 +1,87 @@
+// Column sums of partial gradients, and copies that a captured graph may hold.
+//
+// A workgroup takes 64 columns and a run of rows: its four waves the rows
+// r, r + 4, ..., eight loads in flight each, and their sums meet in LDS.
+// Many rows are cut into runs first, whose sums the same kernel adds up.
+// The order of the additions depends on the two sizes alone.
+#include "block.hpp"
+
+namespace rl {
+
+namespace {
+
+constexpr int kRun = 64;      // rows of a run, at least
+constexpr int kMostRuns = 64;
+
+int64_t runs_of(int64_t rows) {
+  const int64_t runs = (rows + kRun - 1) / kRun;
+  return runs < kMostRuns ? runs : kMostRuns;
+}
+
+__global__ void __launch_bounds__(256) sums_kernel(const float* x, int64_t rows, int32_t columns,
+                                                   int64_t run, float* partial, SumsOut out) {
+  __shared__ float s_sum[4][64];
+  const int32_t lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int32_t c = blockIdx.x * 64 + lane;
+  const int64_t r0 = blockIdx.y * run, r1 = r0 + run < rows ? r0 + run : rows;
+  float sum = 0.0f;
+  if (c < columns) {
+    int64_t r = r0 + w;
+    for (; r + 28 < r1; r += 32) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = x[(r + 4 * i) * columns + c];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += v[i];
+    }
+    for (; r < r1; r += 4) sum += x[r * columns + c];
+  }
+  s_sum[w][lane] = sum;
+  __syncthreads();
+  if (w != 0 || c >= columns) return;
+  sum = (s_sum[0][lane] + s_sum[1][lane]) + (s_sum[2][lane] + s_sum[3][lane]);
+  if (partial) {
+    partial[(int64_t)blockIdx.y * columns + c] = sum;
+    return;
+  }
+  const int k = c < out.end[0] ? 0 : c < out.end[1] ? 1 : 2;
+  float* p = k == 0 ? out.out[0] : k == 1 ? out.out[1] : out.out[2];
+  const int32_t first = k == 0 ? 0 : k == 1 ? out.end[0] : out.end[1];
+  if (p) p[c - first] = sum;
+}
+
+__global__ void __launch_bounds__(256) copy_kernel(const uint8_t* src, uint8_t* dst, int64_t bytes) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; 2 * i < bytes; i += (int64_t)gridDim.x * 256)
+    reinterpret_cast<uint16_t*>(dst)[i] = src ? reinterpret_cast<const uint16_t*>(src)[i] : (uint16_t)0;
+}
+
+}  // namespace
+
+int64_t sums_floats(int64_t rows, int32_t columns) {
+  const int64_t runs = runs_of(rows);
+  return runs > 1 ? runs * columns : 0;
+}
+
+hipError_t sums_launch(const float* x, int64_t rows, int32_t columns, float* scratch,
+                       const SumsOut& out, hipStream_t stream) {
+  const int64_t runs = runs_of(rows);
+  const uint32_t across = (uint32_t)((columns + 63) / 64);
+  if (runs > 1) {
+    const int64_t run = (rows + runs - 1) / runs;
+    sums_kernel<<<dim3(across, (uint32_t)runs), 256, 0, stream>>>(x, rows, columns, run, scratch, out);
+    x = scratch;
+    rows = runs;
+  }
+  sums_kernel<<<dim3(across, 1), 256, 0, stream>>>(x, rows, columns, rows, nullptr, out);
+  return hipGetLastError();
+}
+
+hipError_t copy_or_clear_launch(const void* src, void* dst, int64_t bytes, hipStream_t stream) {
+  if (bytes == 0) return hipSuccess;
+  const int64_t groups = (bytes + 511) / 512;
+  copy_kernel<<<dim3((uint32_t)(groups < 4096 ? groups : 4096)), 256, 0, stream>>>(
+      static_cast<const uint8_t*>(src), static_cast<uint8_t*>(dst), bytes);
+  return hipGetLastError();
+}
+
+}  // namespace rl

@@ -1,0 +1,463 @@
+"""The operators of a residual block (include/block.h) without a GPU: exported
+symbols, struct layouts, refusals of the C entry points and of the binding,
+what torch's autograd is told, and the 64-bit reference's gradients against
+differences."""
+import ctypes as C
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+import torch.autograd.forward_ad as fwd
+
+import block_ref as ref
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+EINVAL, OK = -1, 0
+
+
+@pytest.fixture(scope="module")
+def rx():
+    import rl_experience_collection_amd as rx
+    rx.load_library()
+    return rx
+
+
+@pytest.fixture(scope="module")
+def block(rx):
+    from rl_experience_collection_amd import block
+    return block
+
+
+def test_library_exports_the_header(rx, block):
+    txt = open(os.path.join(ROOT, "include", "block.h")).read()
+    txt = re.sub(r"/\*.*?\*/", "", txt, flags=re.S)
+    names = set(re.findall(r"^\s*(?:int|int64_t)\s+(\w+)\s*\(", txt, flags=re.M))
+    assert names == set(block.EXPORTED)
+    for n in names:
+        assert hasattr(rx.load_library(), n)
+
+
+def test_struct_sizes(block):
+    assert C.sizeof(block.ConvArgs) == 24 + 8 * (4 + 7)
+    assert C.sizeof(block.ConvGradArgs) == C.sizeof(block.ConvArgs) + 8 * (4 + 7 + 1)
+    assert C.sizeof(block.ScanArgs) == 32 + 8 * (14 + 14 + 1)  # seven ints, padded
+    assert C.sizeof(block.ScanGradArgs) == C.sizeof(block.ScanArgs) + 8 * (14 + 11)
+    assert C.sizeof(block.NormArgs) == 8 + 16 + 16 + 16 + 8 + 8 * 8
+    assert C.sizeof(block.NormGradArgs) == C.sizeof(block.NormArgs) + 8 * 12
+
+
+# ------------------------------------------------------------ the C refusals
+def conv_args(block, **kw):
+    a = block.ConvArgs(steps=4, rows=2, width=3, taps=4, dtype=0, activation=2, x_step=6, x_row=3, y_step=6, y_row=3,
+                       x=64, weight=64, y=64)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+CONV = [(dict(steps=-1), "negative size"), (dict(rows=1 << 14, width=1 << 14), "2\\^28"),
+        (dict(steps=(1 << 30) + 1), "2\\^30"), (dict(dtype=3), "dtype"), (dict(taps=0), "taps"),
+        (dict(taps=9), "taps"), (dict(activation=1), "activation"), (dict(x=None), "x is NULL"),
+        (dict(weight=None), "weight is NULL"), (dict(x=66), "aligned"), (dict(state=2), "state is not aligned"),
+        (dict(x_row=-1), "stride"), (dict(bias=2), "bias is not aligned"),
+        (dict(rows=1, width=(1 << 28) - 1), "2\\^30")]
+
+
+@pytest.mark.parametrize("change,text", CONV + [(dict(y=None), "y is NULL"), (dict(new_state=2), "new_state")])
+def test_conv_forward_refuses(rx, block, change, text):
+    lib = rx.load_library()
+    assert lib.conv_forward(C.byref(conv_args(block, **change)), None) == EINVAL
+    assert re.search(text, rx.rollout_last_error()), rx.rollout_last_error()
+
+
+@pytest.mark.parametrize("change,text", CONV)
+def test_conv_backward_refuses_the_same(rx, block, change, text):
+    g = block.ConvGradArgs(f=conv_args(block, **change), dy=64, dx=64, dweight=64)
+    assert rx.load_library().conv_backward(C.byref(g), None) == EINVAL
+    assert re.search(text, rx.rollout_last_error()), rx.rollout_last_error()
+
+
+def test_conv_other_refusals(rx, block):
+    lib = rx.load_library()
+    assert lib.conv_forward(None, None) == EINVAL and lib.conv_backward(None, None) == EINVAL
+    for kw, text in ((dict(), "dy is NULL"), (dict(dy=64), "dx is NULL"), (dict(dy=64, dx=64), "dweight is NULL"),
+                     (dict(dy=64, dx=64, dweight=64), "workspace"), (dict(dy=64, dx=64, dweight=64, dy_row=-1), "stride"),
+                     (dict(dy=64, dx=64, dweight=64, workspace=64, workspace_bytes=8), "workspace"),
+                     (dict(dy=64, dx=64, dweight=64, workspace=72, workspace_bytes=1 << 30), "aligned")):
+        kw.setdefault("dweight", None if "dweight" in text else 64)
+        g = block.ConvGradArgs(f=conv_args(block), **kw)
+        assert lib.conv_backward(C.byref(g), None) == EINVAL
+        assert text in rx.rollout_last_error()
+    assert lib.conv_workspace(4, -1, 3, 4, 0) == EINVAL and lib.conv_workspace(4, 1, 3, 9, 0) == EINVAL
+    assert lib.conv_workspace(0, 2, 3, 4, 0) == 0 and lib.conv_workspace(4, 2, 3, 4, 0) > 0
+    assert lib.conv_step(2, 3, 4, 0, 2, 64, 3, 64, None, None, None, 64, 3, 64, None) == EINVAL
+    assert "state is NULL" in rx.rollout_last_error()
+    assert lib.conv_step(2, 3, 4, 0, 1, 64, 3, 64, None, 64, None, 64, 3, 64, None) == EINVAL
+    assert lib.conv_forward(C.byref(conv_args(block, rows=0)), None) == OK
+    assert lib.conv_step(0, 3, 4, 0, 2, None, 3, None, None, None, None, None, 3, None, None) == OK
+
+
+def scan_args(block, **kw):
+    a = block.ScanArgs(steps=4, rows=2, width=6, states=16, groups=1, dtype=0, softplus=1,
+                       **{k: 64 for k in ("x", "delta", "b", "c", "rate", "y")})
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+SCAN = [(dict(steps=-1), "negative size"), (dict(rows=1 << 14, width=1 << 14), "2\\^28"),
+        (dict(steps=(1 << 30) + 1), "2\\^30"), (dict(dtype=3), "dtype"), (dict(states=0), "states"),
+        (dict(states=65), "states"), (dict(groups=0), "groups"), (dict(groups=4), "groups"),
+        (dict(width=1, rows=(1 << 23) + 1), "2\\^23"), (dict(rows=1, width=1 << 27), "2\\^30"),
+        (dict(x=None), "x is NULL"), (dict(delta=None), "delta is NULL"), (dict(b=None), "b is NULL"),
+        (dict(c=None), "c is NULL"), (dict(rate=None), "rate is NULL"), (dict(gate=2), "gate is not aligned"),
+        (dict(skip=2), "skip"), (dict(delta_bias=2), "delta_bias"), (dict(b_step=-1), "stride"),
+        (dict(c_group=-1), "stride")]
+
+
+@pytest.mark.parametrize("change,text", SCAN + [(dict(y=None), "y is NULL"), (dict(state=2), "state"),
+                                                (dict(new_state=2), "new_state"), (dict(kept=2), "kept"),
+                                                (dict(steps=1000), "workspace")])
+def test_scan_forward_refuses(rx, block, change, text):
+    assert rx.load_library().scan_forward(C.byref(scan_args(block, **change)), None) == EINVAL
+    assert re.search(text, rx.rollout_last_error()), rx.rollout_last_error()
+
+
+@pytest.mark.parametrize("change,text", SCAN + [(dict(kept=None), "kept is NULL"), (dict(), "workspace"),
+                                                (dict(gate=64), "dgate is NULL")])
+def test_scan_backward_refuses(rx, block, change, text):
+    f = scan_args(block, **dict(dict(kept=64), **change))
+    g = block.ScanGradArgs(f=f, **{k: 64 for k in ("dy", "dx", "ddelta", "db", "dc", "drate")})
+    assert rx.load_library().scan_backward(C.byref(g), None) == EINVAL
+    assert re.search(text, rx.rollout_last_error()), rx.rollout_last_error()
+
+
+def test_scan_other_refusals(rx, block):
+    lib = rx.load_library()
+    assert lib.scan_forward(None, None) == EINVAL and lib.scan_backward(None, None) == EINVAL
+    assert lib.scan_step(None, None) == EINVAL
+    for kw, text in ((dict(), "steps must be 1"), (dict(steps=1), "state is NULL"),
+                     (dict(steps=1, state=64), "new_state is NULL"),
+                     (dict(steps=1, state=64, new_state=64, y=None), "y is NULL"),
+                     (dict(steps=1, rows=1 << 20, width=128, states=64), "2^31")):
+        assert lib.scan_step(C.byref(scan_args(block, **kw)), None) == EINVAL
+        assert text in rx.rollout_last_error()
+    for missing in ("dy", "dx", "ddelta", "db", "dc", "drate"):
+        g = block.ScanGradArgs(f=scan_args(block, kept=64),
+                               **{k: 64 for k in ("dy", "dx", "ddelta", "db", "dc", "drate") if k != missing})
+        assert lib.scan_backward(C.byref(g), None) == EINVAL
+        assert f"{missing} is NULL" in rx.rollout_last_error()
+    assert lib.scan_workspace(4, 2, 6, 16, 1) == 0 and lib.scan_workspace(1000, 2, 6, 16, 1) > 0
+    assert lib.scan_workspace(4, 2, 6, 65, 1) == EINVAL and lib.scan_grad_workspace(4, 2, 6, 16, 5) == EINVAL
+    assert lib.scan_grad_workspace(4, 2, 6, 16, 1) > 0 and lib.scan_grad_workspace(0, 2, 6, 16, 1) == 0
+    assert lib.scan_forward(C.byref(scan_args(block, rows=0)), None) == OK
+    assert lib.scan_step(C.byref(scan_args(block, rows=0, steps=1)), None) == OK
+
+
+def norm_args(block, **kw):
+    a = block.NormArgs(rows=2, width=6, dtype=0, branch_norm=1, residual_scale=1, branch_scale=1, eps=1e-6,
+                       residual=64, residual_row=6, branch=64, branch_row=6)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+NORM = [(dict(rows=-1), "rows"), (dict(width=0), "width"), (dict(width=8193), "width"), (dict(dtype=4), "dtype"),
+        (dict(activation=3), "activation"), (dict(drop=1.5), "drop"), (dict(drop=float("nan")), "drop"),
+        (dict(eps=-1.0), "eps"), (dict(branch=None, gate=64), "without a branch"),
+        (dict(branch=None, drop=0.5), "without a branch"), (dict(branch_norm=0, branch_weight=64), "branch_norm"),
+        (dict(residual=None), "residual is NULL"), (dict(residual_row=5), "closer"), (dict(branch_row=5), "closer"),
+        (dict(gate=64, gate_row=3), "closer"), (dict(gate=2), "gate"), (dict(weight=2), "weight"),
+        (dict(seed_at=4), "seed_at"), (dict(rows=(1 << 46) + 1), "2\\^46")]
+
+
+@pytest.mark.parametrize("change,text", NORM)
+def test_norm_refuses(rx, block, change, text):
+    lib = rx.load_library()
+    assert lib.norm_forward(C.byref(norm_args(block, **change)), 64, 6, 64, 6, None, None) == EINVAL
+    assert re.search(text, rx.rollout_last_error()), rx.rollout_last_error()
+    g = block.NormGradArgs(f=norm_args(block, **change), stats=64)
+    assert lib.norm_backward(C.byref(g), None) == EINVAL
+    assert re.search(text, rx.rollout_last_error()), rx.rollout_last_error()
+
+
+def test_norm_and_drop_other_refusals(rx, block):
+    lib = rx.load_library()
+    a = norm_args(block)
+    for args, text in (((64, 5, 64, 6, None), "stream"), ((64, 6, 64, 5, None), "normed"), ((66, 6, 64, 6, None), "stream"),
+                       ((64, 6, 64, 6, 66), "stats")):
+        assert lib.norm_forward(C.byref(a), *args, None) == EINVAL
+        assert text in rx.rollout_last_error()
+    for kw, text in ((dict(), "stats is NULL"), (dict(stats=64), "workspace"), (dict(stats=64, dstream=64, dstream_row=5), "dstream"),
+                     (dict(stats=64, dnormed=66), "dnormed"), (dict(stats=64, dresidual=66), "dresidual")):
+        assert lib.norm_backward(C.byref(block.NormGradArgs(f=a, **kw)), None) == EINVAL
+        assert text in rx.rollout_last_error()
+    assert lib.norm_workspace(-1, 6, 0) == EINVAL and lib.norm_workspace(2, 8193, 0) == EINVAL
+    assert lib.norm_workspace(0, 6, 0) == 0 and lib.norm_workspace(2, 6, 0) > 0
+    assert lib.norm_forward(C.byref(norm_args(block, rows=0, residual=None)), None, 0, None, 0, None, None) == OK
+    for args, text in (((3, 64, 8, 0.1, 1, None, 0, 64), "dtype"), ((0, 64, -1, 0.1, 1, None, 0, 64), "count"),
+                       ((0, 64, 8, 1.1, 1, None, 0, 64), "p must"), ((0, 64, 8, float("nan"), 1, None, 0, 64), "p must"),
+                       ((0, None, 8, 0.1, 1, None, 0, 64), "x is NULL"), ((0, 64, 8, 0.1, 1, None, 0, None), "out is NULL"),
+                       ((1, 65, 8, 0.1, 1, None, 0, 64), "aligned"), ((0, 64, 8, 0.1, 1, 60, 0, 64), "seed_at")):
+        assert lib.drop_forward(*args, None) == EINVAL
+        assert text in rx.rollout_last_error()
+    assert lib.drop_forward(0, None, 0, 0.1, 1, None, 0, None, None) == OK
+
+
+# ------------------------------------------------------ the binding's refusals
+def refuses(call, base, changes):
+    for kw, text in changes:
+        with pytest.raises(ValueError, match=text):
+            call(**dict(base, **kw))
+
+
+def test_conv_binding_refusals(rx):
+    x, w = torch.zeros(4, 2, 3), torch.zeros(3, 4)
+    refuses(rx.causal_conv, dict(x=x, weight=w), [
+        (dict(x=x.double()), "float32"), (dict(x=x[0]), "3 dimensions"), (dict(weight=w.half()), "weight"),
+        (dict(weight=w.t().contiguous()), "weight"), (dict(weight=torch.zeros(3, 9)), "taps"),
+        (dict(weight=torch.zeros(3, 0)), "taps"), (dict(weight=torch.zeros(4, 3).t()), "contiguous"), (dict(bias=w[0]), "bias"),
+        (dict(state=torch.zeros(2, 4, 3)), "state"), (dict(state=torch.zeros(2, 3, 3).half()), "state"),
+        (dict(dones=torch.zeros(2, 4, dtype=torch.bool)), "dones"), (dict(activation="relu"), "activation"),
+        (dict(activation="sigmoid"), "activation"), (dict(x=x.permute(1, 2, 0), weight=torch.zeros(4, 4)), "last dimension")])
+    s = torch.zeros(2, 3, 3)
+    refuses(rx.causal_conv_step, dict(x=x[0], weight=w, state=s), [
+        (dict(state=s[:, :2]), "state"), (dict(resets=torch.zeros(3, dtype=torch.bool)), "resets"),
+        (dict(out_state=torch.zeros(2, 3, 4)), "out_state"), (dict(x=x), "2 dimensions"),
+        (dict(x=x[0].clone().requires_grad_()), "no_grad"), (dict(weight=w.clone().requires_grad_()), "no_grad")])
+
+
+def test_out_state_that_overlaps_in_part_is_refused(rx):
+    x, buf = torch.zeros(2, 3), torch.zeros(2 * 3 * 16 + 8)
+    s, o = buf[:96].view(2, 3, 16), buf[8:104].view(2, 3, 16)
+    bc = torch.zeros(2, 16)
+    with pytest.raises(ValueError, match="out_state"):
+        rx.selective_scan_step(x, x, torch.zeros(3, 16), bc, bc, s, out_state=o)
+    c = buf[:18].view(2, 3, 3)
+    with pytest.raises(ValueError, match="out_state"):
+        rx.causal_conv_step(x, torch.zeros(3, 4), c, out_state=buf[3:21].view(2, 3, 3))
+
+
+def test_scan_binding_refusals(rx):
+    x, r, b = torch.zeros(4, 2, 6), torch.zeros(6, 5), torch.zeros(4, 2, 5)
+    base = dict(x=x, delta=x, rate=r, b=b, c=b)
+    refuses(rx.selective_scan, base, [
+        (dict(x=x.double()), "float32"), (dict(delta=x.half()), "delta"), (dict(delta=x[:, :1]), "delta"),
+        (dict(gate=x[..., :5]), "gate"), (dict(rate=r.t().contiguous()), "rate"), (dict(rate=torch.zeros(6, 65)), "1 to 64"),
+        (dict(rate=torch.zeros(6, 0)), "1 to 64"), (dict(rate=r.half()), "rate"), (dict(b=b[..., :4]), "b must"),
+        (dict(c=b.half()), "c must"), (dict(b=torch.zeros(4, 2, 1, 5)), "one shape"),
+        (dict(b=torch.zeros(4, 2, 4, 5), c=torch.zeros(4, 2, 4, 5)), "divide"),
+        (dict(b=torch.zeros(4, 2, 0, 5), c=torch.zeros(4, 2, 0, 5)), "divide"), (dict(skip=torch.zeros(5)), "skip"),
+        (dict(delta_bias=torch.zeros(6, 1)), "delta_bias"), (dict(state=torch.zeros(2, 5, 6)), "state"),
+        (dict(dones=torch.zeros(4, 3, dtype=torch.uint8)), "dones")])
+    s = torch.zeros(2, 6, 5)
+    step = dict(x=x[0], delta=x[0], rate=r, b=b[0], c=b[0], state=s)
+    refuses(rx.selective_scan_step, step, [
+        (dict(state=s[:, :, :4]), "state"), (dict(resets=torch.zeros(3, dtype=torch.bool)), "resets"),
+        (dict(out_state=s[:1]), "out_state"), (dict(delta=x[0].clone().requires_grad_()), "no_grad"),
+        (dict(gate=x), "gate"), (dict(b=b, c=b), "b must")])
+
+
+def test_norm_and_dropout_binding_refusals(rx):
+    x, w = torch.zeros(4, 6), torch.zeros(6)
+    refuses(rx.residual_norm, dict(residual=x, branch=x), [
+        (dict(residual=x.double()), "float32"), (dict(residual=torch.zeros(2, 0)), "1 to 8192"),
+        (dict(residual=torch.zeros(1, 8193)), "1 to 8192"), (dict(branch=x.half()), "branch"), (dict(branch=x[:3]), "branch"),
+        (dict(branch=None, gate=x), "needs a branch"), (dict(branch=None, dropout=0.1), "needs a branch"),
+        (dict(branch_weight=w, branch_norm=False), "branch_norm"), (dict(weight=w[:5]), "weight"),
+        (dict(branch_weight=w.half()), "branch_weight"), (dict(gate=x[:, :5]), "gate"), (dict(gate=w.half()), "gate"),
+        (dict(activation="tanh"), "activation"), (dict(eps=-1e-6), "eps"), (dict(dropout=1.5), "dropout"),
+        (dict(dropout=0.5, offset=-1), "offset"), (dict(dropout=0.5, seed=torch.zeros(2, dtype=torch.int64)), "int64"),
+        (dict(residual=torch.zeros(6, 4).t()), "last dimension"), (dict(residual=x[:1].expand(4, 6)), "overlap"),
+        (dict(gate=torch.zeros(12)[::2]), "gate")])
+    refuses(rx.dropout, dict(x=x, p=0.1, seed=1), [
+        (dict(x=x.double()), "float32"), (dict(x=x.t()), "contiguous"), (dict(p=-0.1), "p must"), (dict(p=float("nan")), "p must"),
+        (dict(offset=1 << 32), "offset"), (dict(seed=torch.zeros(1)), "int64")])
+
+
+# --------------------------------------------- what torch's autograd is told
+@pytest.fixture
+def silent(rx, block, monkeypatch):
+    monkeypatch.setattr(block, "_here", lambda name, *tensors: 0)
+    monkeypatch.setattr(block, "_there", lambda t: 0)
+    monkeypatch.setattr(block, "_call", lambda fn, *args: None)
+    return rx
+
+
+def calls(rx):
+    """Each operator as a function of one tensor, by input."""
+    x, b, r, d = torch.ones(4, 2, 3), torch.ones(4, 2, 5), torch.ones(3, 5), torch.ones(3)
+    s, cs, cw = torch.ones(2, 3, 5), torch.ones(2, 3, 3), torch.ones(3, 4)
+    scan = dict(x=x, delta=x, rate=r, b=b, c=b, skip=d, gate=x, delta_bias=d, state=s)
+    step = dict(x=x[0], delta=x[0], rate=r, b=b[0], c=b[0], skip=d, gate=x[0], delta_bias=d, state=s)
+    conv = dict(x=x, weight=cw, bias=d, state=cs)
+    norm = dict(residual=x, branch=x, weight=d, branch_weight=d, gate=x)
+    table = {"dropout x": (x, lambda t: rx.dropout(t, 0.1, 3))}
+    for op, fn, base in (("selective_scan", rx.selective_scan, scan), ("selective_scan_step", rx.selective_scan_step, step),
+                         ("causal_conv", rx.causal_conv, conv),
+                         ("causal_conv_step", rx.causal_conv_step, dict(conv, x=x[0])),
+                         ("residual_norm", rx.residual_norm, norm)):
+        for k, v in base.items():
+            table[f"{op} {k}"] = (v, lambda t, fn=fn, base=base, k=k: fn(**dict(base, **{k: t})))
+    table["selective_scan_step out_state"] = (s, lambda t: rx.selective_scan_step(**step, out_state=t))
+    table["causal_conv_step out_state"] = (cs, lambda t: rx.causal_conv_step(**dict(conv, x=x[0]), out_state=t))
+    return table
+
+
+NAMES = [f"{op} {k}" for op, ks in (
+    ("selective_scan", "x delta rate b c skip gate delta_bias state"),
+    ("selective_scan_step", "x delta rate b c skip gate delta_bias state out_state"),
+    ("causal_conv", "x weight bias state"), ("causal_conv_step", "x weight bias state out_state"),
+    ("residual_norm", "residual branch weight branch_weight gate"), ("dropout", "x")) for k in ks.split()]
+
+
+def test_every_call_is_listed(silent):
+    assert sorted(calls(silent)) == sorted(NAMES)
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("grad_mode", [True, False])
+def test_forward_mode_derivatives_are_refused(silent, name, grad_mode):
+    t, call = calls(silent)[name]
+    call(t)
+    with fwd.dual_level():
+        call(t)
+        with torch.set_grad_enabled(grad_mode), pytest.raises(NotImplementedError, match="forward-mode"):
+            call(fwd.make_dual(t.clone(), torch.ones_like(t)))
+
+
+@pytest.mark.parametrize("name", [n for n in NAMES if "step" not in n])
+def test_gradients_have_their_inputs_shapes_and_no_gradient(silent, name):
+    t, call = calls(silent)[name]
+    leaf = t.clone().requires_grad_()
+    out = call(leaf)
+    outs = out if isinstance(out, tuple) else (out,)
+    for o in outs:
+        g, = torch.autograd.grad(o, leaf, torch.ones_like(o), retain_graph=True)
+        assert g.shape == t.shape and g.dtype == t.dtype
+    g, = torch.autograd.grad(outs, leaf, [torch.ones_like(o) for o in outs], retain_graph=True, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable|does not require grad|differentiate twice"):
+        torch.autograd.grad(g.sum(), leaf)
+    with fwd.dual_level(), pytest.raises(NotImplementedError, match="forward-mode"):
+        torch.autograd.grad(outs[0], leaf, fwd.make_dual(torch.ones_like(outs[0]), torch.ones_like(outs[0])))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_steps_take_leaves_under_no_grad_and_others_record_one(silent, name):
+    t, call = calls(silent)[name]
+    leaf = t.clone().requires_grad_()
+    with torch.no_grad():
+        out = call(leaf)
+    if "step" in name:
+        with pytest.raises(ValueError, match="no_grad"):
+            call(leaf)
+    else:
+        out = call(leaf)
+        assert all(o.requires_grad for o in (out if isinstance(out, tuple) else (out,)))
+
+
+def test_written_state_counts_as_changed(silent):
+    s = torch.ones(2, 3, 5)
+    w = torch.ones((), requires_grad=True)
+    y = (w * s).sum()
+    x, b = torch.ones(2, 3), torch.ones(2, 5)
+    silent.selective_scan_step(x, x, torch.ones(3, 5), b, b, s, out_state=s)
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        y.backward()
+
+
+def test_a_seed_that_changed_before_the_gradient_is_refused(silent):
+    seed = torch.ones(1, dtype=torch.int64)
+    x = torch.ones(4, requires_grad=True)
+    y = silent.dropout(x, 0.5, seed)
+    seed += 1
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        torch.autograd.grad(y, x, torch.ones(4))
+
+
+# ------------------------------------------------------- the reference itself
+def slope(f, x, at, h=1e-6):
+    lo, hi = x.copy(), x.copy()
+    lo[at] -= h
+    hi[at] += h
+    return (f(hi) - f(lo)) / (2 * h)
+
+
+def check_slopes(rng, loss, inputs, grads):
+    for k, g in grads.items():
+        for _ in range(4):
+            at = tuple(rng.integers(n) for n in inputs[k].shape)
+            want = slope(lambda v: loss(dict(inputs, **{k: v})), inputs[k], at)
+            assert abs(g[at] - want) < 1e-6 * (1 + abs(want)), (k, at, g[at], want)
+
+
+@pytest.mark.parametrize("W,L", [(1, 5), (4, 2), (4, 9)])
+@pytest.mark.parametrize("silu", [False, True])
+def test_reference_conv_gradient_against_differences(W, L, silu):
+    rng = np.random.default_rng(W + L)
+    N, D = 3, 2
+    i = dict(x=rng.standard_normal((L, N, D)), weight=rng.standard_normal((D, W)), bias=rng.standard_normal(D),
+             state=rng.standard_normal((N, W - 1, D)))
+    dones = (rng.random((L, N)) < 0.3).astype(np.uint8)
+    dy, dn = rng.standard_normal((L, N, D)), rng.standard_normal((N, W - 1, D))
+
+    def loss(v):
+        r = ref.conv(v["x"], v["weight"], v["bias"], v["state"], dones, silu, "f32")
+        return (r["y"] * dy).sum() + (r["new_state"] * dn).sum()
+
+    r = ref.conv(i["x"], i["weight"], i["bias"], i["state"], dones, silu, "f32", dy, dn)
+    check_slopes(rng, loss, i, {k: r["d" + k] for k in i if i[k].size})
+
+
+@pytest.mark.parametrize("soft", [False, True])
+@pytest.mark.parametrize("G", [1, 2])
+def test_reference_scan_gradient_against_differences(soft, G):
+    rng = np.random.default_rng(7 + G)
+    L, N, D, S = 6, 2, 4, 3
+    n = rng.standard_normal
+    i = dict(x=n((L, N, D)), delta=n((L, N, D)) if soft else rng.random((L, N, D)), rate=-rng.random((D, S)) - 0.1,
+             b=n((L, N, G, S)), c=n((L, N, G, S)), skip=n(D), gate=n((L, N, D)), delta_bias=n(D) * 0.1, state=n((N, D, S)))
+    dones = (rng.random((L, N)) < 0.3).astype(np.uint8)
+    dy, dn = n((L, N, D)), n((N, D, S))
+
+    def run(v, **kw):
+        return ref.scan(v["x"], v["delta"], v["rate"], v["b"], v["c"], v["skip"], v["gate"], v["delta_bias"], v["state"],
+                        dones, soft, "f32", **kw)
+
+    def loss(v):
+        r = run(v)
+        return (r["y"] * dy).sum() + (r["new_state"] * dn).sum()
+
+    r = run(i, dy=dy, dnew=dn)
+    check_slopes(rng, loss, i, {k: r["d" + k] for k in i})
+
+
+@pytest.mark.parametrize("act", ["none", "sigmoid", "silu"])
+@pytest.mark.parametrize("full", [False, True])
+def test_reference_norm_gradient_against_differences(act, full):
+    rng = np.random.default_rng(11)
+    R, D = 3, 5
+    n = rng.standard_normal
+    i = dict(residual=n((R, D)), branch=n((R, D)), weight=n(D), branch_weight=n(D), gate=n((R, D) if full else D))
+    kept = rng.random((R, D)) < 0.7
+    ds, dn = n((R, D)), n((R, D))
+    opt = dict(act=act, rs=0.9, bs=0.5, kept=kept, scale=1.4)
+
+    def loss(v):
+        r = ref.norm(*[v[k] for k in ("residual", "branch", "weight", "branch_weight", "gate")], "f32", **opt)
+        return (r["stream"] * ds).sum() + (r["normed"] * dn).sum()
+
+    r = ref.norm(*[i[k] for k in ("residual", "branch", "weight", "branch_weight", "gate")], "f32", dstream=ds,
+                 dnormed=dn, **opt)
+    check_slopes(rng, loss, i, {k: r["d" + k] for k in i})
+
+
+def test_reference_draws_are_philox():
+    # known answers of Philox4x32-10 for counters and keys of zeros and of ones
+    assert ref.philox((0,) * 4, (0, 0)) == [0x6627e8d5, 0xe169c58d, 0xbc57ac4c, 0x9b00dbd8]
+    assert ref.philox((0xffffffff,) * 4, (0xffffffff,) * 2) == [0x408f276d, 0x41c83b0e, 0xa20bc7c6, 0x6d5451fd]
+    kept, scale = ref.kept(4000, 0.25, 5)
+    # a binomial of 4000 draws: five standard deviations are 137
+    assert abs(int(kept.sum()) - 3000) < 137 and scale == 4 / 3
