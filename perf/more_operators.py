@@ -397,7 +397,7 @@ def _own(s):
                                    dropout=case["p"], seed=s["seed"])
         gradients = (s.get("dstream"), s.get("dnormed"))
     if case["what"] != "train":
-        return outputs
+        return outputs[0] if case["op"] == "dropout" else outputs
     return tuple(t.detach() for t in outputs) + \
         torch.autograd.grad(outputs, [s[k] for k in s["leaves"]], gradients)
 
