@@ -119,9 +119,9 @@ typedef struct {
   const uint8_t *dones;                   /* NULL: none */
   void *y;
   float *new_state; /* NULL: not written */
-  /* [ceil(L / 8)][N][D][S]: the states that enter the steps 0, 8, 16, ...
-   * (before a done cuts them), which the gradient starts from.  Written by
-   * the forward call (NULL: not written), read by the backward call. */
+  /* scan_kept() floats, 16-byte aligned: the states that enter the steps 0, 8,
+   * 16, ..., which the gradient starts from.  Written by the forward call
+   * (NULL: not written), read by the backward call; the order is its own. */
   float *kept;
   void *workspace; /* scan_workspace() or scan_grad_workspace() bytes, 16-byte aligned */
   int64_t workspace_bytes;
@@ -139,6 +139,8 @@ typedef struct {
   float *dskip, *ddelta_bias, *dstate; /* NULL: not written */
 } scan_grad_args;
 
+/* Floats of `kept`: about ceil(L / 8) * N * D * S. */
+int64_t scan_kept(int32_t steps, int32_t rows, int32_t width, int32_t states, int32_t groups);
 /* Bytes (0 for most sizes), or a negative ROLLOUT_E* code. */
 int64_t scan_workspace(int32_t steps, int32_t rows, int32_t width, int32_t states, int32_t groups);
 int64_t scan_grad_workspace(int32_t steps, int32_t rows, int32_t width, int32_t states,

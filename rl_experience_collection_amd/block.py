@@ -23,7 +23,7 @@ from .policy import (_DTYPES, _apart_or_same, _call, _element, _exact, _first_or
 
 BLOCK_NONE, BLOCK_SIGMOID, BLOCK_SILU = 0, 1, 2
 EXPORTED = ("conv_forward", "conv_workspace", "conv_backward", "conv_step",
-            "scan_workspace", "scan_grad_workspace", "scan_forward", "scan_backward", "scan_step",
+            "scan_kept", "scan_workspace", "scan_grad_workspace", "scan_forward", "scan_backward", "scan_step",
             "norm_forward", "norm_workspace", "norm_backward", "drop_forward")
 
 _ACTIVATIONS = {"none": BLOCK_NONE, "sigmoid": BLOCK_SIGMOID, "silu": BLOCK_SILU}
@@ -85,7 +85,7 @@ def declare(lib):
     lib.conv_workspace.argtypes = [i32] * 5
     lib.conv_backward.argtypes = [C.POINTER(ConvGradArgs), vp]
     lib.conv_step.argtypes = [i32] * 5 + [vp, i64, vp, vp, vp, vp, vp, i64, vp, vp]
-    lib.scan_workspace.argtypes = lib.scan_grad_workspace.argtypes = [i32] * 5
+    lib.scan_kept.argtypes = lib.scan_workspace.argtypes = lib.scan_grad_workspace.argtypes = [i32] * 5
     lib.scan_forward.argtypes = lib.scan_step.argtypes = [C.POINTER(ScanArgs), vp]
     lib.scan_backward.argtypes = [C.POINTER(ScanGradArgs), vp]
     lib.norm_forward.argtypes = [C.POINTER(NormArgs), vp, i64, vp, i64, vp, vp]
@@ -93,7 +93,7 @@ def declare(lib):
     lib.norm_backward.argtypes = [C.POINTER(NormGradArgs), vp]
     lib.drop_forward.argtypes = [i32, vp, i64, C.c_float, C.c_uint64, vp, C.c_uint32, vp, vp]
     for name in EXPORTED:
-        getattr(lib, name).restype = i64 if name.endswith("_workspace") else C.c_int
+        getattr(lib, name).restype = i64 if name.endswith(("_workspace", "_kept")) else C.c_int
 
 
 def _activation(name, allowed):
@@ -256,7 +256,9 @@ class _SelectiveScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, delta, rate, b, c, skip, gate, delta_bias, state, dones, softplus):
         # the states that the gradient starts from, one of eight
-        kept = torch.empty(((x.shape[0] + 7) // 8, x.shape[1]) + rate.shape, dtype=_f32, device=x.device)
+        L, N, D = x.shape
+        size = _lib().scan_kept(L, N, D, rate.shape[1], b.shape[2] if b.dim() == 4 else 1)
+        kept = torch.empty(max(size, 0), dtype=_f32, device=x.device)
         y, new = _scan_forward(x, delta, rate, b, c, skip, gate, delta_bias, state, dones, softplus, kept)
         ctx.save_for_backward(x, delta, rate, b, c, skip, gate, delta_bias, dones, kept)
         ctx.softplus = softplus

@@ -20,6 +20,7 @@ hipError_t conv_step_launch(int32_t N, int32_t D, int32_t W, int32_t dtype, int3
                             const void* state, const uint8_t* resets, void* y, int64_t y_row,
                             void* new_state, hipStream_t stream);
 
+int64_t scan_kept_floats(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G);
 int64_t scan_workspace_bytes(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G);
 int64_t scan_grad_workspace_bytes(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G);
 hipError_t scan_forward_launch(const scan_args& a, hipStream_t stream);

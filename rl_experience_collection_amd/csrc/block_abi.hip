@@ -183,6 +183,12 @@ int conv_step(int32_t rows, int32_t width, int32_t taps, int32_t dtype, int32_t 
                   who);
 }
 
+int64_t scan_kept(int32_t steps, int32_t rows, int32_t width, int32_t states, int32_t groups) {
+  const char* who = "scan_kept";
+  RL_CHECK(check_sizes(who, steps, rows, width, POLICY_F32));
+  RL_CHECK(check_states(who, width, rows, states, groups));
+  return rl::scan_kept_floats(steps, rows, width, states, groups);
+}
 int64_t scan_workspace(int32_t steps, int32_t rows, int32_t width, int32_t states, int32_t groups) {
   const char* who = "scan_workspace";
   RL_CHECK(check_sizes(who, steps, rows, width, POLICY_F32));
@@ -206,7 +212,7 @@ int scan_forward(const scan_args* a, void* hip_stream) {
   if (a->steps > 0) {
     RL_CHECK(check_scan_inputs(who, *a));
     RL_CHECK(check_array(who, "y", a->y, a->y_step, a->y_row, element_bytes(a->dtype)));
-    RL_CHECK(check_optional(who, "kept", a->kept, 4));
+    RL_CHECK(check_optional(who, "kept", a->kept, 16));
     RL_CHECK(check_workspace(who, rl::scan_workspace_bytes(a->steps, a->rows, a->width, a->states, a->groups),
                              a->workspace, a->workspace_bytes));
   }
@@ -227,7 +233,7 @@ int scan_backward(const scan_grad_args* g, void* hip_stream) {
   if (a.rows > 0 && a.steps > 0) {
     const size_t eb = element_bytes(a.dtype);
     RL_CHECK(check_scan_inputs(who, a));
-    RL_CHECK(check_buffer(who, "kept", a.kept, 4));
+    RL_CHECK(check_buffer(who, "kept", a.kept, 16));
     RL_CHECK(check_array(who, "dy", g->dy, g->dy_step, g->dy_row, eb));
     RL_CHECK(check_array(who, "dx", g->dx, g->dx_step, g->dx_row, eb));
     RL_CHECK(check_array(who, "ddelta", g->ddelta, g->ddelta_step, g->ddelta_row, eb));

@@ -16,25 +16,6 @@ struct ScanRun {
   ScanSummary sum;
 };
 
-// One unit's x, delta and gate of a lane's channel, as loaded.
-template <class T>
-struct UnitColumns {
-  typename T::raw x[kUnit], d[kUnit], z[kUnit];
-  __device__ __forceinline__ void load(const scan_args& a, const ScanWave& k, int32_t t0, bool gate) {
-    using raw = typename T::raw;
-    const raw* px = static_cast<const raw*>(a.x) + k.n * a.x_row;
-    const raw* pd = static_cast<const raw*>(a.delta) + k.n * a.delta_row;
-    const raw* pz = static_cast<const raw*>(a.gate) + k.n * a.gate_row;
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i) {
-      const int32_t t = min(t0 + i, a.steps - 1);
-      x[i] = (px + t * a.x_step)[k.channel];
-      d[i] = (pd + t * a.delta_step)[k.channel];
-      if (gate) z[i] = (pz + t * a.gate_step)[k.channel];
-    }
-  }
-};
-
 // What enters chunk `chunk`: the states that the chunks before leave, one
 // after another.
 __device__ __forceinline__ void enter_chunk(const ScanRun& q, const ScanWave& k, const float (&rate)[4][4],
@@ -61,7 +42,7 @@ __device__ __forceinline__ void enter_chunk(const ScanRun& q, const ScanWave& k,
 }
 
 // A chunk of the scan.  SUMMARY: from a state of zero, without outputs.
-template <class T, int NB, bool SUMMARY>
+template <class T, int NB, bool GATED, bool SUMMARY>
 __global__ void __launch_bounds__(64 * NB) scan_forward_kernel(const ScanRun q) {
   const scan_args& a = q.a;
   const ScanWave k(q.p, a.rows, a.groups, a.states);
@@ -69,7 +50,6 @@ __global__ void __launch_bounds__(64 * NB) scan_forward_kernel(const ScanRun q) 
   __shared__ float s_part[NB > 1 && !SUMMARY ? 2 : 1][NB > 1 && !SUMMARY ? NB : 1][kUnit][64];
   const int32_t L = a.steps, S = a.states;
   const int32_t u0 = k.chunk * q.p.chunk_units, u1 = min(u0 + q.p.chunk_units, q.p.units);
-  const bool gated = !SUMMARY && a.gate != nullptr;
 
   float rate[4][4], h[4][4];
 #pragma unroll
@@ -91,20 +71,23 @@ __global__ void __launch_bounds__(64 * NB) scan_forward_kernel(const ScanRun q) 
   float total = 0.0f;
   uint32_t any_cut = 0;
 
+  const Column<T> cx(a, q.p, k, a.x, a.x_step, a.x_row), cd(a, q.p, k, a.delta, a.delta_step, a.delta_row),
+      cz(a, q.p, k, a.gate, a.gate_step, a.gate_row), cy(a, q.p, k, a.y, a.y_step, a.y_row);
+  const Kept kept(a, q.p, k);
   UnitInputs<T> in;
-  UnitColumns<T> col;
-  in.load(a, k, u0 * kUnit);
-  col.load(a, k, u0 * kUnit, gated);
-  uint32_t cuts = unit_cuts(a, k, u0 * kUnit);
+  typename T::raw rx[kUnit], rd[kUnit], rz[kUnit];
+  const auto fetch = [&](int32_t u) {
+    in.load(a, k, u * kUnit);
+    cx.load(u * kUnit, rx);
+    cd.load(u * kUnit, rd);
+    if (GATED) cz.load(u * kUnit, rz);
+    return unit_cuts(a, k, u * kUnit);
+  };
+  uint32_t cuts = fetch(u0);
   for (int32_t u = u0; u < u1; ++u) {
     const int32_t t0 = u * kUnit;
     if constexpr (!SUMMARY) {
-      if (a.kept) {
-        const int64_t at = ((int64_t)u * a.rows + k.n) * a.width;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (k.quad_has(q.p, r)) store_states(a.kept + (at + k.quad_channel(q.p, r)) * S, k.s0, S, h[r]);
-      }
+      if (a.kept) kept.store(u, h);
     }
     wave_sync();  // (the reads of the unit before)
     in.put(s_bc[k.w], k.lane);
@@ -112,22 +95,19 @@ __global__ void __launch_bounds__(64 * NB) scan_forward_kernel(const ScanRun q) 
     float x[kUnit], dt[kUnit], du[kUnit], z[kUnit], y[kUnit];
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) {
-      x[i] = T::widen(col.x[i]);
-      const float v = T::widen(col.d[i]) + bias;
+      x[i] = T::widen(rx[i]);
+      const float v = T::widen(rd[i]) + bias;
       float E;
-      dt[i] = a.softplus ? softplus_of(v, E) : v;
+      const float sp = softplus_of(v, E);
+      dt[i] = a.softplus ? sp : v;
       du[i] = dt[i] * x[i];
       if (t0 + i >= L) dt[i] = du[i] = 0.0f;  // past the end: the state stays
       if (SUMMARY) total += dt[i];
-      if (gated) z[i] = T::widen(col.z[i]);
+      if (GATED) z[i] = T::widen(rz[i]);
     }
     const uint32_t cut = cuts;
     any_cut |= cut;
-    if (u + 1 < u1) {
-      in.load(a, k, t0 + kUnit);
-      col.load(a, k, t0 + kUnit, gated);
-      cuts = unit_cuts(a, k, t0 + kUnit);
-    }
+    cuts = fetch(min(u + 1, u1 - 1));
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) {
       if ((cut >> i) & 1u) {
@@ -138,8 +118,9 @@ __global__ void __launch_bounds__(64 * NB) scan_forward_kernel(const ScanRun q) 
       }
       const float4 b4 = *reinterpret_cast<const float4*>(&s_bc[k.w][i][4 * k.j]);
       const float b[4] = {b4.x, b4.y, b4.z, b4.w};
-      const float dts[4] = {quad_get<0>(dt[i]), quad_get<1>(dt[i]), quad_get<2>(dt[i]), quad_get<3>(dt[i])};
-      const float dus[4] = {quad_get<0>(du[i]), quad_get<1>(du[i]), quad_get<2>(du[i]), quad_get<3>(du[i])};
+      float dts[4], dus[4];
+      quad_give(dt[i], dts);
+      quad_give(du[i], dus);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -155,7 +136,7 @@ __global__ void __launch_bounds__(64 * NB) scan_forward_kernel(const ScanRun q) 
 #pragma unroll
           for (int s = 1; s < 4; ++s) part[r] = __builtin_fmaf(c[s], h[r][s], part[r]);
         }
-        y[i] = quad_turn(part, k.lane);
+        y[i] = quad_sum(part);
       }
     }
     if constexpr (!SUMMARY) {
@@ -172,14 +153,12 @@ __global__ void __launch_bounds__(64 * NB) scan_forward_kernel(const ScanRun q) 
           for (int v = 1; v < NB; ++v) y[i] += buf[v][i][k.lane];
         }
       }
-      typename T::raw* py = static_cast<typename T::raw*>(a.y) + k.n * a.y_row;
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) {
         if (NB > 1 && i % NB != k.w) continue;
-        if (t0 + i >= L) continue;
         float v = __builtin_fmaf(skip, x[i], y[i]);
-        if (gated) v *= z[i] * sigmoid_of(z[i]);
-        if (k.mine) (py + (t0 + i) * a.y_step)[k.channel] = T::narrow(v);
+        if (GATED) v *= z[i] * sigmoid_of(z[i]);
+        cy.store(t0 + i, v);
       }
     }
   }
@@ -253,22 +232,22 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const scan_args a, int32
 
 template <class T, int NB>
 void launch_forward(const ScanRun& q, hipStream_t stream) {
-  const uint32_t groups = (uint32_t)(q.p.columns * q.p.chunks);
+  const dim3 threads(64 * NB), groups((uint32_t)(q.p.columns * q.p.chunks));
   // (the last chunk's summary is read by none)
   if (q.p.chunks > 1)
-    scan_forward_kernel<T, NB, true>
-        <<<dim3((uint32_t)(q.p.columns * (q.p.chunks - 1))), dim3(64 * NB), 0, stream>>>(q);
-  scan_forward_kernel<T, NB, false><<<dim3(groups), dim3(64 * NB), 0, stream>>>(q);
+    scan_forward_kernel<T, NB, false, true>
+        <<<dim3((uint32_t)(q.p.columns * (q.p.chunks - 1))), threads, 0, stream>>>(q);
+  if (q.a.gate)
+    scan_forward_kernel<T, NB, true, false><<<groups, threads, 0, stream>>>(q);
+  else
+    scan_forward_kernel<T, NB, false, false><<<groups, threads, 0, stream>>>(q);
 }
 
 template <class T>
 void launch_states(const ScanRun& q, hipStream_t stream) {
-  switch (q.p.state_blocks) {
-    case 1: return launch_forward<T, 1>(q, stream);
-    case 2: return launch_forward<T, 2>(q, stream);
-    case 3: return launch_forward<T, 3>(q, stream);
-    default: return launch_forward<T, 4>(q, stream);
-  }
+  if (q.p.state_blocks == 1) return launch_forward<T, 1>(q, stream);
+  if (q.p.state_blocks == 2) return launch_forward<T, 2>(q, stream);
+  return launch_forward<T, 4>(q, stream);
 }
 
 }  // namespace
@@ -281,7 +260,7 @@ ScanPlan scan_plan(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G, bool g
   p.group_width = D / G;
   p.blocks = cdiv(p.group_width, 64);
   p.units = cdiv(L, kUnit);
-  p.state_blocks = cdiv(S, kBlock);
+  p.state_blocks = S <= kBlock ? 1 : S <= 2 * kBlock ? 2 : 4;
   p.columns = (int64_t)N * G * p.blocks;
   const int64_t waves = p.columns * p.state_blocks;
   p.chunks = 1;
@@ -309,6 +288,11 @@ ScanSummary scan_summary(const ScanPlan& p, int32_t N, int32_t D, int32_t S, voi
   char* w = static_cast<char*>(workspace);
   return ScanSummary{reinterpret_cast<float*>(w), reinterpret_cast<float*>(w + up(nd * S * 4)),
                      reinterpret_cast<int32_t*>(w + up(nd * S * 4) + up(nd * 4))};
+}
+
+int64_t scan_kept_floats(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G) {
+  const int64_t quads = (D / G + 3) / 4;
+  return (int64_t)cdiv(L, kUnit) * N * G * quads * 4 * ((S + 3) / 4 * 4);
 }
 
 int64_t scan_workspace_bytes(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G) {

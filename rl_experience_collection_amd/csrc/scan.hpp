@@ -3,13 +3,14 @@
 // A wave takes 64 channels of one episode and group, and 16 of the S states
 // of each.  Lane l reads, converts and writes channel l of its steps; the
 // states are spread the other way: lane 4 i + j holds states 4 j .. 4 j + 3
-// of the channels 4 i .. 4 i + 3 of its quad.  What a step needs of a channel
-// comes by quad broadcasts, what the states sum up to goes back by a
-// transposed sum over the quad, the b and c of a step are four values a lane
-// (one LDS read each, the same for all quads), and sums over channels (the
-// gradients of b and c) run over a lane's own four channels for free before
-// lanes have to meet.  With more than 16 states a workgroup's waves take 16
-// each of the same channels.
+// of the four channels of its quad, channel 4 i + (r ^ j) in its place r.  By
+// that order a channel's value comes to place r, and a sum over its states
+// goes back from there, by the one exchange of lanes j ^ r (nothing has to be
+// selected; places in one order for all lanes took 9 operations a sum, this
+// 3).  The b and c of a step are four values a lane (one LDS read each, the
+// same for all quads), and sums over channels (the gradients of b and c) run
+// over a lane's own four channels for free before lanes have to meet.  With
+// more than 16 states a workgroup's waves take 16 each of the same channels.
 //
 // Steps go in units of eight.  Long scans of few columns are cut into chunks
 // of units: one launch finds what each chunk makes of a state of zero and how
@@ -48,21 +49,26 @@ ScanPlan scan_plan(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G, bool g
 int64_t scan_summary_bytes(const ScanPlan& p, int32_t N, int32_t D, int32_t S);
 ScanSummary scan_summary(const ScanPlan& p, int32_t N, int32_t D, int32_t S, void* workspace);
 
-// The value lane 4 i + R of this lane's quad holds.
+// The value of lane j ^ R of this lane's quad.
 template <int R>
-__device__ __forceinline__ float quad_get(float x) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), R * 0x55, 0xF, 0xF, true));
+__device__ __forceinline__ float quad_xor(float x) {
+  constexpr int kPerm = (R ^ 0) | (R ^ 1) << 2 | (R ^ 2) << 4 | (R ^ 3) << 6;
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), kPerm, 0xF, 0xF, true));
 }
-template <int CTRL>
-__device__ __forceinline__ float from_lane(float x) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
+// A channel's value in the places of its quad's lanes.
+__device__ __forceinline__ void quad_give(float x, float (&v)[4]) {
+  v[0] = x;
+  v[1] = quad_xor<1>(x);
+  v[2] = quad_xor<2>(x);
+  v[3] = quad_xor<3>(x);
 }
-// Lane j of a quad gets the quad's sum of v[j].
-__device__ __forceinline__ float quad_turn(const float (&v)[4], int lane) {
-  const bool odd = lane & 1, high = lane & 2;
-  const float a = (odd ? v[1] : v[0]) + from_lane<0xB1>(odd ? v[0] : v[1]);
-  const float b = (odd ? v[3] : v[2]) + from_lane<0xB1>(odd ? v[2] : v[3]);
-  return (high ? b : a) + from_lane<0x4E>(high ? a : b);
+// The quad's sum for the lane's own channel.  (The empty statement keeps the
+// additions here, where they take the exchanges as operands; moved to where
+// the sum is used they would leave those, which cannot move, on their own.)
+__device__ __forceinline__ float quad_sum(const float (&v)[4]) {
+  float sum = ((v[0] + quad_xor<1>(v[1])) + quad_xor<2>(v[2])) + quad_xor<3>(v[3]);
+  asm("" : "+v"(sum));
+  return sum;
 }
 
 // softplus(v) and sigmoid(v) from E = exp(-|v|): log(1 + E) = 2 artanh(E / (2 + E)),
@@ -119,14 +125,36 @@ struct ScanWave {
     channel = g * p.group_width + min(local, p.group_width - 1);
     first = block * 64 + (lane & ~3);
   }
-  // Channel r of the lane's quad, clamped into the group.
+  // The channel of place r, clamped into the group.
   __device__ __forceinline__ int32_t quad_channel(const ScanPlan& p, int r) const {
-    return g * p.group_width + min(first + r, p.group_width - 1);
+    return g * p.group_width + min(first + (r ^ j), p.group_width - 1);
   }
   __device__ __forceinline__ bool quad_has(const ScanPlan& p, int r) const {
-    return first + r < p.group_width;
+    return first + (r ^ j) < p.group_width;
   }
 };
+
+// Access to a row whose address and length the wave shares.  The hardware
+// drops what lies past the length: lanes without a channel and steps past the
+// end (length 0) read 0 and write nothing, with no branch and no clamping.
+typedef uint32_t words4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_of(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
+}
+template <class T>
+__device__ __forceinline__ typename T::raw row_load(const void* p, uint32_t bytes, uint32_t at) {
+  if constexpr (T::kBytes == 4)
+    return __builtin_amdgcn_raw_buffer_load_b32(row_of(p, bytes), at, 0, 0);
+  else
+    return __builtin_amdgcn_raw_buffer_load_b16(row_of(p, bytes), at, 0, 0);
+}
+template <class T>
+__device__ __forceinline__ void row_store(void* p, uint32_t bytes, uint32_t at, float x) {
+  if constexpr (T::kBytes == 4)
+    __builtin_amdgcn_raw_buffer_store_b32(T::narrow(x), row_of(p, bytes), at, 0, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b16(T::narrow(x), row_of(p, bytes), at, 0, 0);
+}
 
 // The four states from s0 of a row of S; those that do not exist are 0.
 __device__ __forceinline__ void load_states(const float* row, int32_t s0, int32_t S, float (&h)[4]) {
@@ -160,8 +188,9 @@ struct UnitInputs {
     const typename T::raw* row = static_cast<const typename T::raw*>(is_c ? a.c : a.b) +
                                  t * (is_c ? a.c_step : a.b_step) + k.n * (is_c ? a.c_row : a.b_row) +
                                  k.g * (is_c ? a.c_group : a.b_group);
-    if (s0 + 4 <= a.states) {
-      widen_pack<T, 4>(load_pack<T, 4>(row + s0), v);
+    if (a.states % 4 == 0) {
+      widen_pack<T, 4>(load_pack<T, 4>(row + min(s0, a.states - 4)), v);
+      if (s0 >= a.states) v[0] = v[1] = v[2] = v[3] = 0.0f;
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = s0 + i < a.states ? T::widen(row[s0 + i]) : 0.0f;
@@ -169,6 +198,70 @@ struct UnitInputs {
   }
   __device__ __forceinline__ void put(float (&lds)[kUnit][32], int lane) const {
     *reinterpret_cast<float4*>(&lds[lane >> 3][4 * (lane & 7)]) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+};
+
+// A lane's own channel in one of the [L][N][D] arrays.
+template <class T>
+struct Column {
+  char* row;  // the wave's channels at step 0
+  int64_t step;
+  uint32_t bytes, at;
+  int32_t steps;
+  __device__ __forceinline__ Column(const scan_args& a, const ScanPlan& p, const ScanWave& k, const void* base,
+                                    int64_t step_, int64_t row_)
+      : row(const_cast<char*>(static_cast<const char*>(base)) +
+            (k.n * row_ + k.g * p.group_width + k.block * 64) * T::kBytes),
+        step(step_ * T::kBytes),
+        bytes((uint32_t)min(64, p.group_width - k.block * 64) * T::kBytes),
+        at(k.lane * T::kBytes),
+        steps(a.steps) {}
+  __device__ __forceinline__ void load(int32_t t0, typename T::raw (&x)[kUnit]) const {
+    const char* p = row + t0 * step;
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i, p += step) x[i] = row_load<T>(p, t0 + i < steps ? bytes : 0, at);
+  }
+  __device__ __forceinline__ void store(int32_t t, float x) const {
+    row_store<T>(row + t * step, t < steps ? bytes : 0, at, x);
+  }
+};
+
+// The states that enter the units, as they lie in the lanes: [units][N][G][quads]
+// [places][4 ceil(S / 4)], so that a quad's lanes write one run of 64 bytes.
+// (In the order of the channels a store of a wave would touch four times as
+// many lines.)
+struct Kept {
+  float* base;
+  int64_t unit;  // floats of a unit
+  uint32_t bytes, at, place;
+  __device__ __forceinline__ Kept(const scan_args& a, const ScanPlan& p, const ScanWave& k) {
+    const int32_t quads = (p.group_width + 3) / 4, wide = (a.states + 3) / 4 * 4;
+    const int64_t row = (int64_t)quads * 4 * wide;
+    unit = (int64_t)a.rows * a.groups * row;
+    base = a.kept + ((int64_t)k.n * a.groups + k.g) * row + (int64_t)k.block * 64 * wide;
+    bytes = (uint32_t)min(16, quads - k.block * 16) * 16 * wide;
+    place = wide * 4;
+    // (states past the last run: an offset past the end)
+    at = k.s0 < wide ? ((k.lane >> 2) * 4 * wide + k.s0) * 4 : 1u << 31;
+  }
+  __device__ __forceinline__ void load(int32_t u, float (&h)[4][4]) const {
+    const auto rsrc = row_of(base + u * unit, bytes);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const words4 x = __builtin_amdgcn_raw_buffer_load_b128(rsrc, at + r * place, 0, 0);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) h[r][s] = __uint_as_float(x[s]);
+    }
+  }
+  __device__ __forceinline__ void store(int32_t u, const float (&h)[4][4]) const {
+    const auto rsrc = row_of(base + u * unit, bytes);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      words4 x;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) x[s] = __float_as_uint(h[r][s]);
+      __builtin_amdgcn_raw_buffer_store_b128(x, rsrc, at + r * place, 0, 0);
+    }
   }
 };
 

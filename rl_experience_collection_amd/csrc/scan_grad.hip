@@ -8,16 +8,22 @@
 //   dD = x sum over s of b d + sum over s of rate q,  dx = D sum of b d + skip w.
 // A wave runs its units from the last to the first.  Of a unit it takes the
 // state that enters it from what the forward call kept, forms its eight states
-// again, holding kHeld of them in registers at a time, and goes back over
-// them.  Decays are formed twice (an exp2 costs less than the registers that
-// would hold it).
+// again, the first four to LDS and the others in registers, and goes back over
+// them.  (Four in registers alone, formed twice, took half as many more states
+// to form; eight in registers leave a SIMD one wave.)  Decays are formed twice:
+// an exp2 costs less than the place to hold it.
 #include "scan.hpp"
 
 namespace rl {
 
 namespace {
 
-constexpr int kHeld = 4;  // states of a lane's channels held at a time
+constexpr int kHeld = 4;  // steps whose states are held in registers, and as many in LDS
+
+template <int CTRL>
+__device__ __forceinline__ float from_lane(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
+}
 
 struct GradRun {
   scan_grad_args g;
@@ -27,34 +33,6 @@ struct GradRun {
   float* params;  // [chunks][N][D S + 2 D]: drate, dskip, ddelta_bias
 };
 
-template <class T>
-struct GradColumns {
-  typename T::raw x[kUnit], d[kUnit], z[kUnit], dy[kUnit];
-  template <bool SUMMARY>
-  __device__ __forceinline__ void load(const scan_grad_args& g, const ScanWave& k, int32_t t0, bool gate) {
-    using raw = typename T::raw;
-    const scan_args& a = g.f;
-    const raw* px = static_cast<const raw*>(a.x) + k.n * a.x_row;
-    const raw* pd = static_cast<const raw*>(a.delta) + k.n * a.delta_row;
-    const raw* pz = static_cast<const raw*>(a.gate) + k.n * a.gate_row;
-    const raw* pg = static_cast<const raw*>(g.dy) + k.n * g.dy_row;
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i) {
-      const int32_t t = min(t0 + i, a.steps - 1);
-      if (!SUMMARY) x[i] = (px + t * a.x_step)[k.channel];
-      d[i] = (pd + t * a.delta_step)[k.channel];
-      dy[i] = (pg + t * g.dy_step)[k.channel];
-      if (gate) z[i] = (pz + t * a.gate_step)[k.channel];
-    }
-  }
-};
-
-__device__ __forceinline__ void quad_all(float v, float (&q)[4]) {
-  q[0] = quad_get<0>(v);
-  q[1] = quad_get<1>(v);
-  q[2] = quad_get<2>(v);
-  q[3] = quad_get<3>(v);
-}
 __device__ __forceinline__ void read4(const float* p, float (&v)[4]) {
   const float4 x = *reinterpret_cast<const float4*>(p);
   v[0] = x.x;
@@ -115,17 +93,19 @@ __device__ __forceinline__ float meet_pair(float first, float second, int lane) 
   return (up ? second : first) + __int_as_float(x);
 }
 
-template <class T, int NB, bool SUMMARY>
-__global__ void __launch_bounds__(64 * NB) scan_backward_kernel(const GradRun q) {
+template <class T, int NB, bool GATED, bool SUMMARY>
+__global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel(const GradRun q) {
   const scan_grad_args& g = q.g;
   const scan_args& a = g.f;
   ScanWave k(q.p, a.rows, a.groups, a.states);
   if (SUMMARY) ++k.chunk;  // (the first chunk's is read by none)
   __shared__ float s_bc[NB][kUnit][32];
-  __shared__ float s_part[NB > 1 && !SUMMARY ? 2 : 1][NB > 1 && !SUMMARY ? NB : 1][3][kUnit][64];
+  __shared__ float4 s_held[SUMMARY ? 1 : NB][kHeld][4][64];  // the states of a unit's first steps
+  __shared__ float s_slope[SUMMARY ? 1 : NB][kUnit][64];     // D's slopes
+  // the waves' shares of y, p1 and p2
+  __shared__ float s_sums[!SUMMARY && NB > 1 ? NB : 1][3][kUnit][64];
   const int32_t L = a.steps, S = a.states;
   const int32_t u0 = k.chunk * q.p.chunk_units, u1 = min(u0 + q.p.chunk_units, q.p.units);
-  const bool gated = a.gate != nullptr;
 
   float rate[4][4], G[4][4], drate[4][4];
   const bool ended = a.dones && a.dones[(int64_t)(L - 1) * a.rows + k.n] != 0;
@@ -157,17 +137,22 @@ __global__ void __launch_bounds__(64 * NB) scan_backward_kernel(const GradRun q)
   float total = 0.0f, dskip = 0.0f, dbias = 0.0f;
   uint32_t any_cut = 0;
 
+  const Column<T> cx(a, q.p, k, a.x, a.x_step, a.x_row), cd(a, q.p, k, a.delta, a.delta_step, a.delta_row),
+      cz(a, q.p, k, a.gate, a.gate_step, a.gate_row), cy(a, q.p, k, g.dy, g.dy_step, g.dy_row);
+  const Column<T> gx(a, q.p, k, g.dx, g.dx_step, g.dx_row), gd(a, q.p, k, g.ddelta, g.ddelta_step, g.ddelta_row),
+      gz(a, q.p, k, g.dgate, g.dgate_step, g.dgate_row);
+  const Kept states(a, q.p, k);
   UnitInputs<T> in;
-  GradColumns<T> col;
+  typename T::raw rx[kUnit], rd[kUnit], rz[kUnit], ry[kUnit];
   float kept[4][4];
   const auto fetch = [&](int32_t u) {
     in.load(a, k, u * kUnit);
-    col.template load<SUMMARY>(g, k, u * kUnit, gated);
+    cd.load(u * kUnit, rd);
+    cy.load(u * kUnit, ry);
+    if (GATED) cz.load(u * kUnit, rz);
     if constexpr (!SUMMARY) {
-      const int64_t at = ((int64_t)u * a.rows + k.n) * a.width;
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        load_states(a.kept + (at + k.quad_channel(q.p, r)) * S, k.s0, S, kept[r]);
+      cx.load(u * kUnit, rx);
+      states.load(u, kept);
     }
     return unit_cuts(a, k, u * kUnit);
   };
@@ -177,45 +162,41 @@ __global__ void __launch_bounds__(64 * NB) scan_backward_kernel(const GradRun q)
     wave_sync();
     in.put(s_bc[k.w], k.lane);
     wave_sync();
-    // dt: D; w: the gradient of v; sg: D's slope; f: dgate / v
-    float x[kUnit], dt[kUnit], w[kUnit], sg[kUnit], f[kUnit], h[4][4];
+    // dt: D; w: the gradient of v; f: dgate / v
+    float x[kUnit], dt[kUnit], w[kUnit], f[kUnit];
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) {
-      const bool past = t0 + i >= L;
-      const float v = T::widen(col.d[i]) + bias;
+      const float v = T::widen(rd[i]) + bias;
       float E;
-      dt[i] = a.softplus ? softplus_of(v, E) : v;
-      sg[i] = a.softplus ? sigmoid_from(v, E) : 1.0f;
-      w[i] = T::widen(col.dy[i]);
-      if (!SUMMARY) x[i] = T::widen(col.x[i]);
-      f[i] = 0.0f;
-      if (gated) {
-        const float z = T::widen(col.z[i]);
+      const float sp = softplus_of(v, E), sl = sigmoid_from(v, E);
+      dt[i] = a.softplus ? sp : v;
+      float slope = a.softplus ? sl : 1.0f;
+      w[i] = T::widen(ry[i]);
+      if (!SUMMARY) x[i] = T::widen(rx[i]);
+      if (GATED) {
+        const float z = T::widen(rz[i]);
         const float sz = sigmoid_of(z);
         f[i] = w[i] * sz * __builtin_fmaf(z, 1.0f - sz, 1.0f);
         w[i] *= z * sz;
       }
-      if (past) dt[i] = w[i] = 0.0f;  // the gradient of the state passes through
-      if (!k.mine) w[i] = 0.0f;       // (a copy of another channel)
-      if (SUMMARY) total += dt[i];
-    }
-    if constexpr (!SUMMARY) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int s = 0; s < 4; ++s) h[r][s] = kept[r][s];
+      // past the end, where w and x are 0, the gradient of the state passes through
+      if (t0 + i >= L) dt[i] = slope = 0.0f;
+      if (SUMMARY)
+        total += dt[i];
+      else
+        s_slope[k.w][i][k.lane] = slope;  // (read again by this lane alone)
     }
     const uint32_t cut = cuts;
     any_cut |= cut;
-    if (u > u0) cuts = fetch(u - 1);
+    if (SUMMARY) cuts = fetch(max(u - 1, u0));
 
     if constexpr (SUMMARY) {
 #pragma unroll
       for (int i = kUnit - 1; i >= 0; --i) {
         float c[4], dts[4], ws[4];
         read4(&s_bc[k.w][i][16 + 4 * k.j], c);
-        quad_all(dt[i], dts);
-        quad_all(w[i], ws);
+        quad_give(dt[i], dts);
+        quad_give(w[i], ws);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -233,8 +214,8 @@ __global__ void __launch_bounds__(64 * NB) scan_backward_kernel(const GradRun q)
       const auto advance = [&](float(&v)[4][4], int i) {
         float b[4], dts[4], dus[4];
         read4(&s_bc[k.w][i][4 * k.j], b);
-        quad_all(dt[i], dts);
-        quad_all(dt[i] * x[i], dus);
+        quad_give(dt[i], dts);
+        quad_give(dt[i] * x[i], dus);
         if ((cut >> i) & 1u) {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
@@ -250,137 +231,148 @@ __global__ void __launch_bounds__(64 * NB) scan_backward_kernel(const GradRun q)
       float y[kUnit], p1[kUnit], p2[kUnit];
       // A lane's own channel of a step, when the sums over its states are known.
       const auto finish = [&](int i) {
-        if (t0 + i >= L) return;
-        using raw = typename T::raw;
-        const int64_t t = t0 + i;
         const float dD = __builtin_fmaf(x[i], p1[i], p2[i] * kLn2);
-        const float dd = dD * sg[i];
-        if (k.mine) {
-          (static_cast<raw*>(g.dx) + t * g.dx_step + k.n * g.dx_row)[k.channel] =
-              T::narrow(__builtin_fmaf(dt[i], p1[i], skip * w[i]));
-          (static_cast<raw*>(g.ddelta) + t * g.ddelta_step + k.n * g.ddelta_row)[k.channel] = T::narrow(dd);
-          if (gated)
-            (static_cast<raw*>(g.dgate) + t * g.dgate_step + k.n * g.dgate_row)[k.channel] =
-                T::narrow(f[i] * __builtin_fmaf(skip, x[i], y[i]));
-          dskip = __builtin_fmaf(w[i], x[i], dskip);
-          dbias += dd;
-        }
+        const float dd = dD * s_slope[k.w][i][k.lane];
+        gx.store(t0 + i, __builtin_fmaf(dt[i], p1[i], skip * w[i]));
+        gd.store(t0 + i, dd);
+        if (GATED) gz.store(t0 + i, f[i] * __builtin_fmaf(skip, x[i], y[i]));
+        dskip = __builtin_fmaf(w[i], x[i], dskip);
+        dbias += dd;
       };
+      float v[4][4], held[kHeld][4][4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) v[r][s] = kept[r][s];
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (i < kHeld) {
+            s_held[k.w][i][r][k.lane] = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
+          } else {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) held[i < kHeld ? 0 : i - kHeld][r][s] = v[r][s];
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        advance(v, i);
+        if (GATED) {
+          float c[4], sums[4];
+          read4(&s_bc[k.w][i][16 + 4 * k.j], c);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            sums[r] = c[0] * v[r][0];
+#pragma unroll
+            for (int s = 1; s < 4; ++s) sums[r] = __builtin_fmaf(c[s], v[r][s], sums[r]);
+          }
+          y[i] = quad_sum(sums);
+          if (NB > 1) s_sums[NB > 1 ? k.w : 0][0][i][k.lane] = y[i];
+        }
+      }
       float odd = 0.0f;  // the second of a pair of steps
 #pragma unroll
-      for (int part = kUnit / kHeld - 1; part >= 0; --part) {
-        float v[4][4], held[kHeld][4][4];
+      for (int i = kUnit - 1; i >= 0; --i) {
+        // v: the state after step i; before: the one that a done may cut
+        __builtin_amdgcn_sched_barrier(0);
+        float before[4][4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r) {
+          if (i < kHeld) {
+            read4(reinterpret_cast<const float*>(&s_held[k.w][i][r][k.lane]), before[r]);
+          } else {
 #pragma unroll
-          for (int s = 0; s < 4; ++s) v[r][s] = h[r][s];
+            for (int s = 0; s < 4; ++s) before[r][s] = held[i < kHeld ? 0 : i - kHeld][r][s];
+          }
+        }
+        float b[4], c[4], dts[4], dus[4], ws[4], db[4], dc[4], s1[4], s2[4];
+        read4(&s_bc[k.w][i][4 * k.j], b);
+        read4(&s_bc[k.w][i][16 + 4 * k.j], c);
+        // (the empty statement keeps the compiler from holding the decays that
+        // formed the states, a hundred registers)
+        float again = dt[i];
+        asm("" : "+v"(again));
+        quad_give(again, dts);
+        quad_give(dt[i] * x[i], dus);
+        quad_give(w[i], ws);
 #pragma unroll
-        for (int i = 0; i < part * kHeld; ++i) advance(v, i);
+        for (int s = 0; s < 4; ++s) db[s] = dc[s] = 0.0f;
 #pragma unroll
-        for (int m = 0; m < kHeld; ++m) {
-          const int i = part * kHeld + m;
+        for (int r = 0; r < 4; ++r) {
+          s1[r] = s2[r] = 0.0f;
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            G[r][s] = __builtin_fmaf(c[s], ws[r], G[r][s]);
+            dc[s] = __builtin_fmaf(ws[r], v[r][s], dc[s]);
+            db[s] = __builtin_fmaf(G[r][s], dus[r], db[s]);
+            s1[r] = __builtin_fmaf(G[r][s], b[s], s1[r]);
+          }
+        }
+        if ((cut >> i) & 1u) {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) held[m][r][s] = v[r][s];
-          advance(v, i);
-          if (gated) {
-            float c[4], sums[4];
-            read4(&s_bc[k.w][i][16 + 4 * k.j], c);
+            for (int s = 0; s < 4; ++s) G[r][s] = 0.0f;
+        } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              sums[r] = c[0] * v[r][0];
-#pragma unroll
-              for (int s = 1; s < 4; ++s) sums[r] = __builtin_fmaf(c[s], v[r][s], sums[r]);
-            }
-            y[i] = quad_turn(sums, k.lane);
-          }
-        }
-#pragma unroll
-        for (int m = kHeld - 1; m >= 0; --m) {
-          const int i = part * kHeld + m;
-          float b[4], c[4], dts[4], dus[4], ws[4], db[4], dc[4], s1[4], s2[4];
-          read4(&s_bc[k.w][i][4 * k.j], b);
-          read4(&s_bc[k.w][i][16 + 4 * k.j], c);
-          quad_all(dt[i], dts);
-          quad_all(k.mine ? dt[i] * x[i] : 0.0f, dus);
-          quad_all(w[i], ws);
-#pragma unroll
-          for (int s = 0; s < 4; ++s) db[s] = dc[s] = 0.0f;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            s1[r] = s2[r] = 0.0f;
+          for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-              const float after = m == kHeld - 1 ? v[r][s] : held[m < kHeld - 1 ? m + 1 : m][r][s];
-              G[r][s] = __builtin_fmaf(c[s], ws[r], G[r][s]);
-              dc[s] = __builtin_fmaf(ws[r], after, dc[s]);
-              db[s] = __builtin_fmaf(G[r][s], dus[r], db[s]);
-              s1[r] = __builtin_fmaf(G[r][s], b[s], s1[r]);
+              G[r][s] *= __builtin_amdgcn_exp2f(dts[r] * rate[r][s]);
+              const float p = G[r][s] * before[r][s];
+              s2[r] = __builtin_fmaf(rate[r][s], p, s2[r]);
+              drate[r][s] = __builtin_fmaf(dts[r], p, drate[r][s]);
             }
-          }
-          if ((cut >> i) & 1u) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-              for (int s = 0; s < 4; ++s) G[r][s] = 0.0f;
-          } else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-              for (int s = 0; s < 4; ++s) {
-                G[r][s] *= __builtin_amdgcn_exp2f(dts[r] * rate[r][s]);
-                const float p = G[r][s] * held[m][r][s];
-                s2[r] = __builtin_fmaf(rate[r][s], p, s2[r]);
-                drate[r][s] = __builtin_fmaf(dts[r], p, drate[r][s]);
-              }
-          }
-          p1[i] = quad_turn(s1, k.lane);
-          p2[i] = quad_turn(s2, k.lane);
-          if constexpr (NB == 1) finish(i);
-          const float met = meet(db, dc, k.lane);
-          if (i & 1) {
-            odd = met;
-          } else {
-            const float sum = meet_pair(met, odd, k.lane);
-            const int32_t t = t0 + i + ((k.lane >> 2) & 1);
-            const int s = 4 * k.j + 2 * ((k.lane >> 4) & 1) + ((k.lane >> 3) & 1);
-            const bool is_c = k.lane & 32;
-            if (t < L) {
-              if (q.shared) {
-                const int64_t at = (((int64_t)k.block * L + t) * a.rows + k.n) * a.groups + k.g;
-                q.shared[(at * NB + k.w) * 32 + (is_c ? 16 : 0) + s] = sum;
-              } else if (k.w * kBlock + s < S) {
-                using raw = typename T::raw;
-                raw* p = is_c ? static_cast<raw*>(g.dc) + t * g.dc_step + k.n * g.dc_row + k.g * g.dc_group
-                              : static_cast<raw*>(g.db) + t * g.db_step + k.n * g.db_row + k.g * g.db_group;
-                p[k.w * kBlock + s] = T::narrow(sum);
-              }
-            }
+        }
+        p1[i] = quad_sum(s1);
+        p2[i] = quad_sum(s2);
+        if constexpr (NB == 1) {
+          finish(i);
+        } else {
+          s_sums[k.w][1][i][k.lane] = p1[i];
+          s_sums[k.w][2][i][k.lane] = p2[i];
+        }
+        const float met = meet(db, dc, k.lane);
+        if (i & 1) {
+          odd = met;
+        } else {
+          const float sum = meet_pair(met, odd, k.lane);
+          // (the even step's or the odd one's, of the four values of b or c)
+          const int32_t t = t0 + i + ((k.lane >> 2) & 1);
+          const int s = 4 * k.j + 2 * ((k.lane >> 4) & 1) + ((k.lane >> 3) & 1);
+          const bool is_c = k.lane & 32;
+          if (q.shared) {
+            const int64_t at = (((int64_t)k.block * L + t) * a.rows + k.n) * a.groups + k.g;
+            if (t < L) q.shared[(at * NB + k.w) * 32 + (is_c ? 16 : 0) + s] = sum;
+          } else if (t < L && k.w * kBlock + s < S) {
+            using raw = typename T::raw;
+            raw* p = is_c ? static_cast<raw*>(g.dc) + t * g.dc_step + k.n * g.dc_row + k.g * g.dc_group
+                          : static_cast<raw*>(g.db) + t * g.db_step + k.n * g.db_row + k.g * g.db_group;
+            p[k.w * kBlock + s] = T::narrow(sum);
           }
         }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) v[r][s] = before[r][s];
+        // (the registers of the held states are free from here on)
+        if (i == kHeld) cuts = fetch(max(u - 1, u0));
       }
       if constexpr (NB > 1) {
-        float(&buf)[NB][3][kUnit][64] = s_part[u & 1];
-#pragma unroll
-        for (int i = 0; i < kUnit; ++i) {
-          buf[k.w][0][i][k.lane] = gated ? y[i] : 0.0f;
-          buf[k.w][1][i][k.lane] = p1[i];
-          buf[k.w][2][i][k.lane] = p2[i];
-        }
-        __syncthreads();  // (a wave that is a unit ahead writes the other half)
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
           if (i % NB != k.w) continue;
           y[i] = p1[i] = p2[i] = 0.0f;
 #pragma unroll
-          for (int v = 0; v < NB; ++v) {
-            y[i] += buf[v][0][i][k.lane];
-            p1[i] += buf[v][1][i][k.lane];
-            p2[i] += buf[v][2][i][k.lane];
+          for (int o = 0; o < NB; ++o) {
+            if (GATED) y[i] += s_sums[o][0][i][k.lane];
+            p1[i] += s_sums[o][1][i][k.lane];
+            p2[i] += s_sums[o][2][i][k.lane];
           }
           finish(i);
         }
+        __syncthreads();
       }
     }
   }
@@ -404,15 +396,14 @@ __global__ void __launch_bounds__(64 * NB) scan_backward_kernel(const GradRun q)
         store_states(g.dstate + (row + k.quad_channel(q.p, r)) * S, k.s0, S, G[r]);
     }
     if constexpr (NB > 1) {
-      __syncthreads();
-      s_part[0][k.w][0][0][k.lane] = dskip;
-      s_part[0][k.w][1][0][k.lane] = dbias;
+      float4* part = &s_held[0][0][0][0];
+      part[k.w * 64 + k.lane] = make_float4(dskip, dbias, 0.0f, 0.0f);
       __syncthreads();
       dskip = dbias = 0.0f;
 #pragma unroll
-      for (int v = 0; v < NB; ++v) {
-        dskip += s_part[0][v][0][0][k.lane];
-        dbias += s_part[0][v][1][0][k.lane];
+      for (int o = 0; o < NB; ++o) {
+        dskip += part[o * 64 + k.lane].x;
+        dbias += part[o * 64 + k.lane].y;
       }
     }
     if (k.mine && k.w == 0) {
@@ -446,27 +437,29 @@ __global__ void __launch_bounds__(256) scan_shared_kernel(const GradRun q, int64
   }
 }
 
-template <class T, int NB>
+template <class T, int NB, bool GATED>
 void launch_backward(const GradRun& q, hipStream_t stream) {
+  const dim3 threads(64 * NB);
   if (q.p.chunks > 1)
-    scan_backward_kernel<T, NB, true>
-        <<<dim3((uint32_t)(q.p.columns * (q.p.chunks - 1))), dim3(64 * NB), 0, stream>>>(q);
-  scan_backward_kernel<T, NB, false>
-      <<<dim3((uint32_t)(q.p.columns * q.p.chunks)), dim3(64 * NB), 0, stream>>>(q);
+    scan_backward_kernel<T, NB, GATED, true>
+        <<<dim3((uint32_t)(q.p.columns * (q.p.chunks - 1))), threads, 0, stream>>>(q);
+  scan_backward_kernel<T, NB, GATED, false>
+      <<<dim3((uint32_t)(q.p.columns * q.p.chunks)), threads, 0, stream>>>(q);
   if (q.shared) {
     const int64_t total = (int64_t)q.g.f.steps * q.g.f.rows * q.g.f.groups * NB * 32;
     const int64_t groups = (total + 255) / 256;
     scan_shared_kernel<T><<<dim3((uint32_t)(groups < 16384 ? groups : 16384)), 256, 0, stream>>>(q, total);
   }
 }
+template <class T, int NB>
+void launch_gate(const GradRun& q, hipStream_t stream) {
+  q.g.f.gate ? launch_backward<T, NB, true>(q, stream) : launch_backward<T, NB, false>(q, stream);
+}
 template <class T>
 void launch_states(const GradRun& q, hipStream_t stream) {
-  switch (q.p.state_blocks) {
-    case 1: return launch_backward<T, 1>(q, stream);
-    case 2: return launch_backward<T, 2>(q, stream);
-    case 3: return launch_backward<T, 3>(q, stream);
-    default: return launch_backward<T, 4>(q, stream);
-  }
+  if (q.p.state_blocks == 1) return launch_gate<T, 1>(q, stream);
+  if (q.p.state_blocks == 2) return launch_gate<T, 2>(q, stream);
+  return launch_gate<T, 4>(q, stream);
 }
 
 int64_t up(int64_t bytes) { return (bytes + 255) / 256 * 256; }
