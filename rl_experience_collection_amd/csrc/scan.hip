@@ -153,12 +153,13 @@ __global__ void __launch_bounds__(64 * NB) scan_forward_kernel(const ScanRun q) 
           for (int v = 1; v < NB; ++v) y[i] += buf[v][i][k.lane];
         }
       }
+      char* out = cy.unit(t0);
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) {
         if (NB > 1 && i % NB != k.w) continue;
         float v = __builtin_fmaf(skip, x[i], y[i]);
         if (GATED) v *= z[i] * sigmoid_of(z[i]);
-        cy.store(t0 + i, v);
+        cy.store(out, i, t0 + i, v);
       }
     }
   }

@@ -216,13 +216,15 @@ struct Column {
         bytes((uint32_t)min(64, p.group_width - k.block * 64) * T::kBytes),
         at(k.lane * T::kBytes),
         steps(a.steps) {}
+  __device__ __forceinline__ char* unit(int32_t t0) const { return row + t0 * step; }
   __device__ __forceinline__ void load(int32_t t0, typename T::raw (&x)[kUnit]) const {
-    const char* p = row + t0 * step;
+    const char* p = unit(t0);
 #pragma unroll
     for (int i = 0; i < kUnit; ++i, p += step) x[i] = row_load<T>(p, t0 + i < steps ? bytes : 0, at);
   }
-  __device__ __forceinline__ void store(int32_t t, float x) const {
-    row_store<T>(row + t * step, t < steps ? bytes : 0, at, x);
+  // Step t = t0 + i of the unit at `p`.
+  __device__ __forceinline__ void store(char* p, int i, int32_t t, float x) const {
+    row_store<T>(p + i * step, t < steps ? bytes : 0, at, x);
   }
 };
 

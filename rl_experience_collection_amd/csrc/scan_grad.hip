@@ -27,9 +27,10 @@ __device__ __forceinline__ float from_lane(float x) {
 
 struct GradRun {
   scan_grad_args g;
+  int32_t pairs;  // of steps
   ScanPlan p;
   ScanSummary sum;
-  float* shared;  // [blocks][L][N][G][state blocks][32]: db and dc of the blocks, or NULL
+  float* shared;  // [blocks][pairs of steps][N][G][state blocks][2][32]: db and dc of the blocks, or NULL
   float* params;  // [chunks][N][D S + 2 D]: drate, dskip, ddelta_bias
 };
 
@@ -142,8 +143,18 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
   const Column<T> gx(a, q.p, k, g.dx, g.dx_step, g.dx_row), gd(a, q.p, k, g.ddelta, g.ddelta_step, g.ddelta_row),
       gz(a, q.p, k, g.dgate, g.dgate_step, g.dgate_row);
   const Kept states(a, q.p, k);
+  // Which of the sums over channels a lane ends with: of the even step of a
+  // pair or the odd one, of b or c, of a state; and where it goes.
+  const bool met_odd = k.lane & 4, met_c = k.lane & 32;
+  const int met_place = 4 * k.j + 2 * ((k.lane >> 4) & 1) + ((k.lane >> 3) & 1);
+  const int met_state = k.w * kBlock + met_place;
+  const uint32_t met_at = (met_odd * 32 + met_c * 16 + met_place) * 4;
+  using raw = typename T::raw;
+  const int64_t own_step = met_c ? g.dc_step : g.db_step;
+  raw* own = static_cast<raw*>(met_c ? g.dc : g.db) + k.n * (met_c ? g.dc_row : g.db_row) +
+             k.g * (met_c ? g.dc_group : g.db_group) + met_state + (int64_t)(u1 * kUnit - 2 + met_odd) * own_step;
   UnitInputs<T> in;
-  typename T::raw rx[kUnit], rd[kUnit], rz[kUnit], ry[kUnit];
+  raw rx[kUnit], rd[kUnit], rz[kUnit], ry[kUnit];
   float kept[4][4];
   const auto fetch = [&](int32_t u) {
     in.load(a, k, u * kUnit);
@@ -230,12 +241,13 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
       };
       float y[kUnit], p1[kUnit], p2[kUnit];
       // A lane's own channel of a step, when the sums over its states are known.
+      char *ox = gx.unit(t0), *od = gd.unit(t0), *oz = GATED ? gz.unit(t0) : nullptr;
       const auto finish = [&](int i) {
         const float dD = __builtin_fmaf(x[i], p1[i], p2[i] * kLn2);
         const float dd = dD * s_slope[k.w][i][k.lane];
-        gx.store(t0 + i, __builtin_fmaf(dt[i], p1[i], skip * w[i]));
-        gd.store(t0 + i, dd);
-        if (GATED) gz.store(t0 + i, f[i] * __builtin_fmaf(skip, x[i], y[i]));
+        gx.store(ox, i, t0 + i, __builtin_fmaf(dt[i], p1[i], skip * w[i]));
+        gd.store(od, i, t0 + i, dd);
+        if (GATED) gz.store(oz, i, t0 + i, f[i] * __builtin_fmaf(skip, x[i], y[i]));
         dskip = __builtin_fmaf(w[i], x[i], dskip);
         dbias += dd;
       };
@@ -337,18 +349,12 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
           odd = met;
         } else {
           const float sum = meet_pair(met, odd, k.lane);
-          // (the even step's or the odd one's, of the four values of b or c)
-          const int32_t t = t0 + i + ((k.lane >> 2) & 1);
-          const int s = 4 * k.j + 2 * ((k.lane >> 4) & 1) + ((k.lane >> 3) & 1);
-          const bool is_c = k.lane & 32;
           if (q.shared) {
-            const int64_t at = (((int64_t)k.block * L + t) * a.rows + k.n) * a.groups + k.g;
-            if (t < L) q.shared[(at * NB + k.w) * 32 + (is_c ? 16 : 0) + s] = sum;
-          } else if (t < L && k.w * kBlock + s < S) {
-            using raw = typename T::raw;
-            raw* p = is_c ? static_cast<raw*>(g.dc) + t * g.dc_step + k.n * g.dc_row + k.g * g.dc_group
-                          : static_cast<raw*>(g.db) + t * g.db_step + k.n * g.db_row + k.g * g.db_group;
-            p[k.w * kBlock + s] = T::narrow(sum);
+            const int64_t at = (((int64_t)k.block * q.pairs + ((t0 + i) >> 1)) * a.rows + k.n) * a.groups + k.g;
+            row_store<F32>(q.shared + (at * NB + k.w) * 64, t0 + i < L ? 256 : 0, met_at, sum);
+          } else {
+            if (t0 + i + ((k.lane >> 2) & 1) < L && met_state < S) *own = T::narrow(sum);
+            own -= 2 * own_step;
           }
         }
 #pragma unroll
@@ -413,27 +419,35 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
   }
 }
 
-// db and dc: the sums over a group's blocks, rounded.  A thread takes one
-// value of one kind.
+// db and dc: the sums over a group's blocks, rounded.  A thread takes two
+// neighbouring states of one kind and step.
 template <class T>
 __global__ void __launch_bounds__(256) scan_shared_kernel(const GradRun q, int64_t total) {
   const scan_grad_args& g = q.g;
   const scan_args& a = g.f;
-  const int32_t wide = q.p.state_blocks * 32;
+  const int32_t wide = q.p.state_blocks * 32;  // couples of states of a pair of steps
+  using raw = typename T::raw;
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
     const int32_t i = (int32_t)(e % wide);
-    const int64_t row = e / wide;  // (t, n, group)
-    const int32_t s = (i / 32) * kBlock + (i & 15);
-    if (s >= a.states) continue;
-    float sum = 0.0f;
-    for (int32_t b = 0; b < q.p.blocks; ++b) sum += q.shared[(int64_t)b * total + e];
-    const int32_t grp = (int32_t)(row % a.groups);
-    const int64_t tn = row / a.groups;
-    const int64_t n = tn % a.rows, t = tn / a.rows;
-    using raw = typename T::raw;
-    raw* p = i & 16 ? static_cast<raw*>(g.dc) + t * g.dc_step + n * g.dc_row + grp * g.dc_group
-                    : static_cast<raw*>(g.db) + t * g.db_step + n * g.db_row + grp * g.db_group;
-    p[s] = T::narrow(sum);
+    const int64_t row = e / wide;  // (pair of steps, n, group)
+    float s0 = 0.0f, s1 = 0.0f;
+    for (int32_t b = 0; b < q.p.blocks; ++b) {
+      const float2 v = reinterpret_cast<const float2*>(q.shared)[b * total + e];
+      s0 += v.x;
+      s1 += v.y;
+    }
+    const int32_t s = (i / 32) * kBlock + 2 * (i & 7), grp = (int32_t)(row % a.groups);
+    const int64_t pn = row / a.groups;
+    const int64_t n = pn % a.rows, t = 2 * (pn / a.rows) + ((i >> 4) & 1);
+    if (t >= a.steps) continue;
+    raw* p = i & 8 ? static_cast<raw*>(g.dc) + t * g.dc_step + n * g.dc_row + grp * g.dc_group
+                   : static_cast<raw*>(g.db) + t * g.db_step + n * g.db_row + grp * g.db_group;
+    if (s + 1 < a.states) {
+      const float v[2] = {s0, s1};
+      store_pack<T, 2>(p + s, narrow_pack<T, 2>(v));
+    } else if (s < a.states) {
+      p[s] = T::narrow(s0);
+    }
   }
 }
 
@@ -446,7 +460,7 @@ void launch_backward(const GradRun& q, hipStream_t stream) {
   scan_backward_kernel<T, NB, GATED, false>
       <<<dim3((uint32_t)(q.p.columns * q.p.chunks)), threads, 0, stream>>>(q);
   if (q.shared) {
-    const int64_t total = (int64_t)q.g.f.steps * q.g.f.rows * q.g.f.groups * NB * 32;
+    const int64_t total = (int64_t)q.pairs * q.g.f.rows * q.g.f.groups * NB * 32;
     const int64_t groups = (total + 255) / 256;
     scan_shared_kernel<T><<<dim3((uint32_t)(groups < 16384 ? groups : 16384)), 256, 0, stream>>>(q, total);
   }
@@ -473,7 +487,7 @@ Parts parts_of(const ScanPlan& p, int32_t L, int32_t N, int32_t D, int32_t S, in
   const int64_t rows = (int64_t)p.chunks * N;
   Parts b;
   b.summary = scan_summary_bytes(p, N, D, S);
-  b.shared = p.blocks > 1 ? up((int64_t)p.blocks * L * N * G * p.state_blocks * 32 * 4) : 0;
+  b.shared = p.blocks > 1 ? up((int64_t)p.blocks * ((L + 1) / 2) * N * G * p.state_blocks * 64 * 4) : 0;
   b.params = up(rows * D * (S + 2) * 4);
   b.scratch = up(sums_floats(rows, D * (S + 2)) * 4);
   return b;
@@ -501,6 +515,7 @@ hipError_t scan_backward_launch(const scan_grad_args& g, hipStream_t stream) {
   GradRun q;
   q.g = g;
   q.p = scan_plan(a.steps, a.rows, a.width, a.states, a.groups, true);
+  q.pairs = (a.steps + 1) / 2;
   const Parts b = parts_of(q.p, a.steps, a.rows, a.width, a.states, a.groups);
   char* w = static_cast<char*>(a.workspace);
   q.sum = scan_summary(q.p, a.rows, a.width, a.states, w);
