@@ -1,8 +1,8 @@
 // The norms after and before a block, with its gate, dropout, scales and
 // residual between them, and their gradient (include/block.h).
 //
-// A row lies in the registers of a group of threads (8 to 512, 8 or 16
-// elements each), so that it is read once for both norms; the next row's loads
+// A row lies in the registers of a group of threads (8 to 1024, 8 elements
+// each), so that it is read once for both norms; the next row's loads
 // are in flight meanwhile.  Sums over a row meet by lane exchanges, beyond a
 // wave in LDS.  The gradient forms the row again from the forward call's
 // inputs and the two stored factors (8 bytes a row), rather than from a
@@ -53,26 +53,35 @@ __device__ __forceinline__ float lanes_sum(float x) {
   return x;
 }
 
+// TPR up to 64: that many threads a row, 256 a workgroup.  Above: a workgroup a
+// row, of as many waves as the row needs, at most TPR threads.
 constexpr int threads_of(int TPR) { return TPR > 256 ? TPR : 256; }
+template <int TPR>
+__device__ __forceinline__ uint32_t row_threads() {
+  return TPR <= 64 ? TPR : blockDim.x;
+}
+template <int TPR>
+__device__ __forceinline__ uint32_t row_thread() {
+  return TPR <= 64 ? threadIdx.x % TPR : threadIdx.x;
+}
 
-// Sums over the TPR threads of a row.  The two halves of the LDS array are
-// used in turn: a wave that writes one again has passed the barrier of the
-// other, which no wave reaches before it has read the first.
+// Sums over the threads of a row.  The two halves of the LDS array are used in
+// turn: a wave that writes one again has passed the barrier of the other, which
+// no wave reaches before it has read the first.
 template <int TPR>
 struct RowSum {
   int turn = 0;
-  __device__ __forceinline__ float operator()(float x, float (&s)[2][8]) {
+  __device__ __forceinline__ float operator()(float x, float (&s)[2][16]) {
     if constexpr (TPR <= 64) {
       return lanes_sum<TPR>(x);
     } else {
       x = lanes_sum<64>(x);
       if ((threadIdx.x & 63) == 0) s[turn][threadIdx.x >> 6] = x;
       __syncthreads();
-      float sum = s[turn][0];
-#pragma unroll
-      for (int i = 1; i < TPR / 64; ++i) sum += s[turn][i];
+      const uint32_t wave = threadIdx.x & 15;
+      x = lanes_sum<16>(wave < blockDim.x / 64 ? s[turn][wave] : 0.0f);
       turn ^= 1;
-      return sum;
+      return x;
     }
   }
 };
@@ -83,15 +92,18 @@ struct RowSum {
 template <class T, int V, int TPR, int K>
 struct Share {
   int32_t at[K], fresh[K];
-  bool has[K];
+  bool has[K], whole;
   __device__ __forceinline__ explicit Share(int32_t D) {
+    whole = true;
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-      const int32_t e = ((int32_t)(threadIdx.x % TPR) + TPR * i) * V;
+      const int32_t e = ((int32_t)row_thread<TPR>() + row_threads<TPR>() * i) * V;
       at[i] = min(e, D - V);
       fresh[i] = e - at[i];
       has[i] = e < D;
+      whole = whole && fresh[i] == 0;
     }
+    whole = __ballot(!whole) == 0;
   }
   using Row = Pack<T, V>[K];
   __device__ __forceinline__ void load(const void* p, int64_t row, int64_t r, Row& x) const {
@@ -111,13 +123,21 @@ struct Share {
 #pragma unroll
       for (int v = 0; v < V; ++v) f[i][v] = w ? w[at[i] + v] : 1.0f;
   }
-  // The sum of the products, each element once.
+  // The sum of the products, each element once.  (Only waves that have a row's
+  // last pack have anything to leave out.)
   __device__ __forceinline__ float dot(const float (&a)[K][V], const float (&b)[K][V]) const {
     float sum = 0.0f;
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < K; ++i)
+      for (int i = 0; i < K; ++i)
 #pragma unroll
-      for (int v = 0; v < V; ++v) sum = v >= fresh[i] ? __builtin_fmaf(a[i][v], b[i][v], sum) : sum;
+        for (int v = 0; v < V; ++v) sum = __builtin_fmaf(a[i][v], b[i][v], sum);
+    } else {
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) sum = v >= fresh[i] ? __builtin_fmaf(a[i][v], b[i][v], sum) : sum;
+    }
     return sum;
   }
 };
@@ -158,8 +178,8 @@ __device__ __forceinline__ void activate(int32_t kind, float g, float& act, floa
 template <class T, int V, int TPR, int K, int GATE>
 __global__ void __launch_bounds__(threads_of(TPR)) norm_forward_kernel(const NormRun q) {
   const norm_args& a = q.g.f;
-  constexpr int kRows = threads_of(TPR) / TPR;
-  __shared__ float s_sum[2][8];
+  constexpr int kRows = TPR <= 64 ? 256 / TPR : 1;
+  __shared__ float s_sum[2][16];
   const Share<T, V, TPR, K> own(a.width);
   RowSum<TPR> row_sum;
   const bool branch = a.branch != nullptr, drops = q.rule.drop != 0;
@@ -179,7 +199,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_forward_kernel(const Nor
   }
   typename Share<T, V, TPR, K>::Row res, br, ga;
   const int64_t step = (int64_t)gridDim.x * kRows;
-  int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+  int64_t r = (int64_t)blockIdx.x * kRows + (TPR <= 64 ? threadIdx.x / TPR : 0);
   const auto fetch = [&](int64_t at) {
     at = at < a.rows ? at : a.rows - 1;
     own.load(a.residual, a.residual_row, at, res);
@@ -229,7 +249,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_forward_kernel(const Nor
           for (int v = 0; v < V; ++v) s[i][v] *= inv * w[i][v];
         own.store(q.normed, q.normed_row, r, s, q.past);
       }
-      if (q.stats && threadIdx.x % TPR == 0) {
+      if (q.stats && row_thread<TPR>() == 0) {
         q.stats[2 * r] = inv_b;
         q.stats[2 * r + 1] = inv;
       }
@@ -237,32 +257,78 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_forward_kernel(const Nor
   }
 }
 
+// What a thread needs of its own columns at every row, in LDS: the registers
+// that it would take are worth more to the rows in flight (1,024,000 x 128
+// bf16 takes LDS_US us so, REG_US with weights in registers).
+template <int K, int V, int THREADS>
+struct OwnColumns {
+  static constexpr int kQuads = K * V / 4;
+  float4 v[kQuads > 0 ? kQuads : 1][THREADS];
+  __device__ __forceinline__ void put(const float (&f)[K][V]) {
+    if constexpr (V == 1) {
+      v[0][threadIdx.x].x = f[0][0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q)
+          v[i * (V / 4) + q][threadIdx.x] = make_float4(f[i][4 * q], f[i][4 * q + 1], f[i][4 * q + 2], f[i][4 * q + 3]);
+    }
+  }
+  __device__ __forceinline__ void get(int i, float (&f)[V]) const {
+    if constexpr (V == 1) {
+      f[0] = v[0][threadIdx.x].x;
+    } else {
+#pragma unroll
+      for (int q = 0; q < V / 4; ++q) {
+        const float4 x = v[i * (V / 4) + q][threadIdx.x];
+        f[4 * q] = x.x;
+        f[4 * q + 1] = x.y;
+        f[4 * q + 2] = x.z;
+        f[4 * q + 3] = x.w;
+      }
+    }
+  }
+};
+
 template <class T, int V, int TPR, int K, int GATE>
 __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const NormRun q) {
   const norm_grad_args& p = q.g;
   const norm_args& a = p.f;
-  constexpr int kThreads = threads_of(TPR), kRows = kThreads / TPR;
-  __shared__ float s_sum[2][8];
+  constexpr int kThreads = threads_of(TPR), kRows = TPR <= 64 ? 256 / TPR : 1;
+  __shared__ float s_sum[2][16];
+  __shared__ OwnColumns<K, V, kThreads> s_w, s_bw;
+  __shared__ OwnColumns<GATE == kChannelGate ? K : 1, GATE == kChannelGate ? V : 1, GATE == kChannelGate ? kThreads : 1> s_act;
   const Share<T, V, TPR, K> own(a.width);
   RowSum<TPR> row_sum;
   const bool branch = a.branch != nullptr, drops = q.rule.drop != 0;
   const uint64_t seed = q.rule.seed_at ? *q.rule.seed_at : q.rule.seed;
-  float w[K][V], bw[K][V], gc[K][V], gs[K][V];
   float dw[K][V], dbw[K][V], dgc[K][V];
-  own.weights(a.weight, w);
-  own.weights(a.branch_weight, bw);
-  if (GATE == kChannelGate) own.weights(static_cast<const float*>(a.gate), gc);
+  own.weights(a.weight, dw);
+  s_w.put(dw);
+  own.weights(a.branch_weight, dw);
+  s_bw.put(dw);
+  if constexpr (GATE == kChannelGate) {
+    own.weights(static_cast<const float*>(a.gate), dw);
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float slope;
+        activate(a.activation, dw[i][v], dw[i][v], slope);
+      }
+    s_act.put(dw);
+  }
 #pragma unroll
   for (int i = 0; i < K; ++i)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      dw[i][v] = dbw[i][v] = dgc[i][v] = 0.0f;
-      if (GATE == kChannelGate) activate(a.activation, gc[i][v], gc[i][v], gs[i][v]);
-    }
+    for (int v = 0; v < V; ++v) dw[i][v] = dbw[i][v] = dgc[i][v] = 0.0f;
   typename Share<T, V, TPR, K>::Row res, br, ga, ds, dn;
+#pragma unroll
+  for (int i = 0; i < K; ++i) ds[i] = dn[i] = Pack<T, V>{};  // those that are not given
   float inv_b_next = 1.0f, inv_next = 1.0f;
   const int64_t step = (int64_t)gridDim.x * kRows;
-  int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+  int64_t r = (int64_t)blockIdx.x * kRows + (TPR <= 64 ? threadIdx.x / TPR : 0);
   const auto fetch = [&](int64_t at) {
     at = at < a.rows ? at : a.rows - 1;
     own.load(a.residual, a.residual_row, at, res);
@@ -277,26 +343,29 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const No
   for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.rows; first += step, r += step) {
     const bool mine = r < a.rows;
     const float inv_b = inv_b_next, inv = inv_next;
-    // s: the stream; u: the normed branch; act, slope: of the gate; d: dstream
-    float s[K][V], u[K][V], act[K][V], slope[K][V], d[K][V], e[K][V];
+    // s: the normed stream; u: the normed branch; g: the gate; d: dstream; e: dnormed weight
+    float s[K][V], u[K][V], g[K][V], d[K][V], e[K][V];
     uint32_t kept[K];
+    if (kRows > 1 && !mine) {
+      // (a row past the end repeats the last one: its gradients count 0)
+#pragma unroll
+      for (int i = 0; i < K; ++i) ds[i] = dn[i] = Pack<T, V>{};
+    }
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       widen_pack<T, V>(res[i], s[i]);
+      widen_pack<T, V>(ds[i], d[i]);
+      widen_pack<T, V>(dn[i], e[i]);
       if (branch) widen_pack<T, V>(br[i], u[i]);
-      if (GATE == kRowGate) widen_pack<T, V>(ga[i], act[i]);
-      if (p.dstream) widen_pack<T, V>(ds[i], d[i]);
-      if (p.dnormed) widen_pack<T, V>(dn[i], e[i]);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        // (rows past the end repeat the last one: their gradients count 0)
-        if (!p.dstream || !mine) d[i][v] = 0.0f;
-        if (!p.dnormed || !mine) e[i][v] = 0.0f;
-      }
+      if (GATE == kRowGate) widen_pack<T, V>(ga[i], g[i]);
     }
-    if (first + step < a.rows) fetch(r + step);
+    fetch(first + step < a.rows ? r + step : r);
 #pragma unroll
     for (int i = 0; i < K; ++i) {
+      float w[V], bw[V], act[V];
+      s_w.get(i, w);
+      s_bw.get(i, bw);
+      if constexpr (GATE == kChannelGate) s_act.get(i, act);
       kept[i] = ~0u;
       if (branch && drops) kept[i] = kept_bits<V>(q.rule, seed, (uint64_t)(r * a.width + own.at[i]));
 #pragma unroll
@@ -304,22 +373,20 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const No
         s[i][v] *= a.residual_scale;
         if (branch) {
           u[i][v] *= inv_b;
-          float z = u[i][v] * bw[i][v];
-          if (GATE == kRowGate) {
-            activate(a.activation, act[i][v], act[i][v], slope[i][v]);
-            z *= act[i][v];
-          }
-          if (GATE == kChannelGate) z *= gc[i][v];
+          float z = u[i][v] * bw[v], slope;
+          if (GATE == kRowGate) activate(a.activation, g[i][v], act[v], slope);
+          if (GATE != kNoGate) z *= act[v];
           if (drops) z = (kept[i] >> v) & 1u ? z * q.rule.scale : 0.0f;
           s[i][v] = __builtin_fmaf(a.branch_scale, z, s[i][v]);
         }
         s[i][v] *= inv;
         dw[i][v] = __builtin_fmaf(e[i][v], s[i][v], dw[i][v]);
-        e[i][v] *= w[i][v];
+        e[i][v] *= w[v];
       }
     }
+    float mean = 0.0f;
     if (p.dnormed) {
-      const float mean = row_sum(own.dot(e, s), s_sum) * q.inv_width;
+      mean = row_sum(own.dot(e, s), s_sum) * q.inv_width;
 #pragma unroll
       for (int i = 0; i < K; ++i)
 #pragma unroll
@@ -333,27 +400,52 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const No
       own.store(p.dresidual, a.width, r, s, q.past);
     }
     if (!branch) continue;
+    // (the empty statements keep the compiler from holding across the sum what
+    // LDS or two transcendental operations give again)
+    asm volatile("" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < K; ++i)
+    for (int i = 0; i < K; ++i) {
+      float bw[V], act[V];
+      s_bw.get(i, bw);
+      if constexpr (GATE == kChannelGate) s_act.get(i, act);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float dz = a.branch_scale * d[i][v];
+        float dz = a.branch_scale * d[i][v], slope;
         if (drops) dz = (kept[i] >> v) & 1u ? dz * q.rule.scale : 0.0f;
-        if (GATE == kRowGate) s[i][v] = dz * (u[i][v] * bw[i][v]) * slope[i][v];
-        if (GATE == kChannelGate) dgc[i][v] = __builtin_fmaf(dz * (u[i][v] * bw[i][v]), gs[i][v], dgc[i][v]);
-        const float du = GATE == kRowGate ? dz * act[i][v] : GATE == kChannelGate ? dz * gc[i][v] : dz;
+        const float dact = dz * (u[i][v] * bw[v]);
+        if (GATE == kRowGate) {
+          asm("" : "+v"(g[i][v]));
+          activate(a.activation, g[i][v], act[v], slope);
+          g[i][v] = dact * slope;
+        }
+        if (GATE == kChannelGate) dgc[i][v] += dact;
+        const float du = GATE == kNoGate ? dz : dz * act[v];
         dbw[i][v] = __builtin_fmaf(du, u[i][v], dbw[i][v]);
-        e[i][v] = du * bw[i][v];
+        e[i][v] = du * bw[v];
       }
-    if (GATE == kRowGate && p.dgate && mine) own.store(p.dgate, a.width, r, s, q.past);
+    }
+    if (GATE == kRowGate && p.dgate && mine) own.store(p.dgate, a.width, r, g, q.past);
     if (a.branch_norm) {
-      const float mean = row_sum(own.dot(e, u), s_sum) * q.inv_width;
+      mean = row_sum(own.dot(e, u), s_sum) * q.inv_width;
 #pragma unroll
       for (int i = 0; i < K; ++i)
 #pragma unroll
         for (int v = 0; v < V; ++v) e[i][v] = inv_b * __builtin_fmaf(-u[i][v], mean, e[i][v]);
     }
     if (p.dbranch && mine) own.store(p.dbranch, a.width, r, e, q.past);
+  }
+  if constexpr (GATE == kChannelGate) {
+    // the activation's slope is the same for every row
+    float gate[K][V];
+    own.weights(static_cast<const float*>(a.gate), gate);
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float act, slope;
+        activate(a.activation, gate[i][v], act, slope);
+        dgc[i][v] *= slope;
+      }
   }
   // the workgroup's sums over its rows, pack by pack
   __shared__ float s_part[kRows > 1 ? kThreads : 1][V];
@@ -385,46 +477,41 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const No
   if (GATE == kChannelGate) put(2, dgc);
 }
 
-// Threads of a row and elements of a thread: the fewest that hold the row.
-struct Shape {
-  int32_t threads, elements;
-};
-Shape shape_of(int32_t D) {
-  return D <= 64     ? Shape{8, 8}
-         : D <= 128  ? Shape{16, 8}
-         : D <= 512  ? Shape{64, 8}
-         : D <= 2048 ? Shape{256, 8}
-         : D <= 4096 ? Shape{512, 8}
-                     : Shape{512, 16};
+// Threads of a row, of 8 elements each: up to 64 the powers of two that hold
+// it, then as many waves as it needs.
+int32_t threads_for(int32_t D) {
+  return D <= 64 ? 8 : D <= 128 ? 16 : D <= 512 ? 64 : (D + 511) / 512 * 64;
 }
-// Workgroups: each takes many rows, so that weights are read and their
-// gradients written once for all of them.
-constexpr int64_t kForwardGroups = 256 * 8, kBackwardGroups = 256 * 4;
+// Workgroups: what is resident on 256 compute units (20 waves each going
+// forward, 12 backward), so that a workgroup reads its weights and writes
+// their gradients once for many rows.
 uint32_t groups_of(int64_t R, int32_t D, bool grad) {
-  const int32_t rows = std::max(1, 256 / shape_of(D).threads);
-  const int64_t most = grad ? kBackwardGroups : kForwardGroups;
+  const int32_t threads = threads_for(D), rows = threads <= 64 ? 256 / threads : 1;
+  const int64_t most = 256 * std::max(1, (grad ? 12 : 20) * 64 / (threads <= 64 ? 256 : threads));
   return (uint32_t)std::min((R + rows - 1) / rows, most);
 }
 
 template <class T, int V, int TPR, int K, int GATE, bool GRAD>
 void launch(const NormRun& q, hipStream_t stream) {
-  const dim3 grid(groups_of(q.g.f.rows, q.g.f.width, GRAD)), threads(threads_of(TPR));
+  const int32_t D = q.g.f.width;
+  const dim3 grid(groups_of(q.g.f.rows, D, GRAD)), threads(TPR <= 64 ? 256 : threads_for(D));
   if constexpr (GRAD)
     norm_backward_kernel<T, V, TPR, K, GATE><<<grid, threads, 0, stream>>>(q);
   else
     norm_forward_kernel<T, V, TPR, K, GATE><<<grid, threads, 0, stream>>>(q);
 }
+// (768 threads may hold 168 registers each, 1024 hold 128.)
 template <class T, int GATE, bool GRAD>
 void launch_shape(const NormRun& q, hipStream_t stream) {
   constexpr int V = 16 / T::kBytes, K = 8 / V;
-  const Shape s = shape_of(q.g.f.width);
+  const int32_t threads = threads_for(q.g.f.width);
   if (q.g.f.width < V) return launch<T, 1, 8, 1, GATE, GRAD>(q, stream);
-  if (s.threads == 8) return launch<T, V, 8, K, GATE, GRAD>(q, stream);
-  if (s.threads == 16) return launch<T, V, 16, K, GATE, GRAD>(q, stream);
-  if (s.threads == 64) return launch<T, V, 64, K, GATE, GRAD>(q, stream);
-  if (s.threads == 256) return launch<T, V, 256, K, GATE, GRAD>(q, stream);
-  if (s.elements == 8) return launch<T, V, 512, K, GATE, GRAD>(q, stream);
-  return launch<T, V, 512, 2 * K, GATE, GRAD>(q, stream);
+  if (threads == 8) return launch<T, V, 8, K, GATE, GRAD>(q, stream);
+  if (threads == 16) return launch<T, V, 16, K, GATE, GRAD>(q, stream);
+  if (threads == 64) return launch<T, V, 64, K, GATE, GRAD>(q, stream);
+  if (threads <= 256) return launch<T, V, 256, K, GATE, GRAD>(q, stream);
+  if (threads <= 768) return launch<T, V, 768, K, GATE, GRAD>(q, stream);
+  return launch<T, V, 1024, K, GATE, GRAD>(q, stream);
 }
 template <class T, bool GRAD>
 void launch_gate(const NormRun& q, hipStream_t stream) {
