@@ -1,11 +1,12 @@
 // Short causal convolution over a rollout: forward, gradient, single step
 // (include/block.h).
 //
-// A thread takes 16 bytes of an episode's channels and a chunk of steps. It
-// keeps the last W - 1 inputs in registers, so that an input is read once, and
-// reads those before its chunk again; four steps' loads are in flight while
-// the four before are worked on.  A done clears the window, which is all that
-// keeps episodes apart.
+// A thread takes some of an episode's channels and a chunk of steps. It keeps
+// the last W - 1 inputs in registers, so that an input is read once, and reads
+// those before its chunk again.  Steps go in groups of W (or 4), the next
+// group's loads in flight while one is worked on; within a group the window is
+// a ring whose places are known when the kernel is compiled, so that nothing
+// moves.  A done clears the window, which is all that keeps episodes apart.
 //
 // The gradient runs in the same direction: step t adds to the gradients of the
 // inputs t - W + 1 .. t, which wait in W registers until no later step adds
@@ -22,7 +23,8 @@ namespace rl {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;  // steps loaded at a time
+// Steps of a group: a multiple of the W places of a ring.
+constexpr int group_of(int W) { return W <= 2 ? 4 : W; }
 
 struct ConvRun {
   conv_grad_args g;  // forward: g.f alone
@@ -63,7 +65,8 @@ __device__ __forceinline__ bool cut_before(const conv_args& a, int32_t n, int32_
   return a.dones && t > 0 && t <= a.steps && a.dones[(int64_t)(t - 1) * a.rows + n] != 0;
 }
 
-// The inputs before step t0 (age 1 first) and how many belong to its episode.
+// The inputs before step t0, age j at place W - j, and how many belong to its
+// episode.
 template <class T, int V, int W>
 __device__ __forceinline__ int32_t open_window(const conv_args& a, const ConvLane& k,
                                                float (&win)[W][V]) {
@@ -75,16 +78,16 @@ __device__ __forceinline__ int32_t open_window(const conv_args& a, const ConvLan
     const int32_t t = k.t0 - i;
     same = same && !cut_before(a, k.n, t + 1);
 #pragma unroll
-    for (int v = 0; v < V; ++v) win[i][v] = 0.0f;
+    for (int v = 0; v < V; ++v) win[W - i][v] = 0.0f;
     if (!same) continue;
     age = i;
     if (t >= 0)
       widen_pack<T, V>(
-          load_pack<T, V>(static_cast<const raw*>(a.x) + t * a.x_step + k.n * a.x_row + k.d0), win[i]);
+          load_pack<T, V>(static_cast<const raw*>(a.x) + t * a.x_step + k.n * a.x_row + k.d0), win[W - i]);
     else if (a.state)
       widen_pack<T, V>(load_pack<T, V>(static_cast<const raw*>(a.state) +
                                        ((int64_t)k.n * (W - 1) + (W - 1 + t)) * a.width + k.d0),
-                       win[i]);
+                       win[W - i]);
   }
   return age;
 }
@@ -100,75 +103,128 @@ __device__ __forceinline__ void load_weights(const conv_args& a, int32_t d0, flo
   }
 }
 
+// A row of one of the arrays as a thread walks along it.
+template <class T, int V>
+struct Walk {
+  char* p;
+  int64_t step;
+  __device__ __forceinline__ Walk(const void* base, int64_t step_, int64_t row, const ConvLane& k, int32_t t)
+      : p(const_cast<char*>(static_cast<const char*>(base)) + (t * step_ + k.n * row + k.d0) * T::kBytes),
+        step(step_ * T::kBytes) {}
+  // The next A of the `left` steps that remain (1 at least); those past the
+  // end repeat the last one.
+  template <int A>
+  __device__ __forceinline__ void load(int32_t left, Pack<T, V> (&x)[A]) {
+    if (left >= A) {
+#pragma unroll
+      for (int i = 0; i < A; ++i, p += step) x[i] = load_pack<T, V>(reinterpret_cast<const typename T::raw*>(p));
+    } else {
+#pragma unroll
+      for (int i = 0; i < A; ++i) {
+        x[i] = load_pack<T, V>(reinterpret_cast<const typename T::raw*>(p));
+        if (i + 1 < left) p += step;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(const float (&f)[V]) {
+    store_pack<T, V>(reinterpret_cast<typename T::raw*>(p), narrow_pack<T, V>(f));
+    p += step;
+  }
+};
+
+// Bit i: a done lies before step t + i (i < n).
+template <int A>
+__device__ __forceinline__ uint32_t group_cuts(const conv_args& a, int32_t n, int32_t t) {
+  uint32_t cuts = 0;
+  if (a.dones) {
+#pragma unroll
+    for (int i = 0; i < A; ++i) {
+      const int32_t at = min(t + i, a.steps - 1);
+      cuts |= (uint32_t)(at > 0 && a.dones[(int64_t)max(at - 1, 0) * a.rows + n] != 0) << i;
+    }
+  }
+  return cuts;
+}
+
+// Clears the window but for the step at place `now`.
+template <int V, int W>
+__device__ __forceinline__ void forget(float (&win)[W][V], int now) {
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    if (j == now) continue;
+#pragma unroll
+    for (int v = 0; v < V; ++v) win[j][v] = 0.0f;
+  }
+}
+// The input of age j (the steps since it) of group step i lies at this place.
+template <int W>
+constexpr int place(int i, int j) {
+  return ((i - j) % W + W) % W;
+}
+
 template <class T, int V, int W>
 __global__ void __launch_bounds__(kThreads) conv_forward_kernel(const ConvRun q) {
   using raw = typename T::raw;
+  constexpr int A = group_of(W);
   const conv_args& a = q.g.f;
   const ConvLane k(q, V);
   if (!k.active) return;
   float w[W][V], bias[V], win[W][V];
   load_weights<V, W>(a, k.d0, w, bias);
   open_window<T, V, W>(a, k, win);
-  const raw* px = static_cast<const raw*>(a.x) + k.n * a.x_row + k.d0;
-  raw* py = static_cast<raw*>(a.y) + k.n * a.y_row + k.d0;
+  Walk<T, V> x(a.x, a.x_step, a.x_row, k, k.t0), y(a.y, a.y_step, a.y_row, k, k.t0);
   const bool silu = a.activation == BLOCK_SILU;
-  const int32_t last = k.t1 - 1;
 
-  Pack<T, V> next[kAhead];
-  bool next_cut[kAhead];
-  const auto fetch = [&](int32_t t) {
+  Pack<T, V> next[A];
+  x.load(k.t1 - k.t0, next);
+  uint32_t next_cuts = group_cuts<A>(a, k.n, k.t0);
+  int32_t t = k.t0;
+  const auto group = [&](auto whole) {
+    Pack<T, V> now[A];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      next[i] = load_pack<T, V>(px + min(t + i, last) * a.x_step);
-      next_cut[i] = cut_before(a, k.n, min(t + i, last));
+    for (int i = 0; i < A; ++i) now[i] = next[i];
+    const uint32_t cuts = next_cuts;
+    if (t + A < k.t1) {
+      x.load(k.t1 - t - A, next);
+      next_cuts = group_cuts<A>(a, k.n, t + A);
     }
-  };
-  fetch(k.t0);
-  for (int32_t t = k.t0; t < k.t1; t += kAhead) {
-    Pack<T, V> x[kAhead];
-    bool cut[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      x[i] = next[i];
-      cut[i] = next_cut[i];
-    }
-    fetch(t + kAhead);
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (t + i >= k.t1) break;
-      if (cut[i]) {
-#pragma unroll
-        for (int j = 1; j < W; ++j)
-#pragma unroll
-          for (int v = 0; v < V; ++v) win[j][v] = 0.0f;
-      }
-      widen_pack<T, V>(x[i], win[0]);
-      float y[V];
+    for (int i = 0; i < A; ++i) {
+      if (!decltype(whole)::value && t + i >= k.t1) continue;
+      if ((cuts >> i) & 1u) forget<V, W>(win, place<W>(i, 0));
+      widen_pack<T, V>(now[i], win[place<W>(i, 0)]);
+      float out[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float p = bias[v];
 #pragma unroll
-        for (int j = W - 1; j >= 0; --j) p = __builtin_fmaf(w[j][v], win[j][v], p);
-        y[v] = silu ? p * sigmoid_of(p) : p;
+        for (int j = W - 1; j >= 0; --j) p = __builtin_fmaf(w[j][v], win[place<W>(i, j)][v], p);
+        out[v] = silu ? p * sigmoid_of(p) : p;
       }
-      store_pack<T, V>(py + (t + i) * a.y_step, narrow_pack<T, V>(y));
-#pragma unroll
-      for (int j = W - 1; j > 0; --j)
-#pragma unroll
-        for (int v = 0; v < V; ++v) win[j][v] = win[j - 1][v];
+      y.store(out);
     }
-  }
+    t += A;
+  };
+  while (t + A <= k.t1) group(std::true_type());
+  const int32_t rest = k.t1 - t;
+  if (rest > 0) group(std::false_type());
   if (k.t1 == a.steps && a.new_state) {
     const bool ended = cut_before(a, k.n, a.steps);
 #pragma unroll
     for (int j = 1; j < W; ++j) {
-      if (ended) {
+      // (age j of the step after the last: the last group may have ended early)
+      float left[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) win[j][v] = 0.0f;
+      for (int v = 0; v < V; ++v) {
+        left[v] = 0.0f;
+#pragma unroll
+        for (int r = 0; r < W; ++r)
+          if (rest % W == r) left[v] = win[place<W>(r, j)][v];
+        if (ended) left[v] = 0.0f;
       }
       store_pack<T, V>(
           static_cast<raw*>(a.new_state) + ((int64_t)k.n * (W - 1) + (W - 1 - j)) * a.width + k.d0,
-          narrow_pack<T, V>(win[j]));
+          narrow_pack<T, V>(left));
     }
   }
 }
@@ -176,6 +232,7 @@ __global__ void __launch_bounds__(kThreads) conv_forward_kernel(const ConvRun q)
 template <class T, int V, int W>
 __global__ void __launch_bounds__(kThreads) conv_backward_kernel(const ConvRun q) {
   using raw = typename T::raw;
+  constexpr int A = group_of(W);
   const conv_grad_args& g = q.g;
   const conv_args& a = g.f;
   const ConvLane k(q, V);
@@ -187,6 +244,8 @@ __global__ void __launch_bounds__(kThreads) conv_backward_kernel(const ConvRun q
     for (int j = 0; j < W; ++j) dw[j][v] = 0.0f;
   }
   if (k.active) {
+    // acc: the gradients of the last W inputs, as far as they are known, in the
+    // places of the inputs
     float w[W][V], bias[V], win[W][V], acc[W][V];
     load_weights<V, W>(a, k.d0, w, bias);
     int32_t age = open_window<T, V, W>(a, k, win);
@@ -194,107 +253,120 @@ __global__ void __launch_bounds__(kThreads) conv_backward_kernel(const ConvRun q
     for (int j = 0; j < W; ++j)
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[j][v] = 0.0f;
-    const raw* px = static_cast<const raw*>(a.x) + k.n * a.x_row + k.d0;
-    const raw* pd = static_cast<const raw*>(g.dy) + k.n * g.dy_row + k.d0;
-    const bool silu = a.activation == BLOCK_SILU;
     const int32_t end = min(k.t1 + W - 1, a.steps);
+    Walk<T, V> x(a.x, a.x_step, a.x_row, k, k.t0), dy(g.dy, g.dy_step, g.dy_row, k, k.t0),
+        dx(g.dx, g.dx_step, g.dx_row, k, k.t0);
+    const bool silu = a.activation == BLOCK_SILU;
 
-    // The gradient of the input of step e, if it is this chunk's.
-    const auto emit = [&](int32_t e, const float(&v)[V]) {
+    // The gradient of the input of step e, where it is this chunk's.
+    const auto emit = [&](int32_t e, const float(&f)[V]) {
       if (e >= k.t0 && e < k.t1)
-        store_pack<T, V>(static_cast<raw*>(g.dx) + e * g.dx_step + k.n * g.dx_row + k.d0,
-                         narrow_pack<T, V>(v));
+        dx.store(f);
       else if (e < 0 && k.t0 == 0 && g.dstate)
         store_pack<T, V>(static_cast<raw*>(g.dstate) + ((int64_t)k.n * (W - 1) + (W - 1 + e)) * a.width + k.d0,
-                         narrow_pack<T, V>(v));
+                         narrow_pack<T, V>(f));
     };
-    Pack<T, V> next_x[kAhead], next_d[kAhead];
-    bool next_cut[kAhead];
-    const auto fetch = [&](int32_t t) {
+    Pack<T, V> next_x[A], next_d[A];
+    x.load(end - k.t0, next_x);
+    dy.load(end - k.t0, next_d);
+    uint32_t next_cuts = group_cuts<A>(a, k.n, k.t0);
+    int32_t t = k.t0;
+    // `inside`: all steps lie in the chunk, and so do the inputs whose
+    // gradients they complete.
+    const auto group = [&](auto inside) {
+      constexpr bool kInside = decltype(inside)::value;
+      Pack<T, V> now_x[A], now_d[A];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int32_t at = min(t + i, end - 1);
-        next_x[i] = load_pack<T, V>(px + at * a.x_step);
-        next_d[i] = load_pack<T, V>(pd + at * g.dy_step);
-        next_cut[i] = cut_before(a, k.n, at);
+      for (int i = 0; i < A; ++i) {
+        now_x[i] = next_x[i];
+        now_d[i] = next_d[i];
       }
-    };
-    fetch(k.t0);
-    for (int32_t t = k.t0; t < end; t += kAhead) {
-      Pack<T, V> x[kAhead], d[kAhead];
-      bool cut[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        x[i] = next_x[i];
-        d[i] = next_d[i];
-        cut[i] = next_cut[i];
+      const uint32_t cuts = next_cuts;
+      if (t + A < end) {
+        x.load(end - t - A, next_x);
+        dy.load(end - t - A, next_d);
+        next_cuts = group_cuts<A>(a, k.n, t + A);
       }
-      fetch(t + kAhead);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (t + i >= end) break;
-        if (t + i > k.t0) age = min(age + 1, W - 1);
-        if (cut[i]) {
+      for (int i = 0; i < A; ++i) {
+        if (!kInside && t + i >= end) continue;
+        if (kInside || t + i > k.t0) age = min(age + 1, W - 1);
+        if ((cuts >> i) & 1u) {
           age = 0;
-#pragma unroll
-          for (int j = 1; j < W; ++j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) win[j][v] = 0.0f;
+          forget<V, W>(win, place<W>(i, 0));
         }
-        widen_pack<T, V>(x[i], win[0]);
+        widen_pack<T, V>(now_x[i], win[place<W>(i, 0)]);
         float dp[V];
-        widen_pack<T, V>(d[i], dp);
+        widen_pack<T, V>(now_d[i], dp);
         if (silu) {
 #pragma unroll
           for (int v = 0; v < V; ++v) {
             float p = bias[v];
 #pragma unroll
-            for (int j = W - 1; j >= 0; --j) p = __builtin_fmaf(w[j][v], win[j][v], p);
+            for (int j = W - 1; j >= 0; --j) p = __builtin_fmaf(w[j][v], win[place<W>(i, j)][v], p);
             const float s = sigmoid_of(p);
             dp[v] *= s * __builtin_fmaf(p, 1.0f - s, 1.0f);
           }
         }
-        if (t + i < k.t1) {
+        if (kInside || t + i < k.t1) {
 #pragma unroll
           for (int v = 0; v < V; ++v) {
             db[v] += dp[v];
 #pragma unroll
-            for (int j = 0; j < W; ++j) dw[j][v] = __builtin_fmaf(dp[v], win[j][v], dw[j][v]);
+            for (int j = 0; j < W; ++j) dw[j][v] = __builtin_fmaf(dp[v], win[place<W>(i, j)][v], dw[j][v]);
           }
         }
+        if (age == W - 1) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-          if (j > age) continue;  // an input of another episode
+          for (int j = 1; j < W; ++j)
 #pragma unroll
-          for (int v = 0; v < V; ++v) acc[j][v] = __builtin_fmaf(w[j][v], dp[v], acc[j][v]);
+            for (int v = 0; v < V; ++v)
+              acc[place<W>(i, j)][v] = __builtin_fmaf(w[j][v], dp[v], acc[place<W>(i, j)][v]);
+        } else {  // inputs of another episode take nothing
+#pragma unroll
+          for (int j = 1; j < W; ++j)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+              acc[place<W>(i, j)][v] =
+                  j <= age ? __builtin_fmaf(w[j][v], dp[v], acc[place<W>(i, j)][v]) : acc[place<W>(i, j)][v];
         }
-        emit(t + i - (W - 1), acc[W - 1]);
 #pragma unroll
-        for (int j = W - 1; j > 0; --j)
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            win[j][v] = win[j - 1][v];
-            acc[j][v] = acc[j - 1][v];
-          }
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[0][v] = 0.0f;
+        for (int v = 0; v < V; ++v) acc[place<W>(i, 0)][v] = w[0][v] * dp[v];
+        if (kInside)
+          dx.store(acc[place<W>(i, W - 1)]);
+        else
+          emit(t + i - (W - 1), acc[place<W>(i, W - 1)]);
       }
-    }
+      t += A;
+    };
+    // (the first group completes inputs from before the chunk)
+    group(std::false_type());
+    while (t + A <= k.t1) group(std::true_type());
+    while (t < end) group(std::false_type());
     if (end == a.steps) {
-      // The last inputs wait for no step; new_state sends them theirs.  (acc[j]
-      // is now that of step L - j.)
+      // The last inputs wait for no step; new_state sends them theirs.
       age = cut_before(a, k.n, a.steps) ? 0 : min(age + 1, W - 1);
+      const int32_t rest = (end - k.t0) % W;
 #pragma unroll
       for (int j = W - 1; j > 0; --j) {
+        // (age j of step L)
+        float last[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          last[v] = 0.0f;
+#pragma unroll
+          for (int r = 0; r < W; ++r)
+            if (rest == r) last[v] = acc[place<W>(r, j)][v];
+        }
         if (g.dnew_state && j <= age) {
           float ds[V];
           widen_pack<T, V>(load_pack<T, V>(static_cast<const raw*>(g.dnew_state) +
                                            ((int64_t)k.n * (W - 1) + (W - 1 - j)) * a.width + k.d0),
                            ds);
 #pragma unroll
-          for (int v = 0; v < V; ++v) acc[j][v] += ds[v];
+          for (int v = 0; v < V; ++v) last[v] += ds[v];
         }
-        emit(a.steps - j, acc[j]);
+        emit(a.steps - j, last);
       }
     }
   }
@@ -375,9 +447,9 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const StepRun q) {
   }
 }
 
-template <class T>
+template <class T, bool GRAD>
 constexpr int wide() {
-  return 16 / T::kBytes;
+  return GRAD ? 2 : 16 / T::kBytes;
 }
 
 // Chunks are made until threads enough for every place are there (2048 a
@@ -398,8 +470,10 @@ ConvRun plan(int32_t L, int32_t N, int32_t D, int32_t V, bool grad) {
   q.params = nullptr;
   return q;
 }
-int32_t pack_of(int32_t D, int32_t dtype) {
-  const int32_t v = dtype == POLICY_F32 ? 4 : 8;
+// Elements of a thread: 16 bytes going forward, 4 elements of any type backward,
+// where a thread holds four rows of W values for each.
+int32_t pack_of(int32_t D, int32_t dtype, bool grad) {
+  const int32_t v = grad ? 2 : dtype == POLICY_F32 ? 4 : 8;
   return D >= v ? v : 1;
 }
 dim3 grid_of(const ConvRun& q) {
@@ -429,13 +503,13 @@ void launch_taps(const ConvRun& q, hipStream_t stream) {
 template <bool GRAD>
 void launch_any(const ConvRun& q, hipStream_t stream) {
   const int32_t dt = q.g.f.dtype;
-  const bool packed = pack_of(q.g.f.width, dt) > 1;
+  const bool packed = pack_of(q.g.f.width, dt, GRAD) > 1;
   if (dt == POLICY_F32)
-    packed ? launch_taps<F32, wide<F32>(), GRAD>(q, stream) : launch_taps<F32, 1, GRAD>(q, stream);
+    packed ? launch_taps<F32, wide<F32, GRAD>(), GRAD>(q, stream) : launch_taps<F32, 1, GRAD>(q, stream);
   else if (dt == POLICY_BF16)
-    packed ? launch_taps<BF16, wide<BF16>(), GRAD>(q, stream) : launch_taps<BF16, 1, GRAD>(q, stream);
+    packed ? launch_taps<BF16, wide<BF16, GRAD>(), GRAD>(q, stream) : launch_taps<BF16, 1, GRAD>(q, stream);
   else
-    packed ? launch_taps<F16, wide<F16>(), GRAD>(q, stream) : launch_taps<F16, 1, GRAD>(q, stream);
+    packed ? launch_taps<F16, wide<F16, GRAD>(), GRAD>(q, stream) : launch_taps<F16, 1, GRAD>(q, stream);
 }
 
 template <class T, int V>
@@ -464,7 +538,7 @@ hipError_t conv_forward_launch(const conv_args& a, hipStream_t stream) {
                                               (int64_t)a.rows * (a.taps - 1) * a.width * element_bytes(a.dtype),
                                               stream)
                        : hipSuccess;
-  ConvRun q = plan(a.steps, a.rows, a.width, pack_of(a.width, a.dtype), false);
+  ConvRun q = plan(a.steps, a.rows, a.width, pack_of(a.width, a.dtype, false), false);
   q.g = {};
   q.g.f = a;
   launch_any<false>(q, stream);
@@ -473,7 +547,7 @@ hipError_t conv_forward_launch(const conv_args& a, hipStream_t stream) {
 
 int64_t conv_workspace_bytes(int32_t L, int32_t N, int32_t D, int32_t W, int32_t dtype) {
   if (L == 0 || N == 0 || D == 0) return 0;
-  const ConvRun q = plan(L, N, D, pack_of(D, dtype), true);
+  const ConvRun q = plan(L, N, D, pack_of(D, dtype, true), true);
   const int64_t groups = grid_of(q).x;
   return up(groups * D * (W + 1) * 4) + up(sums_floats(groups, D * (W + 1)) * 4);
 }
@@ -488,7 +562,7 @@ hipError_t conv_backward_launch(const conv_grad_args& g, hipStream_t stream) {
       e = copy_or_clear_launch(g.dnew_state, g.dstate, a.rows * (W - 1) * D * element_bytes(a.dtype), stream);
     return e;
   }
-  ConvRun q = plan(a.steps, a.rows, a.width, pack_of(a.width, a.dtype), true);
+  ConvRun q = plan(a.steps, a.rows, a.width, pack_of(a.width, a.dtype, true), true);
   q.g = g;
   q.params = static_cast<float*>(g.workspace);
   launch_any<true>(q, stream);

@@ -75,22 +75,21 @@ __global__ void __launch_bounds__(64 * NB) scan_forward_kernel(const ScanRun q) 
       cz(a, q.p, k, a.gate, a.gate_step, a.gate_row), cy(a, q.p, k, a.y, a.y_step, a.y_row);
   const Kept kept(a, q.p, k);
   UnitInputs<T> in;
+  UnitDones dones;
   typename T::raw rx[kUnit], rd[kUnit], rz[kUnit];
   const auto fetch = [&](int32_t u) {
     in.load(a, k, u * kUnit);
     cx.load(u * kUnit, rx);
     cd.load(u * kUnit, rd);
     if (GATED) cz.load(u * kUnit, rz);
-    return unit_cuts(a, k, u * kUnit);
+    dones.load(a, k, u * kUnit);
   };
-  uint32_t cuts = fetch(u0);
+  fetch(u0);
+  if constexpr (!SUMMARY) no_stores(a.y, kUnit / NB);
   for (int32_t u = u0; u < u1; ++u) {
     const int32_t t0 = u * kUnit;
-    if constexpr (!SUMMARY) {
-      if (a.kept) kept.store(u, h);
-    }
     wave_sync();  // (the reads of the unit before)
-    in.put(s_bc[k.w], k.lane);
+    in.put(s_bc[k.w], k, S);
     wave_sync();
     float x[kUnit], dt[kUnit], du[kUnit], z[kUnit], y[kUnit];
 #pragma unroll
@@ -105,9 +104,12 @@ __global__ void __launch_bounds__(64 * NB) scan_forward_kernel(const ScanRun q) 
       if (SUMMARY) total += dt[i];
       if (GATED) z[i] = T::widen(rz[i]);
     }
-    const uint32_t cut = cuts;
+    const uint32_t cut = dones.cuts(a, k, t0);
     any_cut |= cut;
-    cuts = fetch(min(u + 1, u1 - 1));
+    if constexpr (!SUMMARY) {
+      if (a.kept) kept.store(u, h);
+    }
+    fetch(min(u + 1, u1 - 1));
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) {
       if ((cut >> i) & 1u) {

@@ -177,27 +177,31 @@ __device__ __forceinline__ void store_states(float* row, int32_t s0, int32_t S, 
 }
 
 // The b and c of a unit on their way to LDS: lane l takes four values of step
-// l / 8, of b where l % 8 < 4, else of c.
+// l / 8, of b where l % 8 < 4, else of c.  (As loaded: nothing that follows a
+// load here may wait for it.)
 template <class T>
 struct UnitInputs {
-  float v[4];
+  Pack<T, 4> x;
   __device__ __forceinline__ void load(const scan_args& a, const ScanWave& k, int32_t t0) {
     const int32_t t = min(t0 + (k.lane >> 3), a.steps - 1);
     const bool is_c = k.lane & 4;
-    const int32_t s0 = k.w * kBlock + 4 * (k.lane & 3);
+    const int32_t s0 = k.s0;
     const typename T::raw* row = static_cast<const typename T::raw*>(is_c ? a.c : a.b) +
                                  t * (is_c ? a.c_step : a.b_step) + k.n * (is_c ? a.c_row : a.b_row) +
                                  k.g * (is_c ? a.c_group : a.b_group);
     if (a.states % 4 == 0) {
-      widen_pack<T, 4>(load_pack<T, 4>(row + min(s0, a.states - 4)), v);
-      if (s0 >= a.states) v[0] = v[1] = v[2] = v[3] = 0.0f;
+      x = load_pack<T, 4>(row + min(s0, a.states - 4));
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = s0 + i < a.states ? T::widen(row[s0 + i]) : 0.0f;
+      for (int i = 0; i < 4; ++i) x.v[i] = row[min(s0 + i, a.states - 1)];
     }
   }
-  __device__ __forceinline__ void put(float (&lds)[kUnit][32], int lane) const {
-    *reinterpret_cast<float4*>(&lds[lane >> 3][4 * (lane & 7)]) = make_float4(v[0], v[1], v[2], v[3]);
+  __device__ __forceinline__ void put(float (&lds)[kUnit][32], const ScanWave& k, int32_t states) const {
+    float v[4];
+    widen_pack<T, 4>(x, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = k.s0 + i < states ? v[i] : 0.0f;
+    *reinterpret_cast<float4*>(&lds[k.lane >> 3][4 * (k.lane & 7)]) = make_float4(v[0], v[1], v[2], v[3]);
   }
 };
 
@@ -227,6 +231,16 @@ struct Column {
     row_store<T>(p + i * step, t < steps ? bytes : 0, at, x);
   }
 };
+
+// A wave waits for its loads by the number of accesses it has issued since, the
+// least that any way to that point has.  A unit's loads are followed by `n`
+// stores of the unit before, but those of the first unit are not: this many
+// stores to a row of no length, after the first unit's loads, spare every later
+// unit the wait for its predecessor's stores.
+__device__ __forceinline__ void no_stores(const void* p, int n) {
+#pragma unroll
+  for (int i = 0; i < n; ++i) __builtin_amdgcn_raw_buffer_store_b32(i, row_of(p, 0), 256 * i, 0, 0);
+}
 
 // The states that enter the units, as they lie in the lanes: [units][N][G][quads]
 // [places][4 ceil(S / 4)], so that a quad's lanes write one run of 64 bytes.
@@ -267,12 +281,21 @@ struct Kept {
   }
 };
 
-// Bit k: a done cuts the state that enters step t0 + k.
-__device__ __forceinline__ uint32_t unit_cuts(const scan_args& a, const ScanWave& k, int32_t t0) {
-  if (!a.dones) return 0;
-  const int32_t t = t0 + k.lane - 1;
-  const bool cut = k.lane < kUnit && t >= 0 && t < a.steps - 1 && a.dones[(int64_t)t * a.rows + k.n] != 0;
-  return (uint32_t)__ballot(cut);
-}
+// The dones of a unit: lane l has that of step t0 + l - 1, and bit l of cuts()
+// says that one cuts the state that enters step t0 + l.
+struct UnitDones {
+  uint8_t done;
+  __device__ __forceinline__ void load(const scan_args& a, const ScanWave& k, int32_t t0) {
+    const int32_t first = max(t0 - 1, 0);  // (step -1 has none: an offset past the end)
+    const uint8_t* p = a.dones + (int64_t)first * a.rows + k.n;
+    const uint32_t rows = (uint32_t)min(a.steps - first, kUnit + 1);
+    done = __builtin_amdgcn_raw_buffer_load_b8(row_of(p, a.dones ? rows * a.rows - k.n : 0),
+                                               (uint32_t)(k.lane - (t0 == 0)) * a.rows, 0, 0);
+  }
+  __device__ __forceinline__ uint32_t cuts(const scan_args& a, const ScanWave& k, int32_t t0) const {
+    const int32_t t = t0 + k.lane;
+    return (uint32_t)__ballot(k.lane < kUnit && t < a.steps && done != 0);
+  }
+};
 
 }  // namespace rl

@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
   raw* own = static_cast<raw*>(met_c ? g.dc : g.db) + k.n * (met_c ? g.dc_row : g.db_row) +
              k.g * (met_c ? g.dc_group : g.db_group) + met_state + (int64_t)(u1 * kUnit - 2 + met_odd) * own_step;
   UnitInputs<T> in;
+  UnitDones dones;
   raw rx[kUnit], rd[kUnit], rz[kUnit], ry[kUnit];
   float kept[4][4];
   const auto fetch = [&](int32_t u) {
@@ -165,13 +166,14 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
       cx.load(u * kUnit, rx);
       states.load(u, kept);
     }
-    return unit_cuts(a, k, u * kUnit);
+    dones.load(a, k, u * kUnit);
   };
-  uint32_t cuts = fetch(u1 - 1);
+  fetch(u1 - 1);
+  if constexpr (!SUMMARY) no_stores(g.dx, kHeld * (GATED ? 3 : 2));
   for (int32_t u = u1 - 1; u >= u0; --u) {
     const int32_t t0 = u * kUnit;
     wave_sync();
-    in.put(s_bc[k.w], k.lane);
+    in.put(s_bc[k.w], k, S);
     wave_sync();
     // dt: D; w: the gradient of v; f: dgate / v
     float x[kUnit], dt[kUnit], w[kUnit], f[kUnit];
@@ -197,9 +199,9 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
       else
         s_slope[k.w][i][k.lane] = slope;  // (read again by this lane alone)
     }
-    const uint32_t cut = cuts;
+    const uint32_t cut = dones.cuts(a, k, t0);
     any_cut |= cut;
-    if (SUMMARY) cuts = fetch(max(u - 1, u0));
+    if (SUMMARY) fetch(max(u - 1, u0));
 
     if constexpr (SUMMARY) {
 #pragma unroll
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
 #pragma unroll
           for (int s = 0; s < 4; ++s) v[r][s] = before[r][s];
         // (the registers of the held states are free from here on)
-        if (i == kHeld) cuts = fetch(max(u - 1, u0));
+        if (i == kHeld) fetch(max(u - 1, u0));
       }
       if constexpr (NB > 1) {
         __syncthreads();
