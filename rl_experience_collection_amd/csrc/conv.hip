@@ -16,6 +16,7 @@
 #include <algorithm>
 
 #include "block.hpp"
+#include "buffer.hpp"
 #include "elem.hpp"
 
 namespace rl {
@@ -111,19 +112,14 @@ struct Walk {
   __device__ __forceinline__ Walk(const void* base, int64_t step_, int64_t row, const ConvLane& k, int32_t t)
       : p(const_cast<char*>(static_cast<const char*>(base)) + (t * step_ + k.n * row + k.d0) * T::kBytes),
         step(step_ * T::kBytes) {}
-  // The next A of the `left` steps that remain (1 at least); those past the
-  // end repeat the last one.
+  // The next A of the `left` steps that remain; those past the end repeat the
+  // last one.  (No branch: a wait would stand where its ways meet.)
   template <int A>
   __device__ __forceinline__ void load(int32_t left, Pack<T, V> (&x)[A]) {
-    if (left >= A) {
 #pragma unroll
-      for (int i = 0; i < A; ++i, p += step) x[i] = load_pack<T, V>(reinterpret_cast<const typename T::raw*>(p));
-    } else {
-#pragma unroll
-      for (int i = 0; i < A; ++i) {
-        x[i] = load_pack<T, V>(reinterpret_cast<const typename T::raw*>(p));
-        if (i + 1 < left) p += step;
-      }
+    for (int i = 0; i < A; ++i) {
+      x[i] = load_pack<T, V>(reinterpret_cast<const typename T::raw*>(p));
+      p += i + 1 < left ? step : 0;
     }
   }
   __device__ __forceinline__ void store(const float (&f)[V]) {
@@ -132,19 +128,25 @@ struct Walk {
   }
 };
 
-// Bit i: a done lies before step t + i (i < n).
-template <int A>
-__device__ __forceinline__ uint32_t group_cuts(const conv_args& a, int32_t n, int32_t t) {
-  uint32_t cuts = 0;
-  if (a.dones) {
+// The dones before a thread's steps, as loaded.
+struct WalkDones {
+  const uint8_t* p;
+  int64_t step;
+  bool any;
+  __device__ __forceinline__ WalkDones(const conv_args& a, const ConvLane& k)
+      : p(a.dones ? a.dones + (int64_t)max(k.t0 - 1, 0) * a.rows + k.n : reinterpret_cast<const uint8_t*>(a.weight)),
+        step(a.dones ? a.rows : 0),
+        any(a.dones != nullptr) {}
+  template <int A>
+  __device__ __forceinline__ void load(int32_t t, int32_t left, uint8_t (&x)[A]) {
 #pragma unroll
     for (int i = 0; i < A; ++i) {
-      const int32_t at = min(t + i, a.steps - 1);
-      cuts |= (uint32_t)(at > 0 && a.dones[(int64_t)max(at - 1, 0) * a.rows + n] != 0) << i;
+      x[i] = *p;
+      p += t + i > 0 && i + 1 < left ? step : 0;  // (step 0 has none before it)
     }
   }
-  return cuts;
-}
+  __device__ __forceinline__ bool cuts(uint8_t x, int32_t t) const { return any && t > 0 && x != 0; }
+};
 
 // Clears the window but for the step at place `now`.
 template <int V, int W>
@@ -176,22 +178,26 @@ __global__ void __launch_bounds__(kThreads) conv_forward_kernel(const ConvRun q)
   const bool silu = a.activation == BLOCK_SILU;
 
   Pack<T, V> next[A];
+  uint8_t next_dones[A];
+  WalkDones dones(a, k);
   x.load(k.t1 - k.t0, next);
-  uint32_t next_cuts = group_cuts<A>(a, k.n, k.t0);
+  dones.load(k.t0, k.t1 - k.t0, next_dones);
+  no_stores(a.y, A);
   int32_t t = k.t0;
   const auto group = [&](auto whole) {
     Pack<T, V> now[A];
+    bool cut[A];
 #pragma unroll
-    for (int i = 0; i < A; ++i) now[i] = next[i];
-    const uint32_t cuts = next_cuts;
-    if (t + A < k.t1) {
-      x.load(k.t1 - t - A, next);
-      next_cuts = group_cuts<A>(a, k.n, t + A);
+    for (int i = 0; i < A; ++i) {
+      now[i] = next[i];
+      cut[i] = dones.cuts(next_dones[i], t + i);
     }
+    x.load(k.t1 - t - A, next);
+    dones.load(t + A, k.t1 - t - A, next_dones);
 #pragma unroll
     for (int i = 0; i < A; ++i) {
       if (!decltype(whole)::value && t + i >= k.t1) continue;
-      if ((cuts >> i) & 1u) forget<V, W>(win, place<W>(i, 0));
+      if (cut[i]) forget<V, W>(win, place<W>(i, 0));
       widen_pack<T, V>(now[i], win[place<W>(i, 0)]);
       float out[V];
 #pragma unroll
@@ -267,31 +273,32 @@ __global__ void __launch_bounds__(kThreads) conv_backward_kernel(const ConvRun q
                          narrow_pack<T, V>(f));
     };
     Pack<T, V> next_x[A], next_d[A];
+    uint8_t next_dones[A];
+    WalkDones dones(a, k);
     x.load(end - k.t0, next_x);
     dy.load(end - k.t0, next_d);
-    uint32_t next_cuts = group_cuts<A>(a, k.n, k.t0);
+    dones.load(k.t0, end - k.t0, next_dones);
     int32_t t = k.t0;
     // `inside`: all steps lie in the chunk, and so do the inputs whose
     // gradients they complete.
     const auto group = [&](auto inside) {
       constexpr bool kInside = decltype(inside)::value;
       Pack<T, V> now_x[A], now_d[A];
+      bool cut[A];
 #pragma unroll
       for (int i = 0; i < A; ++i) {
         now_x[i] = next_x[i];
         now_d[i] = next_d[i];
+        cut[i] = dones.cuts(next_dones[i], t + i);
       }
-      const uint32_t cuts = next_cuts;
-      if (t + A < end) {
-        x.load(end - t - A, next_x);
-        dy.load(end - t - A, next_d);
-        next_cuts = group_cuts<A>(a, k.n, t + A);
-      }
+      x.load(end - t - A, next_x);
+      dy.load(end - t - A, next_d);
+      dones.load(t + A, end - t - A, next_dones);
 #pragma unroll
       for (int i = 0; i < A; ++i) {
         if (!kInside && t + i >= end) continue;
         if (kInside || t + i > k.t0) age = min(age + 1, W - 1);
-        if ((cuts >> i) & 1u) {
+        if (cut[i]) {
           age = 0;
           forget<V, W>(win, place<W>(i, 0));
         }
@@ -341,6 +348,7 @@ __global__ void __launch_bounds__(kThreads) conv_backward_kernel(const ConvRun q
     };
     // (the first group completes inputs from before the chunk)
     group(std::false_type());
+    no_stores(g.dx, A);
     while (t + A <= k.t1) group(std::true_type());
     while (t < end) group(std::false_type());
     if (end == a.steps) {
@@ -447,11 +455,6 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const StepRun q) {
   }
 }
 
-template <class T, bool GRAD>
-constexpr int wide() {
-  return GRAD ? 2 : 16 / T::kBytes;
-}
-
 // Chunks are made until threads enough for every place are there (2048 a
 // compute unit; the gradient holds more registers and takes half), of 16 steps
 // at least, since a chunk reads W - 1 steps twice.
@@ -470,46 +473,57 @@ ConvRun plan(int32_t L, int32_t N, int32_t D, int32_t V, bool grad) {
   q.params = nullptr;
   return q;
 }
-// Elements of a thread: 16 bytes going forward, 4 elements of any type backward,
-// where a thread holds four rows of W values for each.
-int32_t pack_of(int32_t D, int32_t dtype, bool grad) {
-  const int32_t v = grad ? 2 : dtype == POLICY_F32 ? 4 : 8;
+// Elements of a thread: 16 bytes going forward (8 from five taps on), 4
+// elements of any type backward (2), where a thread holds four rows of W values
+// for each.
+constexpr int pack_for(int bytes, int W, bool grad) {
+  return grad ? (W <= 4 ? 4 : 2) : (W <= 4 ? 16 : 8) / bytes;
+}
+int32_t pack_of(int32_t D, int32_t W, int32_t dtype, bool grad) {
+  const int32_t v = pack_for(dtype == POLICY_F32 ? 4 : 2, W, grad);
   return D >= v ? v : 1;
 }
 dim3 grid_of(const ConvRun& q) {
   return dim3((uint32_t)((q.items + q.rows - 1) / q.rows), (uint32_t)((q.packs + q.across - 1) / q.across));
 }
 
-template <class T, int V, int W, bool GRAD>
+template <class T, int W, bool GRAD>
 void launch(const ConvRun& q, hipStream_t stream) {
-  if constexpr (GRAD)
-    conv_backward_kernel<T, V, W><<<grid_of(q), kThreads, 0, stream>>>(q);
-  else
-    conv_forward_kernel<T, V, W><<<grid_of(q), kThreads, 0, stream>>>(q);
+  constexpr int V = pack_for(T::kBytes, W, GRAD);
+  const dim3 grid = grid_of(q);
+  if constexpr (GRAD) {
+    if (q.g.f.width >= V)
+      conv_backward_kernel<T, V, W><<<grid, kThreads, 0, stream>>>(q);
+    else
+      conv_backward_kernel<T, 1, W><<<grid, kThreads, 0, stream>>>(q);
+  } else {
+    if (q.g.f.width >= V)
+      conv_forward_kernel<T, V, W><<<grid, kThreads, 0, stream>>>(q);
+    else
+      conv_forward_kernel<T, 1, W><<<grid, kThreads, 0, stream>>>(q);
+  }
 }
-template <class T, int V, bool GRAD>
+template <class T, bool GRAD>
 void launch_taps(const ConvRun& q, hipStream_t stream) {
   switch (q.g.f.taps) {
-    case 1: return launch<T, V, 1, GRAD>(q, stream);
-    case 2: return launch<T, V, 2, GRAD>(q, stream);
-    case 3: return launch<T, V, 3, GRAD>(q, stream);
-    case 4: return launch<T, V, 4, GRAD>(q, stream);
-    case 5: return launch<T, V, 5, GRAD>(q, stream);
-    case 6: return launch<T, V, 6, GRAD>(q, stream);
-    case 7: return launch<T, V, 7, GRAD>(q, stream);
-    default: return launch<T, V, 8, GRAD>(q, stream);
+    case 1: return launch<T, 1, GRAD>(q, stream);
+    case 2: return launch<T, 2, GRAD>(q, stream);
+    case 3: return launch<T, 3, GRAD>(q, stream);
+    case 4: return launch<T, 4, GRAD>(q, stream);
+    case 5: return launch<T, 5, GRAD>(q, stream);
+    case 6: return launch<T, 6, GRAD>(q, stream);
+    case 7: return launch<T, 7, GRAD>(q, stream);
+    default: return launch<T, 8, GRAD>(q, stream);
   }
 }
 template <bool GRAD>
 void launch_any(const ConvRun& q, hipStream_t stream) {
-  const int32_t dt = q.g.f.dtype;
-  const bool packed = pack_of(q.g.f.width, dt, GRAD) > 1;
-  if (dt == POLICY_F32)
-    packed ? launch_taps<F32, wide<F32, GRAD>(), GRAD>(q, stream) : launch_taps<F32, 1, GRAD>(q, stream);
-  else if (dt == POLICY_BF16)
-    packed ? launch_taps<BF16, wide<BF16, GRAD>(), GRAD>(q, stream) : launch_taps<BF16, 1, GRAD>(q, stream);
+  if (q.g.f.dtype == POLICY_F32)
+    launch_taps<F32, GRAD>(q, stream);
+  else if (q.g.f.dtype == POLICY_BF16)
+    launch_taps<BF16, GRAD>(q, stream);
   else
-    packed ? launch_taps<F16, wide<F16, GRAD>(), GRAD>(q, stream) : launch_taps<F16, 1, GRAD>(q, stream);
+    launch_taps<F16, GRAD>(q, stream);
 }
 
 template <class T, int V>
@@ -538,7 +552,7 @@ hipError_t conv_forward_launch(const conv_args& a, hipStream_t stream) {
                                               (int64_t)a.rows * (a.taps - 1) * a.width * element_bytes(a.dtype),
                                               stream)
                        : hipSuccess;
-  ConvRun q = plan(a.steps, a.rows, a.width, pack_of(a.width, a.dtype, false), false);
+  ConvRun q = plan(a.steps, a.rows, a.width, pack_of(a.width, a.taps, a.dtype, false), false);
   q.g = {};
   q.g.f = a;
   launch_any<false>(q, stream);
@@ -547,7 +561,7 @@ hipError_t conv_forward_launch(const conv_args& a, hipStream_t stream) {
 
 int64_t conv_workspace_bytes(int32_t L, int32_t N, int32_t D, int32_t W, int32_t dtype) {
   if (L == 0 || N == 0 || D == 0) return 0;
-  const ConvRun q = plan(L, N, D, pack_of(D, dtype, true), true);
+  const ConvRun q = plan(L, N, D, pack_of(D, W, dtype, true), true);
   const int64_t groups = grid_of(q).x;
   return up(groups * D * (W + 1) * 4) + up(sums_floats(groups, D * (W + 1)) * 4);
 }
@@ -562,7 +576,7 @@ hipError_t conv_backward_launch(const conv_grad_args& g, hipStream_t stream) {
       e = copy_or_clear_launch(g.dnew_state, g.dstate, a.rows * (W - 1) * D * element_bytes(a.dtype), stream);
     return e;
   }
-  ConvRun q = plan(a.steps, a.rows, a.width, pack_of(a.width, a.dtype, true), true);
+  ConvRun q = plan(a.steps, a.rows, a.width, pack_of(a.width, a.taps, a.dtype, true), true);
   q.g = g;
   q.params = static_cast<float*>(g.workspace);
   launch_any<true>(q, stream);

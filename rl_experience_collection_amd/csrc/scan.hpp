@@ -19,6 +19,7 @@
 #pragma once
 
 #include "block.hpp"
+#include "buffer.hpp"
 #include "device.hpp"
 #include "elem.hpp"
 
@@ -134,28 +135,6 @@ struct ScanWave {
   }
 };
 
-// Access to a row whose address and length the wave shares.  The hardware
-// drops what lies past the length: lanes without a channel and steps past the
-// end (length 0) read 0 and write nothing, with no branch and no clamping.
-typedef uint32_t words4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_of(const void* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
-}
-template <class T>
-__device__ __forceinline__ typename T::raw row_load(const void* p, uint32_t bytes, uint32_t at) {
-  if constexpr (T::kBytes == 4)
-    return __builtin_amdgcn_raw_buffer_load_b32(row_of(p, bytes), at, 0, 0);
-  else
-    return __builtin_amdgcn_raw_buffer_load_b16(row_of(p, bytes), at, 0, 0);
-}
-template <class T>
-__device__ __forceinline__ void row_store(void* p, uint32_t bytes, uint32_t at, float x) {
-  if constexpr (T::kBytes == 4)
-    __builtin_amdgcn_raw_buffer_store_b32(T::narrow(x), row_of(p, bytes), at, 0, 0);
-  else
-    __builtin_amdgcn_raw_buffer_store_b16(T::narrow(x), row_of(p, bytes), at, 0, 0);
-}
-
 // The four states from s0 of a row of S; those that do not exist are 0.
 __device__ __forceinline__ void load_states(const float* row, int32_t s0, int32_t S, float (&h)[4]) {
   if (s0 + 4 <= S) {
@@ -231,16 +210,6 @@ struct Column {
     row_store<T>(p + i * step, t < steps ? bytes : 0, at, x);
   }
 };
-
-// A wave waits for its loads by the number of accesses it has issued since, the
-// least that any way to that point has.  A unit's loads are followed by `n`
-// stores of the unit before, but those of the first unit are not: this many
-// stores to a row of no length, after the first unit's loads, spare every later
-// unit the wait for its predecessor's stores.
-__device__ __forceinline__ void no_stores(const void* p, int n) {
-#pragma unroll
-  for (int i = 0; i < n; ++i) __builtin_amdgcn_raw_buffer_store_b32(i, row_of(p, 0), 256 * i, 0, 0);
-}
 
 // The states that enter the units, as they lie in the lanes: [units][N][G][quads]
 // [places][4 ceil(S / 4)], so that a quad's lanes write one run of 64 bytes.
