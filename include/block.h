@@ -190,8 +190,7 @@ typedef struct {
 } norm_args;
 
 /* stats [R][2] f32: 1 / sqrt(mean + eps) of the branch and of the stream, for
- * the gradient (NULL: not written).  stream or normed may be NULL (not
- * written). */
+ * the gradient (NULL: not written). */
 int norm_forward(const norm_args *args, void *stream, int64_t stream_row, void *normed,
                  int64_t normed_row, float *stats, void *hip_stream);
 typedef struct {

@@ -271,12 +271,12 @@ int norm_forward(const norm_args* a, void* stream, int64_t stream_row, void* nor
   if (!a) return fail(ROLLOUT_EINVAL, "%s: arguments are NULL", who);
   RL_CHECK(check_norm(who, *a));
   const size_t eb = element_bytes(a->dtype);
-  RL_CHECK(check_optional(who, "stream", stream, eb));
-  if (stream) RL_CHECK(check_rows(who, "stream", stream_row, a->width));
-  RL_CHECK(check_optional(who, "normed", normed, eb));
-  if (normed) RL_CHECK(check_rows(who, "normed", normed_row, a->width));
-  RL_CHECK(check_optional(who, "stats", stats, 4));
   if (a->rows == 0) return ROLLOUT_OK;
+  RL_CHECK(check_buffer(who, "stream", stream, eb));
+  RL_CHECK(check_rows(who, "stream", stream_row, a->width));
+  RL_CHECK(check_buffer(who, "normed", normed, eb));
+  RL_CHECK(check_rows(who, "normed", normed_row, a->width));
+  RL_CHECK(check_optional(who, "stats", stats, 4));
   return launched(rl::norm_forward_launch(*a, stream, stream_row, normed, normed_row, stats,
                                           static_cast<hipStream_t>(hip_stream)),
                   who);

@@ -11,6 +11,7 @@
 #include <algorithm>
 
 #include "block.hpp"
+#include "buffer.hpp"
 #include "elem.hpp"
 #include "philox.hpp"
 
@@ -29,6 +30,8 @@ struct NormRun {
   float inv_width;
   bool past;      // outputs are stored past the caches
   float* params;  // gradient: [workgroups][2 or 3][D]
+  void *dresidual, *dbranch, *dgate;  // gradient: the outputs, or a row for all of what is not wanted
+  int64_t dresidual_row, dbranch_row, dgate_row;
 };
 
 enum GateKind { kNoGate, kRowGate, kChannelGate };
@@ -92,7 +95,7 @@ struct RowSum {
 template <class T, int V, int TPR, int K>
 struct Share {
   int32_t at[K], fresh[K];
-  bool has[K], whole;
+  bool whole;
   __device__ __forceinline__ explicit Share(int32_t D) {
     whole = true;
 #pragma unroll
@@ -100,7 +103,6 @@ struct Share {
       const int32_t e = ((int32_t)row_thread<TPR>() + row_threads<TPR>() * i) * V;
       at[i] = min(e, D - V);
       fresh[i] = e - at[i];
-      has[i] = e < D;
       whole = whole && fresh[i] == 0;
     }
     whole = __ballot(!whole) == 0;
@@ -111,11 +113,34 @@ struct Share {
     for (int i = 0; i < K; ++i)
       x[i] = load_pack<T, V>(static_cast<const typename T::raw*>(p) + r * row + at[i]);
   }
-  __device__ __forceinline__ void store(void* p, int64_t row, int64_t r, const float (&f)[K][V], bool past) const {
+  // (Threads past a row's end, and rows past the last one, write what the last
+  // pack or row holds once more: a branch would hide a store from the count of
+  // those that a wait for later loads may leave under way.)
+  template <bool PAST>
+  __device__ __forceinline__ void store(void* p, int64_t row, int64_t r, const float (&f)[K][V]) const {
 #pragma unroll
     for (int i = 0; i < K; ++i)
-      if (has[i])
-        store_pack<T, V>(static_cast<typename T::raw*>(p) + r * row + at[i], narrow_pack<T, V>(f[i]), past);
+      store_pack<T, V>(static_cast<typename T::raw*>(p) + r * row + at[i], narrow_pack<T, V>(f[i]), PAST);
+  }
+  // The compiler keeps `from` and `to` apart: loads into the one may start while
+  // the other is in use, and nothing has to be moved when they have arrived.
+  static __device__ __forceinline__ void take(const Row& from, Row& to) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      if constexpr (V * T::kBytes == 16) {
+        const quad_value x = __builtin_bit_cast(quad_value, from[i]);
+        quad_value y;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t word;
+          asm volatile("v_mov_b32 %0, %1" : "=v"(word) : "v"(x[w]));
+          y[w] = word;
+        }
+        to[i] = __builtin_bit_cast(Pack<T, V>, y);
+      } else {
+        to[i] = from[i];
+      }
+    }
   }
   __device__ __forceinline__ void weights(const float* w, float (&f)[K][V]) const {
 #pragma unroll
@@ -175,8 +200,16 @@ __device__ __forceinline__ void activate(int32_t kind, float g, float& act, floa
   }
 }
 
-template <class T, int V, int TPR, int K, int GATE>
-__global__ void __launch_bounds__(threads_of(TPR)) norm_forward_kernel(const NormRun q) {
+// Waves a SIMD: 6, so that two rows of up to 768 threads share a compute unit
+// (4099 x 5001 fp16 takes 50 us so, 63 with the 5 that the compiler leaves room
+// for), where that leaves enough registers.
+template <class T>
+constexpr int forward_waves(int TPR, int gate) {
+  return TPR > 64 && !(T::kBytes == 4 && gate == kRowGate) ? 6 : 1;
+}
+
+template <class T, int V, int TPR, int K, int GATE, bool PAST>
+__global__ void __launch_bounds__(threads_of(TPR), forward_waves<T>(TPR, GATE)) norm_forward_kernel(const NormRun q) {
   const norm_args& a = q.g.f;
   constexpr int kRows = TPR <= 64 ? 256 / TPR : 1;
   __shared__ float s_sum[2][16];
@@ -198,25 +231,34 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_forward_kernel(const Nor
       }
   }
   typename Share<T, V, TPR, K>::Row res, br, ga;
+#pragma unroll
+  for (int i = 0; i < K; ++i) br[i] = Pack<T, V>{};
   const int64_t step = (int64_t)gridDim.x * kRows;
-  int64_t r = (int64_t)blockIdx.x * kRows + (TPR <= 64 ? threadIdx.x / TPR : 0);
-  const auto fetch = [&](int64_t at) {
-    at = at < a.rows ? at : a.rows - 1;
-    own.load(a.residual, a.residual_row, at, res);
-    if (branch) own.load(a.branch, a.branch_row, at, br);
-    if (GATE == kRowGate) own.load(a.gate, a.gate_row, at, ga);
-  };
-  fetch(r);
   // (all of a workgroup's threads go round as often: they meet in row_sum)
-  for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.rows; first += step, r += step) {
+  int64_t next = (int64_t)blockIdx.x * kRows + (TPR <= 64 ? threadIdx.x / TPR : 0);
+  const auto fetch = [&]() {
+    next = next < a.rows ? next : a.rows - 1;
+    own.load(a.residual, a.residual_row, next, res);
+    if (branch) own.load(a.branch, a.branch_row, next, br);
+    if (GATE == kRowGate) own.load(a.gate, a.gate_row, next, ga);
+  };
+  fetch();
+  no_stores(q.stream, 2 * K);
+  for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.rows; first += step) {
+    const int64_t r = next;
+    typename Share<T, V, TPR, K>::Row xr, xb, xg;
+    own.take(res, xr);
+    own.take(br, xb);
+    if (GATE == kRowGate) own.take(ga, xg);
+    next += step;
+    fetch();
     float s[K][V], b[K][V], g[K][V];
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-      widen_pack<T, V>(res[i], s[i]);
-      if (branch) widen_pack<T, V>(br[i], b[i]);
-      if (GATE == kRowGate) widen_pack<T, V>(ga[i], g[i]);
+      widen_pack<T, V>(xr[i], s[i]);
+      widen_pack<T, V>(xb[i], b[i]);
+      if (GATE == kRowGate) widen_pack<T, V>(xg[i], g[i]);
     }
-    if (first + step < a.rows) fetch(r + step);
     float inv_b = 1.0f;
     if (branch && a.branch_norm)
       inv_b = __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum(own.dot(b, b), s_sum), q.inv_width, a.eps));
@@ -227,7 +269,10 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_forward_kernel(const Nor
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         s[i][v] *= a.residual_scale;
-        if (!branch) continue;
+        if (!branch) {
+      no_stores(q.dresidual, K * (GATE == kRowGate ? 2 : 1));
+      continue;
+    }
         float z = b[i][v] * inv_b * bw[i][v];
         if (GATE == kChannelGate) z *= gc[i][v];
         if (GATE == kRowGate) {
@@ -240,26 +285,22 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_forward_kernel(const Nor
       }
     }
     const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(row_sum(own.dot(s, s), s_sum), q.inv_width, a.eps));
-    if (r < a.rows) {
-      if (q.stream) own.store(q.stream, q.stream_row, r, s, q.past);
-      if (q.normed) {
-#pragma unroll
-        for (int i = 0; i < K; ++i)
-#pragma unroll
-          for (int v = 0; v < V; ++v) s[i][v] *= inv * w[i][v];
-        own.store(q.normed, q.normed_row, r, s, q.past);
-      }
-      if (q.stats && row_thread<TPR>() == 0) {
-        q.stats[2 * r] = inv_b;
-        q.stats[2 * r + 1] = inv;
-      }
+    if (q.stats && row_thread<TPR>() == 0) {
+      q.stats[2 * r] = inv_b;
+      q.stats[2 * r + 1] = inv;
     }
+    own.template store<PAST>(q.stream, q.stream_row, r, s);
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) s[i][v] *= inv * w[i][v];
+    own.template store<PAST>(q.normed, q.normed_row, r, s);
   }
 }
 
 // What a thread needs of its own columns at every row, in LDS: the registers
 // that it would take are worth more to the rows in flight (1,024,000 x 128
-// bf16 takes LDS_US us so, REG_US with weights in registers).
+// bf16 takes 443 us so, 459 with weights in registers).
 template <int K, int V, int THREADS>
 struct OwnColumns {
   static constexpr int kQuads = K * V / 4;
@@ -291,7 +332,7 @@ struct OwnColumns {
   }
 };
 
-template <class T, int V, int TPR, int K, int GATE>
+template <class T, int V, int TPR, int K, int GATE, bool PAST>
 __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const NormRun q) {
   const norm_grad_args& p = q.g;
   const norm_args& a = p.f;
@@ -325,12 +366,12 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const No
     for (int v = 0; v < V; ++v) dw[i][v] = dbw[i][v] = dgc[i][v] = 0.0f;
   typename Share<T, V, TPR, K>::Row res, br, ga, ds, dn;
 #pragma unroll
-  for (int i = 0; i < K; ++i) ds[i] = dn[i] = Pack<T, V>{};  // those that are not given
+  for (int i = 0; i < K; ++i) br[i] = ds[i] = dn[i] = Pack<T, V>{};  // those that are not given
   float inv_b_next = 1.0f, inv_next = 1.0f;
   const int64_t step = (int64_t)gridDim.x * kRows;
-  int64_t r = (int64_t)blockIdx.x * kRows + (TPR <= 64 ? threadIdx.x / TPR : 0);
-  const auto fetch = [&](int64_t at) {
-    at = at < a.rows ? at : a.rows - 1;
+  int64_t wanted = (int64_t)blockIdx.x * kRows + (TPR <= 64 ? threadIdx.x / TPR : 0);
+  const auto fetch = [&]() {
+    const int64_t at = wanted < a.rows ? wanted : a.rows - 1;
     own.load(a.residual, a.residual_row, at, res);
     if (branch) own.load(a.branch, a.branch_row, at, br);
     if (GATE == kRowGate) own.load(a.gate, a.gate_row, at, ga);
@@ -339,27 +380,34 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const No
     inv_b_next = p.stats[2 * at];
     inv_next = p.stats[2 * at + 1];
   };
-  fetch(r);
-  for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.rows; first += step, r += step) {
-    const bool mine = r < a.rows;
-    const float inv_b = inv_b_next, inv = inv_next;
+  fetch();
+  no_stores(q.dresidual, K * (GATE == kRowGate ? 3 : 2));
+  for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.rows; first += step) {
+    // (a row past the end repeats the last one and counts in no sum)
+    const bool mine = kRows == 1 || wanted < a.rows;
+    const int64_t r = mine ? wanted : a.rows - 1;
+    float inv_b, inv;
+    asm volatile("v_mov_b32 %0, %1" : "=v"(inv_b) : "v"(inv_b_next));
+    asm volatile("v_mov_b32 %0, %1" : "=v"(inv) : "v"(inv_next));
     // s: the normed stream; u: the normed branch; g: the gate; d: dstream; e: dnormed weight
     float s[K][V], u[K][V], g[K][V], d[K][V], e[K][V];
     uint32_t kept[K];
-    if (kRows > 1 && !mine) {
-      // (a row past the end repeats the last one: its gradients count 0)
-#pragma unroll
-      for (int i = 0; i < K; ++i) ds[i] = dn[i] = Pack<T, V>{};
-    }
+    typename Share<T, V, TPR, K>::Row xr, xb, xg, xs, xn;
+    own.take(res, xr);
+    own.take(br, xb);
+    if (GATE == kRowGate) own.take(ga, xg);
+    own.take(ds, xs);
+    own.take(dn, xn);
+    wanted += step;
+    fetch();
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-      widen_pack<T, V>(res[i], s[i]);
-      widen_pack<T, V>(ds[i], d[i]);
-      widen_pack<T, V>(dn[i], e[i]);
-      if (branch) widen_pack<T, V>(br[i], u[i]);
-      if (GATE == kRowGate) widen_pack<T, V>(ga[i], g[i]);
+      widen_pack<T, V>(xr[i], s[i]);
+      widen_pack<T, V>(xb[i], u[i]);
+      widen_pack<T, V>(xs[i], d[i]);
+      widen_pack<T, V>(xn[i], e[i]);
+      if (GATE == kRowGate) widen_pack<T, V>(xg[i], g[i]);
     }
-    fetch(first + step < a.rows ? r + step : r);
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       float w[V], bw[V], act[V];
@@ -380,9 +428,13 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const No
           s[i][v] = __builtin_fmaf(a.branch_scale, z, s[i][v]);
         }
         s[i][v] *= inv;
-        dw[i][v] = __builtin_fmaf(e[i][v], s[i][v], dw[i][v]);
-        e[i][v] *= w[v];
       }
+      if (mine) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) dw[i][v] = __builtin_fmaf(e[i][v], s[i][v], dw[i][v]);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) e[i][v] *= w[v];
     }
     float mean = 0.0f;
     if (p.dnormed) {
@@ -392,14 +444,15 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const No
 #pragma unroll
         for (int v = 0; v < V; ++v) d[i][v] = __builtin_fmaf(inv, __builtin_fmaf(-s[i][v], mean, e[i][v]), d[i][v]);
     }
-    if (p.dresidual && mine) {
 #pragma unroll
-      for (int i = 0; i < K; ++i)
+    for (int i = 0; i < K; ++i)
 #pragma unroll
-        for (int v = 0; v < V; ++v) s[i][v] = a.residual_scale * d[i][v];
-      own.store(p.dresidual, a.width, r, s, q.past);
+      for (int v = 0; v < V; ++v) s[i][v] = a.residual_scale * d[i][v];
+    own.template store<PAST>(q.dresidual, q.dresidual_row, r, s);
+    if (!branch) {
+      no_stores(q.dresidual, K * (GATE == kRowGate ? 2 : 1));
+      continue;
     }
-    if (!branch) continue;
     // (the empty statements keep the compiler from holding across the sum what
     // LDS or two transcendental operations give again)
     asm volatile("" ::: "memory");
@@ -418,13 +471,20 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const No
           activate(a.activation, g[i][v], act[v], slope);
           g[i][v] = dact * slope;
         }
-        if (GATE == kChannelGate) dgc[i][v] += dact;
-        const float du = GATE == kNoGate ? dz : dz * act[v];
-        dbw[i][v] = __builtin_fmaf(du, u[i][v], dbw[i][v]);
-        e[i][v] = du * bw[v];
+        if (GATE == kChannelGate) d[i][v] = dact;
+        e[i][v] = GATE == kNoGate ? dz : dz * act[v];
       }
+      if (mine) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (GATE == kChannelGate) dgc[i][v] += d[i][v];
+          dbw[i][v] = __builtin_fmaf(e[i][v], u[i][v], dbw[i][v]);
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) e[i][v] *= bw[v];
     }
-    if (GATE == kRowGate && p.dgate && mine) own.store(p.dgate, a.width, r, g, q.past);
+    if (GATE == kRowGate) own.template store<PAST>(q.dgate, q.dgate_row, r, g);
     if (a.branch_norm) {
       mean = row_sum(own.dot(e, u), s_sum) * q.inv_width;
 #pragma unroll
@@ -432,7 +492,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const No
 #pragma unroll
         for (int v = 0; v < V; ++v) e[i][v] = inv_b * __builtin_fmaf(-u[i][v], mean, e[i][v]);
     }
-    if (p.dbranch && mine) own.store(p.dbranch, a.width, r, e, q.past);
+    own.template store<PAST>(q.dbranch, q.dbranch_row, r, e);
   }
   if constexpr (GATE == kChannelGate) {
     // the activation's slope is the same for every row
@@ -496,9 +556,11 @@ void launch(const NormRun& q, hipStream_t stream) {
   const int32_t D = q.g.f.width;
   const dim3 grid(groups_of(q.g.f.rows, D, GRAD)), threads(TPR <= 64 ? 256 : threads_for(D));
   if constexpr (GRAD)
-    norm_backward_kernel<T, V, TPR, K, GATE><<<grid, threads, 0, stream>>>(q);
+    q.past ? norm_backward_kernel<T, V, TPR, K, GATE, true><<<grid, threads, 0, stream>>>(q)
+           : norm_backward_kernel<T, V, TPR, K, GATE, false><<<grid, threads, 0, stream>>>(q);
   else
-    norm_forward_kernel<T, V, TPR, K, GATE><<<grid, threads, 0, stream>>>(q);
+    q.past ? norm_forward_kernel<T, V, TPR, K, GATE, true><<<grid, threads, 0, stream>>>(q)
+           : norm_forward_kernel<T, V, TPR, K, GATE, false><<<grid, threads, 0, stream>>>(q);
 }
 // (768 threads may hold 168 registers each, 1024 hold 128.)
 template <class T, int GATE, bool GRAD>
@@ -558,7 +620,7 @@ hipError_t norm_forward_launch(const norm_args& a, void* stream_out, int64_t str
 int64_t norm_workspace_bytes(int64_t R, int32_t D, int32_t dtype) {
   if (R == 0) return 0;
   const int64_t groups = groups_of(R, D, true);
-  return up(groups * 3 * D * 4) + up(sums_floats(groups, 3 * D) * 4);
+  return up(groups * 3 * D * 4) + up(sums_floats(groups, 3 * D) * 4) + up(D * 4);
 }
 
 hipError_t norm_backward_launch(const norm_grad_args& g, hipStream_t stream) {
@@ -575,6 +637,15 @@ hipError_t norm_backward_launch(const norm_grad_args& g, hipStream_t stream) {
   NormRun q = run_of(a);
   q.g = g;
   q.params = static_cast<float*>(g.workspace);
+  // (the workspace ends with a row of D values)
+  char* nowhere = static_cast<char*>(g.workspace) + norm_workspace_bytes(a.rows, a.width, a.dtype) - up(D * 4);
+  const auto put = [&](void* wanted, void*& p, int64_t& row) {
+    p = wanted ? wanted : nowhere;
+    row = wanted ? D : 0;
+  };
+  put(g.dresidual, q.dresidual, q.dresidual_row);
+  put(g.dbranch, q.dbranch, q.dbranch_row);
+  put(channel ? nullptr : g.dgate, q.dgate, q.dgate_row);
   launch_any<true>(q, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !(g.dweight || g.dbranch_weight || (channel && g.dgate))) return e;

@@ -16,31 +16,6 @@ struct ScanRun {
   ScanSummary sum;
 };
 
-// What enters chunk `chunk`: the states that the chunks before leave, one
-// after another.
-__device__ __forceinline__ void enter_chunk(const ScanRun& q, const ScanWave& k, const float (&rate)[4][4],
-                                            float (&h)[4][4]) {
-  const scan_args& a = q.a;
-  const int64_t nd = (int64_t)a.rows * a.width;
-  for (int32_t i = 0; i < k.chunk; ++i) {
-    const bool cut = q.sum.cut[(int64_t)i * a.rows + k.n] != 0;
-    const int64_t at = i * nd + (int64_t)k.n * a.width;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t c = at + k.quad_channel(q.p, r);
-      float own[4];
-      load_states(q.sum.state + c * a.states, k.s0, a.states, own);
-      const float total = q.sum.total[c];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        // (a state of 0 stays 0 under any decay)
-        const float left = h[r][s] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(total * rate[r][s]) * h[r][s];
-        h[r][s] = cut ? own[s] : left + own[s];
-      }
-    }
-  }
-}
-
 // A chunk of the scan.  SUMMARY: from a state of zero, without outputs.
 template <class T, int NB, bool GATED, bool SUMMARY>
 __global__ void __launch_bounds__(64 * NB) scan_forward_kernel(const ScanRun q) {
@@ -64,7 +39,7 @@ __global__ void __launch_bounds__(64 * NB) scan_forward_kernel(const ScanRun q) 
     if (!SUMMARY && a.state) load_states(a.state + ((int64_t)k.n * a.width + c) * S, k.s0, S, h[r]);
   }
   if constexpr (!SUMMARY) {
-    if (k.chunk > 0) enter_chunk(q, k, rate, h);
+    join_chunks(q.p, q.sum, k, a.rows, a.width, S, 0, 1, k.chunk, rate, h);
   }
   const float bias = a.delta_bias ? a.delta_bias[k.channel] : 0.0f;
   const float skip = a.skip ? a.skip[k.channel] : 0.0f;
@@ -255,10 +230,11 @@ void launch_states(const ScanRun& q, hipStream_t stream) {
 
 }  // namespace
 
-// A chunk has four units at least, and chunks are made until about two waves
-// a SIMD have work (1024 SIMDs); a scan with half of that many columns is not
+// A chunk has four units at least, and chunks are made until two waves a SIMD
+// have work (1024 SIMDs; 16,385 x 2 x 1000 fp16 takes 327 us so, 334 to 369 with
+// three or four); a scan of more than a quarter of that many columns is not
 // cut, as the second look at its inputs would cost what the cut gains.
-ScanPlan scan_plan(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G, bool grad) {
+ScanPlan scan_plan(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G) {
   ScanPlan p;
   p.group_width = D / G;
   p.blocks = cdiv(p.group_width, 64);
@@ -300,7 +276,7 @@ int64_t scan_kept_floats(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G) 
 
 int64_t scan_workspace_bytes(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G) {
   if (L == 0 || N == 0 || D == 0) return 0;
-  return scan_summary_bytes(scan_plan(L, N, D, S, G, false), N, D, S);
+  return scan_summary_bytes(scan_plan(L, N, D, S, G), N, D, S);
 }
 
 hipError_t scan_forward_launch(const scan_args& a, hipStream_t stream) {
@@ -309,7 +285,7 @@ hipError_t scan_forward_launch(const scan_args& a, hipStream_t stream) {
     return a.new_state ? copy_or_clear_launch(a.state, a.new_state, state_bytes, stream) : hipSuccess;
   ScanRun q;
   q.a = a;
-  q.p = scan_plan(a.steps, a.rows, a.width, a.states, a.groups, false);
+  q.p = scan_plan(a.steps, a.rows, a.width, a.states, a.groups);
   q.sum = scan_summary(q.p, a.rows, a.width, a.states, a.workspace);
   if (a.dtype == POLICY_F32)
     launch_states<F32>(q, stream);

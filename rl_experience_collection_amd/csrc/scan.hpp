@@ -46,7 +46,7 @@ struct ScanSummary {
   int32_t* cut;  // [chunks][N]: a done lies inside
 };
 
-ScanPlan scan_plan(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G, bool grad);
+ScanPlan scan_plan(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G);
 int64_t scan_summary_bytes(const ScanPlan& p, int32_t N, int32_t D, int32_t S);
 ScanSummary scan_summary(const ScanPlan& p, int32_t N, int32_t D, int32_t S, void* workspace);
 
@@ -266,5 +266,41 @@ struct UnitDones {
     return (uint32_t)__ballot(k.lane < kUnit && t < a.steps && done != 0);
   }
 };
+
+// h becomes what `count` chunks make of it one after another, from chunk
+// `first` on in the given direction; four summaries are loaded at a time.
+__device__ __forceinline__ void join_chunks(const ScanPlan& p, const ScanSummary& sum, const ScanWave& k,
+                                            int32_t N, int32_t D, int32_t S, int32_t first, int32_t direction,
+                                            int32_t count, const float (&rate)[4][4], float (&h)[4][4]) {
+  constexpr int kAt = 4;
+  for (int32_t i0 = 0; i0 < count; i0 += kAt) {
+    float own[kAt][4][4], total[kAt][4];
+    int32_t cut[kAt];
+#pragma unroll
+    for (int m = 0; m < kAt; ++m) {
+      const int64_t chunk = first + direction * min(i0 + m, count - 1);
+      cut[m] = sum.cut[chunk * N + k.n];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t c = (chunk * N + k.n) * D + k.quad_channel(p, r);
+        load_states(sum.state + c * S, k.s0, S, own[m][r]);
+        total[m][r] = sum.total[c];
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < kAt; ++m) {
+      if (i0 + m >= count) continue;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          // (a state of 0 stays 0 under any decay)
+          const float left =
+              h[r][s] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(total[m][r] * rate[r][s]) * h[r][s];
+          h[r][s] = cut[m] != 0 ? own[m][r][s] : left + own[m][r][s];
+        }
+    }
+  }
+}
 
 }  // namespace rl

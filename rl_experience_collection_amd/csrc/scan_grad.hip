@@ -42,29 +42,6 @@ __device__ __forceinline__ void read4(const float* p, float (&v)[4]) {
   v[3] = x.w;
 }
 
-// What leaves chunk `chunk` backward enters from the chunks after it.
-__device__ __forceinline__ void enter_backward(const GradRun& q, const ScanWave& k,
-                                               const float (&rate)[4][4], float (&G)[4][4]) {
-  const scan_args& a = q.g.f;
-  const int64_t nd = (int64_t)a.rows * a.width;
-  for (int32_t i = q.p.chunks - 1; i > k.chunk; --i) {
-    const bool cut = q.sum.cut[(int64_t)i * a.rows + k.n] != 0;
-    const int64_t at = i * nd + (int64_t)k.n * a.width;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t c = at + k.quad_channel(q.p, r);
-      float own[4];
-      load_states(q.sum.state + c * a.states, k.s0, a.states, own);
-      const float total = q.sum.total[c];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const float left = G[r][s] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(total * rate[r][s]) * G[r][s];
-        G[r][s] = cut ? own[s] : left + own[s];
-      }
-    }
-  }
-}
-
 // Sums over the wave's quads of the four values of b's and c's gradients that
 // every lane holds.  Halving the values at each meeting, lane l ends with one:
 // of b where its bit 5 is 0, else of c, state 2 (bit 4) + (bit 3) of the four
@@ -130,7 +107,7 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int s = 0; s < 4; ++s) G[r][s] = 0.0f;
-      enter_backward(q, k, rate, G);
+      join_chunks(q.p, q.sum, k, a.rows, a.width, S, q.p.chunks - 1, -1, q.p.chunks - 1 - k.chunk, rate, G);
     }
   }
   const float bias = a.delta_bias ? a.delta_bias[k.channel] : 0.0f;
@@ -499,7 +476,7 @@ Parts parts_of(const ScanPlan& p, int32_t L, int32_t N, int32_t D, int32_t S, in
 
 int64_t scan_grad_workspace_bytes(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G) {
   if (L == 0 || N == 0 || D == 0) return 0;
-  const Parts b = parts_of(scan_plan(L, N, D, S, G, true), L, N, D, S, G);
+  const Parts b = parts_of(scan_plan(L, N, D, S, G), L, N, D, S, G);
   return b.summary + b.shared + b.params + b.scratch;
 }
 
@@ -516,7 +493,7 @@ hipError_t scan_backward_launch(const scan_grad_args& g, hipStream_t stream) {
   }
   GradRun q;
   q.g = g;
-  q.p = scan_plan(a.steps, a.rows, a.width, a.states, a.groups, true);
+  q.p = scan_plan(a.steps, a.rows, a.width, a.states, a.groups);
   q.pairs = (a.steps + 1) / 2;
   const Parts b = parts_of(q.p, a.steps, a.rows, a.width, a.states, a.groups);
   char* w = static_cast<char*>(a.workspace);
