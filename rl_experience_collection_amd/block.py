@@ -14,6 +14,7 @@ policy.py.
 from __future__ import annotations
 
 import ctypes as C
+import struct
 
 import torch
 
@@ -78,6 +79,30 @@ class NormGradArgs(C.Structure):
                 [("workspace_bytes", C.c_int64)])
 
 
+# The same structs as bytes: packing one takes a fraction of what filling a
+# ctypes structure of some forty fields does.
+_CONV = struct.Struct("6i4q7Q").pack
+_CONV_GRAD = struct.Struct("4q7Qq").pack
+_SCAN = struct.Struct("7i4x14q14Qq").pack
+_SCAN_GRAD = struct.Struct("14q11Q").pack
+_NORM = struct.Struct("q4i4fQQIIQqQqQq2Q").pack
+_NORM_GRAD = struct.Struct("QQqQq6Qq").pack
+_packed = {}  # entry points that take them
+
+
+def _at(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _entry(name):
+    fn = _packed.get(name)
+    if fn is None:
+        declared = getattr(_lib(), name)
+        fn = _packed[name] = _lib()[name]
+        fn.argtypes, fn.restype = [C.c_char_p] + list(declared.argtypes[1:]), C.c_int
+    return fn
+
+
 def declare(lib):
     """Argument types of the entry points of include/block.h."""
     vp, i32, i64 = C.c_void_p, C.c_int32, C.c_int64
@@ -116,15 +141,15 @@ def _rows_of(g):
 # --------------------------------------------------------------- convolution
 def _conv_args(x, y, weight, bias, state, dones, new_state, act):
     L, N, D = x.shape
-    return ConvArgs(L, N, D, weight.shape[1], _DTYPES[x.dtype], act, *x.stride()[:2], *y.stride()[:2], _ptr(x),
-                    _ptr(weight), _ptr(bias), _ptr(state), _ptr(dones), _ptr(y), _ptr(new_state))
+    return _CONV(L, N, D, weight.shape[1], _DTYPES[x.dtype], act, *x.stride()[:2], *y.stride()[:2], x.data_ptr(),
+                 weight.data_ptr(), _at(bias), _at(state), _at(dones), y.data_ptr(), _at(new_state))
 
 
 def _conv_forward(x, weight, bias, state, dones, act):
     stream = _here("causal_conv", x, weight, bias, state, dones)
     y = _like(x)
     new = torch.empty((x.shape[1], weight.shape[1] - 1, x.shape[2]), dtype=x.dtype, device=x.device)
-    _call(_lib().conv_forward, C.byref(_conv_args(x, y, weight, bias, state, dones, new, act)), stream)
+    _call(_entry("conv_forward"), _conv_args(x, y, weight, bias, state, dones, new, act), stream)
     return y, new
 
 
@@ -150,11 +175,11 @@ class _CausalConv(torch.autograd.Function):
         dbias = torch.empty_like(bias) if bias is not None and ctx.needs_input_grad[2] else None
         dstate = torch.empty_like(state) if state is not None and ctx.needs_input_grad[3] else None
         f = _conv_args(x, x, weight, bias, state, dones, None, ctx.act)
-        size = lib.conv_workspace(f.steps, f.rows, f.width, f.taps, f.dtype)
+        size = lib.conv_workspace(*x.shape, weight.shape[1], _DTYPES[x.dtype])
         ws = _workspace(x, size)
-        g = ConvGradArgs(f, *dy.stride()[:2], *dx.stride()[:2], _ptr(dy), _ptr(dnew), _ptr(dx), _ptr(dweight),
-                         _ptr(dbias), _ptr(dstate), _ptr(ws), size)
-        _call(lib.conv_backward, C.byref(g), stream)
+        g = f + _CONV_GRAD(*dy.stride()[:2], *dx.stride()[:2], dy.data_ptr(), _at(dnew), dx.data_ptr(),
+                           dweight.data_ptr(), _at(dbias), _at(dstate), _at(ws), size)
+        _call(_entry("conv_backward"), g, stream)
         return dx, dweight, dbias, dstate, None, None
 
 
@@ -213,7 +238,7 @@ def causal_conv_step(x, weight, state, bias=None, resets=None, activation: str =
         _apart_or_same("out_state", out_state, state)
     resets = _flags("resets", resets, (N,))
     stream = _here("causal_conv_step", x, weight, state, bias, resets, out_state)
-    y = torch.empty((N, D), dtype=x.dtype, device=x.device)
+    y = x.new_empty((N, D))
     new = torch.empty_like(state) if out_state is None else out_state
     _call(_lib().conv_step, N, D, W, dt, act, _ptr(x), x_row, _ptr(weight), _ptr(bias), _ptr(state), _ptr(resets),
           _ptr(y), D, _ptr(new), stream)
@@ -229,26 +254,28 @@ def _strides(t, lead):
     return s[:lead + 1] if t.dim() == lead + 2 else s[:lead] + (0,)
 
 
-def _scan_args(x, delta, rate, b, c, skip, gate, delta_bias, state, dones, softplus, y=None, new=None, kept=None):
+def _scan_args(x, delta, rate, b, c, skip, gate, delta_bias, state, dones, softplus, y, new, kept, ws, size):
     L, N, D = x.shape
-    y = x if y is None else y
     G = b.shape[2] if b.dim() == 4 else 1
-    return ScanArgs(L, N, D, rate.shape[1], G, _DTYPES[x.dtype], softplus, *x.stride()[:2], *delta.stride()[:2],
-                    *(gate.stride()[:2] if gate is not None else (0, 0)), *_strides(b, 2), *_strides(c, 2),
-                    *y.stride()[:2], _ptr(x), _ptr(delta), _ptr(gate), _ptr(b), _ptr(c), _ptr(rate), _ptr(skip),
-                    _ptr(delta_bias), _ptr(state), _ptr(dones), _ptr(y), _ptr(new), _ptr(kept), None, 0)
+    return _SCAN(L, N, D, rate.shape[1], G, _DTYPES[x.dtype], softplus, *x.stride()[:2], *delta.stride()[:2],
+                 *(gate.stride()[:2] if gate is not None else (0, 0)), *_strides(b, 2), *_strides(c, 2),
+                 *y.stride()[:2], x.data_ptr(), delta.data_ptr(), _at(gate), b.data_ptr(), c.data_ptr(),
+                 rate.data_ptr(), _at(skip), _at(delta_bias), _at(state), _at(dones), y.data_ptr(), _at(new),
+                 _at(kept), _at(ws), size)
+
+
+def _scan_sizes(x, rate, b):
+    return x.shape + (rate.shape[1], b.shape[2] if b.dim() == 4 else 1)
 
 
 def _scan_forward(x, delta, rate, b, c, skip, gate, delta_bias, state, dones, softplus, kept=None):
-    lib = _lib()
     stream = _here("selective_scan", x, delta, rate, b, c, skip, gate, delta_bias, state, dones)
     y = _like(x)
-    new = torch.empty((x.shape[1],) + rate.shape, dtype=_f32, device=x.device)
-    a = _scan_args(x, delta, rate, b, c, skip, gate, delta_bias, state, dones, softplus, y, new, kept)
-    size = lib.scan_workspace(a.steps, a.rows, a.width, a.states, a.groups)
+    new = rate.new_empty((x.shape[1],) + rate.shape)
+    size = _lib().scan_workspace(*_scan_sizes(x, rate, b))
     ws = _workspace(x, max(size, 0))
-    a.workspace, a.workspace_bytes = _ptr(ws), size
-    _call(lib.scan_forward, C.byref(a), stream)
+    _call(_entry("scan_forward"), _scan_args(x, delta, rate, b, c, skip, gate, delta_bias, state, dones, softplus, y,
+                                             new, kept, ws, size), stream)
     return y, new
 
 
@@ -256,9 +283,7 @@ class _SelectiveScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, delta, rate, b, c, skip, gate, delta_bias, state, dones, softplus):
         # the states that the gradient starts from, one of eight
-        L, N, D = x.shape
-        size = _lib().scan_kept(L, N, D, rate.shape[1], b.shape[2] if b.dim() == 4 else 1)
-        kept = torch.empty(max(size, 0), dtype=_f32, device=x.device)
+        kept = rate.new_empty(max(_lib().scan_kept(*_scan_sizes(x, rate, b)), 0))
         y, new = _scan_forward(x, delta, rate, b, c, skip, gate, delta_bias, state, dones, softplus, kept)
         ctx.save_for_backward(x, delta, rate, b, c, skip, gate, delta_bias, dones, kept)
         ctx.softplus = softplus
@@ -282,16 +307,15 @@ class _SelectiveScan(torch.autograd.Function):
         dbias = torch.empty_like(delta_bias) if delta_bias is not None and needs[7] else None
         dstate = None
         if ctx.has_state and needs[8]:
-            dstate = torch.empty((x.shape[1],) + rate.shape, dtype=_f32, device=x.device)
-        f = _scan_args(x, delta, rate, b, c, skip, gate, delta_bias, None, dones, ctx.softplus, kept=kept)
-        size = lib.scan_grad_workspace(f.steps, f.rows, f.width, f.states, f.groups)
+            dstate = rate.new_empty((x.shape[1],) + rate.shape)
+        size = lib.scan_grad_workspace(*_scan_sizes(x, rate, b))
         ws = _workspace(x, size)
-        f.workspace, f.workspace_bytes = _ptr(ws), size
-        g = ScanGradArgs(f, *dy.stride()[:2], *dx.stride()[:2], *ddelta.stride()[:2],
-                         *(dgate.stride()[:2] if dgate is not None else (0, 0)), *_strides(db, 2),
-                         *_strides(dc, 2), _ptr(dy), _ptr(dnew), _ptr(dx), _ptr(ddelta), _ptr(dgate), _ptr(db),
-                         _ptr(dc), _ptr(drate), _ptr(dskip), _ptr(dbias), _ptr(dstate))
-        _call(lib.scan_backward, C.byref(g), stream)
+        f = _scan_args(x, delta, rate, b, c, skip, gate, delta_bias, None, dones, ctx.softplus, x, None, kept, ws, size)
+        g = f + _SCAN_GRAD(*dy.stride()[:2], *dx.stride()[:2], *ddelta.stride()[:2],
+                           *(dgate.stride()[:2] if dgate is not None else (0, 0)), *_strides(db, 2),
+                           *_strides(dc, 2), dy.data_ptr(), _at(dnew), dx.data_ptr(), ddelta.data_ptr(), _at(dgate),
+                           db.data_ptr(), dc.data_ptr(), drate.data_ptr(), _at(dskip), _at(dbias), _at(dstate))
+        _call(_entry("scan_backward"), g, stream)
         return dx, ddelta, drate, db, dc, dskip, dgate, dbias, dstate, None, None
 
 
@@ -366,16 +390,16 @@ def selective_scan_step(x, delta, rate, b, c, state, skip=None, gate=None, delta
         _apart_or_same("out_state", out_state, state)
     resets = _flags("resets", resets, (N,))
     stream = _here("selective_scan_step", x, delta, rate, b, c, state, skip, gate, delta_bias, resets, out_state)
-    y = torch.empty((N, D), dtype=x.dtype, device=x.device)
+    y = x.new_empty((N, D))
     new = torch.empty_like(state) if out_state is None else out_state
     b_row, b_group = _strides(b, 1)
     c_row, c_group = _strides(c, 1)
-    a = ScanArgs(1, N, D, shape[2], b.shape[1] if b.dim() == 3 else 1, _DTYPES[x.dtype], int(bool(softplus)),
-                 0, x.stride(0), 0, delta.stride(0), 0, gate.stride(0) if gate is not None else 0,
-                 0, b_row, b_group, 0, c_row, c_group, 0, D, _ptr(x), _ptr(delta), _ptr(gate), _ptr(b), _ptr(c),
-                 _ptr(rate), _ptr(skip), _ptr(delta_bias), _ptr(state), _ptr(resets), _ptr(y), _ptr(new), None,
-                 None, 0)
-    _call(_lib().scan_step, C.byref(a), stream)
+    a = _SCAN(1, N, D, shape[2], b.shape[1] if b.dim() == 3 else 1, _DTYPES[x.dtype], bool(softplus),
+              0, x.stride(0), 0, delta.stride(0), 0, gate.stride(0) if gate is not None else 0,
+              0, b_row, b_group, 0, c_row, c_group, 0, D, x.data_ptr(), delta.data_ptr(), _at(gate), b.data_ptr(),
+              c.data_ptr(), rate.data_ptr(), _at(skip), _at(delta_bias), state.data_ptr(), _at(resets), y.data_ptr(),
+              new.data_ptr(), 0, 0, 0)
+    _call(_entry("scan_step"), a, stream)
     if out_state is not None:
         _written(out_state)
     return y, new
@@ -409,18 +433,17 @@ def _norm_args(residual, branch, weight, branch_weight, gate, seed_at, options):
     act, residual_scale, branch_scale, branch_norm, eps, drop, seed, offset = options
     D = residual.shape[-1]
     gate_row = 0 if gate is None or (gate.dim() == 1 and gate.dtype == _f32) else _row(gate)
-    return NormArgs(residual.numel() // D, D, _DTYPES[residual.dtype], branch_norm, act, residual_scale,
-                    branch_scale, eps, drop, seed, _ptr(seed_at), offset, 0, _ptr(residual), _row(residual),
-                    _ptr(branch), 0 if branch is None else _row(branch), _ptr(gate), gate_row, _ptr(weight),
-                    _ptr(branch_weight))
+    return _NORM(residual.numel() // D, D, _DTYPES[residual.dtype], branch_norm, act, residual_scale, branch_scale,
+                 eps, drop, seed, _at(seed_at), offset, 0, residual.data_ptr(), _row(residual), _at(branch),
+                 0 if branch is None else _row(branch), _at(gate), gate_row, _at(weight), _at(branch_weight))
 
 
 def _norm_forward(residual, branch, weight, branch_weight, gate, seed_at, options, stats=None):
     where = _here("residual_norm", residual, branch, weight, branch_weight, gate, seed_at)
-    stream, normed = (torch.empty(residual.shape, dtype=residual.dtype, device=residual.device) for _ in range(2))
+    stream, normed = residual.new_empty(residual.shape), residual.new_empty(residual.shape)
     D = residual.shape[-1]
     a = _norm_args(residual, branch, weight, branch_weight, gate, seed_at, options)
-    _call(_lib().norm_forward, C.byref(a), _ptr(stream), D, _ptr(normed), D, _ptr(stats), where)
+    _call(_entry("norm_forward"), a, stream.data_ptr(), D, normed.data_ptr(), D, _ptr(stats), where)
     return stream, normed
 
 
@@ -443,18 +466,18 @@ class _ResidualNorm(torch.autograd.Function):
         lib, where = _lib(), _there(residual)
         dstream, dnormed = (None if t is None else t.contiguous() for t in (dstream, dnormed))
         f = _norm_args(residual, branch, weight, branch_weight, gate, seed_at, ctx.options)
-        D, needs = f.width, ctx.needs_input_grad
+        D, needs = residual.shape[-1], ctx.needs_input_grad
 
         def like(t, i):
-            return torch.empty(t.shape, dtype=t.dtype, device=t.device) if t is not None and needs[i] else None
+            return t.new_empty(t.shape) if t is not None and needs[i] else None
 
         dresidual, dbranch, dweight, dbranch_weight, dgate = (
             like(t, i) for i, t in enumerate((residual, branch, weight, branch_weight, gate)))
-        size = lib.norm_workspace(f.rows, D, f.dtype)
+        size = lib.norm_workspace(stats.shape[0], D, _DTYPES[residual.dtype])
         ws = _workspace(residual, size)
-        g = NormGradArgs(f, _ptr(stats), _ptr(dstream), D, _ptr(dnormed), D, _ptr(dresidual), _ptr(dbranch),
-                         _ptr(dgate), _ptr(dweight), _ptr(dbranch_weight), _ptr(ws), size)
-        _call(lib.norm_backward, C.byref(g), where)
+        g = f + _NORM_GRAD(stats.data_ptr(), _at(dstream), D, _at(dnormed), D, _at(dresidual), _at(dbranch),
+                           _at(dgate), _at(dweight), _at(dbranch_weight), _at(ws), size)
+        _call(_entry("norm_backward"), g, where)
         return dresidual, dbranch, dweight, dbranch_weight, dgate, None, None
 
 

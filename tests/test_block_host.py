@@ -48,6 +48,18 @@ def test_struct_sizes(block):
     assert C.sizeof(block.NormGradArgs) == C.sizeof(block.NormArgs) + 8 * 12
 
 
+def test_packed_structs_are_the_ctypes_ones(block):
+    """A struct packed from distinct numbers has them in the fields' places."""
+    for kind, pack, base in ((block.ConvArgs, block._CONV, None), (block.ConvGradArgs, block._CONV_GRAD, block.ConvArgs),
+                             (block.ScanArgs, block._SCAN, None), (block.ScanGradArgs, block._SCAN_GRAD, block.ScanArgs),
+                             (block.NormArgs, block._NORM, None), (block.NormGradArgs, block._NORM_GRAD, block.NormArgs)):
+        names = [n for n, _ in kind._fields_ if n != "f"]
+        raw = bytes(C.sizeof(base) if base else 0) + pack(*range(1, len(names) + 1))
+        assert len(raw) == C.sizeof(kind)
+        got = kind.from_buffer_copy(raw)
+        assert [getattr(got, n) for n in names] == list(range(1, len(names) + 1))
+
+
 # ------------------------------------------------------------ the C refusals
 def conv_args(block, **kw):
     a = block.ConvArgs(steps=4, rows=2, width=3, taps=4, dtype=0, activation=2, x_step=6, x_row=3, y_step=6, y_row=3,
