@@ -14,6 +14,7 @@ policy.py.
 from __future__ import annotations
 
 import ctypes as C
+import math
 import struct
 
 import torch
@@ -418,10 +419,11 @@ def _seed(name, seed, offset):
 
 
 def _probability(name, p):
+    """p to the multiple of 2^-16 that the kernels use (exact in their fp32)."""
     p = float(p)
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"{name} must be 0 to 1, got {p}")
-    return p
+    return math.floor(p * 65536 + 0.5) / 65536
 
 
 def _row(t):

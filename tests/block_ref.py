@@ -307,7 +307,7 @@ def philox(counter, key):
 
 def kept(count, p, seed, offset=0, start=0):
     """Whether the elements start .. start + count - 1 are kept, and the scale."""
-    drop = int(np.floor(65536 * float(np.float32(p)) + 0.5))
+    drop = int(np.floor(65536 * p + 0.5))
     seed &= (1 << 64) - 1
     res = np.zeros(count, bool)
     block = None

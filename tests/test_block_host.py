@@ -389,6 +389,14 @@ def test_a_seed_that_changed_before_the_gradient_is_refused(silent):
         torch.autograd.grad(y, x, torch.ones(4))
 
 
+def test_probabilities_become_multiples_that_fp32_holds(block):
+    # 65536 p + 1/2 is just below 6555; of the p rounded to fp32 it is 6555
+    p = (6554.5 - 1e-4) / 65536
+    assert np.floor(np.float64(np.float32(p)) * 65536 + 0.5) == 6555
+    assert block._probability("p", p) == 6554 / 65536 == float(np.float32(6554 / 65536))
+    assert [block._probability("p", v) for v in (0, 1, 1e-9)] == [0, 1, 0]
+
+
 # ------------------------------------------------------- the reference itself
 def slope(f, x, at, h=1e-6):
     lo, hi = x.copy(), x.copy()
