@@ -416,10 +416,10 @@ struct StepRun {
 template <class T, int V, int W>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(const StepRun q) {
   using raw = typename T::raw;
-  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t n = id / q.packs;
+  const uint32_t id = blockIdx.x * kThreads + threadIdx.x;  // (below 2^29)
+  const int64_t n = id / (uint32_t)q.packs;
   if (n >= q.N) return;
-  const int32_t d0 = (int32_t)(id % q.packs) * V;
+  const int32_t d0 = (int32_t)(id % (uint32_t)q.packs) * V;
   const bool reset = q.resets && q.resets[n] != 0;
   const raw* px = static_cast<const raw*>(q.x) + n * q.x_row + d0;
   const raw* ps = static_cast<const raw*>(q.state) + n * (W - 1) * q.D + d0;

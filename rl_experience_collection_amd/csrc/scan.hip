@@ -164,45 +164,65 @@ __global__ void __launch_bounds__(64 * NB) scan_forward_kernel(const ScanRun q) 
   }
 }
 
-// One step: a lane takes four states of a channel, `lanes` (a power of two)
-// lanes a channel.  State in, state out, nothing else of size: what it costs
-// is a launch.
+// One step: a lane takes four states of a channel, 2^`shift` lanes a channel.
+// State in, state out, nothing else of size: what it costs is a launch and the
+// way of one load after another, which is why there is one division and no
+// branch before the loads are out.
 template <class T>
-__global__ void __launch_bounds__(256) scan_step_kernel(const scan_args a, int32_t lanes) {
+__global__ void __launch_bounds__(256) scan_step_kernel(const scan_args a, int32_t shift) {
   using raw = typename T::raw;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t column = id / lanes;
-  if (column >= (int64_t)a.rows * a.width) return;  // (all of a column's lanes together)
-  const int32_t s0 = 4 * (int32_t)(id % lanes), S = a.states;
-  const int32_t n = (int32_t)(column / a.width), d = (int32_t)(column % a.width);
-  const int32_t g = d / (a.width / a.groups);
-  const float x = T::widen((static_cast<const raw*>(a.x) + n * a.x_row)[d]);
-  const float v = T::widen((static_cast<const raw*>(a.delta) + n * a.delta_row)[d]) +
-                  (a.delta_bias ? a.delta_bias[d] : 0.0f);
-  float E;
-  const float dt = a.softplus ? softplus_of(v, E) : v;
-  float y = 0.0f;
-  if (s0 < S) {
-    float h[4], rate[4];
-    load_states(a.state + column * S, s0, S, h);
-    load_states(a.rate + (int64_t)d * S, s0, S, rate);
-    const raw* b = static_cast<const raw*>(a.b) + n * a.b_row + g * a.b_group;
-    const raw* c = static_cast<const raw*>(a.c) + n * a.c_row + g * a.c_group;
-    const bool cut = a.dones && a.dones[n] != 0;
+  const uint32_t id = blockIdx.x * 256 + threadIdx.x;  // (below 2^31)
+  const uint32_t column = id >> shift;
+  if (column >= (uint32_t)(a.rows * a.width)) return;  // (all of a column's lanes together)
+  const int32_t s0 = 4 * (int32_t)(id & ((1u << shift) - 1)), S = a.states;
+  const int32_t n = (int32_t)(column / (uint32_t)a.width), d = (int32_t)column - n * a.width;
+  const int32_t g = a.groups == 1 ? 0 : d / (a.width / a.groups);
+  const raw* b = static_cast<const raw*>(a.b) + n * a.b_row + g * a.b_group;
+  const raw* c = static_cast<const raw*>(a.c) + n * a.c_row + g * a.c_group;
+  const float* state = a.state + (int64_t)column * S;
+  const float* rates = a.rate + (int64_t)d * S;
+  float h[4], rate[4];
+  Pack<T, 4> bs, cs;
+  if (S % 4 == 0) {
+    // (lanes past the last state load it again and use nothing)
+    const int32_t at = min(s0, S - 4);
+    widen_pack<F32, 4>(load_pack<F32, 4>(reinterpret_cast<const uint32_t*>(state + at)), h);
+    widen_pack<F32, 4>(load_pack<F32, 4>(reinterpret_cast<const uint32_t*>(rates + at)), rate);
+    bs = load_pack<T, 4>(b + at);
+    cs = load_pack<T, 4>(c + at);
+  } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (s0 + i >= S) continue;
-      const float decay = __builtin_amdgcn_exp2f(dt * (rate[i] * kLog2e));
-      h[i] = __builtin_fmaf(decay, cut ? 0.0f : h[i], (dt * x) * T::widen(b[s0 + i]));
-      y = __builtin_fmaf(T::widen(c[s0 + i]), h[i], y);
+      const int32_t at = min(s0 + i, S - 1);
+      h[i] = state[at];
+      rate[i] = rates[at];
+      bs.v[i] = b[at];
+      cs.v[i] = c[at];
     }
-    store_states(a.new_state + column * S, s0, S, h);
   }
-  for (int32_t i = 1; i < lanes; i <<= 1) y += __shfl_xor(y, i);
+  const raw xr = (static_cast<const raw*>(a.x) + n * a.x_row)[d];
+  const raw dr = (static_cast<const raw*>(a.delta) + n * a.delta_row)[d];
+  const raw zr = a.gate ? (static_cast<const raw*>(a.gate) + n * a.gate_row)[d] : raw(0);
+  const float bias = a.delta_bias ? a.delta_bias[d] : 0.0f;
+  const float skip = a.skip ? a.skip[d] : 0.0f;
+  const bool cut = a.dones && a.dones[n] != 0;
+  const float x = T::widen(xr), v = T::widen(dr) + bias;
+  float E;
+  const float sp = softplus_of(v, E);
+  const float dt = a.softplus ? sp : v;
+  float y = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float decay = __builtin_amdgcn_exp2f(dt * (rate[i] * kLog2e));
+    h[i] = __builtin_fmaf(decay, cut ? 0.0f : h[i], (dt * x) * T::widen(bs.v[i]));
+    y = s0 + i < S ? __builtin_fmaf(T::widen(cs.v[i]), h[i], y) : y;
+  }
+  if (s0 < S) store_states(a.new_state + (int64_t)column * S, s0, S, h);
+  for (int32_t i = 1; i < 1 << shift; i <<= 1) y += __shfl_xor(y, i);
   if (s0 != 0) return;
-  y = __builtin_fmaf(a.skip ? a.skip[d] : 0.0f, x, y);
+  y = __builtin_fmaf(skip, x, y);
   if (a.gate) {
-    const float z = T::widen((static_cast<const raw*>(a.gate) + n * a.gate_row)[d]);
+    const float z = T::widen(zr);
     y *= z * sigmoid_of(z);
   }
   (static_cast<raw*>(a.y) + n * a.y_row)[d] = T::narrow(y);
@@ -297,16 +317,16 @@ hipError_t scan_forward_launch(const scan_args& a, hipStream_t stream) {
 }
 
 hipError_t scan_step_launch(const scan_args& a, hipStream_t stream) {
-  int32_t lanes = 1;
-  while (4 * lanes < a.states) lanes *= 2;
-  const int64_t threads = (int64_t)a.rows * a.width * lanes;
+  int32_t shift = 0;
+  while ((4 << shift) < a.states) ++shift;
+  const int64_t threads = (int64_t)a.rows * a.width << shift;
   const dim3 grid((uint32_t)((threads + 255) / 256));
   if (a.dtype == POLICY_F32)
-    scan_step_kernel<F32><<<grid, 256, 0, stream>>>(a, lanes);
+    scan_step_kernel<F32><<<grid, 256, 0, stream>>>(a, shift);
   else if (a.dtype == POLICY_BF16)
-    scan_step_kernel<BF16><<<grid, 256, 0, stream>>>(a, lanes);
+    scan_step_kernel<BF16><<<grid, 256, 0, stream>>>(a, shift);
   else
-    scan_step_kernel<F16><<<grid, 256, 0, stream>>>(a, lanes);
+    scan_step_kernel<F16><<<grid, 256, 0, stream>>>(a, shift);
   return hipGetLastError();
 }
 
