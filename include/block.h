@@ -98,7 +98,9 @@ int conv_step(int32_t rows, int32_t width, int32_t taps, int32_t dtype, int32_t 
  *   new_state = 0 where dones[L-1][n] is not 0, else h_{L-1}  (f32, unrounded).
  * m selects: a NaN or infinity of a finished episode does not reach the next
  * one.  Decays are meant to be at most 1 (rate <= 0 with softplus); of larger
- * ones, products over up to L steps must stay in fp32's range.
+ * ones, products over up to L steps must stay in fp32's range.  Where an input
+ * is infinite, outputs that it reaches are infinite or NaN, not always the one
+ * that the formula gives.
  *
  * x, delta, gate, y and their gradients are [L][N][D], element (t, n, d) at
  * t * step + n * row + d; b and c [L][N][G][S], element at t * step + n * row

@@ -184,6 +184,15 @@ struct UnitInputs {
   }
 };
 
+// p + n.  (The empty statement keeps the compiler from making one pointer
+// of a loop's chain into one for each step, which no scalar registers are left for.)
+template <class P>
+__device__ __forceinline__ P walk(P p, int64_t n) {
+  p += n;
+  asm("" : "+s"(p));
+  return p;
+}
+
 // A lane's own channel in one of the [L][N][D] arrays.
 template <class T>
 struct Column {
@@ -204,6 +213,15 @@ struct Column {
     const char* p = unit(t0);
 #pragma unroll
     for (int i = 0; i < kUnit; ++i, p += step) x[i] = row_load<T>(p, t0 + i < steps ? bytes : 0, at);
+  }
+  // The same from the unit's last step, at `p`, to its first; p is left at the
+  // unit before, whose steps may not exist.
+  __device__ __forceinline__ void load_back(const char*& p, int32_t t0, typename T::raw (&x)[kUnit]) const {
+#pragma unroll
+    for (int i = kUnit - 1; i >= 0; --i) {
+      x[i] = row_load<T>(p, (uint32_t)(t0 + i) < (uint32_t)steps ? bytes : 0, at);
+      p = walk(p, -step);
+    }
   }
   // Step t = t0 + i of the unit at `p`.
   __device__ __forceinline__ void store(char* p, int i, int32_t t, float x) const {
@@ -229,8 +247,9 @@ struct Kept {
     // (states past the last run: an offset past the end)
     at = k.s0 < wide ? ((k.lane >> 2) * 4 * wide + k.s0) * 4 : 1u << 31;
   }
-  __device__ __forceinline__ void load(int32_t u, float (&h)[4][4]) const {
-    const auto rsrc = row_of(base + u * unit, bytes);
+  // Of the unit at `p`, which may not exist.
+  __device__ __forceinline__ void load(const float* p, bool exists, float (&h)[4][4]) const {
+    const auto rsrc = row_of(p, exists ? bytes : 0);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const words4 x = __builtin_amdgcn_raw_buffer_load_b128(rsrc, at + r * place, 0, 0);

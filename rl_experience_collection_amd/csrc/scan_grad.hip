@@ -130,18 +130,29 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
   const int64_t own_step = met_c ? g.dc_step : g.db_step;
   raw* own = static_cast<raw*>(met_c ? g.dc : g.db) + k.n * (met_c ? g.dc_row : g.db_row) +
              k.g * (met_c ? g.dc_group : g.db_group) + met_state + (int64_t)(u1 * kUnit - 2 + met_odd) * own_step;
+  // (the last pair of the last unit may lie behind the others: a row of no length)
+  float* shared = q.shared + ((((int64_t)k.block * q.pairs + u1 * (kUnit / 2) - 1) * a.rows + k.n) * a.groups + k.g) *
+                                 NB * 64 + k.w * 64;
   UnitInputs<T> in;
   UnitDones dones;
   raw rx[kUnit], rd[kUnit], rz[kUnit], ry[kUnit];
   float kept[4][4];
-  const auto fetch = [&](int32_t u) {
+  // (pointers that walk with the steps: products of steps and strides would be
+  // held in more scalar registers than there are)
+  const char *px = cx.unit(u1 * kUnit - 1), *pd = cd.unit(u1 * kUnit - 1), *pz = cz.unit(u1 * kUnit - 1),
+             *py = cy.unit(u1 * kUnit - 1);
+  char *ox = gx.unit(u1 * kUnit - 1), *od = gd.unit(u1 * kUnit - 1), *oz = gz.unit(u1 * kUnit - 1);
+  const float* ps = states.base + (int64_t)(u1 - 1) * states.unit;
+  const auto fetch = [&](int32_t unit) {
+    const int32_t u = max(unit, u0);
     in.load(a, k, u * kUnit);
-    cd.load(u * kUnit, rd);
-    cy.load(u * kUnit, ry);
-    if (GATED) cz.load(u * kUnit, rz);
+    cd.load_back(pd, unit * kUnit, rd);
+    cy.load_back(py, unit * kUnit, ry);
+    if (GATED) cz.load_back(pz, unit * kUnit, rz);
     if constexpr (!SUMMARY) {
-      cx.load(u * kUnit, rx);
-      states.load(u, kept);
+      cx.load_back(px, unit * kUnit, rx);
+      states.load(ps, unit >= u0, kept);
+      ps = walk(ps, -states.unit);
     }
     dones.load(a, k, u * kUnit);
   };
@@ -178,7 +189,7 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
     }
     const uint32_t cut = dones.cuts(a, k, t0);
     any_cut |= cut;
-    if (SUMMARY) fetch(max(u - 1, u0));
+    if (SUMMARY) fetch(u - 1);
 
     if constexpr (SUMMARY) {
 #pragma unroll
@@ -220,13 +231,17 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
       };
       float y[kUnit], p1[kUnit], p2[kUnit];
       // A lane's own channel of a step, when the sums over its states are known.
-      char *ox = gx.unit(t0), *od = gd.unit(t0), *oz = GATED ? gz.unit(t0) : nullptr;
+      const auto back = [&] {
+        ox = walk(ox, -gx.step);
+        od = walk(od, -gd.step);
+        oz = walk(oz, -gz.step);
+      };
       const auto finish = [&](int i) {
         const float dD = __builtin_fmaf(x[i], p1[i], p2[i] * kLn2);
         const float dd = dD * s_slope[k.w][i][k.lane];
-        gx.store(ox, i, t0 + i, __builtin_fmaf(dt[i], p1[i], skip * w[i]));
-        gd.store(od, i, t0 + i, dd);
-        if (GATED) gz.store(oz, i, t0 + i, f[i] * __builtin_fmaf(skip, x[i], y[i]));
+        gx.store(ox, 0, t0 + i, __builtin_fmaf(dt[i], p1[i], skip * w[i]));
+        gd.store(od, 0, t0 + i, dd);
+        if (GATED) gz.store(oz, 0, t0 + i, f[i] * __builtin_fmaf(skip, x[i], y[i]));
         dskip = __builtin_fmaf(w[i], x[i], dskip);
         dbias += dd;
       };
@@ -319,6 +334,7 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
         p2[i] = quad_sum(s2);
         if constexpr (NB == 1) {
           finish(i);
+          back();
         } else {
           s_sums[k.w][1][i][k.lane] = p1[i];
           s_sums[k.w][2][i][k.lane] = p2[i];
@@ -329,8 +345,8 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
         } else {
           const float sum = meet_pair(met, odd, k.lane);
           if (q.shared) {
-            const int64_t at = (((int64_t)k.block * q.pairs + ((t0 + i) >> 1)) * a.rows + k.n) * a.groups + k.g;
-            row_store<F32>(q.shared + (at * NB + k.w) * 64, t0 + i < L ? 256 : 0, met_at, sum);
+            row_store<F32>(shared, t0 + i < L ? 256 : 0, met_at, sum);
+            shared = walk(shared, -(int64_t)a.rows * a.groups * NB * 64);
           } else {
             if (t0 + i + ((k.lane >> 2) & 1) < L && met_state < S) *own = T::narrow(sum);
             own -= 2 * own_step;
@@ -341,12 +357,12 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
 #pragma unroll
           for (int s = 0; s < 4; ++s) v[r][s] = before[r][s];
         // (the registers of the held states are free from here on)
-        if (i == kHeld) fetch(max(u - 1, u0));
+        if (i == kHeld) fetch(u - 1);
       }
       if constexpr (NB > 1) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) {
+        for (int i = kUnit - 1; i >= 0; --i, back()) {
           if (i % NB != k.w) continue;
           y[i] = p1[i] = p2[i] = 0.0f;
 #pragma unroll
