@@ -3,7 +3,10 @@
 // Per state of a step the scan takes an exponent's product, an exp2 (a
 // quarter-rate instruction), the input's product and two multiply-adds: eight
 // issue slots, beside some sixty per channel and step for softplus, gate and
-// conversions.  At 16 states that, not memory, bounds it.
+// conversions.  At 16 states that, not memory, bounds it: 500 x 2048 x 128 bf16
+// with a gate takes 610 us (590 where no states are kept for the gradient, so
+// their gigabyte costs little), 3.5 TB/s.  Four waves a SIMD in place of three,
+// or exp2s in runs apart from the rest, gained nothing.
 #include "scan.hpp"
 
 namespace rl {
@@ -228,6 +231,39 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const scan_args a, int32
   (static_cast<raw*>(a.y) + n * a.y_row)[d] = T::narrow(y);
 }
 
+// A thread takes a state, and its summaries sixteen at a time.
+__global__ void __launch_bounds__(256) scan_join_kernel(const ScanSummary sum, int32_t chunks, int64_t states,
+                                                        int32_t D, int32_t S, const float* rates,
+                                                        const float* state, int32_t direction) {
+  constexpr int kAt = 16;
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= states) return;
+  const int64_t column = e / S, columns = states / S;  // column: n * D + d
+  const int32_t n = (int32_t)(column / D), N = (int32_t)(columns / D);
+  const float rate = rates[e % ((int64_t)D * S)] * kLog2e;
+  const int32_t first = direction > 0 ? 0 : chunks - 1, count = chunks - 1;
+  float h = state ? state[e] : 0.0f;
+  for (int32_t i0 = 0; i0 < count; i0 += kAt) {
+    float own[kAt], total[kAt];
+    int32_t cut[kAt];
+#pragma unroll
+    for (int m = 0; m < kAt; ++m) {
+      const int64_t chunk = first + direction * min(i0 + m, count - 1);
+      own[m] = sum.state[chunk * states + e];
+      total[m] = sum.total[chunk * columns + column];
+      cut[m] = sum.cut[chunk * N + n];
+    }
+#pragma unroll
+    for (int m = 0; m < kAt; ++m) {
+      if (i0 + m >= count) continue;
+      // (a state of 0 stays 0 under any decay)
+      const float left = h == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(total[m] * rate) * h;
+      h = cut[m] != 0 ? own[m] : left + own[m];
+      sum.state[(int64_t)(first + direction * (i0 + m)) * states + e] = h;
+    }
+  }
+}
+
 template <class T, int NB>
 void launch_forward(const ScanRun& q, hipStream_t stream) {
   const dim3 threads(64 * NB), groups((uint32_t)(q.p.columns * q.p.chunks));
@@ -235,6 +271,8 @@ void launch_forward(const ScanRun& q, hipStream_t stream) {
   if (q.p.chunks > 1)
     scan_forward_kernel<T, NB, false, true>
         <<<dim3((uint32_t)(q.p.columns * (q.p.chunks - 1))), threads, 0, stream>>>(q);
+  if (q.p.joined)
+    scan_join_launch(q.p, q.sum, q.a.rows, q.a.width, q.a.states, q.a.rate, q.a.state, 1, stream);
   if (q.a.gate)
     scan_forward_kernel<T, NB, true, false><<<groups, threads, 0, stream>>>(q);
   else
@@ -251,9 +289,12 @@ void launch_states(const ScanRun& q, hipStream_t stream) {
 }  // namespace
 
 // A chunk has four units at least, and chunks are made until two waves a SIMD
-// have work (1024 SIMDs; 16,385 x 2 x 1000 fp16 takes 327 us so, 334 to 369 with
-// three or four); a scan of more than a quarter of that many columns is not
-// cut, as the second look at its inputs would cost what the cut gains.
+// have work (1024 SIMDs; 16,385 x 2 x 1000 fp16 takes 319 us so, 347 and 388 with
+// three and four); a scan of more than a quarter of that many columns is not
+// cut, as the second look at its inputs would cost what the cut gains.  More
+// than 16 summaries are joined once for all chunks (that scan of 64 chunks takes
+// 301 us so and 319 where every chunk joins those before it; 32 chunks 280 and
+// 286; 16 chunks 278 and 277, 8 chunks of 64 steps 84 and 77).
 ScanPlan scan_plan(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G) {
   ScanPlan p;
   p.group_width = D / G;
@@ -270,6 +311,7 @@ ScanPlan scan_plan(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G) {
     p.chunks = cdiv(p.units, p.chunk_units);
   }
   if (p.chunks == 1) p.chunk_units = p.units;
+  p.joined = p.chunks > 16;
   return p;
 }
 
@@ -297,6 +339,13 @@ int64_t scan_kept_floats(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G) 
 int64_t scan_workspace_bytes(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G) {
   if (L == 0 || N == 0 || D == 0) return 0;
   return scan_summary_bytes(scan_plan(L, N, D, S, G), N, D, S);
+}
+
+void scan_join_launch(const ScanPlan& p, const ScanSummary& sum, int32_t N, int32_t D, int32_t S,
+                      const float* rate, const float* state, int32_t direction, hipStream_t stream) {
+  const int64_t states = (int64_t)N * D * S;
+  scan_join_kernel<<<dim3((uint32_t)((states + 255) / 256)), 256, 0, stream>>>(sum, p.chunks, states, D, S, rate,
+                                                                              state, direction);
 }
 
 hipError_t scan_forward_launch(const scan_args& a, hipStream_t stream) {

@@ -37,11 +37,12 @@ struct ScanPlan {
   int32_t chunks, chunk_units;
   int32_t state_blocks;  // ceil(S / 16)
   int64_t columns;       // N * G * blocks: workgroups of a chunk
+  bool joined;           // scan_join_launch() has joined the summaries
 };
 
 // Per chunk, for chunks > 1.
 struct ScanSummary {
-  float* state;  // [chunks][N][D][S]: what the chunk makes of a state of zero
+  float* state;  // [chunks][N][D][S]: what the chunk makes of a state of zero, or of what enters it
   float* total;  // [chunks][N][D]: the sum of D_t
   int32_t* cut;  // [chunks][N]: a done lies inside
 };
@@ -49,6 +50,10 @@ struct ScanSummary {
 ScanPlan scan_plan(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G);
 int64_t scan_summary_bytes(const ScanPlan& p, int32_t N, int32_t D, int32_t S);
 ScanSummary scan_summary(const ScanPlan& p, int32_t N, int32_t D, int32_t S, void* workspace);
+// Joins the summaries of all chunks but the last in the direction of the scan
+// (1, from `state`, which may be NULL) or of its gradient (-1, from zero).
+void scan_join_launch(const ScanPlan& p, const ScanSummary& sum, int32_t N, int32_t D, int32_t S,
+                      const float* rate, const float* state, int32_t direction, hipStream_t stream);
 
 // The value of lane j ^ R of this lane's quad.
 template <int R>
@@ -288,9 +293,18 @@ struct UnitDones {
 
 // h becomes what `count` chunks make of it one after another, from chunk
 // `first` on in the given direction; four summaries are loaded at a time.
+// Where they are joined, it is the last one's.
 __device__ __forceinline__ void join_chunks(const ScanPlan& p, const ScanSummary& sum, const ScanWave& k,
                                             int32_t N, int32_t D, int32_t S, int32_t first, int32_t direction,
                                             int32_t count, const float (&rate)[4][4], float (&h)[4][4]) {
+  if (p.joined) {
+    if (count == 0) return;
+    const int64_t chunk = first + direction * (count - 1);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      load_states(sum.state + ((chunk * N + k.n) * D + k.quad_channel(p, r)) * S, k.s0, S, h[r]);
+    return;
+  }
   constexpr int kAt = 4;
   for (int32_t i0 = 0; i0 < count; i0 += kAt) {
     float own[kAt][4][4], total[kAt][4];

@@ -11,7 +11,8 @@
 // again, the first four to LDS and the others in registers, and goes back over
 // them.  (Four in registers alone, formed twice, took half as many more states
 // to form; eight in registers leave a SIMD one wave.)  Decays are formed twice:
-// an exp2 costs less than the place to hold it.
+// an exp2 costs less than the place to hold it.  Some 360 instructions a step at
+// 16 states bound it: 500 x 2048 x 128 bf16 with a gate takes 1540 us, 2 TB/s.
 #include "scan.hpp"
 
 namespace rl {
@@ -452,6 +453,8 @@ void launch_backward(const GradRun& q, hipStream_t stream) {
   if (q.p.chunks > 1)
     scan_backward_kernel<T, NB, GATED, true>
         <<<dim3((uint32_t)(q.p.columns * (q.p.chunks - 1))), threads, 0, stream>>>(q);
+  if (q.p.joined)
+    scan_join_launch(q.p, q.sum, q.g.f.rows, q.g.f.width, q.g.f.states, q.g.f.rate, nullptr, -1, stream);
   scan_backward_kernel<T, NB, GATED, false>
       <<<dim3((uint32_t)(q.p.columns * q.p.chunks)), threads, 0, stream>>>(q);
   if (q.shared) {

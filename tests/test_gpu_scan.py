@@ -96,6 +96,13 @@ def test_chunks(rx, L, N, D, S, G, p_done, name):
     check(rx, *inputs(L, N, D, S, G, name, p_done, L + D, decay=0.1), name)
 
 
+# so many chunks that their summaries are joined by a kernel of their own
+@pytest.mark.parametrize("p_done", [0.0, 0.004])
+@pytest.mark.parametrize("L,N,D,S,G", [(545, 1, 64, 16, 0), (2049, 1, 70, 16, 2), (1500, 2, 7, 37, 0)])
+def test_more_chunks(rx, L, N, D, S, G, p_done):
+    check(rx, *inputs(L, N, D, S, G, "f32", p_done, L + D, decay=0.02), "f32")
+
+
 @pytest.mark.parametrize("name", ["f32", "f16"])
 def test_many_columns_are_not_cut(rx, name):
     check(rx, *inputs(40, 600, 6, 16, 0, name, 0.05, 3), name)
