@@ -8,6 +8,10 @@
 // inputs and the two stored factors (8 bytes a row), rather than from a
 // stream that was rounded when it was stored, and a thread sums the weights'
 // gradients of its own columns over all rows that it takes.
+//
+// HBM bounds them: 1,024,000 x 128 bf16 with gate and dropout takes 265 us
+// forward (4.9 TB/s) and 430 us backward (4.9 TB/s).  Where they fit the caches,
+// latency: 4099 x 5001 fp16 takes 33 and 71 us.
 #include <algorithm>
 
 #include "block.hpp"
@@ -201,8 +205,8 @@ __device__ __forceinline__ void activate(int32_t kind, float g, float& act, floa
 }
 
 // Waves a SIMD: 6, so that two rows of up to 768 threads share a compute unit
-// (4099 x 5001 fp16 takes 50 us so, 63 with the 5 that the compiler leaves room
-// for), where that leaves enough registers.
+// (4099 x 5001 fp16 took 50 us so, 63 with 5; that variant has come down to 6
+// without being told, many others have not), where that leaves enough registers.
 template <class T>
 constexpr int forward_waves(int TPR, int gate) {
   return TPR > 64 && !(T::kBytes == 4 && gate == kRowGate) ? 6 : 1;
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(threads_of(TPR), forward_waves<T>(TPR, GATE)) 
 
 // What a thread needs of its own columns at every row, in LDS: the registers
 // that it would take are worth more to the rows in flight (1,024,000 x 128
-// bf16 takes 443 us so, 459 with weights in registers).
+// bf16 took 443 us so, 459 with weights in registers).
 template <int K, int V, int THREADS>
 struct OwnColumns {
   static constexpr int kQuads = K * V / 4;

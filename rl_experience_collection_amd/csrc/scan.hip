@@ -289,7 +289,7 @@ void launch_states(const ScanRun& q, hipStream_t stream) {
 }  // namespace
 
 // A chunk has four units at least, and chunks are made until two waves a SIMD
-// have work (1024 SIMDs; 16,385 x 2 x 1000 fp16 takes 319 us so, 347 and 388 with
+// have work (1024 SIMDs; 16,385 x 2 x 1000 fp16 took 332 us so, 340 and 378 with
 // three and four); a scan of more than a quarter of that many columns is not
 // cut, as the second look at its inputs would cost what the cut gains.  More
 // than 16 summaries are joined once for all chunks (that scan of 64 chunks takes
