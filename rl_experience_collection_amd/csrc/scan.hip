@@ -43,8 +43,10 @@ __global__ void __launch_bounds__(64 * NB) scan_forward_kernel(const ScanRun q) 
   }
   if constexpr (!SUMMARY) {
     join_chunks(q.p, q.sum, k, a.rows, a.width, S, 0, 1, k.chunk, rate, h);
+    clear_missing(q.p, k, h);
   }
-  const float bias = a.delta_bias ? a.delta_bias[k.channel] : 0.0f;
+  clear_missing(q.p, k, rate);
+  const float bias = a.delta_bias && k.mine ? a.delta_bias[k.channel] : 0.0f;
   const float skip = a.skip ? a.skip[k.channel] : 0.0f;
   float total = 0.0f;
   uint32_t any_cut = 0;

@@ -140,6 +140,19 @@ struct ScanWave {
   }
 };
 
+// Rates and states of channels that the group does not have, which loads
+// take from its last one, become 0: with an input of 0 (what a row's loads
+// give past its end) and no bias their states stay 0 under a decay of 1, whatever
+// the last channel's are, and add nothing to the sums over channels.
+__device__ __forceinline__ void clear_missing(const ScanPlan& p, const ScanWave& k, float (&v)[4][4]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const bool has = k.quad_has(p, r);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) v[r][s] = has ? v[r][s] : 0.0f;
+  }
+}
+
 // The four states from s0 of a row of S; those that do not exist are 0.
 __device__ __forceinline__ void load_states(const float* row, int32_t s0, int32_t S, float (&h)[4]) {
   if (s0 + 4 <= S) {

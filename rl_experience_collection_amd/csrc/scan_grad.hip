@@ -111,7 +111,9 @@ __global__ void __launch_bounds__(64 * NB, NB == 1 ? 2 : 1) scan_backward_kernel
       join_chunks(q.p, q.sum, k, a.rows, a.width, S, q.p.chunks - 1, -1, q.p.chunks - 1 - k.chunk, rate, G);
     }
   }
-  const float bias = a.delta_bias ? a.delta_bias[k.channel] : 0.0f;
+  clear_missing(q.p, k, rate);
+  clear_missing(q.p, k, G);
+  const float bias = a.delta_bias && k.mine ? a.delta_bias[k.channel] : 0.0f;
   const float skip = a.skip ? a.skip[k.channel] : 0.0f;
   float total = 0.0f, dskip = 0.0f, dbias = 0.0f;
   uint32_t any_cut = 0;

@@ -309,3 +309,18 @@ def test_captured_and_replayed(rx, L):
         torch.cuda.synchronize()
         for a, b in zip(out, want):
             assert torch.equal(a, b), turn
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("L,N,D,S,G", [(30, 2, 5, 16, 0), (30, 2, 65, 16, 1), (30, 2, 10, 20, 2), (300, 2, 5, 16, 0),
+                                       (300, 1, 65, 16, 1), (300, 2, 15, 40, 3), (1100, 1, 6, 16, 0)])
+def test_channels_past_a_group_add_nothing(rx, L, N, D, S, G, name):
+    """Step sizes are positive, the bias alone is not: a lane without a channel
+    that took the bias for its step size would grow by exp(4) to exp(8) a step
+    from the state that it was given."""
+    i, g = inputs(L, N, D, S, G, name, 0.0, L + D)
+    u = torch.Generator().manual_seed(D)
+    i["delta"] = (0.59 + 0.02 * torch.rand(L, N, D, generator=u)).to(TYPES[name])
+    i["delta_bias"] = torch.full((D,), -0.5)
+    i["rate"] = -8 - 8 * torch.rand(D, S, generator=u)
+    check(rx, i, g, name, soft=False)
