@@ -273,10 +273,7 @@ __global__ void __launch_bounds__(threads_of(TPR), forward_waves<T>(TPR, GATE)) 
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         s[i][v] *= a.residual_scale;
-        if (!branch) {
-      no_stores(q.dresidual, K * (GATE == kRowGate ? 2 : 1));
-      continue;
-    }
+        if (!branch) continue;
         float z = b[i][v] * inv_b * bw[i][v];
         if (GATE == kChannelGate) z *= gc[i][v];
         if (GATE == kRowGate) {
@@ -546,19 +543,23 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const No
 int32_t threads_for(int32_t D) {
   return D <= 64 ? 8 : D <= 128 ? 16 : D <= 512 ? 64 : (D + 511) / 512 * 64;
 }
-// Workgroups: what is resident on 256 compute units (20 waves each going
-// forward, 12 backward), so that a workgroup reads its weights and writes
-// their gradients once for many rows.
-uint32_t groups_of(int64_t R, int32_t D, bool grad) {
+// Waves of a compute unit: 20 going forward, 16 where there is no branch, whose
+// work would hide the loads of more (419 MB a tensor of bf16: 289 us at width 300
+// and 298 at 600 so, 333 and 332 with 20; 233 either way at 8000), 12 backward.
+constexpr int32_t kGradWaves = 12;
+int32_t waves_of(const norm_args& a, bool grad) { return grad ? kGradWaves : a.branch ? 20 : 16; }
+// Workgroups: what is resident on 256 compute units, so that a workgroup reads
+// its weights and writes their gradients once for many rows.
+uint32_t groups_of(int64_t R, int32_t D, int32_t waves) {
   const int32_t threads = threads_for(D), rows = threads <= 64 ? 256 / threads : 1;
-  const int64_t most = 256 * std::max(1, (grad ? 12 : 20) * 64 / (threads <= 64 ? 256 : threads));
+  const int64_t most = 256 * std::max(1, waves * 64 / (threads <= 64 ? 256 : threads));
   return (uint32_t)std::min((R + rows - 1) / rows, most);
 }
 
 template <class T, int V, int TPR, int K, int GATE, bool GRAD>
 void launch(const NormRun& q, hipStream_t stream) {
   const int32_t D = q.g.f.width;
-  const dim3 grid(groups_of(q.g.f.rows, D, GRAD)), threads(TPR <= 64 ? 256 : threads_for(D));
+  const dim3 grid(groups_of(q.g.f.rows, D, waves_of(q.g.f, GRAD))), threads(TPR <= 64 ? 256 : threads_for(D));
   if constexpr (GRAD)
     q.past ? norm_backward_kernel<T, V, TPR, K, GATE, true><<<grid, threads, 0, stream>>>(q)
            : norm_backward_kernel<T, V, TPR, K, GATE, false><<<grid, threads, 0, stream>>>(q);
@@ -623,7 +624,7 @@ hipError_t norm_forward_launch(const norm_args& a, void* stream_out, int64_t str
 
 int64_t norm_workspace_bytes(int64_t R, int32_t D, int32_t dtype) {
   if (R == 0) return 0;
-  const int64_t groups = groups_of(R, D, true);
+  const int64_t groups = groups_of(R, D, kGradWaves);
   return up(groups * 3 * D * 4) + up(sums_floats(groups, 3 * D) * 4) + up(D * 4);
 }
 
@@ -653,7 +654,7 @@ hipError_t norm_backward_launch(const norm_grad_args& g, hipStream_t stream) {
   launch_any<true>(q, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !(g.dweight || g.dbranch_weight || (channel && g.dgate))) return e;
-  const int64_t groups = groups_of(a.rows, a.width, true);
+  const int64_t groups = groups_of(a.rows, a.width, kGradWaves);
   const int32_t d = a.width, columns = (channel ? 3 : 2) * d;
   const SumsOut out = {{g.dweight, g.dbranch_weight, channel ? static_cast<float*>(g.dgate) : nullptr},
                        {d, 2 * d, columns}};
