@@ -167,7 +167,9 @@ int scan_step(const scan_args *args, void *hip_stream);
  *   stream = residual_scale residual + branch_scale z
  *   normed = rms(stream) weight
  * evaluated in fp32 from end to end.  Without a branch the stream is
- * residual_scale residual.  Weights are [D] f32 (NULL: 1).  The gate is [R][D]
+ * residual_scale residual.  What the gate, and a branch that is not normed,
+ * hold at a dropped place does not matter, nor what the gradient of the stream
+ * holds there to theirs.  Weights are [D] f32 (NULL: 1).  The gate is [R][D]
  * of the rows' dtype (gate_row > 0), or one row [D] f32 for all (gate_row =
  * 0).  Rows are *_row elements apart, at least D. */
 typedef struct {

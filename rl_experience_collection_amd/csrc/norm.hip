@@ -463,10 +463,27 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const No
       s_bw.get(i, bw);
       if constexpr (GATE == kChannelGate) s_act.get(i, act);
 #pragma unroll
+      for (int v = 0; v < V; ++v) d[i][v] *= a.branch_scale;
+      if (drops) {
+        // What a dropped place holds does not matter: its factors become 0 with
+        // its gradient.  (The normed branch is a factor of the whole row.)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const bool keep = (kept[i] >> v) & 1u;
+          d[i][v] = keep ? d[i][v] * q.rule.scale : 0.0f;
+          bw[v] = keep ? bw[v] : 0.0f;
+          if (GATE == kRowGate) g[i][v] = keep ? g[i][v] : 0.0f;
+          if (GATE == kChannelGate) act[v] = keep ? act[v] : 0.0f;
+        }
+        if (GATE != kNoGate && !a.branch_norm) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) u[i][v] = (kept[i] >> v) & 1u ? u[i][v] : 0.0f;
+        }
+      }
+#pragma unroll
       for (int v = 0; v < V; ++v) {
-        float dz = a.branch_scale * d[i][v], slope;
-        if (drops) dz = (kept[i] >> v) & 1u ? dz * q.rule.scale : 0.0f;
-        const float dact = dz * (u[i][v] * bw[v]);
+        const float dz = d[i][v], dact = dz * (u[i][v] * bw[v]);
+        float slope;
         if (GATE == kRowGate) {
           asm("" : "+v"(g[i][v]));
           activate(a.activation, g[i][v], act[v], slope);
@@ -505,7 +522,8 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const No
       for (int v = 0; v < V; ++v) {
         float act, slope;
         activate(a.activation, gate[i][v], act, slope);
-        dgc[i][v] *= slope;
+        // (of a channel that was dropped in every row the slope does not matter either)
+        dgc[i][v] = drops && dgc[i][v] == 0.0f ? 0.0f : dgc[i][v] * slope;
       }
   }
   // the workgroup's sums over its rows, pack by pack

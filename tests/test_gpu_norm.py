@@ -224,3 +224,48 @@ def test_dropout_captured_and_replayed(rx):
         assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
         assert before is None or not torch.equal(before, out[0])
         before = out[0].clone()
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["none", "sigmoid", "silu"])
+@pytest.mark.parametrize("R,D", [(6, 40), (5, 3), (4, 600)])
+def test_gradients_of_dropped_places_hold_anything(rx, R, D, act, name):
+    """NaN and infinities of the gate, the branch (not normed) and the stream's
+    gradient at dropped places: the gradients are those without them."""
+    i, g = inputs(R, D, name, "full", 10)
+    kept, _ = ref.kept(R * D, 0.4, 5)
+    off = torch.from_numpy(~kept.reshape(R, D))
+    nan, inf = torch.tensor(float("nan"), dtype=TYPES[name]), torch.tensor(-float("inf"), dtype=TYPES[name])
+    i["branch_weight"] = None
+
+    def run(i, g, branch_norm):
+        dev = {k: v.cuda() for k, v in dict(i, **g).items() if v is not None}
+        leaves = {k: dev[k].requires_grad_() for k in LEAVES if k in dev}
+        out = rx.residual_norm(**leaves, activation=act, dropout=0.4, seed=5, branch_norm=branch_norm)
+        return dict(zip(leaves, torch.autograd.grad(out, list(leaves.values()), (dev["dstream"], dev["dnormed"]))))
+
+    for branch_norm in (True, False):
+        clean = run(i, g, branch_norm)
+        for bad in (nan, inf):
+            got = run(dict(i, gate=torch.where(off, bad, i["gate"])), g, branch_norm)
+            assert all(torch.equal(got[k], clean[k]) for k in clean)
+            got = run(i, dict(g, dstream=torch.where(off, bad, g["dstream"])), branch_norm)
+            assert all(torch.equal(got[k], clean[k]) for k in clean if k != "residual")
+            if not branch_norm:
+                got = run(dict(i, branch=torch.where(off, bad, i["branch"])), g, branch_norm)
+                assert all(torch.equal(got[k], clean[k]) for k in clean)
+
+
+@pytest.mark.parametrize("act", ["none", "sigmoid", "silu"])
+@pytest.mark.parametrize("D", [40, 600])
+def test_gradients_where_all_is_dropped(rx, D, act):
+    """Weights and a channel gate that are no numbers meet no element."""
+    i, g = inputs(5, D, "f32", "channel", 12)
+    i["gate"][::3], i["gate"][1::3] = float("nan"), float("inf")
+    i["branch_weight"][::2] = float("nan")
+    dev = {k: v.cuda() for k, v in dict(i, **g).items()}
+    leaves = {k: dev[k].requires_grad_() for k in LEAVES}
+    out = rx.residual_norm(**leaves, activation=act, dropout=1.0, seed=5)
+    got = dict(zip(LEAVES, torch.autograd.grad(out, list(leaves.values()), (dev["dstream"], dev["dnormed"]))))
+    assert not got["branch"].any() and not got["branch_weight"].any() and not got["gate"].any()
+    assert torch.isfinite(got["residual"]).all() and torch.isfinite(got["weight"]).all()
