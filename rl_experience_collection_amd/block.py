@@ -98,9 +98,10 @@ def _at(t):
 def _entry(name):
     fn = _packed.get(name)
     if fn is None:
-        declared = getattr(_lib(), name)
-        fn = _packed[name] = _lib()[name]
-        fn.argtypes, fn.restype = [C.c_char_p] + list(declared.argtypes[1:]), C.c_int
+        lib = _lib()
+        fn = lib[name]
+        fn.argtypes, fn.restype = [C.c_char_p] + list(getattr(lib, name).argtypes[1:]), C.c_int
+        _packed[name] = fn  # last: another thread may call what it finds here
     return fn
 
 

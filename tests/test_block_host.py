@@ -481,3 +481,28 @@ def test_reference_draws_are_philox():
     kept, scale = ref.kept(4000, 0.25, 5)
     # a binomial of 4000 draws: five standard deviations are 137
     assert abs(int(kept.sum()) - 3000) < 137 and scale == 4 / 3
+
+
+def test_an_entry_point_is_shared_with_its_argument_types(rx, block, monkeypatch):
+    """Another thread finds an entry point only when ctypes knows its arguments:
+    without their types it would cut addresses to 32 bits."""
+    seen = {}
+
+    class Entry:
+        argtypes = restype = None
+
+        def __setattr__(self, name, value):
+            assert "norm_forward" not in block._packed, name
+            super().__setattr__(name, value)
+
+    class Library:
+        norm_forward = rx.load_library().norm_forward
+
+        def __getitem__(self, name):
+            return seen.setdefault(name, Entry())
+
+    monkeypatch.setattr(block, "_packed", {})
+    monkeypatch.setattr(block, "_lib", Library)
+    fn = block._entry("norm_forward")
+    assert fn is seen["norm_forward"] is block._packed["norm_forward"] is block._entry("norm_forward")
+    assert fn.argtypes[1:] == list(rx.load_library().norm_forward.argtypes[1:]) and fn.restype is C.c_int
