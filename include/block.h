@@ -149,7 +149,7 @@ int64_t scan_grad_workspace(int32_t steps, int32_t rows, int32_t width, int32_t 
                             int32_t groups);
 /* L, N or D of 0 is a no-op, except that L = 0 copies state to new_state (and
  * dnew_state to dstate), and that parameter gradients without a summand are
- * cleared.  Errors as of conv_*. */
+ * cleared (with D of 0, db and dc are left as they are).  Errors as of conv_*. */
 int scan_forward(const scan_args *args, void *hip_stream);
 int scan_backward(const scan_grad_args *args, void *hip_stream);
 /* One step, for acting, with args->steps = 1: the step strides are not used,

@@ -303,6 +303,8 @@ class _SelectiveScan(torch.autograd.Function):
         if dnew is not None:
             dnew = dnew.contiguous()
         dx, ddelta, db, dc, drate = _like(x), _like(delta), _like(b), _like(c), torch.empty_like(rate)
+        if x.shape[2] == 0:  # sums over no channels, which the library does not write
+            db.zero_(), dc.zero_()
         dgate = _like(gate) if gate is not None else None
         needs = ctx.needs_input_grad
         dskip = torch.empty_like(skip) if skip is not None and needs[5] else None

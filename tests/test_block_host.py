@@ -506,3 +506,19 @@ def test_an_entry_point_is_shared_with_its_argument_types(rx, block, monkeypatch
     fn = block._entry("norm_forward")
     assert fn is seen["norm_forward"] is block._packed["norm_forward"] is block._entry("norm_forward")
     assert fn.argtypes[1:] == list(rx.load_library().norm_forward.argtypes[1:]) and fn.restype is C.c_int
+
+
+@pytest.mark.parametrize("groups", [(), (2,)])
+def test_scan_without_channels_has_gradients_of_zero(silent, groups):
+    """b and c meet no channel: torch's memory, filled with NaN here, is not
+    what they get."""
+    bc = [torch.ones(4, 2, *groups, 5, requires_grad=True) for _ in range(2)]
+    x = torch.ones(4, 2, 0)
+    y, new = silent.selective_scan(x, x, torch.ones(0, 5), *bc)
+    torch.use_deterministic_algorithms(True, warn_only=True)
+    try:
+        assert torch.isnan(torch.empty(8)).all()
+        grads = torch.autograd.grad((y, new), bc, (torch.ones_like(y), torch.ones_like(new)))
+    finally:
+        torch.use_deterministic_algorithms(False)
+    assert all(torch.equal(g, torch.zeros_like(t)) for g, t in zip(grads, bc))
