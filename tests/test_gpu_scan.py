@@ -324,3 +324,14 @@ def test_channels_past_a_group_add_nothing(rx, L, N, D, S, G, name):
     i["delta_bias"] = torch.full((D,), -0.5)
     i["rate"] = -8 - 8 * torch.rand(D, S, generator=u)
     check(rx, i, g, name, soft=False)
+
+
+@pytest.mark.parametrize("L,N,D,S", [(1, 4097, 3, 2), (2, 300001, 1, 1), (1, 1 << 20, 1, 1)])
+def test_sums_over_many_rows_have_short_chains(rx, L, N, D, S):
+    """Equal summands, whose roundings go one way: the parameters' gradients
+    stay within the bound, which has no term that grows with the rows."""
+    i, g = inputs(L, N, D, S, 0, "f32", 0.0, N)
+    for k, v in dict(x=1.1, delta=-0.7, b=0.9, c=0.7, gate=0.3, skip=1.3, delta_bias=0.1, state=1.1, rate=-0.7).items():
+        i[k].fill_(v)
+    g["dy"].fill_(1.1), g["dnew"].fill_(0.3)
+    check(rx, i, g, "f32")
