@@ -37,6 +37,7 @@ struct ConvRun {
   int32_t rows;      // (chunk, n) pairs of a workgroup
   int32_t chunk, chunks;
   int64_t items;     // chunks * N
+  uint32_t groups;   // workgroups that share a run of packs; the next run's follow them
   float* params;     // gradient: [workgroups][D (W + 1)]
 };
 
@@ -45,14 +46,18 @@ __device__ __forceinline__ float sigmoid_of(float v) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
 }
 
-// Which rows and channels a thread has.
+// Which rows and channels a thread has.  (One number for all workgroups: a wide
+// row has more runs of packs than a grid's second dimension holds.)
 struct ConvLane {
-  int32_t n, d0, fresh, t0, t1, row, pack;
+  int32_t n, d0, fresh, t0, t1, row, pack, first;  // first: the workgroup's first pack
+  uint32_t group;
   bool active;
   __device__ __forceinline__ ConvLane(const ConvRun& q, int V) {
+    group = blockIdx.x % q.groups;
+    first = (int32_t)(blockIdx.x / q.groups) * q.across;
     row = threadIdx.x / q.across;
-    pack = blockIdx.y * q.across + threadIdx.x % q.across;
-    const int64_t item = (int64_t)blockIdx.x * q.rows + row;
+    pack = first + threadIdx.x % q.across;
+    const int64_t item = (int64_t)group * q.rows + row;
     active = row < q.rows && item < q.items && pack < q.packs;
     const int32_t N = q.g.f.rows;
     n = active ? (int32_t)(item % N) : 0;
@@ -391,14 +396,14 @@ __global__ void __launch_bounds__(kThreads) conv_backward_kernel(const ConvRun q
     for (int v = 0; v < V; ++v) s_sum[threadIdx.x][v] = j < W ? dw[j < W ? j : 0][v] : db[v];
     __syncthreads();
     for (int32_t c = threadIdx.x; c < columns; c += kThreads) {
-      const int32_t pack = blockIdx.y * q.across + c / V;
+      const int32_t pack = k.first + c / V;
       if (pack >= q.packs) continue;
       const int32_t d0 = min(pack * V, a.width - V);
       if (c % V < pack * V - d0) continue;  // (counted in the pack before)
       float sum = 0.0f;
       for (int32_t r = 0; r < q.rows; ++r) sum += s_sum[r * q.across + c / V][c % V];
       const int64_t d = d0 + c % V;
-      q.params[(int64_t)blockIdx.x * a.width * (W + 1) + (j < W ? d * W + (W - 1 - j) : (int64_t)a.width * W + d)] =
+      q.params[(int64_t)k.group * a.width * (W + 1) + (j < W ? d * W + (W - 1 - j) : (int64_t)a.width * W + d)] =
           sum;
     }
   }
@@ -473,6 +478,7 @@ ConvRun plan(int32_t L, int32_t N, int32_t D, int32_t V, bool grad) {
   q.chunk = (L + chunks - 1) / chunks;
   q.chunks = (L + q.chunk - 1) / q.chunk;
   q.items = (int64_t)q.chunks * N;
+  q.groups = (uint32_t)((q.items + q.rows - 1) / q.rows);
   q.params = nullptr;
   return q;
 }
@@ -486,9 +492,8 @@ int32_t pack_of(int32_t D, int32_t W, int32_t dtype, bool grad) {
   const int32_t v = pack_for(dtype == POLICY_F32 ? 4 : 2, W, grad);
   return D >= v ? v : 1;
 }
-dim3 grid_of(const ConvRun& q) {
-  return dim3((uint32_t)((q.items + q.rows - 1) / q.rows), (uint32_t)((q.packs + q.across - 1) / q.across));
-}
+// (below 2^23: what N * D < 2^28 leaves, workgroups half full)
+dim3 grid_of(const ConvRun& q) { return dim3(q.groups * (uint32_t)((q.packs + q.across - 1) / q.across)); }
 
 template <class T, int W, bool GRAD>
 void launch(const ConvRun& q, hipStream_t stream) {
@@ -565,7 +570,7 @@ hipError_t conv_forward_launch(const conv_args& a, hipStream_t stream) {
 int64_t conv_workspace_bytes(int32_t L, int32_t N, int32_t D, int32_t W, int32_t dtype) {
   if (L == 0 || N == 0 || D == 0) return 0;
   const ConvRun q = plan(L, N, D, pack_of(D, W, dtype, true), true);
-  const int64_t groups = grid_of(q).x;
+  const int64_t groups = q.groups;
   return up(groups * D * (W + 1) * 4) + up(sums_floats(groups, D * (W + 1)) * 4);
 }
 
@@ -585,7 +590,7 @@ hipError_t conv_backward_launch(const conv_grad_args& g, hipStream_t stream) {
   launch_any<true>(q, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t groups = grid_of(q).x;
+  const int64_t groups = q.groups;
   const int32_t dw = (int32_t)(D * W), d = (int32_t)D;
   const SumsOut out = {{g.dweight, g.dbias, nullptr}, {dw, dw + d, dw + d}};
   return sums_launch(q.params, groups, dw + d,

@@ -7,6 +7,8 @@
 // The order of the additions depends on the two sizes alone, and no summand
 // goes through more than 46 of them, whatever the rows: 17 in a run of 64 (15 of
 // a wave, 2 in LDS), twice, and 6 in each of at most two times 64 before.
+#include <algorithm>
+
 #include "block.hpp"
 
 namespace rl {
@@ -26,32 +28,37 @@ __global__ void __launch_bounds__(256) sums_kernel(const float* x, int64_t rows,
                                                    int64_t run, float* partial, SumsOut out) {
   __shared__ float s_sum[4][64];
   const int32_t lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int32_t c = blockIdx.x * 64 + lane;
   const int64_t r0 = blockIdx.y * run, r1 = r0 + run < rows ? r0 + run : rows;
-  float sum = 0.0f;
-  if (c < columns) {
-    int64_t r = r0 + w;
-    for (; r + 28 < r1; r += 32) {
-      float v[8];
+  // (one turn but where there are more columns than a grid holds workgroups)
+  for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < columns; c0 += (int64_t)gridDim.x * 64) {
+    const int64_t c = c0 + lane;
+    float sum = 0.0f;
+    if (c < columns) {
+      int64_t r = r0 + w;
+      for (; r + 28 < r1; r += 32) {
+        float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = x[(r + 4 * i) * columns + c];
+        for (int i = 0; i < 8; ++i) v[i] = x[(r + 4 * i) * columns + c];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += v[i];
+        for (int i = 0; i < 8; ++i) sum += v[i];
+      }
+      for (; r < r1; r += 4) sum += x[r * columns + c];
     }
-    for (; r < r1; r += 4) sum += x[r * columns + c];
+    s_sum[w][lane] = sum;
+    __syncthreads();
+    if (w == 0 && c < columns) {
+      sum = (s_sum[0][lane] + s_sum[1][lane]) + (s_sum[2][lane] + s_sum[3][lane]);
+      if (partial) {
+        partial[(int64_t)blockIdx.y * columns + c] = sum;
+      } else {
+        const int k = c < out.end[0] ? 0 : c < out.end[1] ? 1 : 2;
+        float* p = k == 0 ? out.out[0] : k == 1 ? out.out[1] : out.out[2];
+        const int32_t first = k == 0 ? 0 : k == 1 ? out.end[0] : out.end[1];
+        if (p) p[c - first] = sum;
+      }
+    }
+    __syncthreads();
   }
-  s_sum[w][lane] = sum;
-  __syncthreads();
-  if (w != 0 || c >= columns) return;
-  sum = (s_sum[0][lane] + s_sum[1][lane]) + (s_sum[2][lane] + s_sum[3][lane]);
-  if (partial) {
-    partial[(int64_t)blockIdx.y * columns + c] = sum;
-    return;
-  }
-  const int k = c < out.end[0] ? 0 : c < out.end[1] ? 1 : 2;
-  float* p = k == 0 ? out.out[0] : k == 1 ? out.out[1] : out.out[2];
-  const int32_t first = k == 0 ? 0 : k == 1 ? out.end[0] : out.end[1];
-  if (p) p[c - first] = sum;
 }
 
 // partial[run] = the sum of the rows 64 run .. 64 run + 63.  A wave's 16 rows
@@ -100,14 +107,14 @@ hipError_t sums_launch(const float* x, int64_t rows, int32_t columns, float* scr
                        const SumsOut& out, hipStream_t stream) {
   while (rows > kMostRows) {
     const int64_t fewer = (rows + kRun - 1) / kRun, blocks = fewer * ((columns + 63) / 64);
-    far_sums_kernel<<<dim3((uint32_t)(blocks < (1 << 20) ? blocks : 1 << 20)), 256, 0, stream>>>(
+    far_sums_kernel<<<dim3((uint32_t)std::min(blocks, (int64_t)1 << 20)), 256, 0, stream>>>(
         x, rows, columns, blocks, scratch);
     x = scratch;
     scratch += fewer * columns;
     rows = fewer;
   }
   const int64_t runs = runs_of(rows);
-  const uint32_t across = (uint32_t)((columns + 63) / 64);
+  const uint32_t across = (uint32_t)std::min((columns + 63) / 64, 1 << 20);
   if (runs > 1) {
     const int64_t run = (rows + runs - 1) / runs;
     sums_kernel<<<dim3(across, (uint32_t)runs), 256, 0, stream>>>(x, rows, columns, run, scratch, out);

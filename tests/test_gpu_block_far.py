@@ -86,3 +86,30 @@ def test_more_than_2_to_32_elements(rx):
         got = y.view(-1)[start:start + 1000].cpu().double().numpy()
         want = np.where(kept, x.view(-1)[start:start + 1000].cpu().double().numpy() * scale, 0.0)
         assert (np.abs(got - want) <= ref.fin("bf16", want, 2 * ref.U * np.abs(want))).all()
+
+
+@pytest.mark.parametrize("name", [torch.bfloat16, torch.float32])
+def test_as_many_channels_as_are_allowed(rx, name):
+    """2^28 - 1 channels of 3 taps: more workgroups across a row than a grid's
+    second dimension holds, 2^30 - 4 columns of parameters' gradients."""
+    D = 2 ** 28 - 1
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(1, 1, D, generator=g, device="cuda").to(name).requires_grad_()
+    w = torch.randn(D, 3, generator=g, device="cuda").requires_grad_()
+    bias = torch.randn(D, generator=g, device="cuda").requires_grad_()
+    y, _ = rx.causal_conv(x, w, bias, activation="none")
+    dy = torch.randn(1, 1, D, generator=g, device="cuda").to(name)
+    dx, dw, db = torch.autograd.grad(y, (x, w, bias), dy)
+    # one product each, exact in 64 bits, and its roundings to fp32 and to the type
+    u = ref.U if name == torch.float32 else ref.U + 2.0 ** -8
+    with torch.no_grad():
+        xf, dyf = x[0, 0].double(), dy[0, 0].double()
+        for got, want, near in ((dx[0, 0], dyf * w[:, 2], u), (dw[:, 2], dyf * xf, ref.U)):
+            off = (got.double() - want).abs_() - 1.01 * near * want.abs()
+            assert (off <= ref.TINY).all()
+            del off, want
+        p = xf * w[:, 2]
+        off = (y[0, 0].double() - (p + bias)).abs_() - 1.01 * u * (p + bias).abs()
+        off -= 1.01 * ref.U * p.abs_()
+        assert (off <= ref.TINY).all()
+        assert torch.equal(db, dy[0, 0].float()) and not dw[:, :2].any()
