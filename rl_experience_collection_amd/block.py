@@ -135,6 +135,12 @@ def _same(name, t, like, what):
                          f"{t.dtype} {tuple(t.shape)}")
 
 
+def _sizes(*sizes):
+    """The library's sizes are 32-bit; its own limits are below."""
+    if max(sizes) >> 31:
+        raise ValueError(f"sizes must be below 2^31, got {sizes}")
+
+
 def _rows_of(g):
     """A gradient whose last dimension is contiguous."""
     return g.contiguous() if g.shape[-1] > 1 and g.stride(-1) != 1 else g
@@ -187,6 +193,7 @@ class _CausalConv(torch.autograd.Function):
 
 def _conv_weights(x, weight, bias):
     D = x.shape[-1]
+    _sizes(*x.shape)
     if weight.dim() != 2:
         raise ValueError(f"weight must be [D, W], got {tuple(weight.shape)}")
     _exact("weight", weight, _f32, (D, weight.shape[1]))
@@ -345,6 +352,7 @@ def _scan_inputs(x, delta, rate, b, c, skip, gate, delta_bias, lead):
         _unit(name, t, t.dim())
     if b.shape != c.shape:
         raise ValueError(f"b and c must have one shape, got {tuple(b.shape)} and {tuple(c.shape)}")
+    _sizes(*x.shape, *b.shape)
     if b.dim() == lead + 2 and (b.shape[lead] < 1 or D % b.shape[lead]):
         raise ValueError(f"the groups of b and c must divide the width: {b.shape[lead]} of {D}")
     _exact("skip", skip, _f32, (D,))

@@ -522,3 +522,23 @@ def test_scan_without_channels_has_gradients_of_zero(silent, groups):
     finally:
         torch.use_deterministic_algorithms(False)
     assert all(torch.equal(g, torch.zeros_like(t)) for g, t in zip(grads, bc))
+
+
+def test_sizes_that_32_bits_do_not_hold_are_refused(rx):
+    far = 2 ** 31
+    one = torch.zeros(1)
+    for x in (one.expand(far, 1, 1), one.expand(1, far, 1)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            rx.causal_conv(x, torch.zeros(1, 1))
+        b = torch.zeros(5).expand(x.shape[0], x.shape[1], 5)
+        with pytest.raises(ValueError, match="2\\^31"):
+            rx.selective_scan(x, x, torch.zeros(1, 5), b, b)
+    x = one.expand(2 ** 32 + 5, 1)
+    with pytest.raises(ValueError, match="2\\^31"):
+        rx.causal_conv_step(x, torch.zeros(1, 1), torch.zeros(2 ** 32 + 5, 0, 1))
+    b = torch.zeros(5).expand(2 ** 32 + 5, 5)
+    with pytest.raises(ValueError, match="2\\^31"):
+        rx.selective_scan_step(x, x, torch.zeros(1, 5), b, b, one.expand(2 ** 32 + 5, 1, 5))
+    x, b = torch.zeros(0, 3, 0), torch.zeros(0, 3, far, 5)
+    with pytest.raises(ValueError, match="2\\^31"):
+        rx.selective_scan(x, x, torch.zeros(0, 5), b, b)
