@@ -141,7 +141,8 @@ typedef struct {
   float *dskip, *ddelta_bias, *dstate; /* NULL: not written */
 } scan_grad_args;
 
-/* Floats of `kept`: about ceil(L / 8) * N * D * S. */
+/* Floats of `kept`: about ceil(L / 8) * N * D * S (S / 2 bytes for each element
+ * of x: at 16 states four times a bf16 x). */
 int64_t scan_kept(int32_t steps, int32_t rows, int32_t width, int32_t states, int32_t groups);
 /* Bytes (0 for most sizes), or a negative ROLLOUT_E* code. */
 int64_t scan_workspace(int32_t steps, int32_t rows, int32_t width, int32_t states, int32_t groups);
@@ -162,7 +163,7 @@ int scan_step(const scan_args *args, void *hip_stream);
  * Between two blocks, for each row r of D values, with
  * rms(v) = v / sqrt(mean(v^2) + eps):
  *   u = rms(branch) branch_weight  (or branch itself with branch_norm = 0)
- *   z = act(gate) u,               act: none, sigmoid or silu
+ *   z = act(gate) u,               act: none, sigmoid or silu (without a gate z = u)
  *   z = drop(z)                    as drop_forward numbers [R][D], stream included
  *   stream = residual_scale residual + branch_scale z
  *   normed = rms(stream) weight

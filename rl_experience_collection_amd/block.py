@@ -370,7 +370,8 @@ def selective_scan(x, delta, rate, b, c, skip=None, gate=None, delta_bias=None, 
     [N, D, S] float32 or None (zero); dones: [L, N] uint8 or bool, a
     collection's, or None.  The step size is softplus(delta + delta_bias), or
     delta + delta_bias itself.  y has x's dtype, new_state is float32 and
-    starts the next rollout.  Gradients flow to every input but dones."""
+    starts the next rollout.  Gradients flow to every input but dones; a call
+    that records them keeps S / 2 bytes of states for each element of x."""
     if _forward_ad._current_level >= 0:
         _no_tangent("selective_scan", x, delta, rate, b, c, skip, gate, delta_bias, state)
     _scan_inputs(x, delta, rate, b, c, skip, gate, delta_bias, 2)
@@ -516,7 +517,9 @@ def residual_norm(residual, branch=None, weight=None, *, branch_weight=None, gat
     block's norm.  weight, branch_weight: [D] float32 or None (1).
     branch_norm=False takes the branch as it is.  gate: like the branch, or
     [D] float32 for all rows; activation: "none", "sigmoid" or "silu" of the
-    gate.  dropout, seed and offset are `dropout`'s on the stream's shape.
+    gate (without a gate it has no effect).  dropout, seed and offset are
+    `dropout`'s on the stream's shape: two calls of one seed and offset drop the
+    same places.
     Gradients flow to residual, branch, weights and gate."""
     act = _activation(activation, ("none", "sigmoid", "silu"))
     if _forward_ad._current_level >= 0:

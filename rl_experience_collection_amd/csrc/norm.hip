@@ -9,9 +9,9 @@
 // stream that was rounded when it was stored, and a thread sums the weights'
 // gradients of its own columns over all rows that it takes.
 //
-// HBM bounds them: 1,024,000 x 128 bf16 with gate and dropout takes 265 us
-// forward (4.9 TB/s) and 430 us backward (4.9 TB/s).  Where they fit the caches,
-// latency: 4099 x 5001 fp16 takes 33 and 71 us.
+// HBM bounds them: 1,024,000 x 128 bf16 with gate and dropout takes 262 us
+// forward (5.0 TB/s) and 430 us backward (4.9 TB/s).  Where they fit the caches,
+// latency: 4099 x 5001 fp16 takes 32 and 71 us.
 #include <algorithm>
 
 #include "block.hpp"
@@ -171,7 +171,8 @@ struct Share {
   }
 };
 
-// Which of the V elements from i are kept: bit j for element i + j.
+// Which of the V elements from i are kept: bit j for element i + j.  (A pack of
+// four uses half of its draw, one that starts inside eight elements draws twice.)
 template <int V>
 __device__ __forceinline__ uint32_t kept_bits(const DropRule& rule, uint64_t seed, uint64_t i) {
   const uint32_t off = (uint32_t)i & 7;
@@ -204,9 +205,10 @@ __device__ __forceinline__ void activate(int32_t kind, float g, float& act, floa
   }
 }
 
-// Waves a SIMD: 6, so that two rows of up to 768 threads share a compute unit
-// (4099 x 5001 fp16 took 50 us so, 63 with 5; that variant has come down to 6
-// without being told, many others have not), where that leaves enough registers.
+// Waves a SIMD: 6, so that two rows of up to 768 threads share a compute unit,
+// where that leaves enough registers (none are spilled).  With gate and dropout
+// 419 MB a tensor of bf16 take 502 us at width 5001 so, 591 where the compiler is
+// not told, but 555 and 531 at 600; other widths and gates are within 3%.
 template <class T>
 constexpr int forward_waves(int TPR, int gate) {
   return TPR > 64 && !(T::kBytes == 4 && gate == kRowGate) ? 6 : 1;
@@ -556,8 +558,9 @@ __global__ void __launch_bounds__(threads_of(TPR)) norm_backward_kernel(const No
   if (GATE == kChannelGate) put(2, dgc);
 }
 
-// Threads of a row, of 8 elements each: up to 64 the powers of two that hold
-// it, then as many waves as it needs.
+// Threads of a row, of 8 elements each: 8, 16 or 64, then as many waves as it
+// needs.  (Those past its end go over its last pack again: of 64, 32 at width
+// 256, and 47 at 129.)
 int32_t threads_for(int32_t D) {
   return D <= 64 ? 8 : D <= 128 ? 16 : D <= 512 ? 64 : (D + 511) / 512 * 64;
 }

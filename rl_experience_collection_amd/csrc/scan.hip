@@ -292,11 +292,13 @@ void launch_states(const ScanRun& q, hipStream_t stream) {
 
 // A chunk has four units at least, and chunks are made until two waves a SIMD
 // have work (1024 SIMDs; 16,385 x 2 x 1000 fp16 took 332 us so, 340 and 378 with
-// three and four); a scan of more than a quarter of that many columns is not
-// cut, as the second look at its inputs would cost what the cut gains.  More
-// than 16 summaries are joined once for all chunks (that scan of 64 chunks takes
-// 301 us so and 319 where every chunk joins those before it; 32 chunks 280 and
-// 286; 16 chunks 278 and 277, 8 chunks of 64 steps 84 and 77).
+// three and four), from columns of up to a quarter of that: 500 steps of 512
+// waves, fp32 with a gate, take 143 us forward and 291 backward cut in four, 182
+// and 525 whole.  Above, two chunks lose forward (768 waves: 222 us, 181 whole;
+// 520: 178 and 183) what they would gain backward (477 and 521; 361 and 524).
+// More than 16 summaries are joined once for all chunks (16,385 x 2 x 1000 in 64
+// takes 301 us so and 319 where every chunk joins those before it; in 32 280 and
+// 286; in 16 278 and 277, 8 chunks of 64 steps 84 and 77).
 ScanPlan scan_plan(int32_t L, int32_t N, int32_t D, int32_t S, int32_t G) {
   ScanPlan p;
   p.group_width = D / G;

@@ -11,6 +11,8 @@
 // same for all quads), and sums over channels (the gradients of b and c) run
 // over a lane's own four channels for free before lanes have to meet.  With
 // more than 16 states a workgroup's waves take 16 each of the same channels.
+// States and channels that do not exist cost what others do: 1 state as much as
+// 16, 17 as 32, 33 as 64, a group of 16 channels as one of 64.
 //
 // Steps go in units of eight.  Long scans of few columns are cut into chunks
 // of units: one launch finds what each chunk makes of a state of zero and how

@@ -269,3 +269,11 @@ def test_gradients_where_all_is_dropped(rx, D, act):
     got = dict(zip(LEAVES, torch.autograd.grad(out, list(leaves.values()), (dev["dstream"], dev["dnormed"]))))
     assert not got["branch"].any() and not got["branch_weight"].any() and not got["gate"].any()
     assert torch.isfinite(got["residual"]).all() and torch.isfinite(got["weight"]).all()
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_an_activation_without_a_gate_has_no_effect(rx, act):
+    i, g = inputs(5, 40, "f32", "none", 13)
+    dev = {k: v.cuda() for k, v in i.items() if v is not None}
+    for a, b in zip(rx.residual_norm(**dev), rx.residual_norm(**dev, activation=act)):
+        assert torch.equal(a, b)
