@@ -565,8 +565,8 @@ int32_t threads_for(int32_t D) {
   return D <= 64 ? 8 : D <= 128 ? 16 : D <= 512 ? 64 : (D + 511) / 512 * 64;
 }
 // Waves of a compute unit: 20 going forward, 16 where there is no branch, whose
-// work would hide the loads of more (419 MB a tensor of bf16: 289 us at width 300
-// and 298 at 600 so, 333 and 332 with 20; 233 either way at 8000), 12 backward.
+// work would hide the loads of more (419 MB a tensor of bf16: 299 us at width 600
+// so, 332 with 20; 233 either way at 8000), 12 backward.
 constexpr int32_t kGradWaves = 12;
 int32_t waves_of(const norm_args& a, bool grad) { return grad ? kGradWaves : a.branch ? 20 : 16; }
 // Workgroups: what is resident on 256 compute units, so that a workgroup reads
@@ -620,12 +620,20 @@ void launch_any(const NormRun& q, hipStream_t stream) {
 
 int64_t up(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
+// Whether outputs go past the caches: large ones (kPastBytes), but for rows of less
+// than 1 KB that are no whole lines of 128 bytes, whose lines two workgroups fill.
+// Forward of 419 MB a tensor, past and through: bf16 of width 200, no branch 319 and
+// 286 us, with one 431 and 391; fp32 of 100, 403 and 351; bf16 of 600, 432 and 437.
+bool stored_past(int64_t R, int64_t row_bytes) {
+  return R * row_bytes > kPastBytes && (row_bytes % 128 == 0 || row_bytes >= 1024);
+}
+
 NormRun run_of(const norm_args& a) {
   NormRun q = {};
   q.g.f = a;
   q.rule = drop_rule(a.drop, a.seed, a.seed_at, a.offset);
   q.inv_width = (float)(1.0 / a.width);
-  q.past = a.rows * a.width * (a.dtype == POLICY_F32 ? 4 : 2) > kPastBytes;
+  q.past = stored_past(a.rows, (int64_t)a.width * (a.dtype == POLICY_F32 ? 4 : 2));
   return q;
 }
 
